@@ -20,12 +20,14 @@ import ctypes
 import torch
 
 from . import _native
-from ._native import DEVICE_BAD_ID, DEVICE_TIMEOUT, DflashError  # noqa: F401
+from ._native import (DEVICE_BAD_ID, DEVICE_BAD_LENGTH, DEVICE_NO_PAGES,  # noqa: F401
+                      DEVICE_TIMEOUT, DflashError)
 
 __all__ = [
     "dflash_topk_candidates", "dflash_hidden_projection", "dflash_candidate_edges",
     "dflash_selector", "dflash_selector_forward", "dflash_lmhead_topk", "dflash_selector_lmhead",
-    "dflash_best_path",
+    "dflash_best_path", "dflash_block_tables", "dflash_store_kv", "dflash_paged_attention",
+    "dflash_paged_attention_workspace_bytes",
     "dflash_topk_workspace_bytes",
     "dflash_selector_workspace_bytes", "dflash_lmhead_topk_workspace_bytes",
     "dflash_selector_lmhead_workspace_bytes",
@@ -341,6 +343,173 @@ def dflash_best_path(edges: torch.Tensor, cand_ids: torch.Tensor, path: torch.Te
         _native.check(lib.dflash_best_path(_ptr(edges), _ptr(cand_ids), R, S, K, _ptr(path),
                                            _ptr(tokens), _ptr(score), _stream(dev, stream)))
     return path, tokens, score
+
+
+def dflash_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor,
+                        held_pages: torch.Tensor, free_pages: torch.Tensor,
+                        block_table: torch.Tensor, page_size: int, T: int,
+                        query_start: torch.Tensor | None = None,
+                        kv_lens: torch.Tensor | None = None,
+                        held_out: torch.Tensor | None = None,
+                        positions: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                        pages_needed: torch.Tensor | None = None, stream=None):
+    """One step's block tables and slots: returns (query_start [R + 1], kv_lens [R], held_out [R],
+    positions [T], slots [T] int64, pages_needed [1]), all int32 but the slots.
+
+    block_table int32 [R, max_pages] gets each request's new pages, taken in order from
+    free_pages; T is the room for new tokens (their number, or more for a padded batch).
+    """
+    lib = _native.load()
+    if context_lens.dim() != 1 or free_pages.dim() != 1 or block_table.dim() != 2:
+        raise ValueError("context_lens must be [R], free_pages [n], block_table [R, max_pages]")
+    R, max_pages = context_lens.shape[0], block_table.shape[1]
+    _need(context_lens, "context_lens", torch.int32)
+    _need(new_lens, "new_lens", torch.int32, (R,))
+    _need(held_pages, "held_pages", torch.int32, (R,))
+    _need(free_pages, "free_pages", torch.int32)
+    _need(block_table, "block_table", torch.int32, (R, max_pages))
+    dev = context_lens.device
+    with torch.cuda.device(dev):
+        if query_start is None:
+            query_start = torch.empty((R + 1,), dtype=torch.int32, device=dev)
+        if kv_lens is None:
+            kv_lens = torch.empty((R,), dtype=torch.int32, device=dev)
+        if held_out is None:
+            held_out = torch.empty((R,), dtype=torch.int32, device=dev)
+        if positions is None:
+            positions = torch.empty((T,), dtype=torch.int32, device=dev)
+        if slots is None:
+            slots = torch.empty((T,), dtype=torch.int64, device=dev)
+        if pages_needed is None:
+            pages_needed = torch.empty((1,), dtype=torch.int32, device=dev)
+        _need(query_start, "query_start", torch.int32, (R + 1,))
+        _need(kv_lens, "kv_lens", torch.int32, (R,))
+        _need(held_out, "held_out", torch.int32, (R,))
+        _need(positions, "positions", torch.int32, (T,))
+        _need(slots, "slots", torch.int64, (T,))
+        _need(pages_needed, "pages_needed", torch.int32, (1,))
+        _native.check(lib.dflash_block_tables(
+            _ptr(context_lens), _ptr(new_lens), _ptr(held_pages), _ptr(free_pages), R,
+            free_pages.shape[0], page_size, max_pages, T, _ptr(block_table), _ptr(query_start),
+            _ptr(kv_lens), _ptr(held_out), _ptr(positions), _ptr(slots), _ptr(pages_needed),
+            _stream(dev, stream)))
+    return query_start, kv_lens, held_out, positions, slots, pages_needed
+
+
+_DTYPES = {torch.bfloat16: _native.BF16, torch.float16: _native.FP16,
+           torch.float8_e4m3fn: _native.E4M3}
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None) -> None:
+    """Checks a [rows, heads, head_dim] tensor that may be strided in all but the last."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
+        raise ValueError(f"{name} must be [T, heads, head_dim], head_dim contiguous")
+    if t.dtype not in (torch.bfloat16, torch.float16) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be bf16 or fp16 (and of one type), got {t.dtype}")
+
+
+def _kv_cache(key_cache: torch.Tensor, value_cache: torch.Tensor, k_scale: float,
+              v_scale: float) -> _native.KvCache:
+    for t, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] != 1):
+            raise ValueError(f"{name} must be [pages, page_size, kv_heads, head_dim], "
+                             "head_dim contiguous")
+        if t.dtype not in _DTYPES:
+            raise ValueError(f"{name} must be bf16, fp16 or float8_e4m3fn, got {t.dtype}")
+    if (key_cache.shape != value_cache.shape or key_cache.dtype != value_cache.dtype
+            or key_cache.stride() != value_cache.stride()):
+        raise ValueError("key_cache and value_cache must have one shape, type and strides")
+    P, page_size, H, D = key_cache.shape
+    ps, ts, hs, _ = key_cache.stride()
+    return _native.KvCache(key_cache.data_ptr(), value_cache.data_ptr(), ps, ts, hs, P, page_size,
+                           H, D, _DTYPES[key_cache.dtype], k_scale, v_scale)
+
+
+def dflash_store_kv(key: torch.Tensor, value: torch.Tensor, slots: torch.Tensor,
+                    key_cache: torch.Tensor, value_cache: torch.Tensor, k_scale: float = 1.0,
+                    v_scale: float = 1.0, stream=None):
+    """Store key and value [T, kv_heads, head_dim] (bf16 or fp16, strided views allowed) at slots
+    int64 [T] of the caches [pages, page_size, kv_heads, head_dim]: returns (key_cache,
+    value_cache). A float8_e4m3fn cache holds x / scale; a negative slot stores nothing.
+    """
+    lib = _native.load()
+    _rows(key, "key")
+    _rows(value, "value", key.dtype)
+    cache = _kv_cache(key_cache, value_cache, k_scale, v_scale)
+    if tuple(key.shape[1:]) != (cache.kv_heads, cache.head_dim) or value.shape != key.shape:
+        raise ValueError(f"key and value must be [T, {cache.kv_heads}, {cache.head_dim}], got "
+                         f"{tuple(key.shape)} and {tuple(value.shape)}")
+    T = key.shape[0]
+    _need(slots, "slots", torch.int64, (T,))
+    dev = key.device
+    with torch.cuda.device(dev):
+        _native.check(lib.dflash_store_kv(
+            _ptr(key), _ptr(value), _DTYPES[key.dtype], _ptr(slots), T, key.stride(0),
+            key.stride(1), value.stride(0), value.stride(1), ctypes.byref(cache),
+            _stream(dev, stream)))
+    return key_cache, value_cache
+
+
+def dflash_paged_attention_workspace_bytes(R: int, T: int, q_heads: int, kv_heads: int,
+                                           head_dim: int) -> int:
+    return int(_native.load().dflash_paged_attention_workspace_bytes(R, T, q_heads, kv_heads,
+                                                                     head_dim))
+
+
+def dflash_paged_attention(query: torch.Tensor, key_cache: torch.Tensor,
+                           value_cache: torch.Tensor, block_table: torch.Tensor,
+                           query_start: torch.Tensor, kv_lens: torch.Tensor,
+                           scale: float | None = None, window_left: int = -1,
+                           window_right: int = 0, softcap: float = 0.0, k_scale: float = 1.0,
+                           v_scale: float = 1.0, out: torch.Tensor | None = None,
+                           lse: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, stream=None):
+    """Attention of new tokens over the paged cache, which holds their own keys and values too:
+    returns (out [T, q_heads, head_dim], lse fp32 [T, q_heads]).
+
+    query [T, q_heads, head_dim] bf16 or fp16 (strided views allowed); the caches [pages,
+    page_size, kv_heads, head_dim] of its type or float8_e4m3fn, in any order of page rows and
+    heads; block_table int32 [R, max_pages], query_start int32 [R + 1] and kv_lens int32 [R] as
+    dflash_block_tables gives them. A token at position p sees keys p - window_left to
+    p + window_right (-1: no bound; window_right 0 is causal). scale defaults to
+    1 / sqrt(head_dim).
+    """
+    lib = _native.load()
+    _rows(query, "query")
+    cache = _kv_cache(key_cache, value_cache, k_scale, v_scale)
+    T, Hq, D = query.shape
+    if D != cache.head_dim:
+        raise ValueError(f"query has head_dim {D}, the cache {cache.head_dim}")
+    if block_table.dim() != 2 or kv_lens.dim() != 1:
+        raise ValueError("block_table must be [R, max_pages] and kv_lens [R]")
+    R, max_pages = block_table.shape
+    _need(block_table, "block_table", torch.int32)
+    _need(query_start, "query_start", torch.int32, (R + 1,))
+    _need(kv_lens, "kv_lens", torch.int32, (R,))
+    dev = query.device
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty((T, Hq, D), dtype=query.dtype, device=dev)
+        if lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        _need(out, "out", query.dtype, (T, Hq, D))
+        _need(lse, "lse", torch.float32, (T, Hq))
+        ws = _workspace(lib.dflash_paged_attention_workspace_bytes(R, T, Hq, cache.kv_heads, D),
+                        dev, workspace)
+        _native.check(lib.dflash_paged_attention(
+            _ptr(query), _DTYPES[query.dtype], T, Hq, query.stride(0), query.stride(1),
+            ctypes.byref(cache), _ptr(block_table), R, max_pages, _ptr(query_start),
+            _ptr(kv_lens), D ** -0.5 if scale is None else scale, window_left, window_right,
+            softcap, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(dev, stream)))
+    return out, lse
 
 
 def dflash_device_status(clear: bool = True) -> int:

@@ -21,10 +21,26 @@ DFLASH_NO_DEVICE = 5
 
 DEVICE_BAD_ID = 0x1
 DEVICE_TIMEOUT = 0x2
+DEVICE_BAD_LENGTH = 0x4
+DEVICE_NO_PAGES = 0x8
+
+BF16, FP16, E4M3 = 0, 1, 2   # dflash_dtype
 
 HEADER = os.path.join(_build.ROOT, "include", "dflash.h")
 
 _p, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_ll = ctypes.c_longlong
+
+
+class KvCache(ctypes.Structure):
+    """dflash_kv_cache."""
+
+    _fields_ = [("key", _p), ("value", _p), ("page_stride", _ll), ("token_stride", _ll),
+                ("head_stride", _ll), ("num_pages", _i), ("page_size", _i), ("kv_heads", _i),
+                ("head_dim", _i), ("dtype", _i), ("k_scale", _f), ("v_scale", _f)]
+
+
+_cache = ctypes.POINTER(KvCache)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -47,6 +63,12 @@ SIGNATURES = {
     "dflash_selector_lmhead_workspace_bytes": (_sz, [_i, _i, _i, _i]),
     "dflash_selector_lmhead": (_i, [_p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _f, _f, _p,
                                     _p, _p, _p, _p, _sz, _p]),
+    "dflash_block_tables": (_i, [_p, _p, _p, _p, _i, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _p,
+                                 _p]),
+    "dflash_store_kv": (_i, [_p, _p, _i, _p, _i, _ll, _ll, _ll, _ll, _cache, _p]),
+    "dflash_paged_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
+    "dflash_paged_attention": (_i, [_p, _i, _i, _i, _ll, _ll, _cache, _p, _i, _i, _p, _p, _f, _i,
+                                    _i, _f, _p, _p, _p, _sz, _p]),
     "dflash_device_status": (_i, [ctypes.POINTER(ctypes.c_uint32), _i]),
     "dflash_selftest_wait_timeout": (_i, []),
     "dflash_trace_begin": (_i, [_i]),

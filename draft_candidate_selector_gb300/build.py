@@ -1,6 +1,6 @@
 """Builds the selector's CUDA library, libdflash_gb300.so, in-tree with nvcc.
 
-Target: sm_103a only (GB300); tcgen05 and TMA need the "a" architecture. The four
+Target: sm_103a only (GB300); tcgen05 and TMA need the "a" architecture. The
 translation units compile in parallel, then link into one shared library against the
 shared CUDA runtime, so the library and PyTorch use the same runtime in one process.
 Outputs go to draft_candidate_selector_gb300/_build/ (git-ignored).
@@ -20,7 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(OUT_DIR, "libdflash_gb300.so")
-SOURCES = ["api.cu", "topk.cu", "projection.cu", "edges.cu", "lmhead.cu", "path.cu"]
+SOURCES = ["api.cu", "topk.cu", "projection.cu", "edges.cu", "lmhead.cu", "path.cu",
+           "kvcache.cu", "attention_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -163,11 +163,60 @@ dflash_status check_ptr4(const void* p, const char* name) {
     return DFLASH_OK;
 }
 
+// For 8-byte elements.
+dflash_status check_ptr8(const void* p, const char* name) {
+    if (!p) return fail(DFLASH_INVALID_ARGUMENT, "%s is NULL", name);
+    if ((reinterpret_cast<uintptr_t>(p) & 7u) != 0)
+        return fail(DFLASH_INVALID_ARGUMENT, "%s is not 8-byte aligned", name);
+    return DFLASH_OK;
+}
+
 #define DFLASH_TRY(expr)                     \
     do {                                     \
         dflash_status _s = (expr);           \
         if (_s != DFLASH_OK) return _s;      \
     } while (0)
+
+// A stride in elements that keeps rows aligned for loads of 8 elements.
+dflash_status check_stride(long long stride, int multiple, const char* name) {
+    if (stride < 0) return fail(DFLASH_INVALID_ARGUMENT, "%s=%lld must be >= 0", name, stride);
+    if (stride % multiple != 0)
+        return fail(DFLASH_UNSUPPORTED, "%s=%lld: must be a multiple of %d elements", name, stride,
+                    multiple);
+    return DFLASH_OK;
+}
+
+// Checks a dflash_kv_cache whose users have queries, or new keys and values, of type dtype.
+dflash_status check_cache(const dflash_kv_cache* c, int dtype, dflash::KvCache* out) {
+    if (!c) return fail(DFLASH_INVALID_ARGUMENT, "cache is NULL");
+    if (dtype != DFLASH_BF16 && dtype != DFLASH_FP16)
+        return fail(DFLASH_INVALID_ARGUMENT, "dtype=%d: must be DFLASH_BF16 or DFLASH_FP16", dtype);
+    if (c->dtype != dtype && c->dtype != DFLASH_E4M3)
+        return fail(DFLASH_INVALID_ARGUMENT, "cache dtype=%d: must be dtype=%d or DFLASH_E4M3",
+                    c->dtype, dtype);
+    if (c->num_pages < 1 || c->page_size < 1 || c->kv_heads < 1 || c->head_dim < 1)
+        return fail(DFLASH_INVALID_ARGUMENT,
+                    "num_pages, page_size, kv_heads and head_dim must be >= 1 (got %d, %d, %d, %d)",
+                    c->num_pages, c->page_size, c->kv_heads, c->head_dim);
+    const int mult = c->dtype == DFLASH_E4M3 ? 16 : 8;
+    if (c->head_dim % mult != 0 || c->head_dim > 256)
+        return fail(DFLASH_UNSUPPORTED, "head_dim=%d: must be a multiple of %d up to 256",
+                    c->head_dim, mult);
+    DFLASH_TRY(check_stride(c->page_stride, mult, "page_stride"));
+    DFLASH_TRY(check_stride(c->token_stride, mult, "token_stride"));
+    DFLASH_TRY(check_stride(c->head_stride, mult, "head_stride"));
+    if (!(c->k_scale > 0.f) || isinf(c->k_scale) || !(c->v_scale > 0.f) || isinf(c->v_scale))
+        return fail(DFLASH_INVALID_ARGUMENT, "k_scale=%g and v_scale=%g must be finite and > 0",
+                    (double)c->k_scale, (double)c->v_scale);
+    if (c->dtype != DFLASH_E4M3 && (c->k_scale != 1.f || c->v_scale != 1.f))
+        return fail(DFLASH_INVALID_ARGUMENT, "k_scale and v_scale must be 1 without DFLASH_E4M3");
+    DFLASH_TRY(check_ptr(c->key, "cache key"));
+    DFLASH_TRY(check_ptr(c->value, "cache value"));
+    *out = dflash::KvCache{c->key, c->value, c->page_stride, c->token_stride, c->head_stride,
+                           c->num_pages, c->page_size, c->kv_heads, c->head_dim, c->dtype,
+                           c->k_scale, c->v_scale};
+    return DFLASH_OK;
+}
 
 // A named NVTX range around one library call (host side: it brackets the argument checks and
 // the enqueue, and profilers attach the call's CUDA launches to it). Free when no tool is
@@ -555,6 +604,139 @@ dflash_status dflash_selector_lmhead(const uint16_t* hidden, const uint16_t* lm_
                              rank, edges, status, st);
     if (e != cudaSuccess) return cuda_fail(e, "edges launch");
     if (ev && (e = cudaEventRecord(ev[3], st)) != cudaSuccess) return cuda_fail(e, "trace event");
+    return ok();
+}
+
+dflash_status dflash_block_tables(const int32_t* context_lens, const int32_t* new_lens,
+                                  const int32_t* held_pages, const int32_t* free_pages, int R,
+                                  int n_free, int page_size, int max_pages, int T,
+                                  int32_t* block_table, int32_t* query_start, int32_t* kv_lens,
+                                  int32_t* held_out, int32_t* positions, int64_t* slots,
+                                  int32_t* pages_needed, dflash_stream_t stream) {
+    NvtxRange range("dflash_block_tables");
+    if (R < 1 || page_size < 1 || max_pages < 1 || T < 0 || n_free < 0)
+        return fail(DFLASH_INVALID_ARGUMENT,
+                    "R, page_size and max_pages must be >= 1, T and n_free >= 0 (got %d, %d, %d, "
+                    "%d, %d)", R, page_size, max_pages, T, n_free);
+    if (R > dflash::kMaxTableRequests)
+        return fail(DFLASH_UNSUPPORTED, "R=%d: block tables support R <= %d", R,
+                    dflash::kMaxTableRequests);
+    DFLASH_TRY(check_ptr4(context_lens, "context_lens"));
+    DFLASH_TRY(check_ptr4(new_lens, "new_lens"));
+    DFLASH_TRY(check_ptr4(held_pages, "held_pages"));
+    if (n_free > 0) DFLASH_TRY(check_ptr4(free_pages, "free_pages"));
+    DFLASH_TRY(check_ptr4(block_table, "block_table"));
+    DFLASH_TRY(check_ptr4(query_start, "query_start"));
+    DFLASH_TRY(check_ptr4(kv_lens, "kv_lens"));
+    DFLASH_TRY(check_ptr4(held_out, "held_out"));
+    if (T > 0) {
+        DFLASH_TRY(check_ptr4(positions, "positions"));
+        DFLASH_TRY(check_ptr8(slots, "slots"));
+    }
+    DFLASH_TRY(check_ptr4(pages_needed, "pages_needed"));
+    if (held_out == held_pages || kv_lens == context_lens)
+        return fail(DFLASH_INVALID_ARGUMENT,
+                    "held_out must not be held_pages, nor kv_lens context_lens");
+    dflash::DeviceInfo dev;
+    uint32_t* status = nullptr;
+    DFLASH_TRY(current_device(&dev, &status));
+    const dflash::BlockTableArgs a{context_lens, new_lens, held_pages, free_pages, R, n_free,
+                                   page_size, max_pages, T, block_table, query_start, kv_lens,
+                                   held_out, positions, slots, pages_needed};
+    cudaError_t e = dflash::launch_block_tables(dev, a, status,
+                                                reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "block tables launch");
+    return ok();
+}
+
+dflash_status dflash_store_kv(const void* key, const void* value, int dtype, const int64_t* slots,
+                              int T, long long key_token_stride, long long key_head_stride,
+                              long long value_token_stride, long long value_head_stride,
+                              const dflash_kv_cache* cache, dflash_stream_t stream) {
+    NvtxRange range("dflash_store_kv");
+    if (T < 0) return fail(DFLASH_INVALID_ARGUMENT, "T=%d must be >= 0", T);
+    dflash::KvCache c;
+    DFLASH_TRY(check_cache(cache, dtype, &c));
+    DFLASH_TRY(check_stride(key_token_stride, 8, "key_token_stride"));
+    DFLASH_TRY(check_stride(key_head_stride, 8, "key_head_stride"));
+    DFLASH_TRY(check_stride(value_token_stride, 8, "value_token_stride"));
+    DFLASH_TRY(check_stride(value_head_stride, 8, "value_head_stride"));
+    if (T == 0) return ok();
+    DFLASH_TRY(check_ptr(key, "key"));
+    DFLASH_TRY(check_ptr(value, "value"));
+    DFLASH_TRY(check_ptr8(slots, "slots"));
+    dflash::DeviceInfo dev;
+    uint32_t* status = nullptr;
+    DFLASH_TRY(current_device(&dev, &status));
+    cudaError_t e = dflash::launch_store_kv(dev, key, value, dtype, slots, T, key_token_stride,
+                                            key_head_stride, value_token_stride, value_head_stride,
+                                            c, status, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "key-value store launch");
+    return ok();
+}
+
+size_t dflash_paged_attention_workspace_bytes(int R, int T, int q_heads, int kv_heads,
+                                              int head_dim) {
+    if (R < 1 || T < 0 || q_heads < 1 || kv_heads < 1 || head_dim < 1) {
+        fail(DFLASH_INVALID_ARGUMENT, "R, q_heads, kv_heads and head_dim must be >= 1, T >= 0");
+        return 0;
+    }
+    if (current_device(nullptr, nullptr) != DFLASH_OK) return 0;
+    return 16;
+}
+
+dflash_status dflash_paged_attention(const void* query, int dtype, int T, int q_heads,
+                                     long long q_token_stride, long long q_head_stride,
+                                     const dflash_kv_cache* cache, const int32_t* block_table,
+                                     int R, int max_pages, const int32_t* query_start,
+                                     const int32_t* kv_lens, float scale, int window_left,
+                                     int window_right, float softcap, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes,
+                                     dflash_stream_t stream) {
+    NvtxRange range("dflash_paged_attention");
+    if (T < 0 || R < 1 || max_pages < 1 || q_heads < 1)
+        return fail(DFLASH_INVALID_ARGUMENT,
+                    "R, max_pages and q_heads must be >= 1, T >= 0 (got %d, %d, %d, %d)", R,
+                    max_pages, q_heads, T);
+    dflash::KvCache c;
+    DFLASH_TRY(check_cache(cache, dtype, &c));
+    if (q_heads % c.kv_heads != 0)
+        return fail(DFLASH_INVALID_ARGUMENT, "q_heads=%d must be a multiple of kv_heads=%d", q_heads,
+                    c.kv_heads);
+    if ((long long)T * q_heads > (1LL << 31) - 1)
+        return fail(DFLASH_INVALID_ARGUMENT, "T*q_heads=%lld rows exceeds 2^31-1",
+                    (long long)T * q_heads);
+    if (!(scale > 0.f) || isinf(scale))
+        return fail(DFLASH_INVALID_ARGUMENT, "scale=%g must be finite and > 0", (double)scale);
+    if (window_left < -1 || window_right < -1)
+        return fail(DFLASH_INVALID_ARGUMENT, "window_left=%d and window_right=%d must be >= -1",
+                    window_left, window_right);
+    if (!(softcap >= 0.f) || isinf(softcap))
+        return fail(DFLASH_INVALID_ARGUMENT, "softcap=%g must be finite and >= 0 (0 = no cap)",
+                    (double)softcap);
+    DFLASH_TRY(check_stride(q_token_stride, 8, "q_token_stride"));
+    DFLASH_TRY(check_stride(q_head_stride, 8, "q_head_stride"));
+    if (T == 0) return ok();
+    DFLASH_TRY(check_ptr(query, "query"));
+    DFLASH_TRY(check_ptr4(block_table, "block_table"));
+    DFLASH_TRY(check_ptr4(query_start, "query_start"));
+    DFLASH_TRY(check_ptr4(kv_lens, "kv_lens"));
+    DFLASH_TRY(check_ptr(out, "out"));
+    if (lse) DFLASH_TRY(check_ptr4(lse, "lse"));
+    DFLASH_TRY(check_ptr(workspace, "workspace"));
+    dflash::DeviceInfo dev;
+    uint32_t* status = nullptr;
+    DFLASH_TRY(current_device(&dev, &status));
+    const dflash::AttentionArgs a{query, dtype, T, q_heads, q_token_stride, q_head_stride, c,
+                                  block_table, R, max_pages, query_start, kv_lens, scale,
+                                  window_left, window_right, softcap, out, lse};
+    const size_t need = dflash_paged_attention_workspace_bytes(R, T, q_heads, c.kv_heads, c.head_dim);
+    if (workspace_bytes < need)
+        return fail(DFLASH_WORKSPACE_TOO_SMALL, "workspace of %zu bytes; %zu needed",
+                    workspace_bytes, need);
+    cudaError_t e = dflash::launch_attention_rows(dev, a, status,
+                                                  reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
     return ok();
 }
 

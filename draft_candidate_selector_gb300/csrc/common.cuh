@@ -12,6 +12,8 @@ namespace dflash {
 
 constexpr uint32_t kStatusBadId = 0x1u;     // matches DFLASH_DEVICE_BAD_ID
 constexpr uint32_t kStatusTimeout = 0x2u;   // matches DFLASH_DEVICE_TIMEOUT
+constexpr uint32_t kStatusBadLength = 0x4u; // matches DFLASH_DEVICE_BAD_LENGTH
+constexpr uint32_t kStatusNoPages = 0x8u;   // matches DFLASH_DEVICE_NO_PAGES
 
 // Per-device facts the launchers size their grids with.
 struct DeviceInfo {
@@ -151,5 +153,58 @@ constexpr int kMaxPathSteps = 256;   // steps per request the best path supports
 // One warp per request: the max-sum path through E [R,S,K,K] (K <= 32, S <= kMaxPathSteps).
 cudaError_t launch_best_path(const float* edges, const int32_t* cand_ids, int R, int S, int K,
                              int32_t* path, int32_t* tokens, float* score, cudaStream_t stream);
+
+// ---------------------------------------------------------------- paged cache (kvcache.cu)
+
+constexpr int kMaxTableRequests = 16384;   // requests whose running sums fit in shared memory
+
+struct BlockTableArgs {
+    const int32_t *context_lens, *new_lens, *held_pages, *free_pages;
+    int R, n_free, page_size, max_pages, T;
+    int32_t *block_table, *query_start, *kv_lens, *held_out, *positions;
+    int64_t* slots;
+    int32_t* pages_needed;
+};
+
+cudaError_t launch_block_tables(const DeviceInfo& dev, const BlockTableArgs& a,
+                                uint32_t* status_word, cudaStream_t stream);
+
+// Element types, as in dflash_dtype.
+enum : int { kBf16 = 0, kFp16 = 1, kE4m3 = 2 };
+
+// A cache as in dflash_kv_cache (strides in elements).
+struct KvCache {
+    void *key, *value;
+    long long page_stride, token_stride, head_stride;
+    int num_pages, page_size, kv_heads, head_dim, dtype;
+    float k_scale, v_scale;
+};
+
+cudaError_t launch_store_kv(const DeviceInfo& dev, const void* key, const void* value, int dtype,
+                            const int64_t* slots, int T, long long key_token_stride,
+                            long long key_head_stride, long long value_token_stride,
+                            long long value_head_stride, const KvCache& cache,
+                            uint32_t* status_word, cudaStream_t stream);
+
+// ---------------------------------------------------------------- attention (attention*.cu)
+
+struct AttentionArgs {
+    const void* query;
+    int dtype, T, q_heads;
+    long long q_token_stride, q_head_stride;
+    KvCache cache;
+    const int32_t* block_table;
+    int R, max_pages;
+    const int32_t *query_start, *kv_lens;
+    float scale;
+    int window_left, window_right;   // -1: no bound
+    float softcap;
+    void* out;
+    float* lse;                      // may be null
+};
+
+// One warp per (token, query head), for the shapes the tensor-core kernel does not take.
+cudaError_t launch_attention_rows(const DeviceInfo& dev, const AttentionArgs& a,
+                                  uint32_t* status_word, cudaStream_t stream);
 
 }  // namespace dflash

@@ -11,6 +11,9 @@
  *      E[r,p,q,c] = unary[r,p,c] + <pred_cb[cand[r,p-1,q]] * h_p, succ_cb[cand[r,p,c]]>,
  *      where the predecessor at p = 0 is the request's anchor token.
  *                                        DFlash2BeamCandidateSelector (class docstring)
+ * Before them, the paged key-value cache of the draft step's attention: its block tables
+ * (dflash_block_tables), its store (dflash_store_kv) and the attention over it
+ * (dflash_paged_attention).
  * Around these: step 1 straight from the LM head without logits in memory
  * (dflash_lmhead_topk, dflash_selector_lmhead), steps 2 and 3 on given candidates
  * (dflash_selector_forward), and the best path through E (dflash_best_path, a reading: the
@@ -65,6 +68,9 @@ typedef enum {
 /* Bits of the device status word (dflash_device_status). */
 #define DFLASH_DEVICE_BAD_ID 0x1u       /* a gathered token id was outside [0, V)        */
 #define DFLASH_DEVICE_TIMEOUT 0x2u      /* a bounded wait inside a kernel gave up        */
+#define DFLASH_DEVICE_BAD_LENGTH 0x4u   /* a request's lengths contradict each other or  */
+                                        /* do not fit its row of the block table         */
+#define DFLASH_DEVICE_NO_PAGES 0x8u     /* the list of free pages was too short          */
 
 /* A static string naming a status code. Never NULL. */
 const char* dflash_status_string(int status);
@@ -293,6 +299,148 @@ dflash_status dflash_selector_lmhead(const uint16_t* hidden, const uint16_t* lm_
 dflash_status dflash_best_path(const float* edges, const int32_t* cand_ids, int R, int S, int K,
                                int32_t* path, int32_t* tokens, float* score,
                                dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * The paged key-value cache that the drafter and the target model attend to. A cache is a
+ * pool of pages of page_size token rows; a request owns the pages that its row of the block
+ * table lists, and token j of it lives in row j % page_size of its page j / page_size. A slot
+ * numbers a token row of the whole pool: page * page_size + row.
+ * Source: the drafter's context keys and values already sit in a paged cache
+ * (DFlash2BeamAttention), prepare_dflash_inputs builds positions and slots on the GPU, and
+ * store_context_kv scatters keys and values by slot, optionally to fp8. The pages show only
+ * the calls; the arithmetic is the standard one, spelled out below.
+ *
+ * Element types of tensors that are not bf16 alone. */
+typedef enum {
+    DFLASH_BF16 = 0,
+    DFLASH_FP16 = 1,
+    DFLASH_E4M3 = 2    /* 8-bit floating point, 4 exponent bits, no infinities (cache only) */
+} dflash_dtype;
+
+/* One layer's cache: key and value hold [num_pages, page_size, kv_heads, head_dim] elements
+ * of type dtype, at the same strides (in elements; the innermost is 1), so both orders of
+ * page rows and heads, and caches with keys and values interleaved, can be passed. Row
+ * addresses must be 16-byte aligned. With DFLASH_E4M3 an element stands for itself times
+ * k_scale or v_scale; with the other types both scales must be 1. A host struct; the calls read
+ * it before they return. */
+typedef struct {
+    void* key;
+    void* value;
+    long long page_stride;
+    long long token_stride;
+    long long head_stride;
+    int num_pages;
+    int page_size;
+    int kv_heads;
+    int head_dim;
+    int dtype;       /* dflash_dtype */
+    float k_scale;
+    float v_scale;
+} dflash_kv_cache;
+
+/* ------------------------------------------------------------------------------------
+ * Block tables and slots of one step, from the requests' lengths.
+ * Source: prepare_dflash_inputs (third page, DFlashSpeculator.propose), which builds
+ * positions and slot mappings per request on the GPU.
+ *
+ * context_lens [R] int32   tokens each request has in the cache
+ * new_lens     [R] int32   tokens this step adds to it
+ * held_pages   [R] int32   pages its table row lists already (at least enough for its
+ *                          context; more after a step whose tokens were rejected)
+ * free_pages   [n_free]    page ids to take from, in order (int32)
+ * block_table  [R, max_pages] int32  in/out: new pages are written behind the held ones;
+ *                          nothing else of it is written
+ * query_start  [R + 1] int32  out: first token of each request, and their number
+ * kv_lens      [R] int32      out: context_lens + new_lens
+ * held_out     [R] int32      out: pages listed after the call
+ * positions    [T] int32      out: each new token's position in its request
+ * slots        [T] int64      out: its slot
+ * pages_needed [1] int32      out: pages taken from free_pages
+ *
+ * need_r = max(0, ceil((context_lens[r] + new_lens[r]) / page_size) - held_pages[r]); request r
+ * takes the need_r pages of free_pages behind those of the requests before it. T is the room
+ * for tokens: rows at and behind query_start[R] get position 0 and slot -1, which the store
+ * skips. A request whose lengths are negative, whose context is longer than its held pages or
+ * which needs more than max_pages is refused (DFLASH_DEVICE_BAD_LENGTH): it takes no pages. So
+ * is one that free_pages has too few pages for (DFLASH_DEVICE_NO_PAGES; pages_needed is then
+ * more than n_free). A refused request keeps its place in query_start, its slots are -1, its
+ * kv_lens entry is 0 and its table row stays as it was. If the new tokens are more than T,
+ * those past T are not written (DFLASH_DEVICE_BAD_LENGTH); query_start and pages_needed stop at
+ * 2^31 - 1. Outputs must not overlap inputs (nor
+ * kv_lens be context_lens: a step's lengths are the next one's context). 0 <= T; R <= 16384
+ * (DFLASH_UNSUPPORTED beyond). One launch; no workspace; natural alignment suffices.
+ * ---------------------------------------------------------------------------------- */
+dflash_status dflash_block_tables(const int32_t* context_lens, const int32_t* new_lens,
+                                  const int32_t* held_pages, const int32_t* free_pages, int R,
+                                  int n_free, int page_size, int max_pages, int T,
+                                  int32_t* block_table, int32_t* query_start, int32_t* kv_lens,
+                                  int32_t* held_out, int32_t* positions, int64_t* slots,
+                                  int32_t* pages_needed, dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Store new keys and values in the cache.
+ * Source: store_context_kv (DFlash2BeamModel.precompute_and_store_context_kv): scatter by
+ * slot, optionally to e4m3 with a scale for the layer.
+ *
+ * key, value  [T, kv_heads, head_dim] of type dtype (DFLASH_BF16 or DFLASH_FP16), each at its
+ *             own token and head strides (in elements, multiples of 8), so slices of a fused
+ *             projection's output can be passed
+ * slots       [T] int64. A negative slot stores nothing. A slot outside the cache stores
+ *             nothing and sets DFLASH_DEVICE_BAD_ID. Two tokens must not share a slot.
+ *
+ * The cache has the type dtype, and rows are copied; or DFLASH_E4M3, and an element x is stored
+ * as x / scale rounded to the nearest e4m3 value, ties to even, |x / scale| clamped to 448
+ * (NaN stays NaN). head_dim is a multiple of 8 up to 256 (16 for e4m3). T = 0 does nothing.
+ * ---------------------------------------------------------------------------------- */
+dflash_status dflash_store_kv(const void* key, const void* value, int dtype, const int64_t* slots,
+                              int T, long long key_token_stride, long long key_head_stride,
+                              long long value_token_stride, long long value_head_stride,
+                              const dflash_kv_cache* cache, dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Attention of new tokens over the paged cache, which holds their own keys and values too.
+ * Source: DFlash2BeamAttention: a non-causal sliding-window attention of the 1 + N query block
+ * over cached context (window_left, window_right); with window_right = 0 it is the causal
+ * attention of the target model's prompts, verified blocks and single tokens.
+ *
+ * query        [T, q_heads, head_dim] of type dtype (DFLASH_BF16 or DFLASH_FP16) at the
+ *              given strides (elements, multiples of 8); q_heads a multiple of kv_heads, query
+ *              head h reading key head h / (q_heads / kv_heads)
+ * cache        of the same type, or DFLASH_E4M3
+ * block_table  [R, max_pages] int32; query_start [R + 1], kv_lens [R] int32, as
+ *              dflash_block_tables writes them
+ * out          [T, q_heads, head_dim] of type dtype, contiguous
+ * lse          [T, q_heads] float, contiguous, or NULL
+ * workspace    at least dflash_paged_attention_workspace_bytes(...) bytes; its contents on
+ *              entry do not matter
+ *
+ * Token i of request r, of its n = query_start[r+1] - query_start[r], has position
+ * p = kv_lens[r] - n + i and sees the keys j with max(0, p - window_left) <= j <=
+ * min(kv_lens[r] - 1, p + window_right); -1 is no bound. Over them
+ *   s_j = scale * <q, k_j>, then softcap * tanh(s_j / softcap) if softcap > 0,
+ *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)  (natural).
+ * A token that sees no key gets zeros and lse = -inf. What the cache holds at keys that a
+ * token does not see has no effect on it, infinities and NaN included. Scores, maxima and sums
+ * are fp32; the products exp(s_j) v_j take exp(s_j) relative to a running maximum, rounded to
+ * the query's type, and are summed in fp32.
+ * Page ids outside the pool are never followed: the request's outputs are NaN and the status
+ * word records DFLASH_DEVICE_BAD_ID. A request whose kv_lens does not fit max_pages, or
+ * whose query_start is out of order or past T, is refused with DFLASH_DEVICE_BAD_LENGTH: its
+ * rows are NaN or not written. Rows of out at and behind query_start[R] are not written.
+ * head_dim is a multiple of 8 up to 256 (16 for e4m3). A result does not depend on what else
+ * is in the batch beyond the rounding of its sums' order, and equal calls give equal bits.
+ * ---------------------------------------------------------------------------------- */
+size_t dflash_paged_attention_workspace_bytes(int R, int T, int q_heads, int kv_heads,
+                                              int head_dim);
+
+dflash_status dflash_paged_attention(const void* query, int dtype, int T, int q_heads,
+                                     long long q_token_stride, long long q_head_stride,
+                                     const dflash_kv_cache* cache, const int32_t* block_table,
+                                     int R, int max_pages, const int32_t* query_start,
+                                     const int32_t* kv_lens, float scale, int window_left,
+                                     int window_right, float softcap, void* out, float* lse,
+                                     void* workspace, size_t workspace_bytes,
+                                     dflash_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * Device status word. Reads the DFLASH_DEVICE_* bits that kernels on the current device
