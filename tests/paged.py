@@ -123,7 +123,8 @@ def attention(b: Batch, scale=None, left=-1, right=0, softcap=0.0):
     """fp64 (out, lse) and bounds on what a kernel may be off them.
 
     The kernel sums fp32 products and rounds the weights and the output to the query's type, of
-    unit roundoff u (bf16 2^-9, fp16 2^-11). With A = sum_j p_j |v_j| / sum_j p_j:
+    unit roundoff u: half the spacing 2^-7 of bf16's 8 significant bits, 2^-8, and
+    2^-11 for fp16's 11. With A = sum_j p_j |v_j| / sum_j p_j:
       * a score's fp32 sum of D products is off by at most ds = (D + 8) 2^-23 sum|q k| scale,
         plus 2^-20 softcap for the cap's own functions, plus 2^-22 |s| for the rounding of the
         score itself and of its product with log2(e); a weight is then off by ds (relative),
@@ -134,7 +135,7 @@ def attention(b: Batch, scale=None, left=-1, right=0, softcap=0.0):
     lse: the largest ds, the sums' (L + 64) 2^-22, and its own rounding.
     """
     scale = b.D ** -0.5 if scale is None else scale
-    u = 2.0 ** -9 if b.dtype == torch.bfloat16 else 2.0 ** -11
+    u = 2.0 ** -8 if b.dtype == torch.bfloat16 else 2.0 ** -11
     g = b.Hq // b.Hkv
     out = torch.zeros((b.T, b.Hq, b.D), dtype=torch.float64)
     lse = torch.full((b.T, b.Hq), -math.inf, dtype=torch.float64)
