@@ -681,8 +681,9 @@ size_t dflash_paged_attention_workspace_bytes(int R, int T, int q_heads, int kv_
         fail(DFLASH_INVALID_ARGUMENT, "R, q_heads, kv_heads and head_dim must be >= 1, T >= 0");
         return 0;
     }
-    if (current_device(nullptr, nullptr) != DFLASH_OK) return 0;
-    return 16;
+    dflash::DeviceInfo dev;
+    if (current_device(&dev, nullptr) != DFLASH_OK) return 0;
+    return dflash::attention_workspace_bytes(dev, R, head_dim);
 }
 
 dflash_status dflash_paged_attention(const void* query, int dtype, int T, int q_heads,
@@ -734,8 +735,10 @@ dflash_status dflash_paged_attention(const void* query, int dtype, int T, int q_
     if (workspace_bytes < need)
         return fail(DFLASH_WORKSPACE_TOO_SMALL, "workspace of %zu bytes; %zu needed",
                     workspace_bytes, need);
-    cudaError_t e = dflash::launch_attention_rows(dev, a, status,
-                                                  reinterpret_cast<cudaStream_t>(stream));
+    cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = dflash::attention_on_tensor_cores(a)
+                        ? dflash::launch_attention(dev, a, workspace, status, st)
+                        : dflash::launch_attention_rows(dev, a, status, st);
     if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
     return ok();
 }

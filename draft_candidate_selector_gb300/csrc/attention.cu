@@ -1,0 +1,1119 @@
+// attention.cu: attention of new tokens over the paged cache on the tensor cores.
+//
+// Page "vllm.models.beam.nvidia.dflash2", DFlash2BeamAttention: the query block attends to keys
+// and values in a paged cache, inside a sliding window. For a row (a new token and a query head)
+// and its visible keys j:
+//   s_j = scale <q, k_j> (capped), out = sum_j e^{s_j} v_j / sum_j e^{s_j}, lse = log sum_j e^{s_j}.
+// One pass over the keys keeps a running maximum m, the sum l of e^{s_j - m} and the output O
+// relative to m.
+//
+// Rows. The g = q_heads / kv_heads query heads of a key head share its keys, so a row tile is
+// tpt = floor(128 / g) tokens x g heads of one request and key head: at most 128 rows, one
+// tensor-memory lane each. A work item is two row tiles (2 tpt tokens) that walk the same key
+// tiles of 128 tokens, or, where a request has no more than tpt tokens left, one row tile whose
+// even and odd key tiles go to the two halves of the CTA.
+//
+// One CTA per SM, 12 warps:
+//   * warp 0: TMA producer. Each lane fetches one box (a page's rows x 64 values, 128-byte
+//     swizzle) of a key or value tile; tiles go through a ring of 32 KB (16 KB) stages.
+//   * warp 1, one lane: issues the tcgen05.mma: S = Q K^T into tensor memory, and O += P V with P
+//     in tensor memory (over S, in 16 bits) and V transposed by its descriptor.
+//   * warps 2-3: look through the value tiles that some row must not see all of, and clear what
+//     is not finite there (0 x infinity would reach the rows that do not see it). See v_bad.
+//   * warps 4-7 and 8-11: one softmax each, a thread per row. S comes from tensor memory, P goes
+//     back over it. O stays in tensor memory and is scaled there only when the row's maximum has
+//     grown by more than 2^8 since it was last scaled; until then P is taken relative to the old
+//     maximum, which changes nothing but the common factor of P, l and O.
+// While one half's softmax runs, the tensor cores work for the other half.
+//
+// Work split. A planning kernel cuts the flat list of (request, key head, row tile, key tile)
+// into one equal range per SM, wherever that falls. An item cut by a range's end leaves (O, m, l)
+// of its pieces in the workspace, and a joining kernel weighs them together. No CTA waits for
+// another; every mbarrier wait is bounded, and on expiry the CTA sets kStatusTimeout and stops.
+#include "common.cuh"
+#include "ptx.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <mutex>
+
+namespace dflash {
+namespace {
+
+using namespace ptx;
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr int BM = 128;                 // rows of a row tile: tensor-memory lanes
+constexpr int BN = 128;                 // keys of a key tile
+constexpr int kThreads = 384;
+constexpr int kPlanThreads = 1024;
+constexpr int kJoinThreads = 256;
+constexpr int kJoinSlices = 8;          // CTAs that share one cut item's join
+constexpr int kSeqRing = 8;             // items whose flags are kept (the ring runs < 8 ahead)
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kGrowth = 8.f;          // log2 growth of a maximum before O is scaled
+
+struct Problem {
+    int T, q_heads, kv_heads, g, tpt;   // tpt: tokens per row tile
+    int R, max_pages, num_pages, page_size;
+    int left, right;
+    float softcap, scale, v_scale;      // scale includes the keys' scale
+    const int32_t *block_table, *query_start, *kv_lens;
+    int page_shift;
+    void* out;
+    float* lse;
+    const void* value;
+    long long page_stride, token_stride, head_stride;
+    // workspace
+    int4* rec;                          // [R]: first token, tokens, cached tokens, refused
+    long long* cost;                    // [R + 1]: running cost
+    int4* bound;                        // [G + 1]: request, key head, row-tile pair, first step
+    float* part;                        // [2 G][part_floats]
+    int G;
+};
+
+__host__ __device__ inline size_t part_floats(int D) { return 2 * (size_t)BM * (D + 2); }
+
+// Key tiles [begin, end) that tokens tok0 .. tok0 + ntok - 1 of a request see any key of.
+__device__ __forceinline__ void key_tiles(const Problem& p, int n, int L, int tok0, int ntok,
+                                          int& begin, int& end) {
+    const long long first = (long long)L - n + tok0, last = first + ntok - 1;
+    const long long lo = p.left < 0 ? 0 : max(0LL, first - p.left);
+    const long long hi = p.right < 0 ? (long long)L : min((long long)L, last + p.right + 1);
+    begin = (int)(lo / BN);
+    end = hi > lo ? (int)((hi + BN - 1) / BN) : begin;
+}
+
+__device__ __forceinline__ int item_count(const Problem& p, int n) {
+    return (n + 2 * p.tpt - 1) / (2 * p.tpt);
+}
+
+// Cost of an item in half steps of the two-tile kind, which is what the split makes equal.
+__device__ __forceinline__ int step_cost(const Problem& p, int ntok) { return ntok > p.tpt ? 2 : 1; }
+
+__device__ __forceinline__ int item_cost(const Problem& p, int n, int L, int t) {
+    const int tok0 = t * 2 * p.tpt, ntok = min(2 * p.tpt, n - tok0);
+    int b, e;
+    key_tiles(p, n, L, tok0, ntok, b, e);
+    const int w = step_cost(p, ntok);
+    return w * (1 + e - b);
+}
+
+// ---------------------------------------------------------------- plan
+
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(Problem p, uint32_t* status) {
+    __shared__ long long warp_sum[kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    grid_dependents_launch();
+    // Each request's record and cost: a warp per request, its lanes over the row-tile pairs.
+    for (int r = warp; r < p.R; r += kPlanThreads / 32) {
+        const int t0 = p.query_start[r], t1 = p.query_start[r + 1];
+        int L = p.kv_lens[r];
+        const bool rows_ok = t0 >= 0 && t1 >= t0 && t1 <= p.T;
+        const bool len_ok = L >= 0 && (long long)L <= (long long)p.max_pages * p.page_size;
+        const int n = rows_ok ? t1 - t0 : 0;
+        if (!len_ok) L = 0;
+        if (lane == 0) {
+            p.rec[r] = make_int4(t0, n, L, len_ok ? 0 : 1);
+            if (!rows_ok || !len_ok) atomicOr(status, kStatusBadLength);
+        }
+        long long c = 0;
+        for (int t = lane; t < item_count(p, n); t += 32) c += item_cost(p, n, L, t);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(kFull, c, d);
+        if (lane == 0) p.cost[r] = c * p.kv_heads;
+    }
+    __syncthreads();
+    // Running cost over the requests.
+    const int per = (p.R + kPlanThreads - 1) / kPlanThreads;
+    const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
+    long long sum = 0;
+    for (int r = r0; r < r1; ++r) sum += p.cost[r];
+    long long incl = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(kFull, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    long long base = incl - sum;
+    for (int w = 0; w < warp; ++w) base += warp_sum[w];
+    for (int r = r0; r < r1; ++r) {
+        const long long c = p.cost[r];
+        p.cost[r] = base;
+        base += c;
+    }
+    if (tid == kPlanThreads - 1) p.cost[p.R] = base;
+    __syncthreads();
+    // Range starts: a warp per SM. The start b W / G falls on a request, a key head, an item and a
+    // step of it; a start inside an item's last step moves to the next item.
+    const long long W = p.cost[p.R];
+    for (int b = warp; b <= p.G; b += kPlanThreads / 32) {
+        const long long x = W / p.G * b + W % p.G * b / p.G;
+        int4 at = make_int4(p.R, 0, 0, 0);
+        if (x < W) {
+            int lo = 0, hi = p.R;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (p.cost[mid] <= x) lo = mid;
+                else hi = mid;
+            }
+            const int4 rec = p.rec[lo];
+            const int items = item_count(p, rec.y);
+            const long long head = (p.cost[lo + 1] - p.cost[lo]) / p.kv_heads;
+            const int h = (int)((x - p.cost[lo]) / head);
+            long long off = (x - p.cost[lo]) - (long long)h * head;
+            for (int t0 = 0; t0 < items; t0 += 32) {
+                const int t = t0 + lane;
+                const int c = t < items ? item_cost(p, rec.y, rec.z, t) : 0;
+                long long upto = c;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const long long o = __shfl_up_sync(kFull, upto, d);
+                    if (lane >= d) upto += o;
+                }
+                const unsigned past = __ballot_sync(kFull, upto > off);
+                if (past) {
+                    const int k = __ffs(past) - 1;
+                    const int ck = __shfl_sync(kFull, c, k);
+                    off -= __shfl_sync(kFull, upto, k) - ck;
+                    const int tk = t0 + k;
+                    const int w = step_cost(p, min(2 * p.tpt, rec.y - tk * 2 * p.tpt));
+                    const int step = max(0, (int)((off + w - 1) / w) - 1);
+                    at = make_int4(lo, h, tk, step);
+                    if (step * w >= ck - w && step > 0) {    // past the last step: the next item
+                        at.w = 0;
+                        if (++at.z == items) {
+                            at.z = 0;
+                            if (++at.y == p.kv_heads) {
+                                at.y = 0;
+                                do ++at.x;
+                                while (at.x < p.R && p.rec[at.x].y == 0);
+                            }
+                        }
+                    }
+                    break;
+                }
+                off -= __shfl_sync(kFull, upto, 31);
+            }
+        }
+        if (lane == 0) p.bound[b] = at;
+    }
+}
+
+// ---------------------------------------------------------------- items of a range
+
+// One item, or the part [lo, hi) of its steps that lies in this range.
+struct Piece {
+    int r, h, t;
+    int tok0, ntok;      // tokens of the request
+    int t0, n, L, bad;   // the request's record
+    int begin, steps;    // the item's first key tile, and their number
+    int lo, hi;          // this piece's steps
+    bool pair;           // two row tiles
+    bool whole;
+};
+
+struct Walk {
+    int4 at, end;
+    int loaded = -1;
+    int4 rec;
+    __device__ __forceinline__ Walk(const Problem& p, int b) {
+        at = p.bound[b];
+        end = p.bound[b + 1];
+    }
+    __device__ __forceinline__ bool next(const Problem& p, Piece& c) {
+        const bool last = at.x == end.x && at.y == end.y && at.z == end.z;
+        if (at.x >= p.R || (last && at.w >= end.w)) return false;
+        if (at.x != loaded) {
+            rec = p.rec[at.x];
+            loaded = at.x;
+        }
+        c.r = at.x;
+        c.h = at.y;
+        c.t = at.z;
+        c.t0 = rec.x;
+        c.n = rec.y;
+        c.L = rec.z;
+        c.bad = rec.w;
+        c.tok0 = c.t * 2 * p.tpt;
+        c.ntok = min(2 * p.tpt, c.n - c.tok0);
+        c.pair = c.ntok > p.tpt;
+        int e;
+        key_tiles(p, c.n, c.L, c.tok0, c.ntok, c.begin, e);
+        c.steps = e - c.begin;
+        c.lo = at.w;
+        c.hi = last ? end.w : c.steps;
+        c.whole = c.lo == 0 && c.hi == c.steps;
+        if (last) {
+            at = end;
+        } else {
+            at.w = 0;
+            if (++at.z == item_count(p, c.n)) {
+                at.z = 0;
+                if (++at.y == p.kv_heads) {
+                    at.y = 0;
+                    do ++at.x;
+                    while (at.x < p.R && p.rec[at.x].y == 0);
+                }
+            }
+        }
+        return true;
+    }
+};
+
+// Key tiles of an item that every one of its rows sees all of: [from, to). Others are masked
+// row by row, and their values are looked through.
+__device__ __forceinline__ void clear_tiles(const Problem& p, const Piece& c, int tok0, int ntok,
+                                            int& from, int& to) {
+    const long long first = (long long)c.L - c.n + tok0, last = first + ntok - 1;
+    const long long lo = p.left < 0 ? 0 : max(0LL, last - p.left);
+    const long long hi = p.right < 0 ? (long long)c.L : min((long long)c.L, first + p.right + 1);
+    from = (int)((lo + BN - 1) / BN);
+    to = hi > 0 ? (int)(hi / BN) : 0;
+}
+
+// Waits until the shared counter is past q. Gives up after kWaitLimitNs.
+__device__ __forceinline__ bool count_past(const volatile uint32_t* count, uint32_t q) {
+    if ((int32_t)(*count - q) > 0) return true;
+    const unsigned long long t0 = globaltimer();
+    while ((int32_t)(*count - q) <= 0) {
+        if (globaltimer() - t0 > kWaitLimitNs) return false;
+        __nanosleep(64);
+    }
+    return true;
+}
+
+template <int D>
+struct Layout {
+    static constexpr uint32_t kChunk = BN * 128;                 // 128 rows x 64 values
+    static constexpr uint32_t kTile = kChunk * (D / 64);
+    static constexpr int kStages = D == 128 ? 5 : 11;
+    static constexpr uint32_t q = 0;                             // two row tiles
+    static constexpr uint32_t kv = 2 * kTile;
+    static constexpr uint32_t bars = kv + kStages * kTile;
+    static constexpr int kBars = 3 * kStages + 12;
+    static constexpr uint32_t ml = (bars + kBars * 8 + 15) / 16 * 16;   // [128] float2
+    static constexpr uint32_t flags = ml + BM * 8;               // v_bad, id_bad [kSeqRing]
+    static constexpr uint32_t slot = flags + 2 * kSeqRing * 4;   // tensor memory's base
+    static constexpr uint32_t issued = slot + 4;                 // tiles the producer has issued
+    static constexpr uint32_t total = slot + 16;
+};
+
+__device__ __forceinline__ uint32_t pack16(bool half_type, float lo, float hi) {
+    if (half_type) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ float unpack16(bool half_type, uint32_t w) {
+    return half_type ? __half2float(__ushort_as_half((unsigned short)w))
+                     : __uint_as_float(w << 16);
+}
+
+// Bit per 16-bit half of w that is an infinity or a NaN.
+template <bool kHalf>
+__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
+    constexpr uint32_t e = kHalf ? 0x7C00u : 0x7F80u;
+    return ((w & e) == e ? 1u : 0u) | (((w >> 16) & e) == e ? 2u : 0u);
+}
+
+// Add back, in the columns d .. d + 31 of a row's output, the values that are not finite and
+// that the row sees, of the tiles in which they have been cleared: weights are positive, so each
+// gives an infinity of its sign or a NaN. Taken only by items in which one was found.
+template <bool kHalf>
+__device__ __forceinline__ void refill_values(const Problem& p, const Piece& c, int row_lo, int row_hi,
+                                           int d, float (&o)[32]) {
+    int from, to;
+    clear_tiles(p, c, c.tok0, c.ntok, from, to);
+    for (int tile = c.begin + c.lo; tile < c.begin + c.hi; ++tile) {
+        if (tile >= from && tile < to) continue;
+        const int a = max(row_lo, tile * BN), b = min(row_hi - tile * BN, BN) + tile * BN;
+        for (int j = a; j < b; ++j) {
+            const int id = p.block_table[(long long)c.r * p.max_pages + (j >> p.page_shift)];
+            if (id < 0 || id >= p.num_pages) continue;
+            const uint16_t* v = static_cast<const uint16_t*>(p.value) + id * p.page_stride +
+                                (j & (p.page_size - 1)) * p.token_stride + c.h * p.head_stride + d;
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (odd_halves<kHalf>(v[i])) o[i] += unpack16(kHalf, v[i]);
+        }
+    }
+}
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kThreads, 1)
+attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const Problem p, uint32_t* status) {
+    using L = Layout<D>;
+    constexpr int kChunks = D / 64;
+    constexpr int kStages = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    const uint32_t base = smem_u32(smem);
+    const uint32_t bars = base + L::bars;
+    const uint32_t kv_full = bars, kv_empty = bars + 8 * kStages, kv_fix = bars + 16 * kStages;
+    const uint32_t q_full = bars + 24 * kStages, q_empty = q_full + 8;
+    const uint32_t s_full = q_full + 16, p_full = q_full + 32, o_done = q_full + 48;   // [2] each
+    const uint32_t ml_there = q_full + 64, ml_back = q_full + 72, halves_done = q_full + 80;
+    const uint32_t drained = q_full + 88;
+    float2* ml = reinterpret_cast<float2*>(smem + L::ml);
+    volatile int* v_bad = reinterpret_cast<volatile int*>(smem + L::flags);
+    volatile int* id_bad = v_bad + kSeqRing;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::slot);
+    volatile uint32_t* issued = reinterpret_cast<volatile uint32_t*>(smem + L::issued);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(kv_full + 8 * s, 1);
+            mbar_init(kv_empty + 8 * s, 1);
+            mbar_init(kv_fix + 8 * s, 64);
+        }
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(s_full + 8 * w, 1);
+            mbar_init(p_full + 8 * w, BM);
+            mbar_init(o_done + 8 * w, 1);
+        }
+        mbar_init(ml_there, BM);
+        mbar_init(ml_back, BM);
+        mbar_init(halves_done, 2 * BM);
+        mbar_init(drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        for (int i = 0; i < 2 * kSeqRing; ++i) v_bad[i] = -1;
+        *issued = 0;
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(tmem_slot)), "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    grid_dependents_launch();
+    grid_dependency_wait();              // the plan, and with it everything before it
+
+    Walk walk(p, blockIdx.x);
+    Piece c;
+    bool ok = true;
+
+    // Registers: the block is launched with 168 a thread, 504 for three threads of different
+    // warpgroups; the softmax threads hold a row of S and take 216 each, the others keep 72.
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 0) {
+        // ---- TMA producer: the whole warp, a box per lane
+        const int box = min(p.page_size, BN);
+        const int page_lane = lane / kChunks, chunk = lane % kChunks;
+        const bool lane_on = page_lane < BN / box;
+        long long g = 0;                 // tiles issued
+        int seq = 0;
+        while (ok && walk.next(p, c)) {
+            const int steps = c.hi - c.lo;
+            if (steps == 0) continue;
+            if (seq > 0) ok = __all_sync(kFull, mbar_wait(q_empty, (uint32_t)((seq - 1) & 1)));
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t rows = (uint32_t)(p.g * p.tpt);
+                const int tiles = c.pair ? 2 : 1;
+                mbar_expect_tx(q_full, (uint32_t)tiles * rows * D * 2);
+                for (int s = 0; s < tiles; ++s)
+                    for (int k = 0; k < kChunks; ++k)
+                        tma_load_4d(base + L::q + s * L::kTile + k * L::kChunk, &map_q, q_full,
+                                    k * 64, 0, c.h, c.t0 + c.tok0 + s * p.tpt);
+            }
+            const int32_t* table = p.block_table + (long long)c.r * p.max_pages;
+            // This lane's page of a tile: -1 behind the last token, and where it is refused.
+            auto page_of = [&](int step) -> int {
+                const unsigned tok = (unsigned)(c.begin + step) * BN + page_lane * box;
+                if (!lane_on || step >= c.hi || tok >= (unsigned)c.L) return -1;
+                int id = table[tok >> p.page_shift];
+                if (id < 0 || id >= p.num_pages) {
+                    id_bad[seq % kSeqRing] = seq;
+                    atomicOr(status, kStatusBadId);
+                    id = 0;
+                }
+                return id;
+            };
+            auto load = [&](const CUtensorMap* map, int step, int id) {
+                const int s = (int)(g % kStages);
+                if (g >= kStages &&
+                    !__all_sync(kFull, mbar_wait(kv_empty + 8 * s, (uint32_t)((g / kStages - 1) & 1))))
+                    return false;
+                ++g;
+                const unsigned live = __ballot_sync(kFull, id >= 0);
+                if (lane == 0) {
+                    mbar_expect_tx(kv_full + 8 * s, (uint32_t)(__popc(live) * box * 128));
+                    *issued = (uint32_t)g;
+                }
+                __syncwarp();
+                if (id >= 0) {
+                    const unsigned tok = (unsigned)(c.begin + step) * BN + page_lane * box;
+                    tma_load_4d(base + L::kv + s * L::kTile + chunk * L::kChunk +
+                                    page_lane * box * 128,
+                                map, kv_full + 8 * s, chunk * 64, (int)(tok & (p.page_size - 1)), c.h, id);
+                }
+                return true;
+            };
+            int id = page_of(c.lo), id_next = page_of(c.lo + 1);
+            ok = load(&map_k, c.lo, id);
+            for (int j = c.lo; j < c.hi && ok; ++j) {
+                const int id_after = page_of(j + 2);
+                if (j + 1 < c.hi) ok = load(&map_k, j + 1, id_next);
+                if (ok) ok = load(&map_v, j, id);
+                id = id_next;
+                id_next = id_after;
+            }
+            ++seq;
+        }
+        if (!ok) {
+            if (lane == 0) atomicOr(status, kStatusTimeout);
+            // Let the last loads land before this CTA leaves.
+            for (long long q = max(0LL, g - kStages); q < g; ++q)
+                (void)mbar_wait(kv_full + 8 * (int)(q % kStages), (uint32_t)((q / kStages) & 1));
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---- MMA issuer
+            const uint32_t idesc_s = f16_idesc_of(kHalf, false, BM, BN);
+            const uint32_t idesc_o = f16_idesc_of(kHalf, true, BM, D);
+            long long g = 0;             // tiles of earlier items
+            int seq = 0;
+            int np[2] = {0, 0};          // P tiles waited for, by half
+            uint32_t fixed = 0;          // phase bit of each stage's kv_fix
+            while (ok && walk.next(p, c)) {
+                const int steps = c.hi - c.lo;
+                if (steps == 0) continue;
+                int from, to;
+                clear_tiles(p, c, c.tok0, c.ntok, from, to);
+                auto k_tile = [&](int j) { return g + (j == 0 ? 0 : 2 * j - 1); };
+                auto v_tile = [&](int j) { return g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1); };
+                auto landed = [&](long long q) {
+                    return mbar_wait(kv_full + 8 * (int)(q % kStages), (uint32_t)((q / kStages) & 1));
+                };
+                auto scores = [&](int w, int tile, long long q) {
+                    const uint32_t a = base + L::q + tile * L::kTile;
+                    const uint32_t b = base + L::kv + (uint32_t)(q % kStages) * L::kTile;
+                    const uint64_t da = sw128_desc(a), db = sw128_desc(b);
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t o = ((k / 4) * L::kChunk + (k % 4) * 32) >> 4;
+                        umma_bf16(tmem + w * BN, da + o, db + o, idesc_s, k != 0);
+                    }
+                    umma_commit(s_full + 8 * w);
+                };
+                auto values = [&](int w, long long q, bool first) {
+                    const uint32_t b = base + L::kv + (uint32_t)(q % kStages) * L::kTile;
+                    const uint64_t db = sw128_mn_desc(b, L::kChunk);
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < BN / 16; ++k)
+                        umma_f16_tmem_a(tmem + 256 + w * 128, tmem + w * BN + k * 8,
+                                        db + k * (2048 >> 4), idesc_o, !(first && k == 0));
+                    umma_commit(o_done + 8 * w);
+                };
+                auto release = [&](long long q) { umma_commit(kv_empty + 8 * (int)(q % kStages)); };
+                // The value tile has landed, and has been looked through where it has to be.
+                auto value_ready = [&](int j, long long q) {
+                    if (!landed(q)) return false;
+                    const int tile = c.begin + c.lo + j, s = (int)(q % kStages);
+                    if (tile >= from && tile < to) return true;
+                    const uint32_t bit = (fixed >> s) & 1;
+                    fixed ^= 1u << s;
+                    return mbar_wait(kv_fix + 8 * s, bit);
+                };
+                auto p_ready = [&](int w) {
+                    return mbar_wait(p_full + 8 * w, (uint32_t)(np[w]++ & 1));
+                };
+                ok = mbar_wait(q_full, (uint32_t)(seq & 1)) && landed(k_tile(0));
+                if (!ok) break;
+                scores(0, 0, k_tile(0));
+                if (c.pair) {
+                    scores(1, 1, k_tile(0));
+                    release(k_tile(0));
+                    if (steps == 1) umma_commit(q_empty);
+                    for (int j = 0; j < steps && ok; ++j) {
+                        ok = value_ready(j, v_tile(j)) && p_ready(0);
+                        if (!ok) break;
+                        values(0, v_tile(j), j == 0);
+                        if (j + 1 < steps) {
+                            if (!(ok = landed(k_tile(j + 1)))) break;
+                            scores(0, 0, k_tile(j + 1));
+                        }
+                        if (!(ok = p_ready(1))) break;
+                        values(1, v_tile(j), j == 0);
+                        release(v_tile(j));
+                        if (j + 1 < steps) {
+                            scores(1, 1, k_tile(j + 1));
+                            release(k_tile(j + 1));
+                            if (j + 2 == steps) umma_commit(q_empty);
+                        }
+                    }
+                } else {
+                    release(k_tile(0));
+                    if (steps > 1) {
+                        if (!(ok = landed(k_tile(1)))) break;
+                        scores(1, 0, k_tile(1));
+                        release(k_tile(1));
+                    }
+                    if (steps <= 2) umma_commit(q_empty);
+                    for (int j = 0; j < steps && ok; ++j) {
+                        const int w = j & 1;
+                        ok = value_ready(j, v_tile(j)) && p_ready(w);
+                        if (!ok) break;
+                        values(w, v_tile(j), j < 2);
+                        release(v_tile(j));
+                        if (j + 2 < steps) {
+                            if (!(ok = landed(k_tile(j + 2)))) break;
+                            scores(w, 0, k_tile(j + 2));
+                            release(k_tile(j + 2));
+                            if (j + 3 == steps) umma_commit(q_empty);
+                        }
+                    }
+                }
+                g += 2 * steps;
+                ++seq;
+            }
+            if (!ok) {
+                atomicOr(status, kStatusTimeout);
+                umma_commit(drained);            // the MMAs in flight end before this CTA leaves
+                (void)mbar_wait(drained, 0);
+            }
+        }
+    } else {
+        // ---- value tiles that some row must not see all of: clear what is not finite, so that
+        // a weight of 0 gives 0. Rows that do see such a value get it back in the epilogue.
+        const int t = threadIdx.x - 64;
+        long long g = 0;
+        int seq = 0;
+        while (ok && walk.next(p, c)) {
+            const int steps = c.hi - c.lo;
+            if (steps == 0) continue;
+            int from, to;
+            clear_tiles(p, c, c.tok0, c.ntok, from, to);
+            for (int j = 0; j < steps && ok; ++j) {
+                const int tile = c.begin + c.lo + j;
+                if (tile >= from && tile < to) continue;
+                const long long q = g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1);
+                const int s = (int)(q % kStages);
+                // These warps skip tiles, so a stage's barrier may be phases behind the one they
+                // want: only once the tile is issued does its parity say which.
+                ok = __all_sync(kFull, count_past(issued, (uint32_t)q) &&
+                                           mbar_wait(kv_full + 8 * s, (uint32_t)((q / kStages) & 1)));
+                if (!ok) break;
+                uint4* v = reinterpret_cast<uint4*>(smem + L::kv + s * L::kTile);
+                // x * 0 summed over a run of vectors is NaN if any value is not finite.
+                constexpr int kVecs = (int)(L::kTile / 16), kRun = 8;
+                for (int i0 = t; i0 < kVecs; i0 += 64 * kRun) {
+                    uint4 x[kRun];
+#pragma unroll
+                    for (int k = 0; k < kRun; ++k) x[k] = v[i0 + 64 * k];
+                    bool odd;
+                    if constexpr (kHalf) {
+                        __half2 a = __float2half2_rn(0.f);
+                        const __half2 z = a;
+#pragma unroll
+                        for (int k = 0; k < kRun; ++k) {
+                            const __half2* e = reinterpret_cast<const __half2*>(&x[k]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) a = __hfma2(e[i], z, a);
+                        }
+                        odd = __hisnan(a.x) || __hisnan(a.y);
+                    } else {
+                        __nv_bfloat162 a = __float2bfloat162_rn(0.f);
+                        const __nv_bfloat162 z = a;
+#pragma unroll
+                        for (int k = 0; k < kRun; ++k) {
+                            const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&x[k]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) a = __hfma2(e[i], z, a);
+                        }
+                        odd = __hisnan(a.x) || __hisnan(a.y);
+                    }
+                    if (!odd) continue;
+                    for (int k = 0; k < kRun; ++k) {
+                        const int i = i0 + 64 * k;
+                        uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+                        bool hit = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const uint32_t m = odd_halves<kHalf>(w[e]);
+                            hit |= m != 0;
+                            w[e] &= (m & 1 ? 0u : 0xFFFFu) | (m & 2 ? 0u : 0xFFFF0000u);
+                        }
+                        if (!hit) continue;
+                        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        const long long token = (long long)tile * BN + (i * 16 % (int)L::kChunk) / 128;
+                        if (token < c.L) v_bad[seq % kSeqRing] = seq;
+                    }
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                mbar_arrive(kv_fix + 8 * s);
+            }
+            g += 2 * steps;
+            ++seq;
+        }
+        if (!ok && lane == 0) atomicOr(status, kStatusTimeout);
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        // ---- softmax: thread = row = tensor-memory lane
+        const int w = (warp - 4) >> 2;                       // half
+        const int row = (warp & 3) * 32 + lane;
+        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ts = lane_base + w * BN;
+        const uint32_t to_ = lane_base + 256 + w * 128;
+        const int row_token = row / p.g, row_head = row - row_token * p.g;
+        const float unit = p.softcap > 0.f ? 1.f : p.scale * kLog2e;     // S to log2 of a weight
+        const float cap = p.softcap * kLog2e;
+        const float cap_in = p.softcap > 0.f ? 2.f * kLog2e * p.scale / p.softcap : 0.f;
+        int seq = 0, ns = 0, nb = 0;     // items with steps; S tiles of this half; items of one tile
+        while (ok && walk.next(p, c)) {
+            const int steps = c.hi - c.lo;
+            const int sub = c.pair ? w : 0;
+            const int sub0 = c.tok0 + sub * p.tpt;           // the row tile's first token
+            const int nsub = min(p.tpt, c.n - sub0);         // and its tokens
+            const bool live = row_token < nsub;
+            const long long pos = (long long)c.L - c.n + sub0 + row_token;
+            const int row_lo =
+                p.left < 0 ? 0 : (int)max(0LL, pos - p.left);
+            const int row_hi =
+                !live ? 0 : (p.right < 0 ? c.L : (int)max(0LL, min((long long)c.L, pos + p.right + 1)));
+            const bool warp_live = __any_sync(kFull, live);
+            int from, to;
+            clear_tiles(p, c, sub0, nsub, from, to);
+            float m = -INFINITY, l = 0.f;
+            int mine = 0;                                    // S tiles of this item and half
+            for (int j = c.pair ? 0 : w; j < steps; j += c.pair ? 1 : 2) {
+                ok = __all_sync(kFull, mbar_wait(s_full + 8 * w, (uint32_t)(ns & 1)));
+                if (!ok) break;
+                ++ns;
+                ++mine;
+                if (warp_live) {
+                    tc_fence_after();
+                    uint32_t v[BN];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_ld_issue_x32(ts + 32 * k, v + 32 * k);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) tmem_ld_wait_x32(v + 32 * k);
+                    if (p.softcap > 0.f) {
+                        // cap * tanh(s / cap) = cap - 2 cap / (1 + e^{2 s / cap}), in log2 units
+#pragma unroll
+                        for (int k = 0; k < BN; ++k) {
+                            const float e = ex2(__uint_as_float(v[k]) * cap_in);
+                            v[k] = __float_as_uint(cap - __fdividef(2.f * cap, 1.f + e));
+                        }
+                    }
+                    const int tile = c.begin + c.lo + j;
+                    if (tile < from || tile >= to) {
+                        const int k0 = tile * BN;
+                        const int a = max(row_lo - k0, 0);
+                        const unsigned span = (unsigned)max(min(row_hi - k0, BN) - a, 0);
+#pragma unroll
+                        for (int k = 0; k < BN; ++k)
+                            if ((unsigned)(k - a) >= span) v[k] = 0xFF800000u;
+                    }
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < BN; k += 4)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) top[i] = fmaxf(top[i], __uint_as_float(v[k + i]));
+                    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * unit;
+                    const bool grown = most > m + kGrowth;   // also when m is still -inf
+                    const float keep = grown && m > -INFINITY ? ex2(m - most) : 1.f;
+                    if (grown) m = most;
+                    if (__any_sync(kFull, keep != 1.f)) {
+                        // O holds the tiles before this one: wait for the last of them.
+                        ok = __all_sync(kFull, mbar_wait(o_done + 8 * w, (uint32_t)((ns - 2) & 1)));
+                        if (!ok) break;
+                        tc_fence_after();
+                        l *= keep;
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 16) {
+                            uint32_t o[16];
+                            tmem_ld_issue_x16(to_ + d, o);
+                            tmem_ld_wait_x16(o);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                            tmem_st_x16(to_ + d, o);
+                        }
+                        tmem_st_wait();
+                    }
+                    const float off = m == -INFINITY ? 0.f : m;
+                    float add[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            const float x = ex2(fmaf(__uint_as_float(v[h * 32 + 2 * k]), unit, -off));
+                            const float y = ex2(fmaf(__uint_as_float(v[h * 32 + 2 * k + 1]), unit, -off));
+                            add[(2 * k) & 3] += x;
+                            add[(2 * k + 1) & 3] += y;
+                            pk[k] = pack16(kHalf, x, y);
+                        }
+                        tmem_st_x16(ts + 16 * h, pk);
+                    }
+                    l += (add[0] + add[1]) + (add[2] + add[3]);
+                    tmem_st_wait();
+                    tc_fence_before();
+                }
+                mbar_arrive(p_full + 8 * w);
+            }
+            if (!ok) break;
+            // Epilogue, once this half's last tile is in O.
+            if (mine > 0) ok = __all_sync(kFull, mbar_wait(o_done + 8 * w, (uint32_t)((ns - 1) & 1)));
+            if (!ok) break;
+            const bool nan = c.bad || (steps > 0 && id_bad[seq % kSeqRing] == seq);
+            auto finish = [&]() {                            // the factor that ends the quotient
+                if (nan) {
+                    m = 0.f;
+                    l = NAN;
+                }
+                return !c.whole ? 1.f : (l == 0.f ? 0.f : p.v_scale / l);
+            };
+            float f0, f1 = 0.f;                              // factors of the halves' O
+            bool has0 = mine > 0, has1 = false;
+            int d_begin = 0, d_end = D;
+            uint32_t o0 = to_;
+            if (c.pair) {
+                f0 = finish();
+            } else {
+                // One row tile: half 1 passes (m, l) over, half 0 returns the factors of both
+                // halves' O, and each half writes half of the columns.
+                has0 = steps > 0;
+                has1 = steps > 1;
+                if (w == 1) {
+                    ml[row] = make_float2(m, l);
+                    mbar_arrive(ml_there);
+                    ok = __all_sync(kFull, mbar_wait(ml_back, (uint32_t)(nb & 1)));
+                    f0 = ml[row].x;
+                    f1 = ml[row].y;
+                } else {
+                    ok = __all_sync(kFull, mbar_wait(ml_there, (uint32_t)(nb & 1)));
+                    const float2 other = ml[row];
+                    const float top = fmaxf(m, other.x);
+                    const float at = top == -INFINITY ? 0.f : top;
+                    f0 = ex2(m - at);
+                    f1 = ex2(other.x - at);
+                    l = l * f0 + other.y * f1;
+                    m = top;
+                    const float norm = finish();
+                    f0 *= norm;
+                    f1 *= norm;
+                    ml[row] = make_float2(f0, f1);
+                    mbar_arrive(ml_back);
+                }
+                if (!ok) break;
+                o0 = lane_base + 256;
+                d_begin = w * (D / 2);
+                d_end = d_begin + D / 2;
+            }
+            tc_fence_after();
+            if (warp_live) {
+                float4* part = reinterpret_cast<float4*>(
+                    p.part + (size_t)(2 * blockIdx.x + (c.lo > 0 ? 0 : 1)) * part_floats(D) +
+                    (size_t)sub * BM * (D + 2));
+                const long long out_row =
+                    ((long long)c.t0 + sub0 + row_token) * p.q_heads + c.h * p.g + row_head;
+                const bool refill = steps > 0 && v_bad[seq % kSeqRing] == seq;
+                for (int d = d_begin; d < d_end; d += 32) {
+                    uint32_t x[32], y[32];
+                    if (has0) tmem_ld_issue_x32(o0 + d, x);
+                    if (has1) tmem_ld_issue_x32(lane_base + 384 + d, y);
+                    if (has0) tmem_ld_wait_x32(x);
+                    if (has1) tmem_ld_wait_x32(y);
+                    float o[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        o[i] = has0 ? __uint_as_float(x[i]) * f0 : f0 * 0.f;
+                        if (has1) o[i] = fmaf(__uint_as_float(y[i]), f1, o[i]);
+                    }
+                    if (refill) refill_values<kHalf>(p, c, row_lo, row_hi, d, o);
+                    if (!live) continue;
+                    if (c.whole) {
+                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                                              out_row * D + d);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_uint4(pack16(kHalf, o[8 * i], o[8 * i + 1]),
+                                                pack16(kHalf, o[8 * i + 2], o[8 * i + 3]),
+                                                pack16(kHalf, o[8 * i + 4], o[8 * i + 5]),
+                                                pack16(kHalf, o[8 * i + 6], o[8 * i + 7]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            part[(d / 4 + i) * BM + row] =
+                                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    }
+                }
+                if (live && (c.pair || w == 0)) {
+                    if (!c.whole)
+                        reinterpret_cast<float2*>(part + BM * (D / 4))[row] = make_float2(m, l);
+                    else if (p.lse)
+                        p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                }
+            }
+            tc_fence_before();
+            if (!c.pair) {
+                // Neither half's O is written again before both halves have read it.
+                mbar_arrive(halves_done);
+                ok = __all_sync(kFull, mbar_wait(halves_done, (uint32_t)(nb & 1)));
+                ++nb;
+            }
+            if (steps > 0) ++seq;
+        }
+        if (!ok && lane == 0) atomicOr(status, kStatusTimeout);
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                     : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- join
+//
+// For each range start that cuts an item, and is the first to: out = sum_i w_i O_i / sum_i w_i l_i
+// over the item's pieces, w_i = 2^(m_i - max m). blockIdx.x: the range start - 1; blockIdx.y: a
+// slice of the item's rows and columns.
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Problem p, bool half_type) {
+    grid_dependency_wait();
+    const int b = blockIdx.x + 1;
+    const int4 at = p.bound[b], before = p.bound[b - 1];
+    if (at.x >= p.R || at.w == 0) return;
+    if (before.x == at.x && before.y == at.y && before.z == at.z && before.w > 0) return;
+    const int4 rec = p.rec[at.x];
+    const int tok0 = at.z * 2 * p.tpt, ntok = min(2 * p.tpt, rec.y - tok0);
+    int begin, end;
+    key_tiles(p, rec.y, rec.z, tok0, ntok, begin, end);
+    const int steps = end - begin;
+    // The ranges whose pieces follow the first one's (range b - 1, from step 0).
+    int last = b;
+    for (; last + 1 <= p.G; ++last) {
+        const int4 n = p.bound[last + 1];
+        if (!(n.x == at.x && n.y == at.y && n.z == at.z)) break;
+    }
+    auto piece = [&](int m) -> const float* {                // null: no steps
+        if (m < b) return p.part + (size_t)(2 * m + 1) * part_floats(D);
+        const int lo = p.bound[m].w, hi = m == last ? steps : p.bound[m + 1].w;
+        return lo < hi ? p.part + (size_t)(2 * m) * part_floats(D) : nullptr;
+    };
+    const int rows = ntok * p.g;                             // of both row tiles
+    const int in_tile = p.tpt * p.g;
+    for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < rows * (D / 4);
+         e += kJoinSlices * kJoinThreads) {
+        const int col = e / rows, row = e - col * rows;
+        const int sub = row >= in_tile ? 1 : 0, r = row - sub * in_tile;
+        const size_t tile_at = (size_t)sub * BM * (D + 2);
+        float top = -INFINITY;
+        for (int m = b - 1; m <= last; ++m) {
+            const float* q = piece(m);
+            if (q) top = fmaxf(top, reinterpret_cast<const float2*>(q + tile_at + BM * D)[r].x);
+        }
+        const float ref = top == -INFINITY ? 0.f : top;
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int m = b - 1; m <= last; ++m) {
+            const float* q = piece(m);
+            if (!q) continue;
+            const float2 s = reinterpret_cast<const float2*>(q + tile_at + BM * D)[r];
+            const float4 x = reinterpret_cast<const float4*>(q + tile_at)[col * BM + r];
+            const float wt = ex2(s.x - ref);
+            l = fmaf(s.y, wt, l);
+            o.x = fmaf(x.x, wt, o.x);
+            o.y = fmaf(x.y, wt, o.y);
+            o.z = fmaf(x.z, wt, o.z);
+            o.w = fmaf(x.w, wt, o.w);
+        }
+        const float norm = l == 0.f ? 0.f : p.v_scale / l;
+        const long long out_row = ((long long)rec.x + tok0 + row / p.g) * p.q_heads + at.y * p.g +
+                                  row % p.g;
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + out_row * D + col * 4) =
+            make_uint2(pack16(half_type, o.x * norm, o.y * norm),
+                       pack16(half_type, o.z * norm, o.w * norm));
+        if (col == 0 && p.lse)
+            p.lse[out_row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static std::once_flag once;
+    static EncodeTiledFn fn = nullptr;
+    std::call_once(once, [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+        else
+            (void)cudaGetLastError();
+    });
+    return fn;
+}
+
+// A rank-4 tensor of 16-bit values: dims and strides innermost first (strides in elements, of
+// dimensions 1 to 3), boxes of 64 values x box1 x 1 x box3, 128-byte swizzle.
+bool encode_4d(CUtensorMap* map, int dtype, const void* base, const long long (&dim)[4],
+               const long long (&stride)[3], int box1, int box3) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[4], strides[3];
+    for (int i = 0; i < 4; ++i) dims[i] = (cuuint64_t)dim[i];
+    // A dimension of one element is never stepped along; its stride only has to be encodable.
+    for (int i = 0; i < 3; ++i)
+        strides[i] = (cuuint64_t)((dim[i + 1] == 1 ? dim[0] : stride[i]) * 2);
+    const cuuint32_t box[4] = {64, (cuuint32_t)box1, 1, (cuuint32_t)box3};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    return fn(map, dtype == kFp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+              4, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t attention_workspace_bytes(const DeviceInfo& dev, int R, int D) {
+    return align256((size_t)R * sizeof(int4)) + align256((size_t)(R + 1) * sizeof(long long)) +
+           align256((size_t)(dev.sm_count + 1) * sizeof(int4)) +
+           2 * (size_t)dev.sm_count * part_floats(D) * sizeof(float);
+}
+
+bool attention_on_tensor_cores(const AttentionArgs& a) {
+    const KvCache& c = a.cache;
+    const auto fits = [](long long stride, long long dim) {   // a tensor map's stride
+        return dim == 1 || (stride > 0 && stride < (1LL << 38));
+    };
+    const long long g = a.q_heads / c.kv_heads;
+    return (c.head_dim == 64 || c.head_dim == 128) && c.dtype == a.dtype && c.page_size >= 8 &&
+           (c.page_size & (c.page_size - 1)) == 0 && g <= BM &&
+           fits(c.token_stride, c.page_size) && fits(c.head_stride, c.kv_heads) &&
+           fits(c.page_stride, c.num_pages) && fits(a.q_head_stride, a.q_heads) &&
+           fits(a.q_token_stride, a.T);
+}
+
+template <int D, bool kHalf>
+cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a, const Problem& p,
+                                   uint32_t* status, cudaStream_t stream) {
+    static std::once_flag once[64];
+    static cudaError_t attr_err[64];
+    if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
+    auto kernel = attention_kernel<D, kHalf>;
+    const size_t smem = 1024 + Layout<D>::total;
+    std::call_once(once[dev.device], [&] {
+        attr_err[dev.device] = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    });
+    if (attr_err[dev.device] != cudaSuccess) return attr_err[dev.device];
+    const KvCache& c = a.cache;
+    CUtensorMap map_q, map_k, map_v;
+    const int box = std::min(c.page_size, BN);
+    if (!encode_4d(&map_q, a.dtype, a.query, {D, p.g, c.kv_heads, a.T},
+                   {a.q_head_stride, p.g * a.q_head_stride, a.q_token_stride}, p.g, p.tpt) ||
+        !encode_4d(&map_k, a.dtype, c.key, {D, c.page_size, c.kv_heads, c.num_pages},
+                   {c.token_stride, c.head_stride, c.page_stride}, box, 1) ||
+        !encode_4d(&map_v, a.dtype, c.value, {D, c.page_size, c.kv_heads, c.num_pages},
+                   {c.token_stride, c.head_stride, c.page_stride}, box, 1))
+        return cudaErrorInvalidValue;
+    plan_kernel<<<1, kPlanThreads, 0, stream>>>(p, status);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    // Each of the next two kernels may start its prologue before the one in front of it has
+    // ended, and waits for it before it reads anything.
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((unsigned)p.G);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, map_q, map_k, map_v, p, status);
+    if (e != cudaSuccess || p.G < 2) return e;
+    cfg.gridDim = dim3((unsigned)(p.G - 1), kJoinSlices);
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, kHalf);
+}
+
+cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void* workspace,
+                             uint32_t* status_word, cudaStream_t stream) {
+    const KvCache& c = a.cache;
+    const int D = c.head_dim;
+    Problem p = {};
+    p.T = a.T;
+    p.q_heads = a.q_heads;
+    p.kv_heads = c.kv_heads;
+    p.g = a.q_heads / c.kv_heads;
+    p.tpt = BM / p.g;
+    p.R = a.R;
+    p.max_pages = a.max_pages;
+    p.num_pages = c.num_pages;
+    p.page_size = c.page_size;
+    while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
+    p.left = a.window_left;
+    p.right = a.window_right;
+    p.softcap = a.softcap;
+    p.scale = a.scale * c.k_scale;
+    p.v_scale = c.v_scale;
+    p.block_table = a.block_table;
+    p.query_start = a.query_start;
+    p.kv_lens = a.kv_lens;
+    p.out = a.out;
+    p.lse = a.lse;
+    p.value = c.value;
+    p.page_stride = c.page_stride;
+    p.token_stride = c.token_stride;
+    p.head_stride = c.head_stride;
+    char* w = static_cast<char*>(workspace);
+    p.rec = reinterpret_cast<int4*>(w);
+    w += align256((size_t)a.R * sizeof(int4));
+    p.cost = reinterpret_cast<long long*>(w);
+    w += align256((size_t)(a.R + 1) * sizeof(long long));
+    p.bound = reinterpret_cast<int4*>(w);
+    w += align256((size_t)(dev.sm_count + 1) * sizeof(int4));
+    p.part = reinterpret_cast<float*>(w);
+    p.G = dev.sm_count;
+    const bool half_type = a.dtype == kFp16;
+    if (D == 64)
+        return half_type ? launch_on_tensor_cores<64, true>(dev, a, p, status_word, stream)
+                         : launch_on_tensor_cores<64, false>(dev, a, p, status_word, stream);
+    return half_type ? launch_on_tensor_cores<128, true>(dev, a, p, status_word, stream)
+                     : launch_on_tensor_cores<128, false>(dev, a, p, status_word, stream);
+}
+
+}  // namespace dflash

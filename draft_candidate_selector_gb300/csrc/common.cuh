@@ -203,6 +203,14 @@ struct AttentionArgs {
     float* lse;                      // may be null
 };
 
+// Whether the tensor-core kernel takes these arguments: head_dim 64 or 128, a cache of the
+// query's type, pages of a power of two of 8 or more tokens, at most 128 query heads per key
+// head, strides that a tensor map can hold.
+bool attention_on_tensor_cores(const AttentionArgs& a);
+size_t attention_workspace_bytes(const DeviceInfo& dev, int R, int head_dim);
+cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void* workspace,
+                             uint32_t* status_word, cudaStream_t stream);
+
 // One warp per (token, query head), for the shapes the tensor-core kernel does not take.
 cudaError_t launch_attention_rows(const DeviceInfo& dev, const AttentionArgs& a,
                                   uint32_t* status_word, cudaStream_t stream);
