@@ -345,6 +345,40 @@ def dflash_best_path(edges: torch.Tensor, cand_ids: torch.Tensor, path: torch.Te
     return path, tokens, score
 
 
+# The calls below are made once per layer or per step of a serving loop, where the host's time
+# counts: one comparison decides whether an argument is right, and only a wrong one is looked into
+# by _need; addresses go to the library as integers; outputs the caller did not pass are not
+# checked, and those of one type share an allocation.
+
+def _checked(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> int:
+    """The address of a contiguous CUDA tensor of this type and shape."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape
+            and t.is_contiguous()):
+        _need(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+class _On:
+    """The device of a call, current while it is made, and its stream."""
+
+    def __init__(self, dev: torch.device, stream):
+        index = dev.index if dev.index is not None else torch.cuda.current_device()
+        self._guard = None
+        if index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(index)
+        self.stream = (torch._C._cuda_getCurrentRawStream(index) if stream is None
+                       else stream.cuda_stream)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
 def dflash_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor,
                         held_pages: torch.Tensor, free_pages: torch.Tensor,
                         block_table: torch.Tensor, page_size: int, T: int,
@@ -359,57 +393,61 @@ def dflash_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor,
     block_table int32 [R, max_pages] gets each request's new pages, taken in order from
     free_pages; T is the room for new tokens (their number, or more for a padded batch).
     """
-    lib = _native.load()
+    lib = _native._lib or _native.load()
+    i32 = torch.int32
     if context_lens.dim() != 1 or free_pages.dim() != 1 or block_table.dim() != 2:
         raise ValueError("context_lens must be [R], free_pages [n], block_table [R, max_pages]")
-    R, max_pages = context_lens.shape[0], block_table.shape[1]
-    _need(context_lens, "context_lens", torch.int32)
-    _need(new_lens, "new_lens", torch.int32, (R,))
-    _need(held_pages, "held_pages", torch.int32, (R,))
-    _need(free_pages, "free_pages", torch.int32)
-    _need(block_table, "block_table", torch.int32, (R, max_pages))
+    (R,), max_pages, n_free = context_lens.shape, block_table.shape[1], free_pages.shape[0]
+    ctx = _checked(context_lens, "context_lens", i32, (R,))
+    new = _checked(new_lens, "new_lens", i32, (R,))
+    held = _checked(held_pages, "held_pages", i32, (R,))
+    free = _checked(free_pages, "free_pages", i32, (n_free,))
+    table = _checked(block_table, "block_table", i32, (R, max_pages))
     dev = context_lens.device
-    with torch.cuda.device(dev):
-        if query_start is None:
-            query_start = torch.empty((R + 1,), dtype=torch.int32, device=dev)
-        if kv_lens is None:
-            kv_lens = torch.empty((R,), dtype=torch.int32, device=dev)
-        if held_out is None:
-            held_out = torch.empty((R,), dtype=torch.int32, device=dev)
-        if positions is None:
-            positions = torch.empty((T,), dtype=torch.int32, device=dev)
-        if slots is None:
-            slots = torch.empty((T,), dtype=torch.int64, device=dev)
-        if pages_needed is None:
-            pages_needed = torch.empty((1,), dtype=torch.int32, device=dev)
-        _need(query_start, "query_start", torch.int32, (R + 1,))
-        _need(kv_lens, "kv_lens", torch.int32, (R,))
-        _need(held_out, "held_out", torch.int32, (R,))
-        _need(positions, "positions", torch.int32, (T,))
-        _need(slots, "slots", torch.int64, (T,))
-        _need(pages_needed, "pages_needed", torch.int32, (1,))
-        _native.check(lib.dflash_block_tables(
-            _ptr(context_lens), _ptr(new_lens), _ptr(held_pages), _ptr(free_pages), R,
-            free_pages.shape[0], page_size, max_pages, T, _ptr(block_table), _ptr(query_start),
-            _ptr(kv_lens), _ptr(held_out), _ptr(positions), _ptr(slots), _ptr(pages_needed),
-            _stream(dev, stream)))
-    return query_start, kv_lens, held_out, positions, slots, pages_needed
+    sizes = (R + 1, R, R, T, 1)
+    given = (query_start, kv_lens, held_out, positions, pages_needed)
+    names = ("query_start", "kv_lens", "held_out", "positions", "pages_needed")
+    if given == (None, None, None, None, None):
+        room = torch.empty((3 * R + T + 2,), dtype=i32, device=dev)
+        out = room.split(sizes)
+        at = room.data_ptr()
+        ptrs = (at, at + 4 * (R + 1), at + 4 * (2 * R + 1), at + 4 * (3 * R + 1),
+                at + 4 * (3 * R + 1 + T))
+    else:
+        out = tuple(torch.empty((n,), dtype=i32, device=dev) if t is None else t
+                    for t, n in zip(given, sizes))
+        ptrs = tuple(_checked(t, name, i32, (n,)) for t, name, n in zip(out, names, sizes))
+    if slots is None:
+        slots = torch.empty((T,), dtype=torch.int64, device=dev)
+        slots_at = slots.data_ptr()
+    else:
+        slots_at = _checked(slots, "slots", torch.int64, (T,))
+    with _On(dev, stream) as st:
+        status = lib.dflash_block_tables(ctx, new, held, free, R, n_free, page_size, max_pages, T,
+                                         table, ptrs[0], ptrs[1], ptrs[2], ptrs[3], slots_at,
+                                         ptrs[4], st)
+    if status:
+        _native.check(status)
+    return out[0], out[1], out[2], out[3], slots, out[4]
 
 
 _DTYPES = {torch.bfloat16: _native.BF16, torch.float16: _native.FP16,
            torch.float8_e4m3fn: _native.E4M3}
 
 
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None) -> None:
-    """Checks a [rows, heads, head_dim] tensor that may be strided in all but the last."""
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None):
+    """The type code and strides of a [rows, heads, head_dim] tensor that may be strided in all
+    but the last."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] != 1):
         raise ValueError(f"{name} must be [T, heads, head_dim], head_dim contiguous")
-    if t.dtype not in (torch.bfloat16, torch.float16) or (dtype is not None and t.dtype != dtype):
+    code = _DTYPES.get(t.dtype, _native.E4M3)
+    if code == _native.E4M3 or (dtype is not None and t.dtype != dtype):
         raise ValueError(f"{name} must be bf16 or fp16 (and of one type), got {t.dtype}")
+    return code, t.stride()
 
 
 def _kv_cache(key_cache: torch.Tensor, value_cache: torch.Tensor, k_scale: float,
@@ -419,18 +457,18 @@ def _kv_cache(key_cache: torch.Tensor, value_cache: torch.Tensor, k_scale: float
             raise TypeError(f"{name} must be a torch.Tensor")
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-        if t.dim() != 4 or (t.stride(3) != 1 and t.shape[3] != 1):
-            raise ValueError(f"{name} must be [pages, page_size, kv_heads, head_dim], "
-                             "head_dim contiguous")
-        if t.dtype not in _DTYPES:
-            raise ValueError(f"{name} must be bf16, fp16 or float8_e4m3fn, got {t.dtype}")
-    if (key_cache.shape != value_cache.shape or key_cache.dtype != value_cache.dtype
-            or key_cache.stride() != value_cache.stride()):
+    shape, strides, dtype = key_cache.shape, key_cache.stride(), key_cache.dtype
+    if len(shape) != 4 or (strides[3] != 1 and shape[3] != 1):
+        raise ValueError("key_cache must be [pages, page_size, kv_heads, head_dim], "
+                         "head_dim contiguous")
+    if dtype not in _DTYPES:
+        raise ValueError(f"key_cache must be bf16, fp16 or float8_e4m3fn, got {dtype}")
+    if (value_cache.shape != shape or value_cache.dtype != dtype
+            or value_cache.stride() != strides):
         raise ValueError("key_cache and value_cache must have one shape, type and strides")
-    P, page_size, H, D = key_cache.shape
-    ps, ts, hs, _ = key_cache.stride()
-    return _native.KvCache(key_cache.data_ptr(), value_cache.data_ptr(), ps, ts, hs, P, page_size,
-                           H, D, _DTYPES[key_cache.dtype], k_scale, v_scale)
+    return _native.KvCache(key_cache.data_ptr(), value_cache.data_ptr(), strides[0], strides[1],
+                           strides[2], shape[0], shape[1], shape[2], shape[3], _DTYPES[dtype],
+                           k_scale, v_scale)
 
 
 def dflash_store_kv(key: torch.Tensor, value: torch.Tensor, slots: torch.Tensor,
@@ -440,21 +478,21 @@ def dflash_store_kv(key: torch.Tensor, value: torch.Tensor, slots: torch.Tensor,
     int64 [T] of the caches [pages, page_size, kv_heads, head_dim]: returns (key_cache,
     value_cache). A float8_e4m3fn cache holds x / scale; a negative slot stores nothing.
     """
-    lib = _native.load()
-    _rows(key, "key")
-    _rows(value, "value", key.dtype)
+    lib = _native._lib or _native.load()
+    code, ks = _rows(key, "key")
+    _, vs = _rows(value, "value", key.dtype)
     cache = _kv_cache(key_cache, value_cache, k_scale, v_scale)
-    if tuple(key.shape[1:]) != (cache.kv_heads, cache.head_dim) or value.shape != key.shape:
+    shape = key.shape
+    T = shape[0]
+    if shape != (T, cache.kv_heads, cache.head_dim) or value.shape != shape:
         raise ValueError(f"key and value must be [T, {cache.kv_heads}, {cache.head_dim}], got "
                          f"{tuple(key.shape)} and {tuple(value.shape)}")
-    T = key.shape[0]
-    _need(slots, "slots", torch.int64, (T,))
-    dev = key.device
-    with torch.cuda.device(dev):
-        _native.check(lib.dflash_store_kv(
-            _ptr(key), _ptr(value), _DTYPES[key.dtype], _ptr(slots), T, key.stride(0),
-            key.stride(1), value.stride(0), value.stride(1), ctypes.byref(cache),
-            _stream(dev, stream)))
+    at = _checked(slots, "slots", torch.int64, (T,))
+    with _On(key.device, stream) as st:
+        status = lib.dflash_store_kv(key.data_ptr(), value.data_ptr(), code, at, T, ks[0], ks[1],
+                                     vs[0], vs[1], cache, st)
+    if status:
+        _native.check(status)
     return key_cache, value_cache
 
 
@@ -482,8 +520,8 @@ def dflash_paged_attention(query: torch.Tensor, key_cache: torch.Tensor,
     p + window_right (-1: no bound; window_right 0 is causal). scale defaults to
     1 / sqrt(head_dim).
     """
-    lib = _native.load()
-    _rows(query, "query")
+    lib = _native._lib or _native.load()
+    code, qs = _rows(query, "query")
     cache = _kv_cache(key_cache, value_cache, k_scale, v_scale)
     T, Hq, D = query.shape
     if D != cache.head_dim:
@@ -491,24 +529,29 @@ def dflash_paged_attention(query: torch.Tensor, key_cache: torch.Tensor,
     if block_table.dim() != 2 or kv_lens.dim() != 1:
         raise ValueError("block_table must be [R, max_pages] and kv_lens [R]")
     R, max_pages = block_table.shape
-    _need(block_table, "block_table", torch.int32)
-    _need(query_start, "query_start", torch.int32, (R + 1,))
-    _need(kv_lens, "kv_lens", torch.int32, (R,))
+    table = _checked(block_table, "block_table", torch.int32, (R, max_pages))
+    start = _checked(query_start, "query_start", torch.int32, (R + 1,))
+    kv = _checked(kv_lens, "kv_lens", torch.int32, (R,))
     dev = query.device
-    with torch.cuda.device(dev):
-        if out is None:
-            out = torch.empty((T, Hq, D), dtype=query.dtype, device=dev)
-        if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
-        _need(out, "out", query.dtype, (T, Hq, D))
-        _need(lse, "lse", torch.float32, (T, Hq))
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=query.dtype, device=dev)
+        out_at = out.data_ptr()
+    else:
+        out_at = _checked(out, "out", query.dtype, (T, Hq, D))
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse_at = lse.data_ptr()
+    else:
+        lse_at = _checked(lse, "lse", torch.float32, (T, Hq))
+    with _On(dev, stream) as st:
         ws = _workspace(lib.dflash_paged_attention_workspace_bytes(R, T, Hq, cache.kv_heads, D),
                         dev, workspace)
-        _native.check(lib.dflash_paged_attention(
-            _ptr(query), _DTYPES[query.dtype], T, Hq, query.stride(0), query.stride(1),
-            ctypes.byref(cache), _ptr(block_table), R, max_pages, _ptr(query_start),
-            _ptr(kv_lens), D ** -0.5 if scale is None else scale, window_left, window_right,
-            softcap, _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(dev, stream)))
+        status = lib.dflash_paged_attention(
+            query.data_ptr(), code, T, Hq, qs[0], qs[1], cache, table, R, max_pages, start, kv,
+            D ** -0.5 if scale is None else scale, window_left, window_right, softcap, out_at,
+            lse_at, ws.data_ptr(), ws.numel(), st)
+    if status:
+        _native.check(status)
     return out, lse
 
 

@@ -683,7 +683,7 @@ size_t dflash_paged_attention_workspace_bytes(int R, int T, int q_heads, int kv_
     }
     dflash::DeviceInfo dev;
     if (current_device(&dev, nullptr) != DFLASH_OK) return 0;
-    return dflash::attention_workspace_bytes(dev, R, head_dim);
+    return dflash::attention_workspace_bytes(dev, head_dim);
 }
 
 dflash_status dflash_paged_attention(const void* query, int dtype, int T, int q_heads,

@@ -207,7 +207,7 @@ struct AttentionArgs {
 // query's type, pages of a power of two of 8 or more tokens, at most 128 query heads per key
 // head, strides that a tensor map can hold.
 bool attention_on_tensor_cores(const AttentionArgs& a);
-size_t attention_workspace_bytes(const DeviceInfo& dev, int R, int head_dim);
+size_t attention_workspace_bytes(const DeviceInfo& dev, int head_dim);
 cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void* workspace,
                              uint32_t* status_word, cudaStream_t stream);
 

@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <mutex>
 
 namespace dflash {
 namespace {
@@ -261,10 +262,15 @@ __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a, ui
 cudaError_t launch_block_tables(const DeviceInfo& dev, const BlockTableArgs& a,
                                 uint32_t* status_word, cudaStream_t stream) {
     const size_t smem = 2 * ((size_t)a.R + 1) * sizeof(int);
-    cudaError_t e = cudaFuncSetAttribute(block_tables_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)(2 * ((size_t)kMaxTableRequests + 1) * sizeof(int)));
-    if (e != cudaSuccess) return e;
+    static std::once_flag once[64];
+    static cudaError_t attr_err[64];
+    if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[dev.device], [&] {
+        attr_err[dev.device] = cudaFuncSetAttribute(
+            block_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            (int)(2 * ((size_t)kMaxTableRequests + 1) * sizeof(int)));
+    });
+    if (attr_err[dev.device] != cudaSuccess) return attr_err[dev.device];
     const long long items = std::max({((long long)a.T + kTokensPerThread - 1) / kTokensPerThread,
                                       (long long)a.R + 1, 1LL});
     const int blocks = (int)std::min<long long>((items + kTableThreads - 1) / kTableThreads,
