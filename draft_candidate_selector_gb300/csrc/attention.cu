@@ -1,1094 +1,9 @@
-// attention.cu: attention of new tokens over the paged cache on the tensor cores.
-//
-// Page "vllm.models.beam.nvidia.dflash2", DFlash2BeamAttention: the query block attends to keys
-// and values in a paged cache, inside a sliding window. For a row (a new token and a query head)
-// and its visible keys j:
-//   s_j = scale <q, k_j> (capped), out = sum_j e^{s_j} v_j / sum_j e^{s_j}, lse = log sum_j e^{s_j}.
-// One pass over the keys keeps a running maximum m, the sum l of e^{s_j - m} and the output O
-// relative to m.
-//
-// Rows. The g = q_heads / kv_heads query heads of a key head share its keys, so a row tile is
-// tpt = floor(128 / g) tokens x g heads of one request and key head: at most 128 rows, one
-// tensor-memory lane each. A work item is two row tiles (2 tpt tokens) that walk the same key
-// tiles of 128 tokens, or, where a request has no more than tpt tokens left, one row tile whose
-// even and odd key tiles go to the two halves of the CTA.
-//
-// One CTA per SM, 12 warps:
-//   * warp 0: TMA producer. Each lane fetches one box (a page's rows x 64 values, 128-byte
-//     swizzle) of a key or value tile; tiles go through a ring of 32 KB (16 KB) stages.
-//   * warp 1, one lane: issues the tcgen05.mma: S = Q K^T into tensor memory, and O += P V with P
-//     in tensor memory (over S, in 16 bits) and V transposed by its descriptor.
-//   * warp 2: looks through the value tiles that some row must not see all of, and clears what is
-//     not finite there (0 x infinity would reach the rows that do not see it). See Item::v_odd.
-//   * warp 3, one lane: walks the items of this CTA's range and hands them to the others through
-//     a ring in shared memory.
-//   * warps 4-7 and 8-11: one softmax each, a thread per row. S comes from tensor memory, P goes
-//     back over it. O stays in tensor memory and is scaled there only when the row's maximum has
-//     grown by more than 2^8 since it was last scaled; until then P is taken relative to the old
-//     maximum, which changes nothing but the common factor of P, l and O.
-// While one half's softmax runs, the tensor cores work for the other half.
-//
-// Work split. The flat list of (request, key head, item, key tile) is cut into one equal range
-// per SM, wherever that falls. Every CTA takes the running cost over the requests itself (their
-// lengths are a few bytes each) and finds its own range in it. An item cut by a range's end leaves
-// (O, m, l) of its pieces in the workspace, and a joining kernel weighs them together. No CTA waits
-// for another; every mbarrier wait is bounded, and on expiry the CTA sets kStatusTimeout and stops.
-#include "common.cuh"
-#include "ptx.cuh"
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
-#include <algorithm>
-#include <mutex>
+// attention.cu: which attention kernel a call takes, its workspace and its launch. The tensor-core
+// kernel is in attention.cuh; its builds for e4m3 caches are in attention_e4m3.cu.
+#include "attention.cuh"
 
 namespace dflash {
 namespace {
-
-using namespace ptx;
-
-constexpr unsigned kFull = 0xffffffffu;
-constexpr int BM = 128;                 // rows of a row tile: tensor-memory lanes
-constexpr int BN = 128;                 // keys of a key tile
-constexpr int kThreads = 384;
-constexpr int kJoinThreads = 256;
-constexpr int kJoinSlices = 8;          // CTAs that share one cut item's join
-constexpr int kItems = 4;               // slots of the item ring
-constexpr int kReaders = 11;            // arrivals that free a slot: warps 0-2 and 4-11
-constexpr int kSerialItems = 8;         // items of a request that one thread adds up
-constexpr int kWholeSteps = 8;          // key tiles up to which an item is not worth cutting
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kGrowth = 8.f;          // log2 growth of a maximum before O is scaled
-
-struct Problem {
-    int T, q_heads, kv_heads, g, tpt;   // tpt: tokens per row tile
-    int R, max_pages, num_pages, page_size;
-    int left, right;
-    float softcap, scale, v_scale;      // scale includes the keys' scale
-    const int32_t *block_table, *query_start, *kv_lens;
-    int page_shift;
-    void* out;
-    float* lse;
-    const void* value;
-    long long page_stride, token_stride, head_stride;
-    // workspace
-    int4* bound;                        // [G + 1]: request, key head, item, first step
-    float* part;                        // [2 G][part_floats]
-    int G;
-};
-
-__host__ __device__ inline size_t part_floats(int D) { return 2 * (size_t)BM * (D + 2); }
-
-// Key tiles [begin, end) that tokens tok0 .. tok0 + ntok - 1 of a request see any key of.
-__device__ __forceinline__ void key_tiles(const Problem& p, int n, int L, int tok0, int ntok,
-                                          int& begin, int& end) {
-    const long long first = (long long)L - n + tok0, last = first + ntok - 1;
-    const long long lo = p.left < 0 ? 0 : max(0LL, first - p.left);
-    const long long hi = p.right < 0 ? (long long)L : min((long long)L, last + p.right + 1);
-    begin = (int)(lo / BN);
-    end = hi > lo ? (int)((hi + BN - 1) / BN) : begin;
-}
-
-__device__ __forceinline__ int item_count(const Problem& p, int n) {
-    return (n + 2 * p.tpt - 1) / (2 * p.tpt);
-}
-
-// Cost of an item in half steps of the two-tile kind, which is what the split makes equal.
-__device__ __forceinline__ int step_cost(const Problem& p, int ntok) { return ntok > p.tpt ? 2 : 1; }
-
-__device__ __forceinline__ int item_cost(const Problem& p, int n, int L, int t) {
-    const int tok0 = t * 2 * p.tpt, ntok = min(2 * p.tpt, n - tok0);
-    int b, e;
-    key_tiles(p, n, L, tok0, ntok, b, e);
-    return step_cost(p, ntok) * (1 + e - b);
-}
-
-// A request's new and cached tokens; n = 0 where query_start is refused, bad where kv_lens is.
-struct Request {
-    int t0, n, L;
-    bool bad, rows_ok;
-};
-
-__device__ __forceinline__ Request request_of(const Problem& p, int r) {
-    Request q;
-    q.t0 = p.query_start[r];
-    const int t1 = p.query_start[r + 1];
-    q.L = p.kv_lens[r];
-    q.rows_ok = q.t0 >= 0 && t1 >= q.t0 && t1 <= p.T;
-    q.bad = q.L < 0 || (long long)q.L > (long long)p.max_pages * p.page_size;
-    q.n = q.rows_ok ? t1 - q.t0 : 0;
-    if (q.bad) q.L = 0;
-    return q;
-}
-
-// ---------------------------------------------------------------- plan
-
-// The start of range b of G: x = b W / G falls on a request, a key head, an item and a step of
-// it; a start inside an item's last step moves to the next item. Called by a whole warp.
-__device__ __forceinline__ int4 range_start(const Problem& p, const long long* cost, bool flat,
-                                            int b) {
-    const int lane = threadIdx.x & 31;
-    const long long W = cost[p.R];
-    const long long x = W / p.G * b + W % p.G * b / p.G;
-    int4 at = make_int4(p.R, 0, 0, 0);
-    if (x >= W) return at;
-    int lo = 0, hi = p.R;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cost[mid] <= x) lo = mid;
-        else hi = mid;
-    }
-    const Request q = request_of(p, lo);
-    const int items = item_count(p, q.n);
-    const long long head = (cost[lo + 1] - cost[lo]) / p.kv_heads;
-    const int h = (int)((x - cost[lo]) / head);
-    long long off = (x - cost[lo]) - (long long)h * head;
-    if (flat) return make_int4(lo, h, (int)off, 0);
-    for (int t0 = 0; t0 < items; t0 += 32) {
-        const int t = t0 + lane;
-        const int c = t < items ? item_cost(p, q.n, q.L, t) : 0;
-        long long upto = c;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const long long o = __shfl_up_sync(kFull, upto, d);
-            if (lane >= d) upto += o;
-        }
-        const unsigned past = __ballot_sync(kFull, upto > off);
-        if (!past) {
-            off -= __shfl_sync(kFull, upto, 31);
-            continue;
-        }
-        const int k = __ffs(past) - 1;
-        const int ck = __shfl_sync(kFull, c, k);
-        off -= __shfl_sync(kFull, upto, k) - ck;
-        const int tk = t0 + k;
-        const int w = step_cost(p, min(2 * p.tpt, q.n - tk * 2 * p.tpt));
-        const int step = max(0, (int)((off + w - 1) / w) - 1);
-        at = make_int4(lo, h, tk, step);
-        if (step * w >= ck - w && step > 0) {                // past the last step: the next item
-            at.w = 0;
-            if (++at.z == items) {
-                at.z = 0;
-                if (++at.y == p.kv_heads) {
-                    at.y = 0;
-                    do ++at.x;
-                    while (at.x < p.R && request_of(p, at.x).n == 0);
-                }
-            }
-        }
-        break;
-    }
-    return at;
-}
-
-// Every thread of the CTA: the running cost over the requests in cost[R + 1] (shared memory),
-// then this CTA's range. Where there are no more items than SMs and none is long, the cost of
-// each is 1, so that ranges fall on whole items and nothing has to be joined.
-__device__ __forceinline__ void plan_ranges(const Problem& p, long long* cost, int4* range,
-                                            uint32_t* status) {
-    __shared__ long long warp_sum[kThreads / 32], warp_items[kThreads / 32];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long my_items = 0;
-    bool big = false, is_long = false;
-    for (int r = tid; r < p.R; r += kThreads) {
-        const Request q = request_of(p, r);
-        if (blockIdx.x == 0 && (q.bad || !q.rows_ok)) atomicOr(status, kStatusBadLength);
-        const int items = item_count(p, q.n);
-        my_items += items;
-        long long c = -1;                                    // left to a warp
-        if (items <= kSerialItems) {
-            c = 0;
-            for (int t = 0; t < items; ++t) {
-                const int k = item_cost(p, q.n, q.L, t);
-                is_long |= k > 1 + kWholeSteps;
-                c += k;
-            }
-        } else {
-            big = true;
-        }
-        cost[r] = c * (c < 0 ? 1 : p.kv_heads);
-    }
-    if (__syncthreads_or(big)) {
-        for (int r = warp; r < p.R; r += kThreads / 32) {
-            if (cost[r] >= 0) continue;
-            const Request q = request_of(p, r);
-            long long c = 0;
-            for (int t = lane; t < item_count(p, q.n); t += 32) c += item_cost(p, q.n, q.L, t);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) c += __shfl_xor_sync(kFull, c, d);
-            if (lane == 0) cost[r] = c * p.kv_heads;
-        }
-        is_long = true;
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) my_items += __shfl_xor_sync(kFull, my_items, d);
-    if (lane == 0) warp_items[warp] = my_items;
-    bool flat = __syncthreads_or(is_long) == 0;
-    if (flat) {
-        long long all = 0;
-        for (int w = 0; w < kThreads / 32; ++w) all += warp_items[w];
-        flat = all * p.kv_heads <= p.G;
-    }
-    const int per = (p.R + kThreads - 1) / kThreads;
-    const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
-    long long sum = 0;
-    for (int r = r0; r < r1; ++r) {
-        if (flat) cost[r] = (long long)item_count(p, request_of(p, r).n) * p.kv_heads;
-        sum += cost[r];
-    }
-    long long incl = sum;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(kFull, incl, d);
-        if (lane >= d) incl += o;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    long long base = incl - sum;
-    for (int w = 0; w < warp; ++w) base += warp_sum[w];
-    for (int r = r0; r < r1; ++r) {
-        const long long c = cost[r];
-        cost[r] = base;
-        base += c;
-    }
-    if (tid == kThreads - 1) cost[p.R] = base;
-    __syncthreads();
-    if (warp < 2) {
-        const int b = (int)blockIdx.x + warp;
-        const int4 at = range_start(p, cost, flat, b);
-        if (lane == 0) {
-            range[warp] = at;
-            if (warp == 0 || b == p.G) p.bound[b] = at;      // for the join
-        }
-    }
-    __syncthreads();
-}
-
-// ---------------------------------------------------------------- items of a range
-
-// One item, or the part [lo, hi) of its steps that lies in this CTA's range.
-struct __align__(16) Item {
-    int r, h;            // request (-1: no more items) and key head
-    int tok0, ntok;      // tokens of the request
-    int t0, n, L, bad;   // the request's first row, new and cached tokens; refused
-    int begin, steps;    // the item's first key tile, and their number
-    int lo, hi;          // this CTA's steps
-    int from, to;        // key tiles that every row of the item sees all of
-    int v_odd;           // a value that is not finite was cleared
-    int bad_page;        // a page id outside the pool was met
-    __device__ __forceinline__ bool pair(const Problem& p) const { return ntok > p.tpt; }
-    __device__ __forceinline__ bool whole() const { return lo == 0 && hi == steps; }
-};
-
-// Key tiles that all of the tokens tok0 .. tok0 + ntok - 1 of a request see all of: [from, to).
-// Others are masked row by row, and their values are looked through.
-__device__ __forceinline__ void clear_tiles(const Problem& p, int n, int L, int tok0, int ntok,
-                                            int& from, int& to) {
-    const long long first = (long long)L - n + tok0, last = first + ntok - 1;
-    const long long lo = p.left < 0 ? 0 : max(0LL, last - p.left);
-    const long long hi = p.right < 0 ? (long long)L : min((long long)L, first + p.right + 1);
-    from = (int)((lo + BN - 1) / BN);
-    to = hi > 0 ? (int)(hi / BN) : 0;
-}
-
-// Waits until the shared counter is past q. Gives up after kWaitLimitNs.
-__device__ __forceinline__ bool count_past(const volatile uint32_t* count, uint32_t q) {
-    if ((int32_t)(*count - q) > 0) return true;
-    const unsigned long long t0 = globaltimer();
-    while ((int32_t)(*count - q) <= 0) {
-        if (globaltimer() - t0 > kWaitLimitNs) return false;
-        __nanosleep(64);
-    }
-    return true;
-}
-
-template <int D>
-struct Layout {
-    static constexpr uint32_t kChunk = BN * 128;                 // 128 rows x 64 values
-    static constexpr uint32_t kTile = kChunk * (D / 64);
-    static constexpr int kStages = D == 128 ? 5 : 11;
-    static constexpr uint32_t q = 0;                             // two row tiles
-    static constexpr uint32_t kv = 2 * kTile;
-    static constexpr uint32_t bars = kv + kStages * kTile;
-    static constexpr int kBars = 3 * kStages + 12 + 2 * kItems;
-    static constexpr uint32_t ml = (bars + kBars * 8 + 15) / 16 * 16;   // [128] float2
-    static constexpr uint32_t items = ml + BM * 8;               // [kItems] Item
-    static constexpr uint32_t slot = items + kItems * 64;        // tensor memory's base
-    static constexpr uint32_t issued = slot + 4;                 // tiles the producer has issued
-    static constexpr uint32_t total = slot + 16;
-};
-
-__device__ __forceinline__ uint32_t pack16(bool half_type, float lo, float hi) {
-    if (half_type) {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
-}
-
-__device__ __forceinline__ float unpack16(bool half_type, uint32_t w) {
-    return half_type ? __half2float(__ushort_as_half((unsigned short)w))
-                     : __uint_as_float(w << 16);
-}
-
-// Bit per 16-bit half of w that is an infinity or a NaN.
-template <bool kHalf>
-__device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
-    constexpr uint32_t e = kHalf ? 0x7C00u : 0x7F80u;
-    return ((w & e) == e ? 1u : 0u) | (((w >> 16) & e) == e ? 2u : 0u);
-}
-
-// Clears the infinities and NaNs of a value tile in shared memory; whether one of them was at a
-// cached token (one of the first `cached` rows of the tile). By one warp.
-template <int D, bool kHalf>
-__device__ __forceinline__ bool clear_odd(uint8_t* tile, int lane, int cached) {
-    constexpr int kVecs = (int)(Layout<D>::kTile / 16), kRun = 8;
-    uint4* v = reinterpret_cast<uint4*>(tile);
-    bool found = false;
-    for (int i0 = lane; i0 < kVecs; i0 += 32 * kRun) {
-        // x * 0 summed over a run of vectors is NaN if any value is not finite.
-        uint4 x[kRun];
-#pragma unroll
-        for (int r = 0; r < kRun; ++r) x[r] = v[i0 + 32 * r];
-        bool odd;
-        if constexpr (kHalf) {
-            const __half2 z = __float2half2_rn(0.f);
-            __half2 a = z;
-#pragma unroll
-            for (int r = 0; r < kRun; ++r) {
-                const __half2* e = reinterpret_cast<const __half2*>(&x[r]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a = __hfma2(e[i], z, a);
-            }
-            odd = __hisnan(a.x) || __hisnan(a.y);
-        } else {
-            const __nv_bfloat162 z = __float2bfloat162_rn(0.f);
-            __nv_bfloat162 a = z;
-#pragma unroll
-            for (int r = 0; r < kRun; ++r) {
-                const __nv_bfloat162* e = reinterpret_cast<const __nv_bfloat162*>(&x[r]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) a = __hfma2(e[i], z, a);
-            }
-            odd = __hisnan(a.x) || __hisnan(a.y);
-        }
-        if (!odd) continue;
-#pragma unroll 1
-        for (int r = 0; r < kRun; ++r) {
-            const int at = i0 + 32 * r;
-            const uint4 y = v[at];
-            uint32_t word[4] = {y.x, y.y, y.z, y.w};
-            bool hit = false;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t bits = odd_halves<kHalf>(word[i]);
-                hit |= bits != 0;
-                word[i] &= (bits & 1 ? 0u : 0xFFFFu) | (bits & 2 ? 0u : 0xFFFF0000u);
-            }
-            if (!hit) continue;
-            v[at] = make_uint4(word[0], word[1], word[2], word[3]);
-            found |= (at * 16 % (int)Layout<D>::kChunk) / 128 < cached;
-        }
-    }
-    return found;
-}
-
-// Add back, in the columns d .. d + 31 of a row's output, the values that are not finite and
-// that the row sees, of the tiles in which they have been cleared: weights are positive, so each
-// gives an infinity of its sign or a NaN. Taken only by items in which one was found.
-template <bool kHalf>
-__device__ __forceinline__ void refill_values(const Problem& p, const Item& c, int row_lo, int row_hi,
-                                              int d, float (&o)[32]) {
-    for (int tile = c.begin + c.lo; tile < c.begin + c.hi; ++tile) {
-        if (tile >= c.from && tile < c.to) continue;
-        const int a = max(row_lo, tile * BN), b = min(row_hi - tile * BN, BN) + tile * BN;
-        for (int j = a; j < b; ++j) {
-            const int id = p.block_table[(long long)c.r * p.max_pages + (j >> p.page_shift)];
-            if (id < 0 || id >= p.num_pages) continue;
-            const uint16_t* v = static_cast<const uint16_t*>(p.value) + id * p.page_stride +
-                                (j & (p.page_size - 1)) * p.token_stride + c.h * p.head_stride + d;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (odd_halves<kHalf>(v[i])) o[i] += unpack16(kHalf, v[i]);
-        }
-    }
-}
-
-template <int D, bool kHalf, bool kCap>
-__global__ void __launch_bounds__(kThreads, 1)
-attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Problem p,
-                 uint32_t* status) {
-    using L = Layout<D>;
-    constexpr int kChunks = D / 64;
-    constexpr uint32_t kStages = L::kStages;
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ int4 range[2];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const uint32_t base = smem_u32(smem);
-    const uint32_t bars = base + L::bars;
-    const uint32_t kv_full = bars, kv_empty = bars + 8 * kStages, kv_fix = bars + 16 * kStages;
-    const uint32_t q_full = bars + 24 * kStages, q_empty = q_full + 8;
-    const uint32_t s_full = q_full + 16, p_full = q_full + 32, o_done = q_full + 48;   // [2] each
-    const uint32_t ml_there = q_full + 64, ml_back = q_full + 72, halves_done = q_full + 80;
-    const uint32_t drained = q_full + 88;
-    const uint32_t item_full = q_full + 96, item_empty = item_full + 8 * kItems;
-    float2* ml = reinterpret_cast<float2*>(smem + L::ml);
-    Item* items = reinterpret_cast<Item*>(smem + L::items);
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::slot);
-    volatile uint32_t* issued = reinterpret_cast<volatile uint32_t*>(smem + L::issued);
-
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) {
-        for (uint32_t s = 0; s < kStages; ++s) {
-            mbar_init(kv_full + 8 * s, 1);
-            mbar_init(kv_empty + 8 * s, 1);
-            mbar_init(kv_fix + 8 * s, 32);
-        }
-        mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
-        for (int w = 0; w < 2; ++w) {
-            mbar_init(s_full + 8 * w, 1);
-            mbar_init(p_full + 8 * w, BM);
-            mbar_init(o_done + 8 * w, 1);
-        }
-        mbar_init(ml_there, BM);
-        mbar_init(ml_back, BM);
-        mbar_init(halves_done, 2 * BM);
-        mbar_init(drained, 1);
-        for (int i = 0; i < kItems; ++i) {
-            mbar_init(item_full + 8 * i, 1);
-            mbar_init(item_empty + 8 * i, kReaders);
-        }
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-        *issued = 0;
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
-    }
-    if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_u32(tmem_slot)), "r"(512)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-    }
-    grid_dependents_launch();
-    // The running costs use the ring's memory before the first tile does.
-    plan_ranges(p, reinterpret_cast<long long*>(smem + L::kv), range, status);
-    // Generic writes to the ring come before the first asynchronous ones.
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
-    bool ok = true;
-
-    // Item k of the range lies in slot k % kItems. get_item waits for it; done_with frees it, by
-    // one lane of each reading warp.
-    uint32_t k = 0;
-    auto get_item = [&]() -> const Item* {
-        const uint32_t s = k % kItems;
-        ok = __all_sync(kFull, mbar_wait(item_full + 8 * s, (k / kItems) & 1));
-        return ok && items[s].r >= 0 ? &items[s] : nullptr;
-    };
-    auto done_with = [&]() {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(item_empty + 8 * (k % kItems));
-        ++k;
-    };
-
-    // Registers: the block is launched with 168 a thread, 504 for three threads of different
-    // warpgroups; the softmax threads, which hold a row of S, take 208 each and leave 88.
-    if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
-        if (warp == 0) {
-            // ---- TMA producer: the whole warp, a box per lane
-            const int box = min(p.page_size, BN);
-            const int page_lane = lane / kChunks, chunk = lane % kChunks;
-            const bool lane_on = page_lane < BN / box;
-            uint32_t g = 0, nq = 0;      // tiles issued, query tiles issued
-            while (const Item* c = get_item()) {
-                const int lo = c->lo, hi = c->hi, begin = c->begin, h = c->h, L_ = c->L;
-                if (lo < hi) {
-                    if (nq > 0) ok = __all_sync(kFull, mbar_wait(q_empty, (nq - 1) & 1));
-                    if (!ok) break;
-                    ++nq;
-                    if (lane == 0) {
-                        const int tiles = c->pair(p) ? 2 : 1;
-                        mbar_expect_tx(q_full, (uint32_t)(tiles * p.g * p.tpt) * D * 2);
-                        for (int s = 0; s < tiles; ++s)
-                            for (int i = 0; i < kChunks; ++i)
-                                tma_load_4d(base + L::q + s * L::kTile + i * L::kChunk, &map_q,
-                                            q_full, i * 64, 0, h, c->t0 + c->tok0 + s * p.tpt);
-                    }
-                    const int32_t* table = p.block_table + (long long)c->r * p.max_pages;
-                    // This lane's page of a tile: -1 behind the last token. Ids outside the pool
-                    // are not followed: page 0 takes their place, and the item's result is NaN.
-                    auto page_of = [&](int step) -> int {
-                        const unsigned tok = (unsigned)(begin + step) * BN + page_lane * box;
-                        if (!lane_on || step >= hi || tok >= (unsigned)L_) return -1;
-                        int id = table[tok >> p.page_shift];
-                        if (id < 0 || id >= p.num_pages) {
-                            items[k % kItems].bad_page = 1;
-                            atomicOr(status, kStatusBadId);
-                            id = 0;
-                        }
-                        return id;
-                    };
-                    auto load = [&](const CUtensorMap* map, int step, int id) {
-                        const uint32_t s = g % kStages;
-                        if (g >= kStages)
-                            ok = __all_sync(kFull, mbar_wait(kv_empty + 8 * s, (g / kStages - 1) & 1));
-                        if (!ok) return;
-                        ++g;
-                        const unsigned live = __ballot_sync(kFull, id >= 0);
-                        if (lane == 0) {
-                            mbar_expect_tx(kv_full + 8 * s, (uint32_t)(__popc(live) * box * 128));
-                            *issued = g;
-                        }
-                        __syncwarp();
-                        if (id >= 0) {
-                            const unsigned tok = (unsigned)(begin + step) * BN + page_lane * box;
-                            tma_load_4d(base + L::kv + s * L::kTile + chunk * L::kChunk +
-                                            page_lane * box * 128,
-                                        map, kv_full + 8 * s, chunk * 64,
-                                        (int)(tok & (p.page_size - 1)), h, id);
-                        }
-                    };
-                    int id = page_of(lo), id_next = page_of(lo + 1);
-                    load(&map_k, lo, id);
-                    for (int j = lo; j < hi && ok; ++j) {
-                        const int id_after = page_of(j + 2);
-                        if (j + 1 < hi) load(&map_k, j + 1, id_next);
-                        if (ok) load(&map_v, j, id);
-                        id = id_next;
-                        id_next = id_after;
-                    }
-                }
-                if (!ok) break;
-                done_with();
-            }
-            if (!ok) {
-                if (lane == 0) atomicOr(status, kStatusTimeout);
-                // Let the last loads land before this CTA leaves.
-                for (uint32_t q = g > kStages ? g - kStages : 0; q < g; ++q)
-                    (void)mbar_wait(kv_full + 8 * (q % kStages), (q / kStages) & 1);
-            }
-        } else if (warp == 1) {
-            // ---- MMA issuer: one lane
-            const uint32_t idesc_s = f16_idesc_of(kHalf, false, BM, BN);
-            const uint32_t idesc_o = f16_idesc_of(kHalf, true, BM, D);
-            const uint64_t dq = sw128_desc(base + L::q), dk = sw128_desc(base + L::kv);
-            const uint64_t dv = sw128_mn_desc(base + L::kv, L::kChunk);
-            uint32_t g = 0, nq = 0;      // tiles of earlier items; items with steps
-            uint32_t np0 = 0, np1 = 0;   // P tiles waited for, by half
-            uint32_t fixed = 0;          // phase bit of each stage's kv_fix
-            while (const Item* c = get_item()) {
-                const int steps = c->hi - c->lo;
-                if (steps > 0 && lane == 0) {
-                    const bool pair = c->pair(p);
-                    const int first = c->begin + c->lo, from = c->from, to = c->to;
-                    // The ring holds K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1.
-                    auto k_tile = [&](int j) { return g + (j == 0 ? 0 : 2 * j - 1); };
-                    auto v_tile = [&](int j) { return g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1); };
-                    auto landed = [&](uint32_t q) {
-                        return mbar_wait(kv_full + 8 * (q % kStages), (q / kStages) & 1);
-                    };
-                    auto scores = [&](int w, int tile, uint32_t q) {
-                        const uint64_t a = dq + tile * (L::kTile >> 4);
-                        const uint64_t b = dk + (q % kStages) * (L::kTile >> 4);
-                        tc_fence_after();
-#pragma unroll
-                        for (int i = 0; i < D / 16; ++i) {
-                            const uint32_t o = ((i / 4) * L::kChunk + (i % 4) * 32) >> 4;
-                            umma_bf16(tmem + w * BN, a + o, b + o, idesc_s, i != 0);
-                        }
-                        umma_commit(s_full + 8 * w);
-                    };
-                    auto values = [&](int w, uint32_t q, bool start) {
-                        const uint64_t b = dv + (q % kStages) * (L::kTile >> 4);
-                        tc_fence_after();
-#pragma unroll
-                        for (int i = 0; i < BN / 16; ++i)
-                            umma_f16_tmem_a(tmem + 256 + w * 128, tmem + w * BN + i * 8,
-                                            b + i * (2048 >> 4), idesc_o, !(start && i == 0));
-                        umma_commit(o_done + 8 * w);
-                    };
-                    auto release = [&](uint32_t q) { umma_commit(kv_empty + 8 * (q % kStages)); };
-                    // The value tile has landed, and has been looked through where it has to be.
-                    auto value_ready = [&](int j) {
-                        const uint32_t q = v_tile(j), s = q % kStages;
-                        if (!landed(q)) return false;
-                        if (first + j >= from && first + j < to) return true;
-                        const uint32_t bit = (fixed >> s) & 1;
-                        fixed ^= 1u << s;
-                        return mbar_wait(kv_fix + 8 * s, bit);
-                    };
-                    auto p_ready = [&](int w) {
-                        const uint32_t n = w ? np1++ : np0++;
-                        return mbar_wait(p_full + 8 * w, n & 1);
-                    };
-                    // S of step j for half w. In a pair both halves read the step's keys.
-                    auto scores_of = [&](int w, int j) {
-                        const uint32_t q = k_tile(j);
-                        if (!(w && pair) && !landed(q)) return false;
-                        scores(w, pair ? w : 0, q);
-                        if (w || !pair) release(q);
-                        if (j == steps - 1 && (w || !pair)) umma_commit(q_empty);
-                        return true;
-                    };
-                    ok = mbar_wait(q_full, nq & 1) && scores_of(0, 0);
-                    ++nq;
-                    if (ok && (pair || steps > 1)) ok = scores_of(1, pair ? 0 : 1);
-                    // Half i & 1 of the next step: O += P V, then the S after it.
-                    const int n = pair ? 2 * steps : steps;
-#pragma unroll 1
-                    for (int i = 0; i < n && ok; ++i) {
-                        const int w = i & 1, j = pair ? i >> 1 : i;
-                        if (!(w && pair) && !(ok = value_ready(j))) break;
-                        if (!(ok = p_ready(w))) break;
-                        values(w, v_tile(j), pair ? j == 0 : j < 2);
-                        if (w || !pair) release(v_tile(j));
-                        const int next = pair ? j + 1 : j + 2;
-                        if (next < steps) ok = scores_of(w, next);
-                    }
-                    g += 2 * steps;
-                }
-                ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-                if (!ok) break;
-                done_with();
-            }
-            if (!ok && lane == 0) {
-                atomicOr(status, kStatusTimeout);
-                umma_commit(drained);            // the MMAs in flight end before this CTA leaves
-                (void)mbar_wait(drained, 0);
-            }
-        } else if (warp == 2) {
-            // ---- value tiles that some row must not see all of: clear what is not finite, so
-            // that a weight of 0 gives 0. Rows that do see such a value get it back in the
-            // epilogue.
-            uint32_t g = 0;
-            while (const Item* c = get_item()) {
-                const int steps = c->hi - c->lo;
-                for (int j = 0; j < steps && ok; ++j) {
-                    const int tile = c->begin + c->lo + j;
-                    if (tile >= c->from && tile < c->to) continue;
-                    const uint32_t q = g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1);
-                    const uint32_t s = q % kStages;
-                    // This warp skips tiles, so a stage's barrier may be phases behind the one it
-                    // wants: only once the tile is issued does its parity say which.
-                    ok = __all_sync(kFull, count_past(issued, q) &&
-                                               mbar_wait(kv_full + 8 * s, (q / kStages) & 1));
-                    if (!ok) break;
-                    if (clear_odd<D, kHalf>(smem + L::kv + s * L::kTile, lane, c->L - tile * BN))
-                        items[k % kItems].v_odd = 1;
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive(kv_fix + 8 * s);
-                }
-                if (!ok) break;
-                g += 2 * max(steps, 0);
-                done_with();
-            }
-            if (!ok && lane == 0) atomicOr(status, kStatusTimeout);
-        } else if (lane == 0) {
-            // ---- the items of this CTA's range
-            int4 at = range[0];
-            const int4 end = range[1];
-            int loaded = -1;
-            Request q = {};
-            for (;; ++k) {
-                const uint32_t s = k % kItems;
-                if (k >= kItems && !mbar_wait(item_empty + 8 * s, (k / kItems - 1) & 1)) {
-                    atomicOr(status, kStatusTimeout);
-                    break;
-                }
-                const bool last = at.x == end.x && at.y == end.y && at.z == end.z;
-                const bool none = at.x >= p.R || (last && at.w >= end.w);
-                if (!none && at.x != loaded) {
-                    q = request_of(p, at.x);
-                    loaded = at.x;
-                }
-                Item& c = items[s];
-                c.r = none ? -1 : at.x;
-                if (!none) {
-                    c.h = at.y;
-                    c.tok0 = at.z * 2 * p.tpt;
-                    c.ntok = min(2 * p.tpt, q.n - c.tok0);
-                    c.t0 = q.t0;
-                    c.n = q.n;
-                    c.L = q.L;
-                    c.bad = q.bad;
-                    int b, e, from, to;
-                    key_tiles(p, q.n, q.L, c.tok0, c.ntok, b, e);
-                    clear_tiles(p, q.n, q.L, c.tok0, c.ntok, from, to);
-                    c.begin = b;
-                    c.steps = e - b;
-                    c.lo = at.w;
-                    c.hi = last ? end.w : e - b;
-                    c.from = from;
-                    c.to = to;
-                    c.v_odd = 0;
-                    c.bad_page = 0;
-                }
-                mbar_arrive(item_full + 8 * s);
-                if (none) break;
-                if (last) {
-                    at = end;
-                } else {
-                    at.w = 0;
-                    if (++at.z == item_count(p, q.n)) {
-                        at.z = 0;
-                        if (++at.y == p.kv_heads) {
-                            at.y = 0;
-                            do ++at.x;
-                            while (at.x < p.R && request_of(p, at.x).n == 0);
-                        }
-                    }
-                }
-            }
-        }
-    } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        // ---- softmax: thread = row = tensor-memory lane
-        const int w = (warp - 4) >> 2;                       // half
-        const int row = (warp & 3) * 32 + lane;
-        const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ts = lane_base + w * BN;
-        const uint32_t to_ = lane_base + 256 + w * 128;
-        const int row_token = row / p.g;
-        const float unit = kCap ? 1.f : p.scale * kLog2e;    // S to log2 of a weight
-        const float cap = p.softcap * kLog2e;
-        const float cap_in = kCap ? 2.f * kLog2e * p.scale / p.softcap : 0.f;
-        uint32_t ns = 0, nb = 0;         // S tiles of this half; items of one row tile
-        while (const Item* c = get_item()) {
-            const int steps = c->hi - c->lo;
-            const bool pair = c->pair(p);
-            const int sub0 = c->tok0 + (pair ? w : 0) * p.tpt;   // the row tile's first token
-            const int nsub = min(p.tpt, c->n - sub0);            // and its tokens
-            const bool live = row_token < nsub;
-            const long long pos = (long long)c->L - c->n + sub0 + row_token;
-            const int row_lo = p.left < 0 ? 0 : (int)max(0LL, pos - p.left);
-            const int row_hi =
-                !live ? 0
-                      : (p.right < 0 ? c->L
-                                     : (int)max(0LL, min((long long)c->L, pos + p.right + 1)));
-            const bool warp_live = __any_sync(kFull, live);
-            const int first = c->begin + c->lo;
-            int from, to;
-            clear_tiles(p, c->n, c->L, sub0, nsub, from, to);
-            from -= first;
-            to -= first;
-            float m = -INFINITY, l = 0.f;
-            bool any = false;                                // this half has had a tile
-#pragma unroll 1
-            for (int j = pair ? 0 : w; j < steps; j += pair ? 1 : 2) {
-                ok = __all_sync(kFull, mbar_wait(s_full + 8 * w, ns & 1));
-                if (!ok) break;
-                ++ns;
-                any = true;
-                if (warp_live) {
-                    tc_fence_after();
-                    uint32_t v[BN];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld_issue_x32(ts + 32 * i, v + 32 * i);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld_wait_x32(v + 32 * i);
-                    if constexpr (kCap) {
-                        // cap * tanh(s / cap) = cap - 2 cap / (1 + e^{2 s / cap}), in log2 units
-#pragma unroll
-                        for (int i = 0; i < BN; ++i) {
-                            const float e = ex2(__uint_as_float(v[i]) * cap_in);
-                            v[i] = __float_as_uint(cap - __fdividef(2.f * cap, 1.f + e));
-                        }
-                    }
-                    if (j < from || j >= to) {
-                        const int k0 = (first + j) * BN;
-                        const int a = max(row_lo - k0, 0);
-                        const unsigned span = (unsigned)max(min(row_hi - k0, BN) - a, 0);
-#pragma unroll
-                        for (int i = 0; i < BN; ++i)
-                            if ((unsigned)(i - a) >= span) v[i] = 0xFF800000u;
-                    }
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int b = 0; b < BN; b += 8)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            top[i] = fmaxf(fmaxf(top[i], __uint_as_float(v[b + 2 * i])),
-                                           __uint_as_float(v[b + 2 * i + 1]));
-                    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * unit;
-                    const bool grown = most > m + kGrowth;   // also when m is still -inf
-                    const float keep = grown && m > -INFINITY ? ex2(m - most) : 1.f;
-                    if (grown) m = most;
-                    if (__any_sync(kFull, keep != 1.f)) {
-                        // O holds the tiles before this one: wait for the last of them.
-                        ok = __all_sync(kFull, mbar_wait(o_done + 8 * w, ns & 1));
-                        if (!ok) break;
-                        tc_fence_after();
-                        l *= keep;
-#pragma unroll 1
-                        for (int d = 0; d < D; d += 16) {
-                            uint32_t o[16];
-                            tmem_ld_issue_x16(to_ + d, o);
-                            tmem_ld_wait_x16(o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                            tmem_st_x16(to_ + d, o);
-                        }
-                        tmem_st_wait();
-                    }
-                    const float off = m == -INFINITY ? 0.f : m;
-                    const uint64_t unit2 = pair_of(unit, unit), off2 = pair_of(-off, -off);
-                    uint64_t add[2] = {0, 0};
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t pk[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 x = halves_of(
-                                fma_pair(pair_of(__uint_as_float(v[h * 32 + 2 * i]),
-                                                 __uint_as_float(v[h * 32 + 2 * i + 1])),
-                                         unit2, off2));
-                            const float lo = ex2(x.x), hi = ex2(x.y);
-                            add[i & 1] = add_pair(add[i & 1], pair_of(lo, hi));
-                            pk[i] = pack16(kHalf, lo, hi);
-                        }
-                        tmem_st_x16(ts + 16 * h, pk);
-                    }
-                    const float2 sums = halves_of(add_pair(add[0], add[1]));
-                    l += sums.x + sums.y;
-                    tmem_st_wait();
-                    tc_fence_before();
-                }
-                mbar_arrive(p_full + 8 * w);
-            }
-            // Epilogue, once this half's last tile is in O.
-            if (ok && any) ok = __all_sync(kFull, mbar_wait(o_done + 8 * w, (ns - 1) & 1));
-            if (!ok) break;
-            const bool whole = c->whole();
-            const bool nan = c->bad || c->bad_page;
-            auto finish = [&]() {                            // the factor that ends the quotient
-                if (nan) {
-                    m = 0.f;
-                    l = NAN;
-                }
-                return !whole ? 1.f : (l == 0.f ? 0.f : p.v_scale / l);
-            };
-            float f0, f1 = 0.f;                              // factors of the halves' O
-            bool has0 = any, has1 = false;
-            int d_begin = 0, d_end = D;
-            uint32_t o0 = to_;
-            if (pair) {
-                f0 = finish();
-            } else {
-                // One row tile: half 1 passes (m, l) over, half 0 returns the factors of both
-                // halves' O, and each half writes half of the columns.
-                has0 = steps > 0;
-                has1 = steps > 1;
-                if (w == 1) {
-                    ml[row] = make_float2(m, l);
-                    mbar_arrive(ml_there);
-                    ok = __all_sync(kFull, mbar_wait(ml_back, nb & 1));
-                    f0 = ml[row].x;
-                    f1 = ml[row].y;
-                } else {
-                    ok = __all_sync(kFull, mbar_wait(ml_there, nb & 1));
-                    const float2 other = ml[row];
-                    const float top = fmaxf(m, other.x);
-                    const float at = top == -INFINITY ? 0.f : top;
-                    f0 = ex2(m - at);
-                    f1 = ex2(other.x - at);
-                    l = l * f0 + other.y * f1;
-                    m = top;
-                    const float norm = finish();
-                    f0 *= norm;
-                    f1 *= norm;
-                    ml[row] = make_float2(f0, f1);
-                    mbar_arrive(ml_back);
-                }
-                if (!ok) break;
-                o0 = lane_base + 256;
-                d_begin = w * (D / 2);
-                d_end = d_begin + D / 2;
-            }
-            tc_fence_after();
-            if (warp_live) {
-                float4* part = reinterpret_cast<float4*>(
-                    p.part + (size_t)(2 * blockIdx.x + (c->lo > 0 ? 0 : 1)) * part_floats(D) +
-                    (size_t)(pair ? w : 0) * BM * (D + 2));
-                const long long out_row = ((long long)c->t0 + sub0 + row_token) * p.q_heads +
-                                          c->h * p.g + (row - row_token * p.g);
-                const bool refill = c->v_odd != 0;
-                for (int d = d_begin; d < d_end; d += 32) {
-                    uint32_t x[32], y[32];
-                    if (has0) tmem_ld_issue_x32(o0 + d, x);
-                    if (has1) tmem_ld_issue_x32(lane_base + 384 + d, y);
-                    if (has0) tmem_ld_wait_x32(x);
-                    if (has1) tmem_ld_wait_x32(y);
-                    float o[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        o[i] = has0 ? __uint_as_float(x[i]) * f0 : f0 * 0.f;
-                        if (has1) o[i] = fmaf(__uint_as_float(y[i]), f1, o[i]);
-                    }
-                    if (refill) refill_values<kHalf>(p, *c, row_lo, row_hi, d, o);
-                    if (!live) continue;
-                    if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                                                              out_row * D + d);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(pack16(kHalf, o[8 * i], o[8 * i + 1]),
-                                                pack16(kHalf, o[8 * i + 2], o[8 * i + 3]),
-                                                pack16(kHalf, o[8 * i + 4], o[8 * i + 5]),
-                                                pack16(kHalf, o[8 * i + 6], o[8 * i + 7]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            part[(d / 4 + i) * BM + row] =
-                                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-                    }
-                }
-                if (live && (pair || w == 0)) {
-                    if (!whole)
-                        reinterpret_cast<float2*>(part + BM * (D / 4))[row] = make_float2(m, l);
-                    else if (p.lse)
-                        p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
-                }
-            }
-            tc_fence_before();
-            if (!pair) {
-                // Neither half's O is written again before both halves have read it.
-                mbar_arrive(halves_done);
-                ok = __all_sync(kFull, mbar_wait(halves_done, nb & 1));
-                ++nb;
-                if (!ok) break;
-            }
-            done_with();
-        }
-        if (!ok && lane == 0) atomicOr(status, kStatusTimeout);
-    }
-
-    tc_fence_before();
-    __syncthreads();
-    if (warp == 1) {
-        tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
-                     : "memory");
-    }
-}
-
-// ---------------------------------------------------------------- join
-//
-// For each range start that cuts an item, and is the first to: out = sum_i w_i O_i / sum_i w_i l_i
-// over the item's pieces, w_i = 2^(m_i - max m). blockIdx.x: the range start - 1; blockIdx.y: a
-// slice of the item's rows and columns.
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Problem p, bool half_type) {
-    grid_dependency_wait();
-    const int b = blockIdx.x + 1;
-    const int4 at = p.bound[b], before = p.bound[b - 1];
-    if (at.x >= p.R || at.w == 0) return;
-    if (before.x == at.x && before.y == at.y && before.z == at.z && before.w > 0) return;
-    const Request q = request_of(p, at.x);
-    const int tok0 = at.z * 2 * p.tpt, ntok = min(2 * p.tpt, q.n - tok0);
-    int begin, end;
-    key_tiles(p, q.n, q.L, tok0, ntok, begin, end);
-    const int steps = end - begin;
-    // The ranges whose pieces follow the first one's (range b - 1, from step 0).
-    int last = b;
-    for (; last + 1 <= p.G; ++last) {
-        const int4 n = p.bound[last + 1];
-        if (!(n.x == at.x && n.y == at.y && n.z == at.z)) break;
-    }
-    auto piece = [&](int m) -> const float* {                // null: no steps
-        if (m < b) return p.part + (size_t)(2 * m + 1) * part_floats(D);
-        const int lo = p.bound[m].w, hi = m == last ? steps : p.bound[m + 1].w;
-        return lo < hi ? p.part + (size_t)(2 * m) * part_floats(D) : nullptr;
-    };
-    const int rows = ntok * p.g;                             // of both row tiles
-    const int in_tile = p.tpt * p.g;
-    for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < rows * (D / 4);
-         e += kJoinSlices * kJoinThreads) {
-        const int col = e / rows, row = e - col * rows;
-        const int sub = row >= in_tile ? 1 : 0, r = row - sub * in_tile;
-        const size_t tile_at = (size_t)sub * BM * (D + 2);
-        float top = -INFINITY;
-        for (int m = b - 1; m <= last; ++m) {
-            const float* o_ml = piece(m);
-            if (o_ml) top = fmaxf(top, reinterpret_cast<const float2*>(o_ml + tile_at + BM * D)[r].x);
-        }
-        const float ref = top == -INFINITY ? 0.f : top;
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int m = b - 1; m <= last; ++m) {
-            const float* o_ml = piece(m);
-            if (!o_ml) continue;
-            const float2 s = reinterpret_cast<const float2*>(o_ml + tile_at + BM * D)[r];
-            const float4 x = reinterpret_cast<const float4*>(o_ml + tile_at)[col * BM + r];
-            const float wt = ex2(s.x - ref);
-            l = fmaf(s.y, wt, l);
-            o.x = fmaf(x.x, wt, o.x);
-            o.y = fmaf(x.y, wt, o.y);
-            o.z = fmaf(x.z, wt, o.z);
-            o.w = fmaf(x.w, wt, o.w);
-        }
-        const float norm = l == 0.f ? 0.f : p.v_scale / l;
-        const long long out_row = ((long long)q.t0 + tok0 + row / p.g) * p.q_heads + at.y * p.g +
-                                  row % p.g;
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + out_row * D + col * 4) =
-            make_uint2(pack16(half_type, o.x * norm, o.y * norm),
-                       pack16(half_type, o.z * norm, o.w * norm));
-        if (col == 0 && p.lse)
-            p.lse[out_row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
-    }
-}
-
-// ---------------------------------------------------------------- host
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static std::once_flag once;
-    static EncodeTiledFn fn = nullptr;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-        else
-            (void)cudaGetLastError();
-    });
-    return fn;
-}
-
-// A rank-4 tensor of 16-bit values: dims and strides innermost first (strides in elements, of
-// dimensions 1 to 3), boxes of 64 values x box1 x 1 x box3, 128-byte swizzle.
-bool encode_4d(CUtensorMap* map, int dtype, const void* base, const long long (&dim)[4],
-               const long long (&stride)[3], int box1, int box3) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[4], strides[3];
-    for (int i = 0; i < 4; ++i) dims[i] = (cuuint64_t)dim[i];
-    // A dimension of one element is never stepped along; its stride only has to be encodable.
-    for (int i = 0; i < 3; ++i)
-        strides[i] = (cuuint64_t)((dim[i + 1] == 1 ? dim[0] : stride[i]) * 2);
-    const cuuint32_t box[4] = {64, (cuuint32_t)box1, 1, (cuuint32_t)box3};
-    const cuuint32_t step[4] = {1, 1, 1, 1};
-    return fn(map, dtype == kFp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-              4, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
@@ -1105,50 +20,11 @@ bool attention_on_tensor_cores(const AttentionArgs& a) {
         return dim == 1 || (stride > 0 && stride < (1LL << 38));
     };
     const long long g = a.q_heads / c.kv_heads;
-    return (c.head_dim == 64 || c.head_dim == 128) && c.dtype == a.dtype && c.page_size >= 8 &&
-           (c.page_size & (c.page_size - 1)) == 0 && g <= BM &&
-           a.R <= kMaxTableRequests && fits(c.token_stride, c.page_size) && fits(c.head_stride, c.kv_heads) &&
+    return (c.head_dim == 64 || c.head_dim == 128) && c.page_size >= 8 &&
+           (c.page_size & (c.page_size - 1)) == 0 && g <= BM && a.R <= kMaxTableRequests &&
+           fits(c.token_stride, c.page_size) && fits(c.head_stride, c.kv_heads) &&
            fits(c.page_stride, c.num_pages) && fits(a.q_head_stride, a.q_heads) &&
            fits(a.q_token_stride, a.T);
-}
-
-template <int D, bool kHalf, bool kCap>
-cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a, const Problem& p,
-                                   uint32_t* status, cudaStream_t stream) {
-    static std::once_flag once[64];
-    static cudaError_t attr_err[64];
-    if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
-    auto kernel = attention_kernel<D, kHalf, kCap>;
-    const size_t smem = 1024 + Layout<D>::total;
-    std::call_once(once[dev.device], [&] {
-        attr_err[dev.device] = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    });
-    if (attr_err[dev.device] != cudaSuccess) return attr_err[dev.device];
-    const KvCache& c = a.cache;
-    CUtensorMap map_q, map_k, map_v;
-    const int box = std::min(c.page_size, BN);
-    if (!encode_4d(&map_q, a.dtype, a.query, {D, p.g, c.kv_heads, a.T},
-                   {a.q_head_stride, p.g * a.q_head_stride, a.q_token_stride}, p.g, p.tpt) ||
-        !encode_4d(&map_k, a.dtype, c.key, {D, c.page_size, c.kv_heads, c.num_pages},
-                   {c.token_stride, c.head_stride, c.page_stride}, box, 1) ||
-        !encode_4d(&map_v, a.dtype, c.value, {D, c.page_size, c.kv_heads, c.num_pages},
-                   {c.token_stride, c.head_stride, c.page_stride}, box, 1))
-        return cudaErrorInvalidValue;
-    kernel<<<p.G, kThreads, smem, stream>>>(map_q, map_k, map_v, p, status);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.G < 2) return e;
-    // The join may be set up before the attention has ended, and waits for it before it reads.
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((unsigned)(p.G - 1), kJoinSlices);
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, kHalf);
 }
 
 cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void* workspace,
@@ -1156,6 +32,7 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     const KvCache& c = a.cache;
     const int D = c.head_dim;
     Problem p = {};
+    p.D = D;
     p.T = a.T;
     p.q_heads = a.q_heads;
     p.kv_heads = c.kv_heads;
@@ -1185,13 +62,12 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     w += align256((size_t)(dev.sm_count + 1) * sizeof(int4));
     p.part = reinterpret_cast<float*>(w);
     p.G = dev.sm_count;
-    using Launch = cudaError_t (*)(const DeviceInfo&, const AttentionArgs&, const Problem&, uint32_t*,
-                                   cudaStream_t);
+    if (c.dtype == kE4m3) return launch_attention_e4m3(dev, a, p, status_word, stream);
     static constexpr Launch launch[8] = {
-        launch_on_tensor_cores<64, false, false>,  launch_on_tensor_cores<64, false, true>,
-        launch_on_tensor_cores<64, true, false>,   launch_on_tensor_cores<64, true, true>,
-        launch_on_tensor_cores<128, false, false>, launch_on_tensor_cores<128, false, true>,
-        launch_on_tensor_cores<128, true, false>,  launch_on_tensor_cores<128, true, true>};
+        launch_on_tensor_cores<64, false, false, false>,  launch_on_tensor_cores<64, false, true, false>,
+        launch_on_tensor_cores<64, true, false, false>,   launch_on_tensor_cores<64, true, true, false>,
+        launch_on_tensor_cores<128, false, false, false>, launch_on_tensor_cores<128, false, true, false>,
+        launch_on_tensor_cores<128, true, false, false>,  launch_on_tensor_cores<128, true, true, false>};
     return launch[(D == 128 ? 4 : 0) + (a.dtype == kFp16 ? 2 : 0) + (a.softcap > 0.f ? 1 : 0)](
         dev, a, p, status_word, stream);
 }

@@ -203,8 +203,7 @@ struct AttentionArgs {
     float* lse;                      // may be null
 };
 
-// Whether the tensor-core kernel takes these arguments: head_dim 64 or 128, a cache of the
-// query's type, pages of a power of two of 8 or more tokens, at most 128 query heads per key
+// Whether the tensor-core kernel takes these arguments: head_dim 64 or 128, pages of a power of two of 8 or more tokens, at most 128 query heads per key
 // head, strides that a tensor map can hold.
 bool attention_on_tensor_cores(const AttentionArgs& a);
 size_t attention_workspace_bytes(const DeviceInfo& dev, int head_dim);
