@@ -88,14 +88,22 @@ constexpr float kGrowth = 8.f;          // log2 growth of a maximum before O is 
 
 __host__ __device__ inline size_t part_floats(int D) { return 2 * (size_t)BM * (D + 2); }
 
+// The keys [first_key, keys_end) that the token at position pos of L sees (pos < 0 sees none to its
+// left). No sum here leaves 32 bits: pos < L.
+__device__ __forceinline__ int first_key(const Problem& p, int pos) {
+    return p.left < 0 || pos <= p.left ? 0 : pos - p.left;
+}
+__device__ __forceinline__ int keys_end(const Problem& p, int L, int pos) {
+    return p.right < 0 || p.right >= L - pos ? L : max(0, pos + p.right + 1);
+}
+
 // Key tiles [begin, end) that tokens tok0 .. tok0 + ntok - 1 of a request see any key of.
 __device__ __forceinline__ void key_tiles(const Problem& p, int n, int L, int tok0, int ntok,
                                           int& begin, int& end) {
-    const long long first = (long long)L - n + tok0, last = first + ntok - 1;
-    const long long lo = p.left < 0 ? 0 : max(0LL, first - p.left);
-    const long long hi = p.right < 0 ? (long long)L : min((long long)L, last + p.right + 1);
-    begin = (int)(lo / BN);
-    end = hi > lo ? (int)((hi + BN - 1) / BN) : begin;
+    const int first = L - n + tok0;
+    const int lo = first_key(p, first), hi = keys_end(p, L, first + ntok - 1);
+    begin = lo / BN;
+    end = hi > lo ? (hi - 1) / BN + 1 : begin;
 }
 
 __device__ __forceinline__ int item_count(const Problem& p, int n) {
@@ -294,11 +302,9 @@ struct __align__(16) Item {
 // Others are masked row by row, and their values are looked through.
 __device__ __forceinline__ void clear_tiles(const Problem& p, int n, int L, int tok0, int ntok,
                                             int& from, int& to) {
-    const long long first = (long long)L - n + tok0, last = first + ntok - 1;
-    const long long lo = p.left < 0 ? 0 : max(0LL, last - p.left);
-    const long long hi = p.right < 0 ? (long long)L : min((long long)L, first + p.right + 1);
-    from = (int)((lo + BN - 1) / BN);
-    to = hi > 0 ? (int)(hi / BN) : 0;
+    const int first = L - n + tok0;
+    from = (first_key(p, first + ntok - 1) + BN - 1) / BN;
+    to = keys_end(p, L, first) / BN;
 }
 
 // Waits until the shared counter is past q. Gives up after kWaitLimitNs.
@@ -325,7 +331,7 @@ struct Layout {
     static constexpr uint32_t kv = 2 * kTile;
     static constexpr uint32_t raw = kv + kStages * kTile;
     static constexpr uint32_t bars = raw + kRawStages * kRaw;
-    static constexpr int kBars = 3 * kStages + 2 * kRawStages + 13 + 2 * kItems;
+    static constexpr int kBars = 3 * kStages + 2 * kRawStages + 15 + 2 * kItems;
     static constexpr uint32_t ml = (bars + kBars * 8 + 15) / 16 * 16;   // [128] float2
     static constexpr uint32_t items = ml + BM * 8;               // [kItems] Item
     static constexpr uint32_t slot = items + kItems * 64;        // tensor memory's base
@@ -409,12 +415,13 @@ __device__ __forceinline__ bool clear_odd(uint8_t* tile, int lane, int cached) {
     return found;
 }
 
-// Add back, in the columns d .. d + 31 of a row's output, the values that are not finite and
-// that the row sees, of the tiles in which they have been cleared: weights are positive, so each
-// gives an infinity of its sign or a NaN. Taken only by items in which one was found.
+// Add back to the columns d_begin .. d_end of a row's output (16-bit `out`, or fp32 `part` where
+// out is null) the values that are not finite and that the row sees, of the tiles in which they
+// have been cleared: weights are positive, so each gives an infinity of its sign or a NaN. By the
+// thread that has written the row; taken only by items in which such a value was found.
 template <bool kHalf, bool kSmall>
-__device__ __forceinline__ void refill_values(const Problem& p, const Item& c, int row_lo, int row_hi,
-                                              int d, float (&o)[32]) {
+__device__ __noinline__ void refill_values(const Problem& p, const Item& c, int row_lo, int row_hi,
+                                           int d_begin, int d_end, uint16_t* out, float* part) {
     for (int tile = c.begin + c.lo; tile < c.begin + c.hi; ++tile) {
         if (tile >= c.from && tile < c.to) continue;
         const int a = max(row_lo, tile * BN), b = min(row_hi - tile * BN, BN) + tile * BN;
@@ -422,15 +429,21 @@ __device__ __forceinline__ void refill_values(const Problem& p, const Item& c, i
             const int id = p.block_table[(long long)c.r * p.max_pages + (j >> p.page_shift)];
             if (id < 0 || id >= p.num_pages) continue;
             const long long at = id * p.page_stride + (j & (p.page_size - 1)) * p.token_stride +
-                                 c.h * p.head_stride + d;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
+                                 c.h * p.head_stride;
+            for (int d = d_begin; d < d_end; ++d) {
+                float v = 0.f;
                 if constexpr (kSmall) {
-                    const uint8_t x = static_cast<const uint8_t*>(p.value)[at + i];
-                    if ((x & 0x7F) == 0x7F) o[i] = NAN;
+                    const uint8_t x = static_cast<const uint8_t*>(p.value)[at + d];
+                    if ((x & 0x7F) == 0x7F) v = NAN;
                 } else {
-                    const uint16_t x = static_cast<const uint16_t*>(p.value)[at + i];
-                    if (odd_halves<kHalf>(x)) o[i] += unpack16(kHalf, x);
+                    const uint16_t x = static_cast<const uint16_t*>(p.value)[at + d];
+                    if (odd_halves<kHalf>(x)) v = unpack16(kHalf, x);
+                }
+                if (v == 0.f) continue;
+                if (out) {
+                    out[d] = (uint16_t)pack16(kHalf, unpack16(kHalf, out[d]) + v, 0.f);
+                } else {
+                    part[(size_t)(d / 4) * BM * 4 + d % 4] += v;
                 }
             }
         }
@@ -525,6 +538,26 @@ __device__ __forceinline__ bool widen_tile(const uint8_t* raw, uint8_t* tile, in
     return found;
 }
 
+// tanh z of the cap, cap tanh(s / cap). With e = e^(2|z|): tanh |z| = 1 - 2 / (1 + e), off by a few
+// 2^-23 absolutely. For |z| <= kSmallTanh its Taylor series to z^11, whose next term is 0.0036 z^13,
+// under 2^-26 z; two values at a time, without the special-function unit.
+constexpr float kSmallTanh = 0.35f;
+
+__device__ __forceinline__ float tanh_of(float z) {
+    const float e = ex2(fabsf(z) * (2.f * kLog2e));
+    return copysignf(1.f - __fdividef(2.f, 1.f + e), z);
+}
+
+__device__ __forceinline__ uint64_t tanh_small_pair(uint64_t z) {
+    const uint64_t z2 = mul_pair(z, z);
+    const auto both = [](float x) { return pair_of(x, x); };
+    uint64_t t = fma_pair(z2, both(-1382.f / 155925.f), both(62.f / 2835.f));
+    t = fma_pair(t, z2, both(-17.f / 315.f));
+    t = fma_pair(t, z2, both(2.f / 15.f));
+    t = fma_pair(t, z2, both(-1.f / 3.f));
+    return fma_pair(mul_pair(t, z2), z, z);
+}
+
 template <int D, bool kHalf, bool kCap, bool kSmall>
 __global__ void __launch_bounds__(Layout<D, kSmall>::kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -544,11 +577,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     const uint32_t bars = base + L::bars;
     const uint32_t kv_full = bars, kv_empty = bars + 8 * kStages, kv_fix = bars + 16 * kStages;
     const uint32_t q_full = bars + 24 * kStages, q_empty = q_full + 8;
-    const uint32_t s_full = q_full + 16, p_full = q_full + 32, o_done = q_full + 48;   // [2] each
-    const uint32_t ml_there = q_full + 64, ml_back = q_full + 72, halves_done = q_full + 80;
-    const uint32_t drained = q_full + 88;
-    const uint32_t q_ready = q_full + 96;
-    const uint32_t item_full = q_full + 104, item_empty = item_full + 8 * kItems;
+    // by half: S there, P of the upper and of the lower 64 keys there, O has the tile
+    const uint32_t s_full = q_full + 16, p_up = q_full + 32, p_low = q_full + 48;
+    const uint32_t o_done = q_full + 64;
+    const uint32_t ml_there = q_full + 80, ml_back = q_full + 88, halves_done = q_full + 96;
+    const uint32_t drained = q_full + 104, q_ready = q_full + 112;
+    const uint32_t item_full = q_full + 120, item_empty = item_full + 8 * kItems;
     const uint32_t raw_full = item_empty + 8 * kItems, raw_empty = raw_full + 8 * L::kRawStages;
     float2* ml = reinterpret_cast<float2*>(smem + L::ml);
     Item* items = reinterpret_cast<Item*>(smem + L::items);
@@ -560,20 +594,21 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         for (uint32_t s = 0; s < kStages; ++s) {
             mbar_init(kv_full + 8 * s, kSmall ? 4 : 1);
             mbar_init(kv_empty + 8 * s, 1);
-            mbar_init(kv_fix + 8 * s, 32);
+            mbar_init(kv_fix + 8 * s, 1);
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
         for (int w = 0; w < 2; ++w) {
             mbar_init(s_full + 8 * w, 1);
-            mbar_init(p_full + 8 * w, BM);
+            mbar_init(p_up + 8 * w, 4);          // warps
+            mbar_init(p_low + 8 * w, 4);
             mbar_init(o_done + 8 * w, 1);
         }
-        mbar_init(ml_there, BM);
-        mbar_init(ml_back, BM);
-        mbar_init(halves_done, 2 * BM);
+        mbar_init(ml_there, 4);
+        mbar_init(ml_back, 4);
+        mbar_init(halves_done, 8);
         mbar_init(drained, 1);
-        mbar_init(q_ready, 2 * BM);
+        mbar_init(q_ready, 8);
         for (int s = 0; s < L::kRawStages; ++s) {
             mbar_init(raw_full + 8 * s, 1);
             mbar_init(raw_empty + 8 * s, 4);
@@ -610,7 +645,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     uint32_t k = 0;
     auto get_item = [&]() -> const Item* {
         const uint32_t s = k % kItems;
-        ok = __all_sync(kFull, mbar_wait(item_full + 8 * s, (k / kItems) & 1));
+        ok = mbar_wait_warp(item_full + 8 * s, (k / kItems) & 1);
         return ok && items[s].r >= 0 ? &items[s] : nullptr;
     };
     auto done_with = [&]() {
@@ -620,11 +655,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     };
 
     // Registers: the block is launched with 168 a thread (128 of 512 threads), 504 (512) for threads
-    // of different warpgroups; the softmax threads, which hold a row of S, take 208 (184) each and
-    // leave 88 (72).
+    // of different warpgroups; the softmax threads, which hold a row of S, take 216 (184) each and
+    // leave 72.
     if (warp < 4) {
         if constexpr (kSmall) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
             // ---- TMA producer: the whole warp, a box per lane
             const int box = min(p.page_size, BN);
@@ -634,7 +669,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             while (const Item* c = get_item()) {
                 const int lo = c->lo, hi = c->hi, begin = c->begin, h = c->h, L_ = c->L;
                 if (lo < hi) {
-                    if (nq > 0) ok = __all_sync(kFull, mbar_wait(q_empty, (nq - 1) & 1));
+                    if (nq > 0) ok = mbar_wait_warp(q_empty, (nq - 1) & 1);
                     if (!ok) break;
                     ++nq;
                     if (lane == 0) {
@@ -664,7 +699,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         const uint32_t full = kSmall ? raw_full : kv_full;
                         const uint32_t empty = kSmall ? raw_empty : kv_empty;
                         const uint32_t s = g % n;
-                        if (g >= n) ok = __all_sync(kFull, mbar_wait(empty + 8 * s, (g / n - 1) & 1));
+                        if (g >= n) ok = mbar_wait_warp(empty + 8 * s, (g / n - 1) & 1);
                         if (!ok) return;
                         ++g;
                         const unsigned live = __ballot_sync(kFull, id >= 0);
@@ -705,92 +740,97 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     (void)mbar_wait((kSmall ? raw_full : kv_full) + 8 * (q % n), (q / n) & 1);
             }
         } else if (warp == 1) {
-            // ---- MMA issuer: one lane
+            // ---- MMA issuer: the warp together, an elected lane issues
             const uint32_t idesc_s = f16_idesc_of(kMmaHalf, false, BM, BN);
             const uint32_t idesc_o = f16_idesc_of(kMmaHalf, true, BM, D);
-            const uint64_t dq = sw128_desc(base + L::q), dk = sw128_desc(base + L::kv);
-            const uint64_t dv = sw128_mn_desc(base + L::kv, L::kChunk);
+            const uint32_t ubase = __shfl_sync(kFull, base, 0), utmem = __shfl_sync(kFull, tmem, 0);
+            const uint64_t dq = sw128_desc(ubase + L::q), dk = sw128_desc(ubase + L::kv);
+            const uint64_t dv = sw128_mn_desc(ubase + L::kv, L::kChunk);
             uint32_t g = 0, nq = 0;      // tiles of earlier items; items with steps
             uint32_t np0 = 0, np1 = 0;   // P tiles waited for, by half
             uint32_t fixed = 0;          // phase bit of each stage's kv_fix
+            auto wait_for = [&](uint32_t bar, uint32_t parity) {
+                ok = mbar_wait_warp(bar, parity);
+                return ok;
+            };
             while (const Item* c = get_item()) {
-                const int steps = c->hi - c->lo;
-                if (steps > 0 && lane == 0) {
-                    const bool pair = c->pair(p);
-                    const int first = c->begin + c->lo, from = c->from, to = c->to;
+                const int steps = __shfl_sync(kFull, c->hi - c->lo, 0);
+                if (steps > 0) {
+                    const bool pair = __shfl_sync(kFull, c->pair(p) ? 1 : 0, 0) != 0;
+                    // Steps whose values need no look.
+                    const int from = __shfl_sync(kFull, c->from - c->begin - c->lo, 0);
+                    const int to = __shfl_sync(kFull, c->to - c->begin - c->lo, 0);
                     // The ring holds K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1.
                     auto k_tile = [&](int j) { return g + (j == 0 ? 0 : 2 * j - 1); };
                     auto v_tile = [&](int j) { return g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1); };
                     auto landed = [&](uint32_t q) {
-                        return mbar_wait(kv_full + 8 * (q % kStages), (q / kStages) & 1);
+                        return wait_for(kv_full + 8 * (q % kStages), (q / kStages) & 1);
                     };
-                    auto scores = [&](int w, int tile, uint32_t q) {
-                        const uint64_t a = dq + tile * (L::kTile >> 4);
+                    auto release = [&](uint32_t q) { umma_commit_warp(kv_empty + 8 * (q % kStages)); };
+                    // S of step j for half w. In a pair both halves read the step's keys.
+                    auto scores = [&](int w, int j) {
+                        const uint32_t q = k_tile(j);
+                        if (!(w && pair) && !landed(q)) return;
+                        const uint64_t a = dq + (pair ? w : 0) * (L::kTile >> 4);
                         const uint64_t b = dk + (q % kStages) * (L::kTile >> 4);
                         tc_fence_after();
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             const uint32_t o = ((i / 4) * L::kChunk + (i % 4) * 32) >> 4;
-                            umma_bf16(tmem + w * BN, a + o, b + o, idesc_s, i != 0);
+                            umma_f16_warp(utmem + w * BN, a + o, b + o, idesc_s, i != 0);
                         }
-                        umma_commit(s_full + 8 * w);
+                        umma_commit_warp(s_full + 8 * w);
+                        if (w || !pair) {
+                            release(q);
+                            if (j == steps - 1) umma_commit_warp(q_empty);
+                        }
                     };
-                    auto values = [&](int w, uint32_t q, bool start) {
-                        const uint64_t b = dv + (q % kStages) * (L::kTile >> 4);
-                        tc_fence_after();
-#pragma unroll
-                        for (int i = 0; i < BN / 16; ++i)
-                            umma_f16_tmem_a(tmem + 256 + w * 128, tmem + w * BN + i * 8,
-                                            b + i * (2048 >> 4), idesc_o, !(start && i == 0));
-                        umma_commit(o_done + 8 * w);
-                    };
-                    auto release = [&](uint32_t q) { umma_commit(kv_empty + 8 * (q % kStages)); };
-                    // The value tile has landed, and has been looked through where it has to be.
-                    auto value_ready = [&](int j) {
-                        const uint32_t q = v_tile(j), s = q % kStages;
-                        if (!landed(q)) return false;
-                        if (kSmall || (first + j >= from && first + j < to)) return true;
-                        const uint32_t bit = (fixed >> s) & 1;
-                        fixed ^= 1u << s;
-                        return mbar_wait(kv_fix + 8 * s, bit);
-                    };
-                    auto p_ready = [&](int w) {
-                        const uint32_t n = w ? np1++ : np0++;
-                        return mbar_wait(p_full + 8 * w, n & 1);
-                    };
-                    // S of step j for half w. In a pair both halves read the step's keys.
-                    auto scores_of = [&](int w, int j) {
-                        const uint32_t q = k_tile(j);
-                        if (!(w && pair) && !landed(q)) return false;
-                        scores(w, pair ? w : 0, q);
-                        if (w || !pair) release(q);
-                        if (j == steps - 1 && (w || !pair)) umma_commit(q_empty);
-                        return true;
-                    };
-                    ok = mbar_wait(kScaleQ ? q_ready : q_full, nq & 1) && scores_of(0, 0);
+                    if (!wait_for(kScaleQ ? q_ready : q_full, nq & 1)) break;
                     ++nq;
-                    if (ok && (pair || steps > 1)) ok = scores_of(1, pair ? 0 : 1);
+                    scores(0, 0);
+                    if (ok && (pair || steps > 1)) scores(1, pair ? 0 : 1);
                     // Half i & 1 of the next step: O += P V, then the S after it.
                     const int n = pair ? 2 * steps : steps;
 #pragma unroll 1
                     for (int i = 0; i < n && ok; ++i) {
                         const int w = i & 1, j = pair ? i >> 1 : i;
-                        if (!(w && pair) && !(ok = value_ready(j))) break;
-                        if (!(ok = p_ready(w))) break;
-                        values(w, v_tile(j), pair ? j == 0 : j < 2);
-                        if (w || !pair) release(v_tile(j));
+                        const uint32_t q = v_tile(j), s = q % kStages;
+                        if (!(w && pair)) {
+                            // The values have landed, and been looked through where they must be.
+                            if (!landed(q)) break;
+                            if (!kSmall && !(j >= from && j < to)) {
+                                if (!wait_for(kv_fix + 8 * s, (fixed >> s) & 1)) break;
+                                fixed ^= 1u << s;
+                            }
+                        }
+                        const uint64_t b = dv + s * (L::kTile >> 4);
+                        const uint32_t o = utmem + 256 + w * 128, pt = utmem + w * BN + 64;
+                        const uint32_t more = !(pair ? j == 0 : j < 2);
+                        const uint32_t np = w ? np1++ : np0++;
+                        if (!wait_for(p_up + 8 * w, np & 1)) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int x = 4; x < 8; ++x)
+                            umma_f16_tmem_a_warp(o, pt + x * 8, b + x * (2048 >> 4), idesc_o,
+                                                 x > 4 ? 1u : more);
+                        if (!wait_for(p_low + 8 * w, np & 1)) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            umma_f16_tmem_a_warp(o, pt + x * 8, b + x * (2048 >> 4), idesc_o, 1u);
+                        umma_commit_warp(o_done + 8 * w);
+                        if (w || !pair) release(q);
                         const int next = pair ? j + 1 : j + 2;
-                        if (next < steps) ok = scores_of(w, next);
+                        if (next < steps) scores(w, next);
                     }
                     g += 2 * steps;
                 }
-                ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
                 if (!ok) break;
                 done_with();
             }
-            if (!ok && lane == 0) {
-                atomicOr(status, kStatusTimeout);
-                umma_commit(drained);            // the MMAs in flight end before this CTA leaves
+            if (!ok) {
+                if (lane == 0) atomicOr(status, kStatusTimeout);
+                umma_commit_warp(drained);       // the MMAs in flight end before this CTA leaves
                 (void)mbar_wait(drained, 0);
             }
         } else if (!kSmall && warp == 2) {
@@ -807,13 +847,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     const uint32_t s = q % kStages;
                     // This warp skips tiles, so a stage's barrier may be phases behind the one it
                     // wants: only once the tile is issued does its parity say which.
-                    ok = __all_sync(kFull, count_past(issued, q) &&
-                                               mbar_wait(kv_full + 8 * s, (q / kStages) & 1));
+                    ok = __all_sync(kFull, count_past(issued, q));
+                    if (ok) ok = mbar_wait_warp(kv_full + 8 * s, (q / kStages) & 1);
                     if (!ok) break;
                     if (clear_odd<D, kMmaHalf>(smem + L::kv + s * L::kTile, lane, c->L - tile * BN))
                         items[k % kItems].v_odd = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive(kv_fix + 8 * s);
+                    mbar_arrive_warp(kv_fix + 8 * s);
                 }
                 if (!ok) break;
                 g += 2 * max(steps, 0);
@@ -892,19 +932,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     const int tile = c->begin + c->lo + j;
                     const bool look = value && !(tile >= c->from && tile < c->to);
                     const uint32_t r = g % L::kRawStages, s = g % kStages;
-                    ok = mbar_wait(raw_full + 8 * r, (g / L::kRawStages) & 1) &&
-                         (g < kStages || mbar_wait(kv_empty + 8 * s, (g / kStages - 1) & 1));
-                    ok = __all_sync(kFull, ok);
+                    ok = mbar_wait_warp(raw_full + 8 * r, (g / L::kRawStages) & 1);
+                    if (ok && g >= kStages) ok = mbar_wait_warp(kv_empty + 8 * s, (g / kStages - 1) & 1);
                     if (!ok) break;
                     if (widen_tile<D>(smem + L::raw + r * L::kRaw, smem + L::kv + s * L::kTile, t,
                                       look, c->L - tile * BN))
                         items[k % kItems].v_odd = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(raw_empty + 8 * r);
-                        mbar_arrive(kv_full + 8 * s);
-                    }
+                    mbar_arrive_warp(raw_empty + 8 * r);
+                    mbar_arrive_warp(kv_full + 8 * s);
                 }
                 if (!ok) break;
                 done_with();
@@ -913,7 +949,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         }
     } else {
         if constexpr (kSmall) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         // ---- softmax: thread = row = tensor-memory lane
         const int w = (warp - 4) >> 2;                       // half
         const int row = (warp & 3) * 32 + lane;
@@ -929,12 +965,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const int sub0 = c->tok0 + (pair ? w : 0) * p.tpt;   // the row tile's first token
             const int nsub = min(p.tpt, c->n - sub0);            // and its tokens
             const bool live = row_token < nsub;
-            const long long pos = (long long)c->L - c->n + sub0 + row_token;
-            const int row_lo = p.left < 0 ? 0 : (int)max(0LL, pos - p.left);
-            const int row_hi =
-                !live ? 0
-                      : (p.right < 0 ? c->L
-                                     : (int)max(0LL, min((long long)c->L, pos + p.right + 1)));
+            const int pos = c->L - c->n + sub0 + row_token;
+            const int row_lo = first_key(p, pos);
+            const int row_hi = live ? keys_end(p, c->L, pos) : 0;
             const bool warp_live = __any_sync(kFull, live);
             const int first = c->begin + c->lo;
             int from, to;
@@ -942,12 +975,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             from -= first;
             to -= first;
             float unit = kCap ? 1.f : p.scale * kLog2e;      // S to log2 of a weight
-            float cap_in = kCap ? 2.f * kLog2e * p.scale / p.softcap : 0.f;
+            float cap_in = kCap ? p.scale / p.softcap : 0.f;
             if constexpr (kScaleQ) {
                 // Half w scales the row tile it will read the scores of; one row tile is half 0's,
                 // which leaves the factors for half 1.
                 if (steps > 0) {
-                    ok = __all_sync(kFull, mbar_wait(q_full, nq++ & 1));
+                    ok = mbar_wait_warp(q_full, nq++ & 1);
                     if (!ok) break;
                     if (pair || w == 0) {
                         const float undo = widen_query_row<D>(smem + L::q + w * L::kTile, row);
@@ -956,14 +989,14 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         else unit *= undo;
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     }
-                    mbar_arrive(q_ready);
+                    mbar_arrive_warp(q_ready);
                 }
             }
             float m = -INFINITY, l = 0.f;
             bool any = false;                                // this half has had a tile
 #pragma unroll 1
             for (int j = pair ? 0 : w; j < steps; j += pair ? 1 : 2) {
-                ok = __all_sync(kFull, mbar_wait(s_full + 8 * w, ns & 1));
+                ok = mbar_wait_warp(s_full + 8 * w, ns & 1);
                 if (!ok) break;
                 if constexpr (kScaleQ) {
                     if (!pair && w == 1 && !any) {           // S of half 1 follows the scaling
@@ -973,85 +1006,140 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
                 ++ns;
                 any = true;
-                if (warp_live) {
+                if (!warp_live) {
+                    mbar_arrive_warp(p_up + 8 * w);
+                    mbar_arrive_warp(p_low + 8 * w);
+                    continue;
+                }
+                tc_fence_after();
+                // S in quarters of 32 keys, first for the maximum, then, from the top, for the
+                // weights. P of a quarter overwrites S that has been read for good: quarter c goes
+                // to columns 64 + 16 c.
+                const bool masked = j < from || j >= to;
+                const int k0 = (first + j) * BN;
+                const int a0 = max(row_lo - k0, 0);
+                const unsigned span = (unsigned)max(min(row_hi - k0, BN) - a0, 0);
+                auto mask = [&](uint32_t (&v)[32], int c0) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if ((unsigned)(i + c0 - a0) >= span) v[i] = 0xFF800000u;
+                };
+                float top[2] = {-INFINITY, -INFINITY}, low[2] = {INFINITY, INFINITY};
+                auto raise = [&](const uint32_t (&v)[32]) {
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x) {
+                            const float a = __uint_as_float(v[i + 2 * x]);
+                            const float b = __uint_as_float(v[i + 2 * x + 1]);
+                            top[x] = fmaxf(fmaxf(top[x], a), b);
+                            if (kCap) low[x] = fminf(fminf(low[x], a), b);
+                        }
+                };
+                uint32_t va[32], vb[32];
+                tmem_ld_issue_x32(ts, va);
+                tmem_ld_issue_x32(ts + 32, vb);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    tmem_ld_wait_x32(va);
+                    tmem_ld_wait_x32(vb);
+                    if (masked) {
+                        mask(va, 64 * h);
+                        mask(vb, 64 * h + 32);
+                    }
+                    raise(va);
+                    if (h == 0) tmem_ld_issue_x32(ts + 64, va);
+                    raise(vb);
+                    if (h == 0) tmem_ld_issue_x32(ts + 96, vb);
+                }
+                float most = fmaxf(top[0], top[1]);
+                bool flat = true;                            // every score far below the cap
+                if constexpr (kCap) {
+                    flat = __all_sync(kFull, most * cap_in <= kSmallTanh &&
+                                                 (masked || fminf(low[0], low[1]) * cap_in >=
+                                                                -kSmallTanh));
+                    if (!(masked && most == -INFINITY)) most = cap * tanh_of(most * cap_in);
+                } else {
+                    most *= unit;
+                }
+                const bool grown = most > m + kGrowth;       // also when m is still -inf
+                const float keep = grown && m > -INFINITY ? ex2(m - most) : 1.f;
+                if (grown) m = most;
+                if (__any_sync(kFull, keep != 1.f)) {
+                    // O holds the tiles before this one: wait for the last of them.
+                    ok = mbar_wait_warp(o_done + 8 * w, ns & 1);
+                    if (!ok) break;
                     tc_fence_after();
-                    uint32_t v[BN];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld_issue_x32(ts + 32 * i, v + 32 * i);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld_wait_x32(v + 32 * i);
-                    if constexpr (kCap) {
-                        // cap * tanh(s / cap) = cap - 2 cap / (1 + e^{2 s / cap}), in log2 units
-#pragma unroll
-                        for (int i = 0; i < BN; ++i) {
-                            const float e = ex2(__uint_as_float(v[i]) * cap_in);
-                            v[i] = __float_as_uint(cap - __fdividef(2.f * cap, 1.f + e));
-                        }
-                    }
-                    if (j < from || j >= to) {
-                        const int k0 = (first + j) * BN;
-                        const int a = max(row_lo - k0, 0);
-                        const unsigned span = (unsigned)max(min(row_hi - k0, BN) - a, 0);
-#pragma unroll
-                        for (int i = 0; i < BN; ++i)
-                            if ((unsigned)(i - a) >= span) v[i] = 0xFF800000u;
-                    }
-                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int b = 0; b < BN; b += 8)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            top[i] = fmaxf(fmaxf(top[i], __uint_as_float(v[b + 2 * i])),
-                                           __uint_as_float(v[b + 2 * i + 1]));
-                    const float most = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * unit;
-                    const bool grown = most > m + kGrowth;   // also when m is still -inf
-                    const float keep = grown && m > -INFINITY ? ex2(m - most) : 1.f;
-                    if (grown) m = most;
-                    if (__any_sync(kFull, keep != 1.f)) {
-                        // O holds the tiles before this one: wait for the last of them.
-                        ok = __all_sync(kFull, mbar_wait(o_done + 8 * w, ns & 1));
-                        if (!ok) break;
-                        tc_fence_after();
-                        l *= keep;
+                    l *= keep;
 #pragma unroll 1
-                        for (int d = 0; d < D; d += 16) {
-                            uint32_t o[16];
-                            tmem_ld_issue_x16(to_ + d, o);
-                            tmem_ld_wait_x16(o);
+                    for (int d = 0; d < D; d += 16) {
+                        uint32_t o[16];
+                        tmem_ld_issue_x16(to_ + d, o);
+                        tmem_ld_wait_x16(o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                            tmem_st_x16(to_ + d, o);
-                        }
-                        tmem_st_wait();
+                        for (int i = 0; i < 16; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
+                        tmem_st_x16(to_ + d, o);
                     }
-                    const float off = m == -INFINITY ? 0.f : m;
-                    const uint64_t unit2 = pair_of(unit, unit), off2 = pair_of(-off, -off);
-                    uint64_t add[2] = {0, 0};
+                }
+                const float off = m == -INFINITY ? 0.f : m;
+                const uint64_t off2 = pair_of(-off, -off);
+                uint64_t add[2] = {0, 0};
+                // The weights of the quarter whose scores v holds.
+                auto weigh = [&](uint32_t (&v)[32], int quarter) {
+                    if constexpr (kCap) {
+                        if (flat) {
+                            const uint64_t in2 = pair_of(cap_in, cap_in), cap2 = pair_of(cap, cap);
 #pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        uint32_t pk[16];
+                            for (int i = 0; i < 32; i += 2) {
+                                const uint64_t z = mul_pair(pair_of(__uint_as_float(v[i]),
+                                                                    __uint_as_float(v[i + 1])), in2);
+                                const float2 y = halves_of(fma_pair(tanh_small_pair(z), cap2, off2));
+                                v[i] = __float_as_uint(y.x);
+                                v[i + 1] = __float_as_uint(y.y);
+                            }
+                        } else {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float2 x = halves_of(
-                                fma_pair(pair_of(__uint_as_float(v[h * 32 + 2 * i]),
-                                                 __uint_as_float(v[h * 32 + 2 * i + 1])),
-                                         unit2, off2));
-                            const float lo = ex2(x.x), hi = ex2(x.y);
-                            add[i & 1] = add_pair(add[i & 1], pair_of(lo, hi));
-                            pk[i] = pack16(kMmaHalf, lo, hi);
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = __float_as_uint(cap * tanh_of(__uint_as_float(v[i]) * cap_in) - off);
                         }
-                        tmem_st_x16(ts + 16 * h, pk);
+                        if (masked) mask(v, 32 * quarter);
                     }
-                    const float2 sums = halves_of(add_pair(add[0], add[1]));
-                    l += sums.x + sums.y;
+                    const uint64_t unit2 = pair_of(unit, unit);
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float2 x = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                        if constexpr (!kCap) x = halves_of(fma_pair(pair_of(x.x, x.y), unit2, off2));
+                        const float lo = ex2(x.x), hi = ex2(x.y);
+                        add[i & 1] = add_pair(add[i & 1], pair_of(lo, hi));
+                        pk[i] = pack16(kMmaHalf, lo, hi);
+                    }
+                    tmem_st_x16(ts + 64 + 16 * quarter, pk);
+                };
+#pragma unroll
+                for (int h = 1; h >= 0; --h) {
+                    if (h == 0) {
+                        tmem_ld_wait_x32(vb);
+                        if (!kCap && masked) mask(vb, 32);
+                    }
+                    weigh(vb, 2 * h + 1);
+                    if (h == 1) tmem_ld_issue_x32(ts + 32, vb);
+                    if (h == 0) {
+                        tmem_ld_wait_x32(va);
+                        if (!kCap && masked) mask(va, 0);
+                    }
+                    weigh(va, 2 * h);
+                    if (h == 1) tmem_ld_issue_x32(ts, va);
                     tmem_st_wait();
                     tc_fence_before();
+                    mbar_arrive_warp((h == 1 ? p_up : p_low) + 8 * w);
                 }
-                mbar_arrive(p_full + 8 * w);
+                const float2 sums = halves_of(add_pair(add[0], add[1]));
+                l += sums.x + sums.y;
             }
             // Epilogue, once this half's last tile is in O.
-            if (ok && any) ok = __all_sync(kFull, mbar_wait(o_done + 8 * w, (ns - 1) & 1));
+            if (ok && any) ok = mbar_wait_warp(o_done + 8 * w, (ns - 1) & 1);
             if (!ok) break;
             const bool whole = c->whole();
             const bool nan = c->bad || c->bad_page;
@@ -1075,12 +1163,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 has1 = steps > 1;
                 if (w == 1) {
                     ml[row] = make_float2(m, l);
-                    mbar_arrive(ml_there);
-                    ok = __all_sync(kFull, mbar_wait(ml_back, nb & 1));
+                    mbar_arrive_warp(ml_there);
+                    ok = mbar_wait_warp(ml_back, nb & 1);
                     f0 = ml[row].x;
                     f1 = ml[row].y;
                 } else {
-                    ok = __all_sync(kFull, mbar_wait(ml_there, nb & 1));
+                    ok = mbar_wait_warp(ml_there, nb & 1);
                     const float2 other = ml[row];
                     const float top = fmaxf(m, other.x);
                     const float at = top == -INFINITY ? 0.f : top;
@@ -1092,7 +1180,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     f0 *= norm;
                     f1 *= norm;
                     ml[row] = make_float2(f0, f1);
-                    mbar_arrive(ml_back);
+                    mbar_arrive_warp(ml_back);
                 }
                 if (!ok) break;
                 o0 = lane_base + 256;
@@ -1106,9 +1194,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     (size_t)(pair ? w : 0) * BM * (D + 2));
                 const long long out_row = ((long long)c->t0 + sub0 + row_token) * p.q_heads +
                                           c->h * p.g + (row - row_token * p.g);
-                const bool refill = c->v_odd != 0;
+                uint16_t* out = static_cast<uint16_t*>(p.out) + out_row * D;
+#pragma unroll 1
                 for (int d = d_begin; d < d_end; d += 32) {
-                    uint32_t x[32], y[32];
+                    uint32_t x[32] = {}, y[32] = {};
                     if (has0) tmem_ld_issue_x32(o0 + d, x);
                     if (has1) tmem_ld_issue_x32(lane_base + 384 + d, y);
                     if (has0) tmem_ld_wait_x32(x);
@@ -1119,11 +1208,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         o[i] = has0 ? __uint_as_float(x[i]) * f0 : f0 * 0.f;
                         if (has1) o[i] = fmaf(__uint_as_float(y[i]), f1, o[i]);
                     }
-                    if (refill) refill_values<kHalf, kSmall>(p, *c, row_lo, row_hi, d, o);
                     if (!live) continue;
                     if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
-                                                              out_row * D + d);
+                        uint4* dst = reinterpret_cast<uint4*>(out + d);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             dst[i] = make_uint4(pack16(kHalf, o[8 * i], o[8 * i + 1]),
@@ -1137,6 +1224,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                 make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
+                if (c->v_odd != 0 && live)
+                    refill_values<kHalf, kSmall>(p, *c, row_lo, row_hi, d_begin, d_end,
+                                                 whole ? out : nullptr,
+                                                 reinterpret_cast<float*>(part) + row * 4);
                 if (live && (pair || w == 0)) {
                     if (!whole)
                         reinterpret_cast<float2*>(part + BM * (D / 4))[row] = make_float2(m, l);
@@ -1147,8 +1238,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             tc_fence_before();
             if (!pair) {
                 // Neither half's O is written again before both halves have read it.
-                mbar_arrive(halves_done);
-                ok = __all_sync(kFull, mbar_wait(halves_done, nb & 1));
+                mbar_arrive_warp(halves_done);
+                ok = mbar_wait_warp(halves_done, nb & 1);
                 ++nb;
                 if (!ok) break;
             }
