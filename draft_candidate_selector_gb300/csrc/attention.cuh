@@ -32,7 +32,8 @@
 // per SM, wherever that falls. Every CTA takes the running cost over the requests itself (their
 // lengths are a few bytes each) and finds its own range in it. An item cut by a range's end leaves
 // (O, m, l) of its pieces in the workspace, and a joining kernel weighs them together. No CTA waits
-// for another; every mbarrier wait is bounded, and on expiry the CTA sets kStatusTimeout and stops.
+// for another. Every mbarrier wait is bounded; one that runs out sets kStatusTimeout, its warp goes
+// to the end of its item without further waits, and takes no other.
 #pragma once
 
 #include "common.cuh"
@@ -538,6 +539,11 @@ __device__ __forceinline__ bool widen_tile(const uint8_t* raw, uint8_t* tile, in
     return found;
 }
 
+// The lowest n bits, for any n.
+__device__ __forceinline__ uint32_t below(int n) {
+    return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
+}
+
 // tanh z of the cap, cap tanh(s / cap). With e = e^(2|z|): tanh |z| = 1 - 2 / (1 + e), off by a few
 // 2^-23 absolutely. For |z| <= kSmallTanh its Taylor series to z^11, whose next term is 0.0036 z^13,
 // under 2^-26 z; two values at a time, without the special-function unit.
@@ -638,14 +644,17 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    bool ok = true;
+    uint32_t tries = kWaitTries;         // 0 once a wait of this thread has run out
+    auto wait = [&](uint32_t bar, uint32_t parity) { mbar_wait_tries(bar, parity, tries); };
+    bool ok = true;                      // no wait of this warp has run out, as of its last item
 
     // Item k of the range lies in slot k % kItems. get_item waits for it; done_with frees it, by
     // one lane of each reading warp.
     uint32_t k = 0;
     auto get_item = [&]() -> const Item* {
         const uint32_t s = k % kItems;
-        ok = mbar_wait_warp(item_full + 8 * s, (k / kItems) & 1);
+        wait(item_full + 8 * s, (k / kItems) & 1);
+        ok = __all_sync(kFull, tries != 0);
         return ok && items[s].r >= 0 ? &items[s] : nullptr;
     };
     auto done_with = [&]() {
@@ -669,8 +678,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             while (const Item* c = get_item()) {
                 const int lo = c->lo, hi = c->hi, begin = c->begin, h = c->h, L_ = c->L;
                 if (lo < hi) {
-                    if (nq > 0) ok = mbar_wait_warp(q_empty, (nq - 1) & 1);
-                    if (!ok) break;
+                    if (nq > 0) wait(q_empty, (nq - 1) & 1);
+                    if (!(ok = __all_sync(kFull, tries != 0))) break;
                     ++nq;
                     if (lane == 0) {
                         const int tiles = c->pair(p) ? 2 : 1;
@@ -699,8 +708,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         const uint32_t full = kSmall ? raw_full : kv_full;
                         const uint32_t empty = kSmall ? raw_empty : kv_empty;
                         const uint32_t s = g % n;
-                        if (g >= n) ok = mbar_wait_warp(empty + 8 * s, (g / n - 1) & 1);
-                        if (!ok) return;
+                        if (g >= n) wait(empty + 8 * s, (g / n - 1) & 1);
+                        if (!(ok = __all_sync(kFull, tries != 0))) return;
                         ++g;
                         const unsigned live = __ballot_sync(kFull, id >= 0);
                         if (lane == 0) {
@@ -749,10 +758,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             uint32_t g = 0, nq = 0;      // tiles of earlier items; items with steps
             uint32_t np0 = 0, np1 = 0;   // P tiles waited for, by half
             uint32_t fixed = 0;          // phase bit of each stage's kv_fix
-            auto wait_for = [&](uint32_t bar, uint32_t parity) {
-                ok = mbar_wait_warp(bar, parity);
-                return ok;
-            };
             while (const Item* c = get_item()) {
                 const int steps = __shfl_sync(kFull, c->hi - c->lo, 0);
                 if (steps > 0) {
@@ -764,13 +769,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     auto k_tile = [&](int j) { return g + (j == 0 ? 0 : 2 * j - 1); };
                     auto v_tile = [&](int j) { return g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1); };
                     auto landed = [&](uint32_t q) {
-                        return wait_for(kv_full + 8 * (q % kStages), (q / kStages) & 1);
+                        wait(kv_full + 8 * (q % kStages), (q / kStages) & 1);
                     };
                     auto release = [&](uint32_t q) { umma_commit_warp(kv_empty + 8 * (q % kStages)); };
                     // S of step j for half w. In a pair both halves read the step's keys.
                     auto scores = [&](int w, int j) {
                         const uint32_t q = k_tile(j);
-                        if (!(w && pair) && !landed(q)) return;
+                        if (!(w && pair)) landed(q);
                         const uint64_t a = dq + (pair ? w : 0) * (L::kTile >> 4);
                         const uint64_t b = dk + (q % kStages) * (L::kTile >> 4);
                         tc_fence_after();
@@ -785,21 +790,21 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             if (j == steps - 1) umma_commit_warp(q_empty);
                         }
                     };
-                    if (!wait_for(kScaleQ ? q_ready : q_full, nq & 1)) break;
+                    wait(kScaleQ ? q_ready : q_full, nq & 1);
                     ++nq;
                     scores(0, 0);
-                    if (ok && (pair || steps > 1)) scores(1, pair ? 0 : 1);
+                    if (pair || steps > 1) scores(1, pair ? 0 : 1);
                     // Half i & 1 of the next step: O += P V, then the S after it.
                     const int n = pair ? 2 * steps : steps;
 #pragma unroll 1
-                    for (int i = 0; i < n && ok; ++i) {
+                    for (int i = 0; i < n; ++i) {
                         const int w = i & 1, j = pair ? i >> 1 : i;
                         const uint32_t q = v_tile(j), s = q % kStages;
                         if (!(w && pair)) {
                             // The values have landed, and been looked through where they must be.
-                            if (!landed(q)) break;
+                            landed(q);
                             if (!kSmall && !(j >= from && j < to)) {
-                                if (!wait_for(kv_fix + 8 * s, (fixed >> s) & 1)) break;
+                                wait(kv_fix + 8 * s, (fixed >> s) & 1);
                                 fixed ^= 1u << s;
                             }
                         }
@@ -807,13 +812,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         const uint32_t o = utmem + 256 + w * 128, pt = utmem + w * BN + 64;
                         const uint32_t more = !(pair ? j == 0 : j < 2);
                         const uint32_t np = w ? np1++ : np0++;
-                        if (!wait_for(p_up + 8 * w, np & 1)) break;
+                        wait(p_up + 8 * w, np & 1);
                         tc_fence_after();
 #pragma unroll
                         for (int x = 4; x < 8; ++x)
                             umma_f16_tmem_a_warp(o, pt + x * 8, b + x * (2048 >> 4), idesc_o,
                                                  x > 4 ? 1u : more);
-                        if (!wait_for(p_low + 8 * w, np & 1)) break;
+                        wait(p_low + 8 * w, np & 1);
                         tc_fence_after();
 #pragma unroll
                         for (int x = 0; x < 4; ++x)
@@ -825,7 +830,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                     g += 2 * steps;
                 }
-                if (!ok) break;
                 done_with();
             }
             if (!ok) {
@@ -848,8 +852,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     // This warp skips tiles, so a stage's barrier may be phases behind the one it
                     // wants: only once the tile is issued does its parity say which.
                     ok = __all_sync(kFull, count_past(issued, q));
-                    if (ok) ok = mbar_wait_warp(kv_full + 8 * s, (q / kStages) & 1);
                     if (!ok) break;
+                    wait(kv_full + 8 * s, (q / kStages) & 1);
                     if (clear_odd<D, kMmaHalf>(smem + L::kv + s * L::kTile, lane, c->L - tile * BN))
                         items[k % kItems].v_odd = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -925,16 +929,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             uint32_t g = 0;
             while (const Item* c = get_item()) {
                 const int steps = c->hi - c->lo;
-                for (int i = 0; i < 2 * steps && ok; ++i, ++g) {
+                for (int i = 0; i < 2 * steps; ++i, ++g) {
                     // K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1
                     const bool value = i == 2 * steps - 1 || (i > 0 && (i & 1) == 0);
                     const int j = i == 2 * steps - 1 ? steps - 1 : (i - 1) / 2;
                     const int tile = c->begin + c->lo + j;
                     const bool look = value && !(tile >= c->from && tile < c->to);
                     const uint32_t r = g % L::kRawStages, s = g % kStages;
-                    ok = mbar_wait_warp(raw_full + 8 * r, (g / L::kRawStages) & 1);
-                    if (ok && g >= kStages) ok = mbar_wait_warp(kv_empty + 8 * s, (g / kStages - 1) & 1);
-                    if (!ok) break;
+                    wait(raw_full + 8 * r, (g / L::kRawStages) & 1);
+                    if (g >= kStages) wait(kv_empty + 8 * s, (g / kStages - 1) & 1);
                     if (widen_tile<D>(smem + L::raw + r * L::kRaw, smem + L::kv + s * L::kTile, t,
                                       look, c->L - tile * BN))
                         items[k % kItems].v_odd = 1;
@@ -942,7 +945,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     mbar_arrive_warp(raw_empty + 8 * r);
                     mbar_arrive_warp(kv_full + 8 * s);
                 }
-                if (!ok) break;
                 done_with();
             }
             if (!ok && lane == 0) atomicOr(status, kStatusTimeout);
@@ -980,8 +982,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 // Half w scales the row tile it will read the scores of; one row tile is half 0's,
                 // which leaves the factors for half 1.
                 if (steps > 0) {
-                    ok = mbar_wait_warp(q_full, nq++ & 1);
-                    if (!ok) break;
+                    wait(q_full, nq++ & 1);
                     if (pair || w == 0) {
                         const float undo = widen_query_row<D>(smem + L::q + w * L::kTile, row);
                         if (!pair) ml[row].x = undo;
@@ -996,8 +997,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             bool any = false;                                // this half has had a tile
 #pragma unroll 1
             for (int j = pair ? 0 : w; j < steps; j += pair ? 1 : 2) {
-                ok = mbar_wait_warp(s_full + 8 * w, ns & 1);
-                if (!ok) break;
+                wait(s_full + 8 * w, ns & 1);
                 if constexpr (kScaleQ) {
                     if (!pair && w == 1 && !any) {           // S of half 1 follows the scaling
                         if (kCap) cap_in *= ml[row].x;
@@ -1017,12 +1017,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 // to columns 64 + 16 c.
                 const bool masked = j < from || j >= to;
                 const int k0 = (first + j) * BN;
-                const int a0 = max(row_lo - k0, 0);
-                const unsigned span = (unsigned)max(min(row_hi - k0, BN) - a0, 0);
                 auto mask = [&](uint32_t (&v)[32], int c0) {
+                    const uint32_t seen = below(row_hi - k0 - c0) & ~below(row_lo - k0 - c0);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
-                        if ((unsigned)(i + c0 - a0) >= span) v[i] = 0xFF800000u;
+                        if (!(seen & (1u << i))) v[i] = 0xFF800000u;
                 };
                 float top[2] = {-INFINITY, -INFINITY}, low[2] = {INFINITY, INFINITY};
                 auto raise = [&](const uint32_t (&v)[32]) {
@@ -1067,8 +1066,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 if (grown) m = most;
                 if (__any_sync(kFull, keep != 1.f)) {
                     // O holds the tiles before this one: wait for the last of them.
-                    ok = mbar_wait_warp(o_done + 8 * w, ns & 1);
-                    if (!ok) break;
+                    wait(o_done + 8 * w, ns & 1);
                     tc_fence_after();
                     l *= keep;
 #pragma unroll 1
@@ -1139,8 +1137,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 l += sums.x + sums.y;
             }
             // Epilogue, once this half's last tile is in O.
-            if (ok && any) ok = mbar_wait_warp(o_done + 8 * w, (ns - 1) & 1);
-            if (!ok) break;
+            if (any) wait(o_done + 8 * w, (ns - 1) & 1);
             const bool whole = c->whole();
             const bool nan = c->bad || c->bad_page;
             auto finish = [&]() {                            // the factor that ends the quotient
@@ -1164,11 +1161,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 if (w == 1) {
                     ml[row] = make_float2(m, l);
                     mbar_arrive_warp(ml_there);
-                    ok = mbar_wait_warp(ml_back, nb & 1);
+                    wait(ml_back, nb & 1);
                     f0 = ml[row].x;
                     f1 = ml[row].y;
                 } else {
-                    ok = mbar_wait_warp(ml_there, nb & 1);
+                    wait(ml_there, nb & 1);
                     const float2 other = ml[row];
                     const float top = fmaxf(m, other.x);
                     const float at = top == -INFINITY ? 0.f : top;
@@ -1182,7 +1179,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     ml[row] = make_float2(f0, f1);
                     mbar_arrive_warp(ml_back);
                 }
-                if (!ok) break;
                 o0 = lane_base + 256;
                 d_begin = w * (D / 2);
                 d_end = d_begin + D / 2;
@@ -1239,9 +1235,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             if (!pair) {
                 // Neither half's O is written again before both halves have read it.
                 mbar_arrive_warp(halves_done);
-                ok = mbar_wait_warp(halves_done, nb & 1);
+                wait(halves_done, nb & 1);
                 ++nb;
-                if (!ok) break;
             }
             done_with();
         }

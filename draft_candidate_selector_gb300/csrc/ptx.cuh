@@ -227,20 +227,17 @@ __device__ __forceinline__ uint32_t pack_bf16x2(uint32_t lo_bits, uint32_t hi_bi
 }
 
 
-// A whole warp's wait on an mbarrier; the lanes agree on the result. A bare loop of tries, with a
-// look at the clock now and then: reading it after the first try (as mbar_wait does), or polling
-// with one lane and passing the result on, took up to twice the time of the attention kernel as a
-// whole. Gives up after kWaitLimitNs.
-__device__ __forceinline__ bool mbar_wait_warp(uint32_t bar, uint32_t parity) {
-    unsigned long long t0 = 0;
-    for (;;) {
-        bool ok = false;
-        for (int i = 0; i < 4096 && !ok; ++i) ok = mbar_try_wait(bar, parity);
-        if (__all_sync(0xffffffffu, ok)) return true;
-        const unsigned long long t = globaltimer();
-        if (t0 == 0) t0 = t;
-        if (__any_sync(0xffffffffu, t - t0 > kWaitLimitNs)) return false;
-    }
+// A whole warp's wait on an mbarrier, in at most `tries` tries. A wait that runs out of them sets
+// tries to 0 in its lane: later waits do not wait, and whoever looks at tries learns of it. The hot
+// waits of a kernel are long chains of short ones, so nothing else is done here: reading the clock,
+// agreeing on the result after each wait, or polling with one lane each cost the attention kernel 5
+// to 50% of its time.
+constexpr uint32_t kWaitTries = 1u << 22;
+__device__ __forceinline__ void mbar_wait_tries(uint32_t bar, uint32_t parity, uint32_t& tries) {
+    bool done = false;
+    for (uint32_t i = 0; i < tries && !done; ++i) done = mbar_try_wait(bar, parity);
+    if (!done) tries = 0;
+    __syncwarp();
 }
 
 // A whole warp's arrival, as one: after what its lanes have done before.
