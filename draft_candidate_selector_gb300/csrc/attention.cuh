@@ -16,12 +16,14 @@
 // One CTA per SM, 12 warps:
 //   * warp 0: TMA producer. Each lane fetches one box (a page's rows x 64 values, 128-byte
 //     swizzle) of a key or value tile; tiles go through a ring of 32 KB (16 KB) stages.
-//   * warp 1, one lane: issues the tcgen05.mma: S = Q K^T into tensor memory, and O += P V with P
-//     in tensor memory (over S, in 16 bits) and V transposed by its descriptor.
-//   * warp 2: looks through the value tiles that some row must not see all of, and clears what is
-//     not finite there (0 x infinity would reach the rows that do not see it). See Item::v_odd.
-//   * warp 3, one lane: walks the items of this CTA's range and hands them to the others through
-//     a ring in shared memory.
+//   * warps 1 and 2, one for each half: issue the tcgen05.mma: S = Q K^T into tensor memory, and
+//     O += P V with P in tensor memory (over S, in 16 bits) and V transposed by its descriptor.
+//     Two warps, because the tensor cores idle through the waits of one (16001-token prompt: 833 us
+//     with one).
+//   * warp 3: walks the items of this CTA's range and hands them to the others through a ring in
+//     shared memory; then looks through the value tiles that some row must not see all of, and
+//     clears what is not finite there (0 x infinity would reach the rows that do not see it). See
+//     Item::v_odd.
 //   * warps 4-7 and 8-11: one softmax each, a thread per row. S comes from tensor memory, P goes
 //     back over it. O stays in tensor memory and is scaled there only when the row's maximum has
 //     grown by more than 2^8 since it was last scaled; until then P is taken relative to the old
@@ -322,7 +324,7 @@ __device__ __forceinline__ bool count_past(const volatile uint32_t* count, uint3
 template <int D, bool kSmall>
 struct Layout {
     static constexpr int kThreads = kSmall ? 512 : 384;
-    static constexpr int kReaders = kSmall ? 14 : 11;            // warps that read the items
+    static constexpr int kReaders = kSmall ? 15 : 11;            // warps that wait for items
     static constexpr uint32_t kChunk = BN * 128;                 // 128 rows x 64 values
     static constexpr uint32_t kTile = kChunk * (D / 64);
     static constexpr uint32_t kRaw = BN * D;                     // a tile in 8 bits
@@ -332,11 +334,11 @@ struct Layout {
     static constexpr uint32_t kv = 2 * kTile;
     static constexpr uint32_t raw = kv + kStages * kTile;
     static constexpr uint32_t bars = raw + kRawStages * kRaw;
-    static constexpr int kBars = 3 * kStages + 2 * kRawStages + 15 + 2 * kItems;
+    static constexpr int kBars = 3 * kStages + 2 * kRawStages + 16 + 2 * kItems;
     static constexpr uint32_t ml = (bars + kBars * 8 + 15) / 16 * 16;   // [128] float2
     static constexpr uint32_t items = ml + BM * 8;               // [kItems] Item
     static constexpr uint32_t slot = items + kItems * 64;        // tensor memory's base
-    static constexpr uint32_t issued = slot + 4;                 // tiles the producer has issued
+    static constexpr uint32_t issued = slot + 4;                 // tiles whose stage is theirs
     static constexpr uint32_t total = slot + 16;
 };
 
@@ -564,6 +566,50 @@ __device__ __forceinline__ uint64_t tanh_small_pair(uint64_t z) {
     return fma_pair(mul_pair(t, z2), z, z);
 }
 
+// A 4 x 4 transpose of 16-byte pieces over groups of four lanes: before, lane l holds pieces 0..3
+// of its row; after, piece l % 4 of the group's rows 0..3.
+__device__ __forceinline__ void turn_pieces(uint32_t (&piece)[4][4], int lane) {
+#pragma unroll
+    for (int step = 1; step < 4; step <<= 1) {
+        const bool up = (lane & step) != 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i & step) continue;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                // The upper lane gives its lower piece for the lower lane's upper one.
+                const uint32_t give = up ? piece[i][x] : piece[i | step][x];
+                const uint32_t take = __shfl_xor_sync(kFull, give, step);
+                if (up) piece[i][x] = take;
+                else piece[i | step][x] = take;
+            }
+        }
+    }
+}
+
+// v = cap tanh(v in) of 32 scores, the cap in log2 units.
+__device__ __forceinline__ void cap_scores(uint32_t (&v)[32], float in, float cap) {
+    float most = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+        most = fmaxf(fmaxf(most, fabsf(__uint_as_float(v[i]))), fabsf(__uint_as_float(v[i + 1])));
+    if (__all_sync(kFull, most * in <= kSmallTanh)) {
+        const uint64_t in2 = pair_of(in, in), cap2 = pair_of(cap, cap);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const uint64_t z =
+                mul_pair(pair_of(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), in2);
+            const float2 y = halves_of(mul_pair(tanh_small_pair(z), cap2));
+            v[i] = __float_as_uint(y.x);
+            v[i + 1] = __float_as_uint(y.y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] = __float_as_uint(cap * tanh_of(__uint_as_float(v[i]) * in));
+    }
+}
+
 template <int D, bool kHalf, bool kCap, bool kSmall>
 __global__ void __launch_bounds__(Layout<D, kSmall>::kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
@@ -587,8 +633,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     const uint32_t s_full = q_full + 16, p_up = q_full + 32, p_low = q_full + 48;
     const uint32_t o_done = q_full + 64;
     const uint32_t ml_there = q_full + 80, ml_back = q_full + 88, halves_done = q_full + 96;
-    const uint32_t drained = q_full + 104, q_ready = q_full + 112;
-    const uint32_t item_full = q_full + 120, item_empty = item_full + 8 * kItems;
+    const uint32_t drained = q_full + 104, q_ready = q_full + 120;   // drained: [2]
+    const uint32_t item_full = q_full + 128, item_empty = item_full + 8 * kItems;
     const uint32_t raw_full = item_empty + 8 * kItems, raw_empty = raw_full + 8 * L::kRawStages;
     float2* ml = reinterpret_cast<float2*>(smem + L::ml);
     Item* items = reinterpret_cast<Item*>(smem + L::items);
@@ -599,11 +645,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < kStages; ++s) {
             mbar_init(kv_full + 8 * s, kSmall ? 4 : 1);
-            mbar_init(kv_empty + 8 * s, 1);
+            mbar_init(kv_empty + 8 * s, 2);      // both halves' warps
             mbar_init(kv_fix + 8 * s, 1);
         }
         mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
+        mbar_init(q_empty, 2);
         for (int w = 0; w < 2; ++w) {
             mbar_init(s_full + 8 * w, 1);
             mbar_init(p_up + 8 * w, 4);          // warps
@@ -614,6 +660,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(ml_back, 4);
         mbar_init(halves_done, 8);
         mbar_init(drained, 1);
+        mbar_init(drained + 8, 1);
         mbar_init(q_ready, 8);
         for (int s = 0; s < L::kRawStages; ++s) {
             mbar_init(raw_full + 8 * s, 1);
@@ -715,7 +762,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         if (lane == 0) {
                             mbar_expect_tx(full + 8 * s,
                                            (uint32_t)(__popc(live) * box * (kSmall ? D : 128)));
-                            *issued = g;
+                            if (!kSmall) {
+                                __threadfence_block();
+                                *issued = g;
+                            }
                         }
                         __syncwarp();
                         if (id >= 0) {
@@ -741,22 +791,23 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 if (!ok) break;
                 done_with();
             }
-            if (!ok) {
-                if (lane == 0) atomicOr(status, kStatusTimeout);
-                // Let the last loads land before this CTA leaves.
-                constexpr uint32_t n = kSmall ? L::kRawStages : kStages;
-                for (uint32_t q = g > n ? g - n : 0; q < g; ++q)
-                    (void)mbar_wait((kSmall ? raw_full : kv_full) + 8 * (q % n), (q / n) & 1);
-            }
-        } else if (warp == 1) {
-            // ---- MMA issuer: the warp together, an elected lane issues
+            if (!ok && lane == 0) atomicOr(status, kStatusTimeout);
+            // The last loads land before this CTA leaves, whatever has become of those who use them.
+            constexpr uint32_t n = kSmall ? L::kRawStages : kStages;
+            for (uint32_t q = g > n ? g - n : 0; q < g; ++q)
+                (void)mbar_wait((kSmall ? raw_full : kv_full) + 8 * (q % n), (q / n) & 1);
+            if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
+        } else if (warp <= 2) {
+            // ---- MMA issuer of half w: the warp together, an elected lane issues
+            const int w = warp - 1;
             const uint32_t idesc_s = f16_idesc_of(kMmaHalf, false, BM, BN);
             const uint32_t idesc_o = f16_idesc_of(kMmaHalf, true, BM, D);
             const uint32_t ubase = __shfl_sync(kFull, base, 0), utmem = __shfl_sync(kFull, tmem, 0);
             const uint64_t dq = sw128_desc(ubase + L::q), dk = sw128_desc(ubase + L::kv);
             const uint64_t dv = sw128_mn_desc(ubase + L::kv, L::kChunk);
+            const uint32_t acc = utmem + 256 + w * 128, st = utmem + w * BN, pt = st + 64;
             uint32_t g = 0, nq = 0;      // tiles of earlier items; items with steps
-            uint32_t np0 = 0, np1 = 0;   // P tiles waited for, by half
+            uint32_t np = 0;             // P tiles waited for
             uint32_t fixed = 0;          // phase bit of each stage's kv_fix
             while (const Item* c = get_item()) {
                 const int steps = __shfl_sync(kFull, c->hi - c->lo, 0);
@@ -768,147 +819,124 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     // The ring holds K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1.
                     auto k_tile = [&](int j) { return g + (j == 0 ? 0 : 2 * j - 1); };
                     auto v_tile = [&](int j) { return g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1); };
+                    // A half that skips the other's tiles cannot tell by a parity alone which use of a
+                    // stage has landed: the barrier may still be one use behind. Once the tile is
+                    // issued, the uses before it are over.
                     auto landed = [&](uint32_t q) {
+                        if (!pair && !__all_sync(kFull, count_past(issued, q))) tries = 0;
                         wait(kv_full + 8 * (q % kStages), (q / kStages) & 1);
                     };
-                    auto release = [&](uint32_t q) { umma_commit_warp(kv_empty + 8 * (q % kStages)); };
-                    // S of step j for half w. In a pair both halves read the step's keys.
-                    auto scores = [&](int w, int j) {
+                    // A tile of a pair is freed by both halves, another by its half alone.
+                    auto release = [&](uint32_t q) {
+                        umma_commit_warp(kv_empty + 8 * (q % kStages));
+                        if (!pair) umma_commit_warp(kv_empty + 8 * (q % kStages));
+                    };
+                    const int stride = pair ? 1 : 2, j0 = pair ? 0 : w;
+                    auto scores = [&](int j) {               // S of step j; its keys have landed
                         const uint32_t q = k_tile(j);
-                        if (!(w && pair)) landed(q);
                         const uint64_t a = dq + (pair ? w : 0) * (L::kTile >> 4);
                         const uint64_t b = dk + (q % kStages) * (L::kTile >> 4);
                         tc_fence_after();
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             const uint32_t o = ((i / 4) * L::kChunk + (i % 4) * 32) >> 4;
-                            umma_f16_warp(utmem + w * BN, a + o, b + o, idesc_s, i != 0);
+                            umma_f16_warp(st, a + o, b + o, idesc_s, i != 0);
                         }
                         umma_commit_warp(s_full + 8 * w);
-                        if (w || !pair) {
-                            release(q);
-                            if (j == steps - 1) umma_commit_warp(q_empty);
-                        }
+                        release(q);
+                        if (j + stride >= steps) umma_commit_warp(q_empty);
                     };
                     wait(kScaleQ ? q_ready : q_full, nq & 1);
                     ++nq;
-                    scores(0, 0);
-                    if (pair || steps > 1) scores(1, pair ? 0 : 1);
-                    // Half i & 1 of the next step: O += P V, then the S after it.
-                    const int n = pair ? 2 * steps : steps;
+                    if (j0 < steps) {
+                        landed(k_tile(j0));
+                        scores(j0);
+                    } else if (lane == 0) {
+                        mbar_arrive(q_empty);
+                    }
 #pragma unroll 1
-                    for (int i = 0; i < n; ++i) {
-                        const int w = i & 1, j = pair ? i >> 1 : i;
+                    for (int j = 0; j < steps; ++j) {
                         const uint32_t q = v_tile(j), s = q % kStages;
-                        if (!(w && pair)) {
+                        const bool mine = pair || (j & 1) == w;
+                        const bool look = !kSmall && !(j >= from && j < to);
+                        if (mine) {
+                            const int next = j + stride;
+                            const uint64_t b = dv + s * (L::kTile >> 4);
+                            const uint32_t more = j != j0;
                             // The values have landed, and been looked through where they must be.
                             landed(q);
-                            if (!kSmall && !(j >= from && j < to)) {
-                                wait(kv_fix + 8 * s, (fixed >> s) & 1);
-                                fixed ^= 1u << s;
-                            }
+                            if (look) wait(kv_fix + 8 * s, (fixed >> s) & 1);
+                            wait(p_up + 8 * w, np & 1);
+                            tc_fence_after();
+#pragma unroll
+                            for (int x = 4; x < 8; ++x)
+                                umma_f16_tmem_a_warp(acc, pt + x * 8, b + x * (2048 >> 4), idesc_o,
+                                                     x > 4 ? 1u : more);
+                            if (next < steps) landed(k_tile(next));
+                            wait(p_low + 8 * w, np & 1);
+                            ++np;
+                            tc_fence_after();
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                umma_f16_tmem_a_warp(acc, pt + x * 8, b + x * (2048 >> 4), idesc_o, 1u);
+                            umma_commit_warp(o_done + 8 * w);
+                            release(q);
+                            if (next < steps) scores(next);
                         }
-                        const uint64_t b = dv + s * (L::kTile >> 4);
-                        const uint32_t o = utmem + 256 + w * 128, pt = utmem + w * BN + 64;
-                        const uint32_t more = !(pair ? j == 0 : j < 2);
-                        const uint32_t np = w ? np1++ : np0++;
-                        wait(p_up + 8 * w, np & 1);
-                        tc_fence_after();
-#pragma unroll
-                        for (int x = 4; x < 8; ++x)
-                            umma_f16_tmem_a_warp(o, pt + x * 8, b + x * (2048 >> 4), idesc_o,
-                                                 x > 4 ? 1u : more);
-                        wait(p_low + 8 * w, np & 1);
-                        tc_fence_after();
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            umma_f16_tmem_a_warp(o, pt + x * 8, b + x * (2048 >> 4), idesc_o, 1u);
-                        umma_commit_warp(o_done + 8 * w);
-                        if (w || !pair) release(q);
-                        const int next = pair ? j + 1 : j + 2;
-                        if (next < steps) scores(w, next);
+                        if (look) fixed ^= 1u << s;
                     }
                     g += 2 * steps;
                 }
                 done_with();
             }
-            if (!ok) {
-                if (lane == 0) atomicOr(status, kStatusTimeout);
-                umma_commit_warp(drained);       // the MMAs in flight end before this CTA leaves
-                (void)mbar_wait(drained, 0);
-            }
-        } else if (!kSmall && warp == 2) {
-            // ---- value tiles that some row must not see all of: clear what is not finite, so
-            // that a weight of 0 gives 0. Rows that do see such a value get it back in the
-            // epilogue.
-            uint32_t g = 0;
-            while (const Item* c = get_item()) {
-                const int steps = c->hi - c->lo;
-                for (int j = 0; j < steps && ok; ++j) {
-                    const int tile = c->begin + c->lo + j;
-                    if (tile >= c->from && tile < c->to) continue;
-                    const uint32_t q = g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1);
-                    const uint32_t s = q % kStages;
-                    // This warp skips tiles, so a stage's barrier may be phases behind the one it
-                    // wants: only once the tile is issued does its parity say which.
-                    ok = __all_sync(kFull, count_past(issued, q));
-                    if (!ok) break;
-                    wait(kv_full + 8 * s, (q / kStages) & 1);
-                    if (clear_odd<D, kMmaHalf>(smem + L::kv + s * L::kTile, lane, c->L - tile * BN))
-                        items[k % kItems].v_odd = 1;
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive_warp(kv_fix + 8 * s);
-                }
-                if (!ok) break;
-                g += 2 * max(steps, 0);
-                done_with();
-            }
             if (!ok && lane == 0) atomicOr(status, kStatusTimeout);
-        } else if (warp == 3 && lane == 0) {
-            // ---- the items of this CTA's range
+            umma_commit_warp(drained + 8 * w);       // all MMAs and arrivals end before the CTA does
+            (void)mbar_wait(drained + 8 * w, 0);
+        } else {
+            // ---- the items of this CTA's range, and the look through their value tiles. Items are
+            // handed out two ahead of the one whose tiles are looked through.
             int4 at = range[0];
             const int4 end = range[1];
             int loaded = -1;
             Request q = {};
-            for (;; ++k) {
-                const uint32_t s = k % kItems;
-                if (k >= kItems && !mbar_wait(item_empty + 8 * s, (k / kItems - 1) & 1)) {
-                    atomicOr(status, kStatusTimeout);
-                    break;
-                }
+            bool over = false;
+            auto hand_out = [&](uint32_t n) {
+                const uint32_t s = n % kItems;
+                if (n >= kItems) wait(item_empty + 8 * s, (n / kItems - 1) & 1);
                 const bool last = at.x == end.x && at.y == end.y && at.z == end.z;
-                const bool none = at.x >= p.R || (last && at.w >= end.w);
-                if (!none && at.x != loaded) {
+                over = at.x >= p.R || (last && at.w >= end.w);
+                if (!over && at.x != loaded) {
                     q = request_of(p, at.x);
                     loaded = at.x;
                 }
-                Item& c = items[s];
-                c.r = none ? -1 : at.x;
-                if (!none) {
-                    c.h = at.y;
-                    c.tok0 = at.z * 2 * p.tpt;
-                    c.ntok = min(2 * p.tpt, q.n - c.tok0);
-                    c.t0 = q.t0;
-                    c.n = q.n;
-                    c.L = q.L;
-                    c.bad = q.bad;
-                    int b, e, from, to;
-                    key_tiles(p, q.n, q.L, c.tok0, c.ntok, b, e);
-                    clear_tiles(p, q.n, q.L, c.tok0, c.ntok, from, to);
-                    c.begin = b;
-                    c.steps = e - b;
-                    c.lo = at.w;
-                    c.hi = last ? end.w : e - b;
-                    c.from = from;
-                    c.to = to;
-                    c.v_odd = 0;
-                    c.bad_page = 0;
+                if (lane == 0) {
+                    Item& c = items[s];
+                    c.r = over ? -1 : at.x;
+                    if (!over) {
+                        c.h = at.y;
+                        c.tok0 = at.z * 2 * p.tpt;
+                        c.ntok = min(2 * p.tpt, q.n - c.tok0);
+                        c.t0 = q.t0;
+                        c.n = q.n;
+                        c.L = q.L;
+                        c.bad = q.bad;
+                        int b, e, from, to;
+                        key_tiles(p, q.n, q.L, c.tok0, c.ntok, b, e);
+                        clear_tiles(p, q.n, q.L, c.tok0, c.ntok, from, to);
+                        c.begin = b;
+                        c.steps = e - b;
+                        c.lo = at.w;
+                        c.hi = last ? end.w : e - b;
+                        c.from = from;
+                        c.to = to;
+                        c.v_odd = 0;
+                        c.bad_page = 0;
+                    }
                 }
-                mbar_arrive(item_full + 8 * s);
-                if (none) break;
+                mbar_arrive_warp(item_full + 8 * s);
                 if (last) {
                     at = end;
-                } else {
+                } else if (!over) {
                     at.w = 0;
                     if (++at.z == item_count(p, q.n)) {
                         at.z = 0;
@@ -919,7 +947,30 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         }
                     }
                 }
+            };
+            uint32_t handed = 0, g = 0;
+            for (;; ++k) {
+                while (!over && handed < k + 3) hand_out(handed++);
+                const Item* c = &items[k % kItems];
+                if (c->r < 0 || !__all_sync(kFull, tries != 0)) break;
+                const int steps = c->hi - c->lo;
+                for (int j = 0; j < steps && !kSmall; ++j) {
+                    const int tile = c->begin + c->lo + j;
+                    if (tile >= c->from && tile < c->to) continue;
+                    const uint32_t t = g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1);
+                    const uint32_t s = t % kStages;
+                    // This warp skips tiles, so a stage's barrier may be phases behind the one it
+                    // wants: only once the tile is issued does its parity say which.
+                    if (!__all_sync(kFull, count_past(issued, t))) tries = 0;
+                    wait(kv_full + 8 * s, (t / kStages) & 1);
+                    if (clear_odd<D, kMmaHalf>(smem + L::kv + s * L::kTile, lane, c->L - tile * BN))
+                        items[k % kItems].v_odd = 1;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    mbar_arrive_warp(kv_fix + 8 * s);
+                }
+                g += 2 * max(steps, 0);
             }
+            if (!__all_sync(kFull, tries != 0) && lane == 0) atomicOr(status, kStatusTimeout);
         }
     } else if (kSmall && warp >= 12) {
         if constexpr (kSmall) {
@@ -938,6 +989,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     const uint32_t r = g % L::kRawStages, s = g % kStages;
                     wait(raw_full + 8 * r, (g / L::kRawStages) & 1);
                     if (g >= kStages) wait(kv_empty + 8 * s, (g / kStages - 1) & 1);
+                    if (t == 0) *issued = g + 1;             // the uses of the stage before it are over
                     if (widen_tile<D>(smem + L::raw + r * L::kRaw, smem + L::kv + s * L::kTile, t,
                                       look, c->L - tile * BN))
                         items[k % kItems].v_odd = 1;
@@ -1012,55 +1064,53 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     continue;
                 }
                 tc_fence_after();
-                // S in quarters of 32 keys, first for the maximum, then, from the top, for the
-                // weights. P of a quarter overwrites S that has been read for good: quarter c goes
-                // to columns 64 + 16 c.
+                // Tiles that need more than the common steps (a cap, rows that do not see all of the
+                // tile) get it first, in tensor memory, a quarter of 32 keys at a time.
+                uint32_t va[32], vb[32];
                 const bool masked = j < from || j >= to;
-                const int k0 = (first + j) * BN;
-                auto mask = [&](uint32_t (&v)[32], int c0) {
-                    const uint32_t seen = below(row_hi - k0 - c0) & ~below(row_lo - k0 - c0);
+                if (kCap || masked) {
+                    const int k0 = (first + j) * BN;
+#pragma unroll 1
+                    for (int c0 = 0; c0 < BN; c0 += 32) {
+                        tmem_ld_issue_x32(ts + c0, va);
+                        tmem_ld_wait_x32(va);
+                        if constexpr (kCap) cap_scores(va, cap_in, cap);
+                        if (masked) {
+                            const uint32_t seen =
+                                below(row_hi - k0 - c0) & ~below(row_lo - k0 - c0);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!(seen & (1u << i))) v[i] = 0xFF800000u;
-                };
-                float top[2] = {-INFINITY, -INFINITY}, low[2] = {INFINITY, INFINITY};
+                            for (int i = 0; i < 32; ++i)
+                                if (!(seen & (1u << i))) va[i] = 0xFF800000u;
+                        }
+                        tmem_st_x32(ts + c0, va);
+                    }
+                    tmem_st_wait();
+                }
+                // S in quarters, first for the maximum, then, from the top, for the weights. P of a
+                // quarter overwrites S that has been read for good: quarter c goes to columns
+                // 64 + 16 c.
+                float top[2] = {-INFINITY, -INFINITY};
                 auto raise = [&](const uint32_t (&v)[32]) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 4)
 #pragma unroll
-                        for (int x = 0; x < 2; ++x) {
-                            const float a = __uint_as_float(v[i + 2 * x]);
-                            const float b = __uint_as_float(v[i + 2 * x + 1]);
-                            top[x] = fmaxf(fmaxf(top[x], a), b);
-                            if (kCap) low[x] = fminf(fminf(low[x], a), b);
-                        }
+                        for (int x = 0; x < 2; ++x)
+                            top[x] = fmaxf(fmaxf(top[x], __uint_as_float(v[i + 2 * x])),
+                                           __uint_as_float(v[i + 2 * x + 1]));
                 };
-                uint32_t va[32], vb[32];
                 tmem_ld_issue_x32(ts, va);
                 tmem_ld_issue_x32(ts + 32, vb);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    tmem_ld_wait_x32(va);
-                    tmem_ld_wait_x32(vb);
-                    if (masked) {
-                        mask(va, 64 * h);
-                        mask(vb, 64 * h + 32);
-                    }
-                    raise(va);
-                    if (h == 0) tmem_ld_issue_x32(ts + 64, va);
-                    raise(vb);
-                    if (h == 0) tmem_ld_issue_x32(ts + 96, vb);
-                }
-                float most = fmaxf(top[0], top[1]);
-                bool flat = true;                            // every score far below the cap
-                if constexpr (kCap) {
-                    flat = __all_sync(kFull, most * cap_in <= kSmallTanh &&
-                                                 (masked || fminf(low[0], low[1]) * cap_in >=
-                                                                -kSmallTanh));
-                    if (!(masked && most == -INFINITY)) most = cap * tanh_of(most * cap_in);
-                } else {
-                    most *= unit;
-                }
+                tmem_ld_wait_x32(va);
+                tmem_ld_wait_x32(vb);
+                raise(va);
+                tmem_ld_issue_x32(ts + 64, va);
+                raise(vb);
+                tmem_ld_issue_x32(ts + 96, vb);
+                tmem_ld_wait_x32(va);
+                tmem_ld_wait_x32(vb);
+                raise(va);
+                raise(vb);
+                const float most = fmaxf(top[0], top[1]) * unit;
                 const bool grown = most > m + kGrowth;       // also when m is still -inf
                 const float keep = grown && m > -INFINITY ? ex2(m - most) : 1.f;
                 if (grown) m = most;
@@ -1081,58 +1131,36 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                 }
                 const float off = m == -INFINITY ? 0.f : m;
-                const uint64_t off2 = pair_of(-off, -off);
+                const uint64_t unit2 = pair_of(unit, unit), off2 = pair_of(-off, -off);
                 uint64_t add[2] = {0, 0};
-                // The weights of the quarter whose scores v holds.
-                auto weigh = [&](uint32_t (&v)[32], int quarter) {
-                    if constexpr (kCap) {
-                        if (flat) {
-                            const uint64_t in2 = pair_of(cap_in, cap_in), cap2 = pair_of(cap, cap);
-#pragma unroll
-                            for (int i = 0; i < 32; i += 2) {
-                                const uint64_t z = mul_pair(pair_of(__uint_as_float(v[i]),
-                                                                    __uint_as_float(v[i + 1])), in2);
-                                const float2 y = halves_of(fma_pair(tanh_small_pair(z), cap2, off2));
-                                v[i] = __float_as_uint(y.x);
-                                v[i + 1] = __float_as_uint(y.y);
-                            }
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[i] = __float_as_uint(cap * tanh_of(__uint_as_float(v[i]) * cap_in) - off);
-                        }
-                        if (masked) mask(v, 32 * quarter);
-                    }
-                    const uint64_t unit2 = pair_of(unit, unit);
+                // The weights of one quarter, from its scores.
+                auto weigh = [&](const uint32_t (&v)[32], int quarter) {
                     uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float2 x = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                        if constexpr (!kCap) x = halves_of(fma_pair(pair_of(x.x, x.y), unit2, off2));
+                        const float2 x = halves_of(
+                            fma_pair(pair_of(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                     unit2, off2));
                         const float lo = ex2(x.x), hi = ex2(x.y);
                         add[i & 1] = add_pair(add[i & 1], pair_of(lo, hi));
                         pk[i] = pack16(kMmaHalf, lo, hi);
                     }
                     tmem_st_x16(ts + 64 + 16 * quarter, pk);
                 };
-#pragma unroll
-                for (int h = 1; h >= 0; --h) {
-                    if (h == 0) {
-                        tmem_ld_wait_x32(vb);
-                        if (!kCap && masked) mask(vb, 32);
-                    }
-                    weigh(vb, 2 * h + 1);
-                    if (h == 1) tmem_ld_issue_x32(ts + 32, vb);
-                    if (h == 0) {
-                        tmem_ld_wait_x32(va);
-                        if (!kCap && masked) mask(va, 0);
-                    }
-                    weigh(va, 2 * h);
-                    if (h == 1) tmem_ld_issue_x32(ts, va);
-                    tmem_st_wait();
-                    tc_fence_before();
-                    mbar_arrive_warp((h == 1 ? p_up : p_low) + 8 * w);
-                }
+                weigh(vb, 3);
+                tmem_ld_issue_x32(ts + 32, vb);
+                weigh(va, 2);
+                tmem_ld_wait_x32(vb);
+                tmem_ld_issue_x32(ts, va);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive_warp(p_up + 8 * w);
+                weigh(vb, 1);
+                tmem_ld_wait_x32(va);
+                weigh(va, 0);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive_warp(p_low + 8 * w);
                 const float2 sums = halves_of(add_pair(add[0], add[1]));
                 l += sums.x + sums.y;
             }
@@ -1191,6 +1219,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 const long long out_row = ((long long)c->t0 + sub0 + row_token) * p.q_heads +
                                           c->h * p.g + (row - row_token * p.g);
                 uint16_t* out = static_cast<uint16_t*>(p.out) + out_row * D;
+                // The rows whose output this lane stores: 16-byte pieces pass through groups of four
+                // lanes, so that a store covers 8 rows x 64 bytes and not 32 rows x 16.
+                int rows_out[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    rows_out[i] = __shfl_sync(kFull, live ? (int)out_row : -1, (lane & ~3) + i);
 #pragma unroll 1
                 for (int d = d_begin; d < d_end; d += 32) {
                     uint32_t x[32] = {}, y[32] = {};
@@ -1204,22 +1238,29 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         o[i] = has0 ? __uint_as_float(x[i]) * f0 : f0 * 0.f;
                         if (has1) o[i] = fmaf(__uint_as_float(y[i]), f1, o[i]);
                     }
-                    if (!live) continue;
                     if (whole) {
-                        uint4* dst = reinterpret_cast<uint4*>(out + d);
+                        uint32_t piece[4][4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(pack16(kHalf, o[8 * i], o[8 * i + 1]),
-                                                pack16(kHalf, o[8 * i + 2], o[8 * i + 3]),
-                                                pack16(kHalf, o[8 * i + 4], o[8 * i + 5]),
-                                                pack16(kHalf, o[8 * i + 6], o[8 * i + 7]));
-                    } else {
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                piece[i][x] = pack16(kHalf, o[8 * i + 2 * x], o[8 * i + 2 * x + 1]);
+                        turn_pieces(piece, lane);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (rows_out[i] >= 0)
+                                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                                          (long long)rows_out[i] * D + d +
+                                                          8 * (lane & 3)) =
+                                    make_uint4(piece[i][0], piece[i][1], piece[i][2], piece[i][3]);
+                    } else if (live) {
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             part[(d / 4 + i) * BM + row] =
                                 make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
                     }
                 }
+                if (c->v_odd != 0) __syncwarp();             // the rows are written by other lanes
                 if (c->v_odd != 0 && live)
                     refill_values<kHalf, kSmall>(p, *c, row_lo, row_hi, d_begin, d_end,
                                                  whole ? out : nullptr,
@@ -1363,7 +1404,7 @@ bool encode_4d(CUtensorMap* map, int dtype, const void* base, const long long (&
     return fn(map, type, 4, const_cast<void*>(base), dims, strides, box, step,
               CU_TENSOR_MAP_INTERLEAVE_NONE,
               dtype == kE4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              dtype == kE4m3 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

@@ -262,6 +262,18 @@ def test_attention_long_contexts(dev, dtype, cache, D):
     check(b, left=6000, right=-1)
 
 
+@pytest.mark.parametrize("dtype,cache", TYPES)
+def test_attention_many_steps(dev, dtype, cache):
+    """Single tokens over contexts long enough that each part of a split has many key tiles, from
+    pages all over a large pool: right, and the same bits every time."""
+    b = paged.Batch([60000, 90001], [1, 1], 4, 1, 128, 16, dtype, cache, seed=14, spread=2.0)
+    want = check(b)
+    for _ in range(40):
+        for g, w in zip(ds.dflash_paged_attention(*b.args(), **b.scales()), want):
+            assert torch.equal(g, w)
+    clean()
+
+
 def test_attention_empty_rows(dev):
     """A request with no cached key at all gives zeros and -inf; so does one whose length is less
     than its new tokens, for the tokens in front of it; requests without tokens give nothing."""
