@@ -334,11 +334,11 @@ struct Layout {
     static constexpr uint32_t kv = 2 * kTile;
     static constexpr uint32_t raw = kv + kStages * kTile;
     static constexpr uint32_t bars = raw + kRawStages * kRaw;
-    static constexpr int kBars = 3 * kStages + 2 * kRawStages + 16 + 2 * kItems;
+    static constexpr int kBars = 4 * kStages + 2 * kRawStages + 16 + 2 * kItems;
     static constexpr uint32_t ml = (bars + kBars * 8 + 15) / 16 * 16;   // [128] float2
     static constexpr uint32_t items = ml + BM * 8;               // [kItems] Item
     static constexpr uint32_t slot = items + kItems * 64;        // tensor memory's base
-    static constexpr uint32_t issued = slot + 4;                 // tiles whose stage is theirs
+    static constexpr uint32_t issued = slot + 4;                 // tiles the producer has issued
     static constexpr uint32_t total = slot + 16;
 };
 
@@ -627,8 +627,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t base = smem_u32(smem);
     const uint32_t bars = base + L::bars;
-    const uint32_t kv_full = bars, kv_empty = bars + 8 * kStages, kv_fix = bars + 16 * kStages;
-    const uint32_t q_full = bars + 24 * kStages, q_empty = q_full + 8;
+    // Two kv_full barriers a stage, for its uses by turns: a half that skips the other half's tiles
+    // may look at a barrier before the use in front of the one it wants has landed, never before
+    // the one in front of that (the tile it used last was issued after that one had been freed), so
+    // with two the parity cannot be mistaken.
+    const uint32_t kv_full = bars, kv_empty = bars + 16 * kStages, kv_fix = bars + 24 * kStages;
+    const uint32_t q_full = bars + 32 * kStages, q_empty = q_full + 8;
     // by half: S there, P of the upper and of the lower 64 keys there, O has the tile
     const uint32_t s_full = q_full + 16, p_up = q_full + 32, p_low = q_full + 48;
     const uint32_t o_done = q_full + 64;
@@ -645,6 +649,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < kStages; ++s) {
             mbar_init(kv_full + 8 * s, kSmall ? 4 : 1);
+            mbar_init(kv_full + 8 * (kStages + s), kSmall ? 4 : 1);
             mbar_init(kv_empty + 8 * s, 2);      // both halves' warps
             mbar_init(kv_fix + 8 * s, 1);
         }
@@ -752,20 +757,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     };
                     auto load = [&](const CUtensorMap* map, int step, int id) {
                         constexpr uint32_t n = kSmall ? L::kRawStages : kStages;
-                        const uint32_t full = kSmall ? raw_full : kv_full;
                         const uint32_t empty = kSmall ? raw_empty : kv_empty;
                         const uint32_t s = g % n;
+                        const uint32_t full = kSmall ? raw_full + 8 * s : kv_full + 8 * (g % (2 * kStages));
                         if (g >= n) wait(empty + 8 * s, (g / n - 1) & 1);
                         if (!(ok = __all_sync(kFull, tries != 0))) return;
                         ++g;
                         const unsigned live = __ballot_sync(kFull, id >= 0);
                         if (lane == 0) {
-                            mbar_expect_tx(full + 8 * s,
-                                           (uint32_t)(__popc(live) * box * (kSmall ? D : 128)));
-                            if (!kSmall) {
-                                __threadfence_block();
-                                *issued = g;
-                            }
+                            mbar_expect_tx(full, (uint32_t)(__popc(live) * box * (kSmall ? D : 128)));
+                            if (!kSmall) *issued = g;
                         }
                         __syncwarp();
                         if (id >= 0) {
@@ -774,7 +775,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                 kSmall ? base + L::raw + s * L::kRaw + page_lane * box * D
                                        : base + L::kv + s * L::kTile + chunk * L::kChunk +
                                              page_lane * box * 128;
-                            tma_load_4d(to, map, full + 8 * s, chunk * 64,
+                            tma_load_4d(to, map, full, chunk * 64,
                                         (int)(tok & (p.page_size - 1)), h, id);
                         }
                     };
@@ -795,7 +796,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             // The last loads land before this CTA leaves, whatever has become of those who use them.
             constexpr uint32_t n = kSmall ? L::kRawStages : kStages;
             for (uint32_t q = g > n ? g - n : 0; q < g; ++q)
-                (void)mbar_wait((kSmall ? raw_full : kv_full) + 8 * (q % n), (q / n) & 1);
+                (void)(kSmall ? mbar_wait(raw_full + 8 * (q % n), (q / n) & 1)
+                              : mbar_wait(kv_full + 8 * (q % (2 * n)), (q / (2 * n)) & 1));
             if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
         } else if (warp <= 2) {
             // ---- MMA issuer of half w: the warp together, an elected lane issues
@@ -819,12 +821,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     // The ring holds K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1.
                     auto k_tile = [&](int j) { return g + (j == 0 ? 0 : 2 * j - 1); };
                     auto v_tile = [&](int j) { return g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1); };
-                    // A half that skips the other's tiles cannot tell by a parity alone which use of a
-                    // stage has landed: the barrier may still be one use behind. Once the tile is
-                    // issued, the uses before it are over.
                     auto landed = [&](uint32_t q) {
-                        if (!pair && !__all_sync(kFull, count_past(issued, q))) tries = 0;
-                        wait(kv_full + 8 * (q % kStages), (q / kStages) & 1);
+                        wait(kv_full + 8 * (q % (2 * kStages)), (q / (2 * kStages)) & 1);
                     };
                     // A tile of a pair is freed by both halves, another by its half alone.
                     auto release = [&](uint32_t q) {
@@ -959,10 +957,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     if (tile >= c->from && tile < c->to) continue;
                     const uint32_t t = g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1);
                     const uint32_t s = t % kStages;
-                    // This warp skips tiles, so a stage's barrier may be phases behind the one it
-                    // wants: only once the tile is issued does its parity say which.
+                    // This warp may be any number of tiles ahead: only once the tile is issued does a
+                    // parity say which use has landed.
                     if (!__all_sync(kFull, count_past(issued, t))) tries = 0;
-                    wait(kv_full + 8 * s, (t / kStages) & 1);
+                    wait(kv_full + 8 * (t % (2 * kStages)), (t / (2 * kStages)) & 1);
                     if (clear_odd<D, kMmaHalf>(smem + L::kv + s * L::kTile, lane, c->L - tile * BN))
                         items[k % kItems].v_odd = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -989,13 +987,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     const uint32_t r = g % L::kRawStages, s = g % kStages;
                     wait(raw_full + 8 * r, (g / L::kRawStages) & 1);
                     if (g >= kStages) wait(kv_empty + 8 * s, (g / kStages - 1) & 1);
-                    if (t == 0) *issued = g + 1;             // the uses of the stage before it are over
                     if (widen_tile<D>(smem + L::raw + r * L::kRaw, smem + L::kv + s * L::kTile, t,
                                       look, c->L - tile * BN))
                         items[k % kItems].v_odd = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive_warp(raw_empty + 8 * r);
-                    mbar_arrive_warp(kv_full + 8 * s);
+                    mbar_arrive_warp(kv_full + 8 * (g % (2 * kStages)));
                 }
                 done_with();
             }
