@@ -13,9 +13,12 @@
 // tiles of 128 tokens, or, where a request has no more than tpt tokens left, one row tile whose
 // even and odd key tiles go to the two halves of the CTA.
 //
-// One CTA per SM, 12 warps:
-//   * warp 0: TMA producer. Each lane fetches one box (a page's rows x 64 values, 128-byte
-//     swizzle) of a key or value tile; tiles go through a ring of 32 KB (16 KB) stages.
+// One CTA per SM, 16 warps (13-15 work for 8-bit caches only):
+//   * warps 0 and 12: TMA producers, of keys (and queries) and of values. Each lane looks up one page
+//     of a tile; the pages' boxes (a page's rows x 64 values, 128-byte swizzle) are issued one after
+//     another by the warp together. Keys and values go through a ring of stages each. Two warps,
+//     because a box takes some 60 ns to issue whatever its size, and a tile of 16-token pages has
+//     16.
 //   * warps 1 and 2, one for each half: issue the tcgen05.mma: S = Q K^T into tensor memory, and
 //     O += P V with P in tensor memory (over S, in 16 bits) and V transposed by its descriptor.
 //     Two warps, because the tensor cores idle through the waits of one (16001-token prompt: 833 us
@@ -79,6 +82,7 @@ using Problem = AttentionProblem;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int BM = 128;                 // rows of a row tile: tensor-memory lanes
 constexpr int BN = 128;                 // keys of a key tile
+constexpr int kThreads = 512;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinSlices = 8;          // CTAs that share one cut item's join
 constexpr int kItems = 4;               // slots of the item ring
@@ -204,7 +208,6 @@ __device__ __forceinline__ int4 range_start(const Problem& p, const long long* c
 // Every thread of the CTA: the running cost over the requests in cost[R + 1] (shared memory),
 // then this CTA's range. Where there are no more items than SMs and none is long, the cost of
 // each is 1, so that ranges fall on whole items and nothing has to be joined.
-template <int kThreads>
 __device__ __forceinline__ void plan_ranges(const Problem& p, long long* cost, int4* range,
                                             uint32_t* status) {
     __shared__ long long warp_sum[kThreads / 32], warp_items[kThreads / 32];
@@ -323,22 +326,23 @@ __device__ __forceinline__ bool count_past(const volatile uint32_t* count, uint3
 
 template <int D, bool kSmall>
 struct Layout {
-    static constexpr int kThreads = kSmall ? 512 : 384;
-    static constexpr int kReaders = kSmall ? 15 : 11;            // warps that wait for items
+    static constexpr int kReaders = kSmall ? 15 : 12;            // warps that wait for items
     static constexpr uint32_t kChunk = BN * 128;                 // 128 rows x 64 values
     static constexpr uint32_t kTile = kChunk * (D / 64);
     static constexpr uint32_t kRaw = BN * D;                     // a tile in 8 bits
-    static constexpr int kRawStages = kSmall ? (D == 128 ? 4 : 8) : 0;
-    static constexpr int kStages = kSmall ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 11);
+    static constexpr int kRawStages = kSmall ? (D == 128 ? 2 : 8) : 0;
+    static constexpr int kK = kSmall ? (D == 128 ? 2 : 3) : (D == 128 ? 2 : 5);   // key stages
+    static constexpr int kV = kSmall ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);   // value stages
     static constexpr uint32_t q = 0;                             // two row tiles
-    static constexpr uint32_t kv = 2 * kTile;
-    static constexpr uint32_t raw = kv + kStages * kTile;
+    static constexpr uint32_t keys = 2 * kTile;
+    static constexpr uint32_t values = keys + kK * kTile;
+    static constexpr uint32_t raw = values + kV * kTile;
     static constexpr uint32_t bars = raw + kRawStages * kRaw;
-    static constexpr int kBars = 4 * kStages + 2 * kRawStages + 16 + 2 * kItems;
+    static constexpr int kBars = 3 * kK + 4 * kV + 2 * kRawStages + 16 + 2 * kItems;
     static constexpr uint32_t ml = (bars + kBars * 8 + 15) / 16 * 16;   // [128] float2
     static constexpr uint32_t items = ml + BM * 8;               // [kItems] Item
     static constexpr uint32_t slot = items + kItems * 64;        // tensor memory's base
-    static constexpr uint32_t issued = slot + 4;                 // tiles the producer has issued
+    static constexpr uint32_t issued = slot + 4;                 // value tiles issued
     static constexpr uint32_t total = slot + 16;
 };
 
@@ -611,28 +615,29 @@ __device__ __forceinline__ void cap_scores(uint32_t (&v)[32], float in, float ca
 }
 
 template <int D, bool kHalf, bool kCap, bool kSmall>
-__global__ void __launch_bounds__(Layout<D, kSmall>::kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Problem p,
                  uint32_t* status) {
     using L = Layout<D, kSmall>;
-    constexpr int kThreads = L::kThreads;
     constexpr bool kMmaHalf = kHalf || kSmall;               // the tensor cores' operands are fp16
     constexpr bool kScaleQ = kSmall && !kHalf;               // bf16 queries are scaled to fp16
     constexpr int kChunks = kSmall ? 1 : D / 64;             // boxes across a row
-    constexpr uint32_t kStages = L::kStages;
+    constexpr uint32_t kK = L::kK, kV = L::kV;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int4 range[2];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const uint32_t base = smem_u32(smem);
     const uint32_t bars = base + L::bars;
-    // Two kv_full barriers a stage, for its uses by turns: a half that skips the other half's tiles
-    // may look at a barrier before the use in front of the one it wants has landed, never before
-    // the one in front of that (the tile it used last was issued after that one had been freed), so
-    // with two the parity cannot be mistaken.
-    const uint32_t kv_full = bars, kv_empty = bars + 16 * kStages, kv_fix = bars + 24 * kStages;
-    const uint32_t q_full = bars + 32 * kStages, q_empty = q_full + 8;
+    // Two barriers a stage for its landings, for its uses by turns: a half that skips the other
+    // half's tiles may look at a barrier before the use in front of the one it wants has landed,
+    // never before the one in front of that (the tile it used last was issued after that one had
+    // been freed), so with two the parity cannot be mistaken.
+    const uint32_t k_full = bars, k_empty = k_full + 16 * kK;            // [2 kK], [kK]
+    const uint32_t v_full = k_empty + 8 * kK, v_empty = v_full + 16 * kV;   // [2 kV], [kV]
+    const uint32_t v_fix = v_empty + 8 * kV;                             // [kV]
+    const uint32_t q_full = v_fix + 8 * kV, q_empty = q_full + 8;
     // by half: S there, P of the upper and of the lower 64 keys there, O has the tile
     const uint32_t s_full = q_full + 16, p_up = q_full + 32, p_low = q_full + 48;
     const uint32_t o_done = q_full + 64;
@@ -647,11 +652,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
-        for (uint32_t s = 0; s < kStages; ++s) {
-            mbar_init(kv_full + 8 * s, kSmall ? 4 : 1);
-            mbar_init(kv_full + 8 * (kStages + s), kSmall ? 4 : 1);
-            mbar_init(kv_empty + 8 * s, 2);      // both halves' warps
-            mbar_init(kv_fix + 8 * s, 1);
+        // Landings: the producer, or the four widening warps. Releases: both halves' warps.
+        for (uint32_t s = 0; s < 2 * kK; ++s) mbar_init(k_full + 8 * s, kSmall ? 4 : 1);
+        for (uint32_t s = 0; s < 2 * kV; ++s) mbar_init(v_full + 8 * s, kSmall ? 4 : 1);
+        for (uint32_t s = 0; s < kK; ++s) mbar_init(k_empty + 8 * s, 2);
+        for (uint32_t s = 0; s < kV; ++s) {
+            mbar_init(v_empty + 8 * s, 2);
+            mbar_init(v_fix + 8 * s, 1);
         }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 2);
@@ -689,7 +696,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     }
     grid_dependents_launch();
     // The running costs use the ring's memory before the first tile does.
-    plan_ranges<kThreads>(p, reinterpret_cast<long long*>(smem + L::kv), range, status);
+    plan_ranges(p, reinterpret_cast<long long*>(smem + L::keys), range, status);
     // Generic writes to the ring come before the first asynchronous ones.
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     tc_fence_before();
@@ -715,20 +722,54 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         ++k;
     };
 
-    // Registers: the block is launched with 168 a thread (128 of 512 threads), 504 (512) for threads
-    // of different warpgroups; the softmax threads, which hold a row of S, take 216 (184) each and
-    // leave 72.
+    // One tile of keys or values of this range: tile g of its ring. `id`: this lane's page, -1 behind
+    // the last token.
+    auto issue_tile = [&](const CUtensorMap* map, uint32_t to, uint32_t full, int h, int row0, int id) {
+        const int box = min(p.page_size, BN);
+        const int n = __popc(__ballot_sync(kFull, id >= 0));
+        if (lane == 0) mbar_expect_tx(full, (uint32_t)(n * box * D * (kSmall ? 1 : 2)));
+        __syncwarp();
+        int next = __shfl_sync(kFull, id, 0);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i, to += box * (kSmall ? D : 128)) {
+            const int page = next;
+            next = __shfl_sync(kFull, id, i + 1);
+#pragma unroll
+            for (int x = 0; x < kChunks; ++x)
+                tma_load_4d_warp(to + x * L::kChunk, map, full, x * 64, row0, h, page);
+        }
+    };
+    // This lane's page of an item's tile: -1 behind the last token. Ids outside the pool are not
+    // followed: page 0 takes their place, and the item's result is NaN.
+    auto page_of = [&](const Item* c, int step) -> int {
+        const int box = min(p.page_size, BN);
+        const unsigned tok = (unsigned)(c->begin + step) * BN + lane * box;
+        if (lane >= BN / box || step >= c->hi || tok >= (unsigned)c->L) return -1;
+        int id = p.block_table[(long long)c->r * p.max_pages + (tok >> p.page_shift)];
+        if (id < 0 || id >= p.num_pages) {
+            items[k % kItems].bad_page = 1;
+            atomicOr(status, kStatusBadId);
+            id = 0;
+        }
+        return id;
+    };
+    auto row_of = [&](const Item* c, int step) {             // of its page, where the tile begins
+        return ((c->begin + step) * BN) & (p.page_size - 1);
+    };
+
+    // Registers: the block is launched with 128 a thread, 512 for threads of the four warpgroups;
+    // the softmax threads, which hold half a row of S, take 184 each, the others keep 72.
     if (warp < 4) {
-        if constexpr (kSmall) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
-            // ---- TMA producer: the whole warp, a box per lane
-            const int box = min(p.page_size, BN);
-            const int page_lane = lane / kChunks, chunk = lane % kChunks;
-            const bool lane_on = page_lane < BN / box;
-            uint32_t g = 0, nq = 0;      // tiles issued, query tiles issued
+            // ---- TMA producer of queries and keys; of an 8-bit cache's raw tiles, keys and values
+            uint32_t g = 0, nq = 0;      // tiles issued, items with steps
+            auto free_stage = [&](uint32_t empty, uint32_t n) {
+                if (g >= n) wait(empty + 8 * (g % n), (g / n - 1) & 1);
+                return ok = __all_sync(kFull, tries != 0);
+            };
             while (const Item* c = get_item()) {
-                const int lo = c->lo, hi = c->hi, begin = c->begin, h = c->h, L_ = c->L;
+                const int lo = c->lo, hi = c->hi, h = c->h;
                 if (lo < hi) {
                     if (nq > 0) wait(q_empty, (nq - 1) & 1);
                     if (!(ok = __all_sync(kFull, tries != 0))) break;
@@ -741,52 +782,34 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                 tma_load_4d(base + L::q + s * L::kTile + i * L::kChunk, &map_q,
                                             q_full, i * 64, 0, h, c->t0 + c->tok0 + s * p.tpt);
                     }
-                    const int32_t* table = p.block_table + (long long)c->r * p.max_pages;
-                    // This lane's page of a tile: -1 behind the last token. Ids outside the pool
-                    // are not followed: page 0 takes their place, and the item's result is NaN.
-                    auto page_of = [&](int step) -> int {
-                        const unsigned tok = (unsigned)(begin + step) * BN + page_lane * box;
-                        if (!lane_on || step >= hi || tok >= (unsigned)L_) return -1;
-                        int id = table[tok >> p.page_shift];
-                        if (id < 0 || id >= p.num_pages) {
-                            items[k % kItems].bad_page = 1;
-                            atomicOr(status, kStatusBadId);
-                            id = 0;
+                    __syncwarp();
+                    if constexpr (kSmall) {
+                        // K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1
+                        constexpr uint32_t n = L::kRawStages;
+                        auto load = [&](const CUtensorMap* map, int step, int id) {
+                            if (!free_stage(raw_empty, n)) return;
+                            issue_tile(map, base + L::raw + (g % n) * L::kRaw, raw_full + 8 * (g % n),
+                                       h, row_of(c, step), id);
+                            ++g;
+                        };
+                        int id = page_of(c, lo), id_next = page_of(c, lo + 1);
+                        load(&map_k, lo, id);
+                        for (int j = lo; j < hi && ok; ++j) {
+                            const int id_after = page_of(c, j + 2);
+                            if (j + 1 < hi) load(&map_k, j + 1, id_next);
+                            if (ok) load(&map_v, j, id);
+                            id = id_next;
+                            id_next = id_after;
                         }
-                        return id;
-                    };
-                    auto load = [&](const CUtensorMap* map, int step, int id) {
-                        constexpr uint32_t n = kSmall ? L::kRawStages : kStages;
-                        const uint32_t empty = kSmall ? raw_empty : kv_empty;
-                        const uint32_t s = g % n;
-                        const uint32_t full = kSmall ? raw_full + 8 * s : kv_full + 8 * (g % (2 * kStages));
-                        if (g >= n) wait(empty + 8 * s, (g / n - 1) & 1);
-                        if (!(ok = __all_sync(kFull, tries != 0))) return;
-                        ++g;
-                        const unsigned live = __ballot_sync(kFull, id >= 0);
-                        if (lane == 0) {
-                            mbar_expect_tx(full, (uint32_t)(__popc(live) * box * (kSmall ? D : 128)));
-                            if (!kSmall) *issued = g;
+                    } else {
+                        int id = page_of(c, lo);
+                        for (int j = lo; j < hi; ++j, ++g) {
+                            const int id_next = page_of(c, j + 1);
+                            if (!free_stage(k_empty, kK)) break;
+                            issue_tile(&map_k, base + L::keys + (g % kK) * L::kTile,
+                                       k_full + 8 * (g % (2 * kK)), h, row_of(c, j), id);
+                            id = id_next;
                         }
-                        __syncwarp();
-                        if (id >= 0) {
-                            const unsigned tok = (unsigned)(begin + step) * BN + page_lane * box;
-                            const uint32_t to =
-                                kSmall ? base + L::raw + s * L::kRaw + page_lane * box * D
-                                       : base + L::kv + s * L::kTile + chunk * L::kChunk +
-                                             page_lane * box * 128;
-                            tma_load_4d(to, map, full, chunk * 64,
-                                        (int)(tok & (p.page_size - 1)), h, id);
-                        }
-                    };
-                    int id = page_of(lo), id_next = page_of(lo + 1);
-                    load(&map_k, lo, id);
-                    for (int j = lo; j < hi && ok; ++j) {
-                        const int id_after = page_of(j + 2);
-                        if (j + 1 < hi) load(&map_k, j + 1, id_next);
-                        if (ok) load(&map_v, j, id);
-                        id = id_next;
-                        id_next = id_after;
                     }
                 }
                 if (!ok) break;
@@ -794,10 +817,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             }
             if (!ok && lane == 0) atomicOr(status, kStatusTimeout);
             // The last loads land before this CTA leaves, whatever has become of those who use them.
-            constexpr uint32_t n = kSmall ? L::kRawStages : kStages;
-            for (uint32_t q = g > n ? g - n : 0; q < g; ++q)
-                (void)(kSmall ? mbar_wait(raw_full + 8 * (q % n), (q / n) & 1)
-                              : mbar_wait(kv_full + 8 * (q % (2 * n)), (q / (2 * n)) & 1));
+            constexpr uint32_t n = kSmall ? L::kRawStages : kK;
+            for (uint32_t t = g > n ? g - n : 0; t < g; ++t)
+                (void)(kSmall ? mbar_wait(raw_full + 8 * (t % n), (t / n) & 1)
+                              : mbar_wait(k_full + 8 * (t % (2 * n)), (t / (2 * n)) & 1));
             if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
         } else if (warp <= 2) {
             // ---- MMA issuer of half w: the warp together, an elected lane issues
@@ -805,12 +828,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const uint32_t idesc_s = f16_idesc_of(kMmaHalf, false, BM, BN);
             const uint32_t idesc_o = f16_idesc_of(kMmaHalf, true, BM, D);
             const uint32_t ubase = __shfl_sync(kFull, base, 0), utmem = __shfl_sync(kFull, tmem, 0);
-            const uint64_t dq = sw128_desc(ubase + L::q), dk = sw128_desc(ubase + L::kv);
-            const uint64_t dv = sw128_mn_desc(ubase + L::kv, L::kChunk);
+            const uint64_t dq = sw128_desc(ubase + L::q), dk = sw128_desc(ubase + L::keys);
+            const uint64_t dv = sw128_mn_desc(ubase + L::values, L::kChunk);
             const uint32_t acc = utmem + 256 + w * 128, st = utmem + w * BN, pt = st + 64;
-            uint32_t g = 0, nq = 0;      // tiles of earlier items; items with steps
+            uint32_t g = 0, nq = 0;      // steps of earlier items; items with steps
             uint32_t np = 0;             // P tiles waited for
-            uint32_t fixed = 0;          // phase bit of each stage's kv_fix
+            uint32_t fixed = 0;          // phase bit of each stage's v_fix
             while (const Item* c = get_item()) {
                 const int steps = __shfl_sync(kFull, c->hi - c->lo, 0);
                 if (steps > 0) {
@@ -818,22 +841,19 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     // Steps whose values need no look.
                     const int from = __shfl_sync(kFull, c->from - c->begin - c->lo, 0);
                     const int to = __shfl_sync(kFull, c->to - c->begin - c->lo, 0);
-                    // The ring holds K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1.
-                    auto k_tile = [&](int j) { return g + (j == 0 ? 0 : 2 * j - 1); };
-                    auto v_tile = [&](int j) { return g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1); };
-                    auto landed = [&](uint32_t q) {
-                        wait(kv_full + 8 * (q % (2 * kStages)), (q / (2 * kStages)) & 1);
+                    auto k_landed = [&](int j) {
+                        wait(k_full + 8 * ((g + j) % (2 * kK)), ((g + j) / (2 * kK)) & 1);
                     };
                     // A tile of a pair is freed by both halves, another by its half alone.
-                    auto release = [&](uint32_t q) {
-                        umma_commit_warp(kv_empty + 8 * (q % kStages));
-                        if (!pair) umma_commit_warp(kv_empty + 8 * (q % kStages));
+                    auto release = [&](uint32_t empty) {
+                        umma_commit_warp(empty);
+                        if (!pair) umma_commit_warp(empty);
                     };
                     const int stride = pair ? 1 : 2, j0 = pair ? 0 : w;
                     auto scores = [&](int j) {               // S of step j; its keys have landed
-                        const uint32_t q = k_tile(j);
+                        const uint32_t s = (g + j) % kK;
                         const uint64_t a = dq + (pair ? w : 0) * (L::kTile >> 4);
-                        const uint64_t b = dk + (q % kStages) * (L::kTile >> 4);
+                        const uint64_t b = dk + s * (L::kTile >> 4);
                         tc_fence_after();
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
@@ -841,20 +861,20 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             umma_f16_warp(st, a + o, b + o, idesc_s, i != 0);
                         }
                         umma_commit_warp(s_full + 8 * w);
-                        release(q);
+                        release(k_empty + 8 * s);
                         if (j + stride >= steps) umma_commit_warp(q_empty);
                     };
                     wait(kScaleQ ? q_ready : q_full, nq & 1);
                     ++nq;
                     if (j0 < steps) {
-                        landed(k_tile(j0));
+                        k_landed(j0);
                         scores(j0);
                     } else if (lane == 0) {
                         mbar_arrive(q_empty);
                     }
 #pragma unroll 1
                     for (int j = 0; j < steps; ++j) {
-                        const uint32_t q = v_tile(j), s = q % kStages;
+                        const uint32_t t = g + j, s = t % kV;
                         const bool mine = pair || (j & 1) == w;
                         const bool look = !kSmall && !(j >= from && j < to);
                         if (mine) {
@@ -862,15 +882,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             const uint64_t b = dv + s * (L::kTile >> 4);
                             const uint32_t more = j != j0;
                             // The values have landed, and been looked through where they must be.
-                            landed(q);
-                            if (look) wait(kv_fix + 8 * s, (fixed >> s) & 1);
+                            wait(v_full + 8 * (t % (2 * kV)), (t / (2 * kV)) & 1);
+                            if (look) wait(v_fix + 8 * s, (fixed >> s) & 1);
                             wait(p_up + 8 * w, np & 1);
                             tc_fence_after();
 #pragma unroll
                             for (int x = 4; x < 8; ++x)
                                 umma_f16_tmem_a_warp(acc, pt + x * 8, b + x * (2048 >> 4), idesc_o,
                                                      x > 4 ? 1u : more);
-                            if (next < steps) landed(k_tile(next));
+                            if (next < steps) k_landed(next);
                             wait(p_low + 8 * w, np & 1);
                             ++np;
                             tc_fence_after();
@@ -878,12 +898,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             for (int x = 0; x < 4; ++x)
                                 umma_f16_tmem_a_warp(acc, pt + x * 8, b + x * (2048 >> 4), idesc_o, 1u);
                             umma_commit_warp(o_done + 8 * w);
-                            release(q);
+                            release(v_empty + 8 * s);
                             if (next < steps) scores(next);
                         }
                         if (look) fixed ^= 1u << s;
                     }
-                    g += 2 * steps;
+                    g += steps;
                 }
                 done_with();
             }
@@ -955,52 +975,72 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 for (int j = 0; j < steps && !kSmall; ++j) {
                     const int tile = c->begin + c->lo + j;
                     if (tile >= c->from && tile < c->to) continue;
-                    const uint32_t t = g + (j < steps - 1 ? 2 * j + 2 : 2 * j + 1);
-                    const uint32_t s = t % kStages;
+                    const uint32_t t = g + j, s = t % kV;
                     // This warp may be any number of tiles ahead: only once the tile is issued does a
                     // parity say which use has landed.
                     if (!__all_sync(kFull, count_past(issued, t))) tries = 0;
-                    wait(kv_full + 8 * (t % (2 * kStages)), (t / (2 * kStages)) & 1);
-                    if (clear_odd<D, kMmaHalf>(smem + L::kv + s * L::kTile, lane, c->L - tile * BN))
+                    wait(v_full + 8 * (t % (2 * kV)), (t / (2 * kV)) & 1);
+                    if (clear_odd<D, kMmaHalf>(smem + L::values + s * L::kTile, lane, c->L - tile * BN))
                         items[k % kItems].v_odd = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive_warp(kv_fix + 8 * s);
+                    mbar_arrive_warp(v_fix + 8 * s);
                 }
-                g += 2 * max(steps, 0);
+                g += max(steps, 0);
             }
             if (!__all_sync(kFull, tries != 0) && lane == 0) atomicOr(status, kStatusTimeout);
         }
-    } else if (kSmall && warp >= 12) {
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if constexpr (kSmall) {
             // ---- 8-bit tiles to fp16
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
             const int t = threadIdx.x - 384;
-            uint32_t g = 0;
+            uint32_t g = 0, raw = 0;     // steps of earlier items; raw tiles taken
             while (const Item* c = get_item()) {
-                const int steps = c->hi - c->lo;
-                for (int i = 0; i < 2 * steps; ++i, ++g) {
+                const int steps = max(c->hi - c->lo, 0);
+                for (int i = 0; i < 2 * steps; ++i, ++raw) {
                     // K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1
                     const bool value = i == 2 * steps - 1 || (i > 0 && (i & 1) == 0);
-                    const int j = i == 2 * steps - 1 ? steps - 1 : (i - 1) / 2;
+                    const int j = value ? (i - 1) / 2 : (i + 1) / 2;
                     const int tile = c->begin + c->lo + j;
                     const bool look = value && !(tile >= c->from && tile < c->to);
-                    const uint32_t r = g % L::kRawStages, s = g % kStages;
-                    wait(raw_full + 8 * r, (g / L::kRawStages) & 1);
-                    if (g >= kStages) wait(kv_empty + 8 * s, (g / kStages - 1) & 1);
-                    if (widen_tile<D>(smem + L::raw + r * L::kRaw, smem + L::kv + s * L::kTile, t,
-                                      look, c->L - tile * BN))
+                    const uint32_t n = value ? kV : kK, u = g + j, r = raw % L::kRawStages;
+                    wait(raw_full + 8 * r, (raw / L::kRawStages) & 1);
+                    if (u >= n) wait((value ? v_empty : k_empty) + 8 * (u % n), (u / n - 1) & 1);
+                    uint8_t* to = smem + (value ? L::values : L::keys) + (u % n) * L::kTile;
+                    if (widen_tile<D>(smem + L::raw + r * L::kRaw, to, t, look, c->L - tile * BN))
                         items[k % kItems].v_odd = 1;
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     mbar_arrive_warp(raw_empty + 8 * r);
-                    mbar_arrive_warp(kv_full + 8 * (g % (2 * kStages)));
+                    mbar_arrive_warp((value ? v_full : k_full) + 8 * (u % (2 * n)));
                 }
+                g += steps;
                 done_with();
             }
             if (!ok && lane == 0) atomicOr(status, kStatusTimeout);
+        } else if (warp == 12) {
+            // ---- TMA producer of values
+            uint32_t g = 0;
+            while (const Item* c = get_item()) {
+                const int hi = c->hi, h = c->h;
+                int id = page_of(c, c->lo);
+                for (int j = c->lo; j < hi; ++j, ++g) {
+                    const int id_next = page_of(c, j + 1);
+                    if (g >= kV) wait(v_empty + 8 * (g % kV), (g / kV - 1) & 1);
+                    if (!(ok = __all_sync(kFull, tries != 0))) break;
+                    if (lane == 0) *issued = g + 1;
+                    issue_tile(&map_v, base + L::values + (g % kV) * L::kTile,
+                               v_full + 8 * (g % (2 * kV)), h, row_of(c, j), id);
+                    id = id_next;
+                }
+                if (!ok) break;
+                done_with();
+            }
+            if (!ok && lane == 0) atomicOr(status, kStatusTimeout);
+            for (uint32_t t = g > kV ? g - kV : 0; t < g; ++t)
+                (void)mbar_wait(v_full + 8 * (t % (2 * kV)), (t / (2 * kV)) & 1);
         }
     } else {
-        if constexpr (kSmall) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ---- softmax: thread = row = tensor-memory lane
         const int w = (warp - 4) >> 2;                       // half
         const int row = (warp & 3) * 32 + lane;
@@ -1432,7 +1472,7 @@ cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a
         !encode_4d(&map_v, c.dtype, c.value, {D, c.page_size, c.kv_heads, c.num_pages},
                    {c.token_stride, c.head_stride, c.page_stride}, box, 1))
         return cudaErrorInvalidValue;
-    kernel<<<p.G, L::kThreads, smem, stream>>>(map_q, map_k, map_v, p, status);
+    kernel<<<p.G, kThreads, smem, stream>>>(map_q, map_k, map_v, p, status);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.G < 2) return e;
     // The join may be set up before the attention has ended, and waits for it before it reads.

@@ -258,6 +258,18 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+// The same, called by a whole converged warp with equal operands; one lane issues.
+__device__ __forceinline__ void tma_load_4d_warp(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                                 int x, int y, int z, int w) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];\n\t}" ::"r"(dst),
+        "l"(map), "r"(bar), "r"(x), "r"(y), "r"(z), "r"(w)
+        : "memory");
+}
+
 // Shared-memory matrix descriptor of an operand whose rows run along K (K x 64 elements of MN
 // in 128-byte rows, 128-byte swizzle): 8-row groups are 1024 B apart (the stride byte offset),
 // and the next 64 elements of MN are `next_mn` bytes away (the leading byte offset).
