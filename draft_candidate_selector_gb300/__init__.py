@@ -352,31 +352,28 @@ def dflash_best_path(edges: torch.Tensor, cand_ids: torch.Tensor, path: torch.Te
 
 def _checked(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> int:
     """The address of a contiguous CUDA tensor of this type and shape."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_cuda and t.shape == shape
-            and t.is_contiguous()):
-        _need(t, name, dtype, shape)
+    try:
+        if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, dtype, shape)
     return t.data_ptr()
 
 
-class _On:
-    """The device of a call, current while it is made, and its stream."""
-
-    def __init__(self, dev: torch.device, stream):
-        index = dev.index if dev.index is not None else torch.cuda.current_device()
-        self._guard = None
-        if index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(index)
-        self.stream = (torch._C._cuda_getCurrentRawStream(index) if stream is None
-                       else stream.cuda_stream)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+def _launch(fn, dev: torch.device, stream, *args) -> None:
+    """fn(*args, stream) with dev current."""
+    index, current = dev.index, torch.cuda.current_device()
+    if index is None:
+        index = current
+    st = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == current:
+        status = fn(*args, st)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, st)
+    if status:
+        _native.check(status)
 
 
 def dflash_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor,
@@ -409,7 +406,7 @@ def dflash_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor,
     names = ("query_start", "kv_lens", "held_out", "positions", "pages_needed")
     if given == (None, None, None, None, None):
         room = torch.empty((3 * R + T + 2,), dtype=i32, device=dev)
-        out = room.split(sizes)
+        out = room.split_with_sizes(sizes)
         at = room.data_ptr()
         ptrs = (at, at + 4 * (R + 1), at + 4 * (2 * R + 1), at + 4 * (3 * R + 1),
                 at + 4 * (3 * R + 1 + T))
@@ -422,12 +419,8 @@ def dflash_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor,
         slots_at = slots.data_ptr()
     else:
         slots_at = _checked(slots, "slots", torch.int64, (T,))
-    with _On(dev, stream) as st:
-        status = lib.dflash_block_tables(ctx, new, held, free, R, n_free, page_size, max_pages, T,
-                                         table, ptrs[0], ptrs[1], ptrs[2], ptrs[3], slots_at,
-                                         ptrs[4], st)
-    if status:
-        _native.check(status)
+    _launch(lib.dflash_block_tables, dev, stream, ctx, new, held, free, R, n_free, page_size,
+            max_pages, T, table, ptrs[0], ptrs[1], ptrs[2], ptrs[3], slots_at, ptrs[4])
     return out[0], out[1], out[2], out[3], slots, out[4]
 
 
@@ -488,11 +481,8 @@ def dflash_store_kv(key: torch.Tensor, value: torch.Tensor, slots: torch.Tensor,
         raise ValueError(f"key and value must be [T, {cache.kv_heads}, {cache.head_dim}], got "
                          f"{tuple(key.shape)} and {tuple(value.shape)}")
     at = _checked(slots, "slots", torch.int64, (T,))
-    with _On(key.device, stream) as st:
-        status = lib.dflash_store_kv(key.data_ptr(), value.data_ptr(), code, at, T, ks[0], ks[1],
-                                     vs[0], vs[1], cache, st)
-    if status:
-        _native.check(status)
+    _launch(lib.dflash_store_kv, key.device, stream, key.data_ptr(), value.data_ptr(), code, at, T,
+            ks[0], ks[1], vs[0], vs[1], cache)
     return key_cache, value_cache
 
 
@@ -500,6 +490,21 @@ def dflash_paged_attention_workspace_bytes(R: int, T: int, q_heads: int, kv_head
                                            head_dim: int) -> int:
     return int(_native.load().dflash_paged_attention_workspace_bytes(R, T, q_heads, kv_heads,
                                                                      head_dim))
+
+
+_workspace_sizes: dict = {}
+
+
+def _attention_workspace(dev: torch.device, head_dim: int) -> int:
+    """The workspace bytes of any call with this head_dim on a device: they depend on nothing else."""
+    nbytes = _workspace_sizes.get((dev, head_dim), 0)
+    if nbytes == 0:
+        with torch.cuda.device(dev):
+            nbytes = dflash_paged_attention_workspace_bytes(1, 1, 1, 1, head_dim)
+        if nbytes == 0:
+            _native.check(_native.DFLASH_INVALID_ARGUMENT)
+        _workspace_sizes[(dev, head_dim)] = nbytes
+    return nbytes
 
 
 def dflash_paged_attention(query: torch.Tensor, key_cache: torch.Tensor,
@@ -543,15 +548,12 @@ def dflash_paged_attention(query: torch.Tensor, key_cache: torch.Tensor,
         lse_at = lse.data_ptr()
     else:
         lse_at = _checked(lse, "lse", torch.float32, (T, Hq))
-    with _On(dev, stream) as st:
-        ws = _workspace(lib.dflash_paged_attention_workspace_bytes(R, T, Hq, cache.kv_heads, D),
-                        dev, workspace)
-        status = lib.dflash_paged_attention(
-            query.data_ptr(), code, T, Hq, qs[0], qs[1], cache, table, R, max_pages, start, kv,
-            D ** -0.5 if scale is None else scale, window_left, window_right, softcap, out_at,
-            lse_at, ws.data_ptr(), ws.numel(), st)
-    if status:
-        _native.check(status)
+    if workspace is None:
+        workspace = torch.empty(_attention_workspace(dev, D), dtype=torch.uint8, device=dev)
+    _launch(lib.dflash_paged_attention, dev, stream, query.data_ptr(), code, T, Hq, qs[0], qs[1],
+            cache, table, R, max_pages, start, kv, D ** -0.5 if scale is None else scale,
+            window_left, window_right, softcap, out_at, lse_at, workspace.data_ptr(),
+            workspace.numel())
     return out, lse
 
 

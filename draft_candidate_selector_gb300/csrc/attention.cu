@@ -62,6 +62,13 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     w += align256((size_t)(dev.sm_count + 1) * sizeof(int4));
     p.part = reinterpret_cast<float*>(w);
     p.G = dev.sm_count;
+    // Nothing is cut, and no join is launched, where the table's width and the number of tokens alone
+    // say that plan_ranges will take whole items (about 2 us of a short call).
+    const long long steps = ((long long)a.max_pages * c.page_size + BN - 1) / BN;
+    const long long per_request = ((long long)a.T + 2 * p.tpt - 1) / (2 * p.tpt);
+    const long long items = (a.R + (long long)a.T / (2 * p.tpt)) * c.kv_heads;
+    p.join = p.G > 1 && ((a.T > p.tpt ? 2 : 1) * (1 + steps) > 1 + kWholeSteps ||
+                         per_request > kSerialItems || items > p.G);
     if (c.dtype == kE4m3) return launch_attention_e4m3(dev, a, p, status_word, stream);
     static constexpr Launch launch[8] = {
         launch_on_tensor_cores<64, false, false, false>,  launch_on_tensor_cores<64, false, true, false>,

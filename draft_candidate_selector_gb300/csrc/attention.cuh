@@ -68,6 +68,7 @@ struct AttentionProblem {
     int4* bound;                        // [G + 1]: request, key head, item, first step
     float* part;                        // [2 G][part_floats]
     int G;
+    bool join;                          // items may be cut
 };
 
 // The call with an e4m3 cache (attention_e4m3.cu).
@@ -147,13 +148,19 @@ __device__ __forceinline__ Request request_of(const Problem& p, int r) {
 
 // ---------------------------------------------------------------- plan
 
+// a / b for a >= 0, b > 0; a 64-bit division takes several times a 32-bit one.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 // The start of range b of G: x = b W / G falls on a request, a key head, an item and a step of
 // it; a start inside an item's last step moves to the next item. Called by a whole warp.
 __device__ __forceinline__ int4 range_start(const Problem& p, const long long* cost, bool flat,
                                             int b) {
     const int lane = threadIdx.x & 31;
     const long long W = cost[p.R];
-    const long long x = W / p.G * b + W % p.G * b / p.G;
+    const long long each = quotient(W, p.G);
+    const long long x = each * b + quotient((W - each * p.G) * b, p.G);
     int4 at = make_int4(p.R, 0, 0, 0);
     if (x >= W) return at;
     int lo = 0, hi = p.R;
@@ -164,8 +171,8 @@ __device__ __forceinline__ int4 range_start(const Problem& p, const long long* c
     }
     const Request q = request_of(p, lo);
     const int items = item_count(p, q.n);
-    const long long head = (cost[lo + 1] - cost[lo]) / p.kv_heads;
-    const int h = (int)((x - cost[lo]) / head);
+    const long long head = quotient(cost[lo + 1] - cost[lo], p.kv_heads);
+    const int h = (int)quotient(x - cost[lo], head);
     long long off = (x - cost[lo]) - (long long)h * head;
     if (flat) return make_int4(lo, h, (int)off, 0);
     for (int t0 = 0; t0 < items; t0 += 32) {
@@ -187,7 +194,7 @@ __device__ __forceinline__ int4 range_start(const Problem& p, const long long* c
         off -= __shfl_sync(kFull, upto, k) - ck;
         const int tk = t0 + k;
         const int w = step_cost(p, min(2 * p.tpt, q.n - tk * 2 * p.tpt));
-        const int step = max(0, (int)((off + w - 1) / w) - 1);
+        const int step = max(0, (w == 2 ? ((int)off + 1) >> 1 : (int)off) - 1);
         at = make_int4(lo, h, tk, step);
         if (step * w >= ck - w && step > 0) {                // past the last step: the next item
             at.w = 0;
@@ -213,12 +220,14 @@ __device__ __forceinline__ void plan_ranges(const Problem& p, long long* cost, i
     __shared__ long long warp_sum[kThreads / 32], warp_items[kThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     long long my_items = 0;
+    int first_items = 0;                 // of request tid
     bool big = false, is_long = false;
     for (int r = tid; r < p.R; r += kThreads) {
         const Request q = request_of(p, r);
         if (blockIdx.x == 0 && (q.bad || !q.rows_ok)) atomicOr(status, kStatusBadLength);
         const int items = item_count(p, q.n);
         my_items += items;
+        if (r == tid) first_items = items;
         long long c = -1;                                    // left to a warp
         if (items <= kSerialItems) {
             c = 0;
@@ -257,7 +266,10 @@ __device__ __forceinline__ void plan_ranges(const Problem& p, long long* cost, i
     const int r0 = min(tid * per, p.R), r1 = min(r0 + per, p.R);
     long long sum = 0;
     for (int r = r0; r < r1; ++r) {
-        if (flat) cost[r] = (long long)item_count(p, request_of(p, r).n) * p.kv_heads;
+        if (flat) {
+            const int items = per == 1 ? first_items : item_count(p, request_of(p, r).n);
+            cost[r] = (long long)items * p.kv_heads;
+        }
         sum += cost[r];
     }
     long long incl = sum;
@@ -550,26 +562,6 @@ __device__ __forceinline__ uint32_t below(int n) {
     return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 
-// tanh z of the cap, cap tanh(s / cap). With e = e^(2|z|): tanh |z| = 1 - 2 / (1 + e), off by a few
-// 2^-23 absolutely. For |z| <= kSmallTanh its Taylor series to z^11, whose next term is 0.0036 z^13,
-// under 2^-26 z; two values at a time, without the special-function unit.
-constexpr float kSmallTanh = 0.35f;
-
-__device__ __forceinline__ float tanh_of(float z) {
-    const float e = ex2(fabsf(z) * (2.f * kLog2e));
-    return copysignf(1.f - __fdividef(2.f, 1.f + e), z);
-}
-
-__device__ __forceinline__ uint64_t tanh_small_pair(uint64_t z) {
-    const uint64_t z2 = mul_pair(z, z);
-    const auto both = [](float x) { return pair_of(x, x); };
-    uint64_t t = fma_pair(z2, both(-1382.f / 155925.f), both(62.f / 2835.f));
-    t = fma_pair(t, z2, both(-17.f / 315.f));
-    t = fma_pair(t, z2, both(2.f / 15.f));
-    t = fma_pair(t, z2, both(-1.f / 3.f));
-    return fma_pair(mul_pair(t, z2), z, z);
-}
-
 // A 4 x 4 transpose of 16-byte pieces over groups of four lanes: before, lane l holds pieces 0..3
 // of its row; after, piece l % 4 of the group's rows 0..3.
 __device__ __forceinline__ void turn_pieces(uint32_t (&piece)[4][4], int lane) {
@@ -588,29 +580,6 @@ __device__ __forceinline__ void turn_pieces(uint32_t (&piece)[4][4], int lane) {
                 else piece[i | step][x] = take;
             }
         }
-    }
-}
-
-// v = cap tanh(v in) of 32 scores, the cap in log2 units.
-__device__ __forceinline__ void cap_scores(uint32_t (&v)[32], float in, float cap) {
-    float most = 0.f;
-#pragma unroll
-    for (int i = 0; i < 32; i += 2)
-        most = fmaxf(fmaxf(most, fabsf(__uint_as_float(v[i]))), fabsf(__uint_as_float(v[i + 1])));
-    if (__all_sync(kFull, most * in <= kSmallTanh)) {
-        const uint64_t in2 = pair_of(in, in), cap2 = pair_of(cap, cap);
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            const uint64_t z =
-                mul_pair(pair_of(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), in2);
-            const float2 y = halves_of(mul_pair(tanh_small_pair(z), cap2));
-            v[i] = __float_as_uint(y.x);
-            v[i + 1] = __float_as_uint(y.y);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            v[i] = __float_as_uint(cap * tanh_of(__uint_as_float(v[i]) * in));
     }
 }
 
@@ -1066,7 +1035,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             from -= first;
             to -= first;
             float unit = kCap ? 1.f : p.scale * kLog2e;      // S to log2 of a weight
-            float cap_in = kCap ? p.scale / p.softcap : 0.f;
+            float cap_in = kCap ? 2.f * kLog2e * p.scale / p.softcap : 0.f;
             if constexpr (kScaleQ) {
                 // Half w scales the row tile it will read the scores of; one row tile is half 0's,
                 // which leaves the factors for half 1.
@@ -1101,25 +1070,37 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     continue;
                 }
                 tc_fence_after();
-                // Tiles that need more than the common steps (a cap, rows that do not see all of the
-                // tile) get it first, in tensor memory, a quarter of 32 keys at a time.
                 uint32_t va[32], vb[32];
                 const bool masked = j < from || j >= to;
                 if (kCap || masked) {
+                    // Caps and masks first, in tensor memory, in quarters of 32 keys: the steps that
+                    // every tile takes stay short.
                     const int k0 = (first + j) * BN;
-#pragma unroll 1
-                    for (int c0 = 0; c0 < BN; c0 += 32) {
-                        tmem_ld_issue_x32(ts + c0, va);
-                        tmem_ld_wait_x32(va);
-                        if constexpr (kCap) cap_scores(va, cap_in, cap);
+                    auto prepare = [&](uint32_t (&v)[32], int c0) {
+                        if constexpr (kCap) {
+                            // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), in log2 units
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[i] = __float_as_uint(fmaf(
+                                    rcp(1.f + ex2(__uint_as_float(v[i]) * cap_in)), -2.f * cap, cap));
+                        }
                         if (masked) {
                             const uint32_t seen =
                                 below(row_hi - k0 - c0) & ~below(row_lo - k0 - c0);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (!(seen & (1u << i))) va[i] = 0xFF800000u;
+                                if (!(seen & (1u << i))) v[i] = 0xFF800000u;
                         }
-                        tmem_st_x32(ts + c0, va);
+                        tmem_st_x32(ts + c0, v);
+                    };
+#pragma unroll 1
+                    for (int c0 = 0; c0 < BN; c0 += 64) {
+                        tmem_ld_issue_x32(ts + c0, va);
+                        tmem_ld_issue_x32(ts + c0 + 32, vb);
+                        tmem_ld_wait_x32(va);
+                        tmem_ld_wait_x32(vb);
+                        prepare(va, c0);
+                        prepare(vb, c0 + 32);
                     }
                     tmem_st_wait();
                 }
@@ -1474,7 +1455,7 @@ cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a
         return cudaErrorInvalidValue;
     kernel<<<p.G, kThreads, smem, stream>>>(map_q, map_k, map_v, p, status);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.G < 2) return e;
+    if (e != cudaSuccess || !p.join) return e;
     // The join may be set up before the attention has ended, and waits for it before it reads.
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];

@@ -13,6 +13,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <cmath>
 #include <mutex>
 
 namespace dflash {
@@ -181,8 +182,9 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(BlockTableA
 
 // ---------------------------------------------------------------- store
 //
-// One thread moves 8 elements of a key or value row: 16 bytes in, 16 or 8 out. The rows are
-// streamed once; nothing is reused. Bound by HBM.
+// A thread moves 8 elements of a key or value row at a time: 16 bytes in, 16 or 8 out. The threads of
+// a block lie along a token's vectors and over tokens, so that a thread keeps its head and vector
+// and finds a token's place in the cache once for several. The rows are streamed once; bound by HBM.
 
 template <typename T>
 __device__ __forceinline__ float to_float(T x);
@@ -195,22 +197,20 @@ __device__ __forceinline__ float to_float<__half>(__half x) {
     return __half2float(x);
 }
 
-// x / scale in e4m3: an IEEE division, then one rounding to the nearest, clamped to 448.
-template <typename T>
+// x / scale in e4m3: an IEEE division, then one rounding to the nearest, clamped to 448. Where scale
+// is a power of two (and its inverse one too) the product with the inverse is the same value.
+template <typename T, bool kDivide>
 __device__ __forceinline__ uint2 to_e4m3(const uint4& v, float scale) {
     const T* x = reinterpret_cast<const T*>(&v);
-    uint32_t o[2];
+    uint32_t o[4];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        uint32_t lo = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(to_float(x[4 * w]), scale),
-                        __fdiv_rn(to_float(x[4 * w + 1]), scale)), __NV_SATFINITE, __NV_E4M3);
-        uint32_t hi = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(to_float(x[4 * w + 2]), scale),
-                        __fdiv_rn(to_float(x[4 * w + 3]), scale)), __NV_SATFINITE, __NV_E4M3);
-        o[w] = lo | (hi << 16);
+    for (int w = 0; w < 4; ++w) {
+        float2 f = make_float2(to_float(x[2 * w]), to_float(x[2 * w + 1]));
+        f.x = kDivide ? __fdiv_rn(f.x, scale) : f.x * scale;
+        f.y = kDivide ? __fdiv_rn(f.y, scale) : f.y * scale;
+        o[w] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
     }
-    return make_uint2(o[0], o[1]);
+    return make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
 }
 
 struct StoreArgs {
@@ -218,43 +218,73 @@ struct StoreArgs {
     long long kt, kh, vt, vh;      // strides in elements
     const int64_t* slots;
     int T, vecs;                   // 8-element vectors per head row
+    int across;                    // threads along a token's vectors; a divisor of the block
+    int page_shift;                // -1: page_size is no power of two
+    float k_mul, v_mul;            // scales, or their inverses
     KvCache cache;
 };
 
 constexpr int kStoreThreads = 256;
+constexpr int kStoreTokens = 4;    // tokens a thread has in flight
 
-template <typename T, bool kSmall>
+template <typename T, bool kSmall, bool kDivide>
 __global__ void __launch_bounds__(kStoreThreads) store_kv_kernel(StoreArgs a, uint32_t* status) {
     const int row = a.cache.kv_heads * a.vecs;               // vectors of one token's keys
-    const long long n = 2LL * a.T * row;
+    const int down = kStoreThreads / a.across;               // tokens of a block at a time
+    const int x0 = threadIdx.x % a.across, y = threadIdx.x / a.across;
     const long long slots_in_pool = (long long)a.cache.num_pages * a.cache.page_size;
-    for (long long i = (long long)blockIdx.x * kStoreThreads + threadIdx.x; i < n;
-         i += (long long)gridDim.x * kStoreThreads) {
-        const int token = (int)(i / (2 * row));
-        int at = (int)(i - (long long)token * 2 * row);
-        const bool is_value = at >= row;
-        at -= is_value ? row : 0;
-        const int head = at / a.vecs, vec = at - head * a.vecs;
-        const long long slot = a.slots[token];
-        if (slot < 0) continue;
+    const long long first = (long long)blockIdx.x * down * kStoreTokens + y;
+    long long to[kStoreTokens];                              // the token's row in the cache, or -1
+#pragma unroll
+    for (int i = 0; i < kStoreTokens; ++i) {
+        const long long t = first + (long long)i * down;
+        const long long slot = t < a.T ? a.slots[t] : -1;
+        to[i] = -1;
         if (slot >= slots_in_pool) {
-            atomicOr(status, kStatusBadId);
-            continue;
+            if (x0 == 0) atomicOr(status, kStatusBadId);
+        } else if (slot >= 0) {
+            const long long page = a.page_shift >= 0 ? slot >> a.page_shift : slot / a.cache.page_size;
+            to[i] = page * a.cache.page_stride +
+                    (slot - page * a.cache.page_size) * a.cache.token_stride;
         }
-        const uint16_t* src = is_value ? a.value + token * a.vt + head * a.vh
-                                       : a.key + token * a.kt + head * a.kh;
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(src + vec * 8));
-        const long long page = slot / a.cache.page_size;
-        const long long to = page * a.cache.page_stride +
-                             (slot - page * a.cache.page_size) * a.cache.token_stride +
-                             head * a.cache.head_stride + vec * 8;
-        void* base = is_value ? a.cache.value : a.cache.key;
-        if constexpr (kSmall)
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + to) =
-                to_e4m3<T>(v, is_value ? a.cache.v_scale : a.cache.k_scale);
-        else
-            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + to) = v;
     }
+    for (int x = x0; x < 2 * row; x += a.across) {
+        const bool is_value = x >= row;
+        const int at = is_value ? x - row : x;
+        const int head = at / a.vecs, vec = at - head * a.vecs;
+        const uint16_t* src = is_value ? a.value + head * a.vh : a.key + head * a.kh;
+        const long long step = is_value ? a.vt : a.kt;
+        const long long in_row = head * a.cache.head_stride + vec * 8;
+        void* base = is_value ? a.cache.value : a.cache.key;
+        uint4 v[kStoreTokens];
+#pragma unroll
+        for (int i = 0; i < kStoreTokens; ++i)
+            if (to[i] >= 0)
+                v[i] = __ldcs(reinterpret_cast<const uint4*>(
+                    src + (first + (long long)i * down) * step + vec * 8));
+#pragma unroll
+        for (int i = 0; i < kStoreTokens; ++i) {
+            if (to[i] < 0) continue;
+            if constexpr (kSmall)
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + to[i] + in_row) =
+                    to_e4m3<T, kDivide>(v[i], is_value ? a.v_mul : a.k_mul);
+            else
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + to[i] + in_row) = v[i];
+        }
+    }
+}
+
+// Whether x is a power of two with one as its inverse.
+bool exact_inverse(float x) {
+    int e;
+    return frexpf(x, &e) == 0.5f && e > -120 && e < 120;
+}
+
+template <typename T>
+void store_small(const StoreArgs& a, bool divide, unsigned blocks, uint32_t* status,
+                 cudaStream_t stream) {
+    if (divide) store_kv_kernel<T, true, true><<<blocks, kStoreThreads, 0, stream>>>(a, status);
+    else store_kv_kernel<T, true, false><<<blocks, kStoreThreads, 0, stream>>>(a, status);
 }
 
 }  // namespace
@@ -284,18 +314,23 @@ cudaError_t launch_store_kv(const DeviceInfo& dev, const void* key, const void* 
                             long long key_head_stride, long long value_token_stride,
                             long long value_head_stride, const KvCache& cache,
                             uint32_t* status_word, cudaStream_t stream) {
+    const bool divide = !exact_inverse(cache.k_scale) || !exact_inverse(cache.v_scale);
     StoreArgs a{static_cast<const uint16_t*>(key), static_cast<const uint16_t*>(value),
                 key_token_stride, key_head_stride, value_token_stride, value_head_stride,
-                slots, T, cache.head_dim / 8, cache};
-    const long long n = 2LL * T * cache.kv_heads * a.vecs;
-    const int blocks = (int)std::min<long long>((n + kStoreThreads - 1) / kStoreThreads,
-                                                16LL * dev.sm_count);
+                slots, T, cache.head_dim / 8, 1, -1,
+                divide ? cache.k_scale : 1.f / cache.k_scale,
+                divide ? cache.v_scale : 1.f / cache.v_scale, cache};
+    while (a.across < kStoreThreads && a.across < 2 * cache.kv_heads * a.vecs) a.across *= 2;
+    if ((cache.page_size & (cache.page_size - 1)) == 0)
+        for (a.page_shift = 0; (1 << a.page_shift) < cache.page_size;) ++a.page_shift;
+    const long long per_block = (long long)(kStoreThreads / a.across) * kStoreTokens;
+    const unsigned blocks = (unsigned)((T + per_block - 1) / per_block);
     if (cache.dtype != kE4m3)
-        store_kv_kernel<__nv_bfloat16, false><<<blocks, kStoreThreads, 0, stream>>>(a, status_word);
+        store_kv_kernel<__nv_bfloat16, false, false><<<blocks, kStoreThreads, 0, stream>>>(a, status_word);
     else if (dtype == kBf16)
-        store_kv_kernel<__nv_bfloat16, true><<<blocks, kStoreThreads, 0, stream>>>(a, status_word);
+        store_small<__nv_bfloat16>(a, divide, blocks, status_word, stream);
     else
-        store_kv_kernel<__half, true><<<blocks, kStoreThreads, 0, stream>>>(a, status_word);
+        store_small<__half>(a, divide, blocks, status_word, stream);
     return cudaGetLastError();
 }
 

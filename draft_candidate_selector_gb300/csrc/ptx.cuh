@@ -410,6 +410,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// 1 / x to the hardware's approximation (1 ulp); 1 / inf = 0.
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Two fp32 values in one register pair: one instruction for both.
 __device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
     uint64_t r;
@@ -424,11 +431,6 @@ __device__ __forceinline__ float2 halves_of(uint64_t v) {
 __device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t r;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
 __device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
