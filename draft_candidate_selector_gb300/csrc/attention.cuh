@@ -13,6 +13,12 @@
 // tiles of 128 tokens, or, where a request has no more than tpt tokens left, one row tile whose
 // even and odd key tiles go to the two halves of the CTA.
 //
+// Few rows. A row tile of at most 32 rows (single tokens, small blocks) would keep one softmax warp
+// of each half busy and the others idle. Its queries go into all four quarters of the tile's lanes
+// instead: S then has four copies, and each warp takes 32 of the 128 keys of every row. The warps
+// agree on a row's maximum through shared memory, and P meets there too: it is the A operand from
+// shared memory in place of tensor memory.
+//
 // One CTA per SM, 16 warps (13-15 work for 8-bit caches only):
 //   * warps 0 and 12: TMA producers, of keys (and queries) and of values. Each lane looks up one page
 //     of a tile; the pages' boxes (a page's rows x 64 values, 128-byte swizzle) are issued one after
@@ -86,6 +92,7 @@ constexpr int BN = 128;                 // keys of a key tile
 constexpr int kThreads = 512;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinSlices = 8;          // CTAs that share one cut item's join
+constexpr int kFew = 32;                // rows of a tile that is copied to all quarters
 constexpr int kItems = 4;               // slots of the item ring
 constexpr int kSerialItems = 8;         // items of a request that one thread adds up
 constexpr int kWholeSteps = 8;          // key tiles up to which an item is not worth cutting
@@ -313,6 +320,7 @@ struct __align__(16) Item {
     int v_odd;           // a value that is not finite was cleared
     int bad_page;        // a page id outside the pool was met
     __device__ __forceinline__ bool pair(const Problem& p) const { return ntok > p.tpt; }
+    __device__ __forceinline__ bool few(const Problem& p) const { return ntok * p.g <= kFew; }
     __device__ __forceinline__ bool whole() const { return lo == 0 && hi == steps; }
 };
 
@@ -344,18 +352,23 @@ struct Layout {
     static constexpr uint32_t kRaw = BN * D;                     // a tile in 8 bits
     static constexpr int kRawStages = kSmall ? (D == 128 ? 2 : 8) : 0;
     static constexpr int kK = kSmall ? (D == 128 ? 2 : 3) : (D == 128 ? 2 : 5);   // key stages
-    static constexpr int kV = kSmall ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 6);   // value stages
+    static constexpr int kV = kSmall ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 5);   // value stages
     static constexpr uint32_t q = 0;                             // two row tiles
-    static constexpr uint32_t keys = 2 * kTile;
+    // P of few rows, in the place of the second row tile: 16 KB for each half, 4 KB for 64 keys
+    // and a row's maxima and sums behind them.
+    static constexpr uint32_t p = kTile;
+    static constexpr uint32_t pHalf = 16384, pKeys = kFew * 128, pShare = 2 * pKeys;
+    static constexpr uint32_t keys = p + (kTile > 2 * pHalf ? kTile : 2 * pHalf);
     static constexpr uint32_t values = keys + kK * kTile;
     static constexpr uint32_t raw = values + kV * kTile;
     static constexpr uint32_t bars = raw + kRawStages * kRaw;
-    static constexpr int kBars = 3 * kK + 4 * kV + 2 * kRawStages + 16 + 2 * kItems;
+    static constexpr int kBars = 3 * kK + 4 * kV + 2 * kRawStages + 20 + 2 * kItems;
     static constexpr uint32_t ml = (bars + kBars * 8 + 15) / 16 * 16;   // [128] float2
     static constexpr uint32_t items = ml + BM * 8;               // [kItems] Item
     static constexpr uint32_t slot = items + kItems * 64;        // tensor memory's base
     static constexpr uint32_t issued = slot + 4;                 // value tiles issued
     static constexpr uint32_t total = slot + 16;
+    static_assert(total + 1024 + 288 <= 232448, "a block's shared memory, with its alignment and the plan's own");
 };
 
 __device__ __forceinline__ uint32_t pack16(bool half_type, float lo, float hi) {
@@ -562,6 +575,21 @@ __device__ __forceinline__ uint32_t below(int n) {
     return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 
+// cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), in log2 units; in = 2 log2(e) scale / cap.
+__device__ __forceinline__ uint32_t capped(uint32_t s, float in, float cap) {
+    return __float_as_uint(fmaf(rcp(1.f + ex2(__uint_as_float(s) * in)), -2.f * cap, cap));
+}
+
+// 16 columns of this thread's lane times `by`.
+__device__ __forceinline__ void scale_columns(uint32_t taddr, float by) {
+    uint32_t o[16];
+    tmem_ld_issue_x16(taddr, o);
+    tmem_ld_wait_x16(o);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * by);
+    tmem_st_x16(taddr, o);
+}
+
 // A 4 x 4 transpose of 16-byte pieces over groups of four lanes: before, lane l holds pieces 0..3
 // of its row; after, piece l % 4 of the group's rows 0..3.
 __device__ __forceinline__ void turn_pieces(uint32_t (&piece)[4][4], int lane) {
@@ -585,8 +613,8 @@ __device__ __forceinline__ void turn_pieces(uint32_t (&piece)[4][4], int lane) {
 
 template <int D, bool kHalf, bool kCap, bool kSmall>
 __global__ void __launch_bounds__(kThreads, 1)
-attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
-                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Problem p,
+attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_few,
+                 const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Problem p,
                  uint32_t* status) {
     using L = Layout<D, kSmall>;
     constexpr bool kMmaHalf = kHalf || kSmall;               // the tensor cores' operands are fp16
@@ -612,7 +640,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     const uint32_t o_done = q_full + 64;
     const uint32_t ml_there = q_full + 80, ml_back = q_full + 88, halves_done = q_full + 96;
     const uint32_t drained = q_full + 104, q_ready = q_full + 120;   // drained: [2]
-    const uint32_t item_full = q_full + 128, item_empty = item_full + 8 * kItems;
+    const uint32_t p_free = q_full + 128, share = q_full + 144;          // [2] by turns, [2] by half
+    const uint32_t item_full = q_full + 160, item_empty = item_full + 8 * kItems;
     const uint32_t raw_full = item_empty + 8 * kItems, raw_empty = raw_full + 8 * L::kRawStages;
     float2* ml = reinterpret_cast<float2*>(smem + L::ml);
     Item* items = reinterpret_cast<Item*>(smem + L::items);
@@ -643,6 +672,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(drained, 1);
         mbar_init(drained + 8, 1);
         mbar_init(q_ready, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(p_free + 8 * i, 2);
+            mbar_init(share + 8 * i, 4);
+        }
         for (int s = 0; s < L::kRawStages; ++s) {
             mbar_init(raw_full + 8 * s, 1);
             mbar_init(raw_empty + 8 * s, 4);
@@ -733,6 +766,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (warp == 0) {
             // ---- TMA producer of queries and keys; of an 8-bit cache's raw tiles, keys and values
             uint32_t g = 0, nq = 0;      // tiles issued, items with steps
+            bool few_before = false;     // P of few rows may still be in use
             auto free_stage = [&](uint32_t empty, uint32_t n) {
                 if (g >= n) wait(empty + 8 * (g % n), (g / n - 1) & 1);
                 return ok = __all_sync(kFull, tries != 0);
@@ -743,13 +777,24 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     if (nq > 0) wait(q_empty, (nq - 1) & 1);
                     if (!(ok = __all_sync(kFull, tries != 0))) break;
                     ++nq;
+                    const bool few = c->few(p), pair = c->pair(p);
+                    if (pair && few_before) {
+                        // The second row tile lies where P of the few rows before it has been.
+                        wait(p_free + 8 * ((nq - 2) & 1), ((nq - 2) >> 1) & 1);
+                        if (!(ok = __all_sync(kFull, tries != 0))) break;
+                        few_before = false;
+                    }
+                    few_before |= few;
                     if (lane == 0) {
-                        const int tiles = c->pair(p) ? 2 : 1;
-                        mbar_expect_tx(q_full, (uint32_t)(tiles * p.g * p.tpt) * D * 2);
+                        const int tiles = few ? 4 : (pair ? 2 : 1);
+                        const uint32_t apart = few ? kFew * 128 : L::kTile;
+                        mbar_expect_tx(q_full,
+                                       (uint32_t)(tiles * p.g * (few ? kFew / p.g : p.tpt)) * D * 2);
                         for (int s = 0; s < tiles; ++s)
                             for (int i = 0; i < D / 64; ++i)
-                                tma_load_4d(base + L::q + s * L::kTile + i * L::kChunk, &map_q,
-                                            q_full, i * 64, 0, h, c->t0 + c->tok0 + s * p.tpt);
+                                tma_load_4d(base + L::q + s * apart + i * L::kChunk,
+                                            few ? &map_few : &map_q, q_full, i * 64, 0, h,
+                                            c->t0 + c->tok0 + (pair ? s * p.tpt : 0));
                     }
                     __syncwarp();
                     if constexpr (kSmall) {
@@ -799,14 +844,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const uint32_t ubase = __shfl_sync(kFull, base, 0), utmem = __shfl_sync(kFull, tmem, 0);
             const uint64_t dq = sw128_desc(ubase + L::q), dk = sw128_desc(ubase + L::keys);
             const uint64_t dv = sw128_mn_desc(ubase + L::values, L::kChunk);
+            const uint64_t dp = sw128_desc(ubase + L::p + w * L::pHalf);
             const uint32_t acc = utmem + 256 + w * 128, st = utmem + w * BN, pt = st + 64;
             uint32_t g = 0, nq = 0;      // steps of earlier items; items with steps
-            uint32_t np = 0;             // P tiles waited for
+            uint32_t np = 0, nl = 0;     // P tiles waited for, their lower halves
             uint32_t fixed = 0;          // phase bit of each stage's v_fix
             while (const Item* c = get_item()) {
                 const int steps = __shfl_sync(kFull, c->hi - c->lo, 0);
                 if (steps > 0) {
                     const bool pair = __shfl_sync(kFull, c->pair(p) ? 1 : 0, 0) != 0;
+                    const bool few = __shfl_sync(kFull, c->few(p) ? 1 : 0, 0) != 0;
                     // Steps whose values need no look.
                     const int from = __shfl_sync(kFull, c->from - c->begin - c->lo, 0);
                     const int to = __shfl_sync(kFull, c->to - c->begin - c->lo, 0);
@@ -855,23 +902,34 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             if (look) wait(v_fix + 8 * s, (fixed >> s) & 1);
                             wait(p_up + 8 * w, np & 1);
                             tc_fence_after();
+                            if (few) {
 #pragma unroll
-                            for (int x = 4; x < 8; ++x)
-                                umma_f16_tmem_a_warp(acc, pt + x * 8, b + x * (2048 >> 4), idesc_o,
-                                                     x > 4 ? 1u : more);
+                                for (int x = 0; x < 8; ++x)
+                                    umma_f16_warp(acc, dp + (((x / 4) * L::pKeys + (x % 4) * 32) >> 4),
+                                                  b + x * (2048 >> 4), idesc_o, x > 0 ? 1u : more);
+                            } else {
+#pragma unroll
+                                for (int x = 4; x < 8; ++x)
+                                    umma_f16_tmem_a_warp(acc, pt + x * 8, b + x * (2048 >> 4), idesc_o,
+                                                         x > 4 ? 1u : more);
+                            }
                             if (next < steps) k_landed(next);
-                            wait(p_low + 8 * w, np & 1);
-                            ++np;
-                            tc_fence_after();
+                            if (!few) {
+                                wait(p_low + 8 * w, nl++ & 1);
+                                tc_fence_after();
 #pragma unroll
-                            for (int x = 0; x < 4; ++x)
-                                umma_f16_tmem_a_warp(acc, pt + x * 8, b + x * (2048 >> 4), idesc_o, 1u);
+                                for (int x = 0; x < 4; ++x)
+                                    umma_f16_tmem_a_warp(acc, pt + x * 8, b + x * (2048 >> 4), idesc_o,
+                                                         1u);
+                            }
+                            ++np;
                             umma_commit_warp(o_done + 8 * w);
                             release(v_empty + 8 * s);
                             if (next < steps) scores(next);
                         }
                         if (look) fixed ^= 1u << s;
                     }
+                    umma_commit_warp(p_free + 8 * ((nq - 1) & 1));
                     g += steps;
                 }
                 done_with();
@@ -1016,19 +1074,22 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ts = lane_base + w * BN;
         const uint32_t to_ = lane_base + 256 + w * 128;
-        const int row_token = row / p.g;
+        const int quarter = warp & 3;
         const float cap = p.softcap * kLog2e;
-        uint32_t ns = 0, nb = 0, nq = 0;   // S tiles of this half; items of one row tile, with steps
+        // S tiles of this half; items of one row tile, with steps; times that few rows were shared
+        uint32_t ns = 0, nb = 0, nq = 0, nshare = 0;
         while (const Item* c = get_item()) {
             const int steps = c->hi - c->lo;
             const bool pair = c->pair(p);
             const int sub0 = c->tok0 + (pair ? w : 0) * p.tpt;   // the row tile's first token
             const int nsub = min(p.tpt, c->n - sub0);            // and its tokens
-            const bool live = row_token < nsub;
+            const bool few = c->few(p);
+            const int row_token = (few ? lane : row) / p.g;
+            bool live = row_token < nsub;
             const int pos = c->L - c->n + sub0 + row_token;
             const int row_lo = first_key(p, pos);
             const int row_hi = live ? keys_end(p, c->L, pos) : 0;
-            const bool warp_live = __any_sync(kFull, live);
+            bool warp_live = __any_sync(kFull, live);
             const int first = c->begin + c->lo;
             int from, to;
             clear_tiles(p, c->n, c->L, sub0, nsub, from, to);
@@ -1064,6 +1125,81 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 }
                 ++ns;
                 any = true;
+                if (few) {
+                    // This warp's 32 keys of all rows, which lie in every quarter's lanes.
+                    uint32_t v[32];
+                    const uint32_t shared = base + L::p + w * L::pHalf;
+                    tc_fence_after();
+                    tmem_ld_issue_x32(ts + 32 * quarter, v);
+                    tmem_ld_wait_x32(v);
+                    if constexpr (kCap) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = capped(v[i], cap_in, cap);
+                    }
+                    if (j < from || j >= to) {
+                        const int k0 = (first + j) * BN + 32 * quarter;
+                        const uint32_t seen = below(row_hi - k0) & ~below(row_lo - k0);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!(seen & (1u << i))) v[i] = 0xFF800000u;
+                    }
+                    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4)
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            top[x] = fmaxf(fmaxf(top[x], __uint_as_float(v[i + 2 * x])),
+                                           __uint_as_float(v[i + 2 * x + 1]));
+                    // The tile's maximum of the row, from all four warps.
+                    float* maxima = reinterpret_cast<float*>(smem + L::p + w * L::pHalf + L::pShare);
+                    maxima[quarter * kFew + lane] = fmaxf(top[0], top[1]);
+                    mbar_arrive_warp(share + 8 * w);
+                    wait(share + 8 * w, nshare++ & 1);
+                    const float most = fmaxf(fmaxf(maxima[lane], maxima[kFew + lane]),
+                                             fmaxf(maxima[2 * kFew + lane], maxima[3 * kFew + lane])) *
+                                       unit;
+                    const bool grown = most > m + kGrowth;
+                    const float keep = grown && m > -INFINITY ? ex2(m - most) : 1.f;
+                    if (grown) m = most;
+                    if (__any_sync(kFull, keep != 1.f)) {
+                        l *= keep;
+                        // The scores are here, so the MMAs before them are over; O lies in the first
+                        // quarter's lanes.
+                        if (quarter == 0) {
+#pragma unroll 1
+                            for (int d = 0; d < D; d += 16) scale_columns(to_ + d, keep);
+                        }
+                    }
+                    const float off = m == -INFINITY ? 0.f : m;
+                    const uint64_t unit2 = pair_of(unit, unit), off2 = pair_of(-off, -off);
+                    uint64_t add[2] = {0, 0};
+                    const uint32_t to_p = shared + (quarter >> 1) * L::pKeys + lane * 128;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t pk[4];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int at = 8 * i + 2 * x;
+                            const float2 y = halves_of(
+                                fma_pair(pair_of(__uint_as_float(v[at]), __uint_as_float(v[at + 1])),
+                                         unit2, off2));
+                            const float lo = ex2(y.x), hi = ex2(y.y);
+                            add[x & 1] = add_pair(add[x & 1], pair_of(lo, hi));
+                            pk[x] = pack16(kMmaHalf, lo, hi);
+                        }
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         to_p + ((((quarter & 1) * 4 + i) ^ (lane & 7)) * 16)),
+                                     "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3])
+                                     : "memory");
+                    }
+                    const float2 sums = halves_of(add_pair(add[0], add[1]));
+                    l += sums.x + sums.y;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive_warp(p_up + 8 * w);
+                    continue;
+                }
                 if (!warp_live) {
                     mbar_arrive_warp(p_up + 8 * w);
                     mbar_arrive_warp(p_low + 8 * w);
@@ -1078,11 +1214,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     const int k0 = (first + j) * BN;
                     auto prepare = [&](uint32_t (&v)[32], int c0) {
                         if constexpr (kCap) {
-                            // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), in log2 units
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                v[i] = __float_as_uint(fmaf(
-                                    rcp(1.f + ex2(__uint_as_float(v[i]) * cap_in)), -2.f * cap, cap));
+                            for (int i = 0; i < 32; ++i) v[i] = capped(v[i], cap_in, cap);
                         }
                         if (masked) {
                             const uint32_t seen =
@@ -1138,15 +1271,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     tc_fence_after();
                     l *= keep;
 #pragma unroll 1
-                    for (int d = 0; d < D; d += 16) {
-                        uint32_t o[16];
-                        tmem_ld_issue_x16(to_ + d, o);
-                        tmem_ld_wait_x16(o);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            o[i] = __float_as_uint(__uint_as_float(o[i]) * keep);
-                        tmem_st_x16(to_ + d, o);
-                    }
+                    for (int d = 0; d < D; d += 16) scale_columns(to_ + d, keep);
                 }
                 const float off = m == -INFINITY ? 0.f : m;
                 const uint64_t unit2 = pair_of(unit, unit), off2 = pair_of(-off, -off);
@@ -1184,6 +1309,18 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             }
             // Epilogue, once this half's last tile is in O.
             if (any) wait(o_done + 8 * w, (ns - 1) & 1);
+            if (few) {
+                // The four warps' sums; O and the rest of the item are the first one's.
+                if (any) {
+                    float* sums = reinterpret_cast<float*>(smem + L::p + w * L::pHalf + L::pShare);
+                    sums[quarter * kFew + lane] = l;
+                    mbar_arrive_warp(share + 8 * w);
+                    wait(share + 8 * w, nshare++ & 1);
+                    l = (sums[lane] + sums[kFew + lane]) + (sums[2 * kFew + lane] + sums[3 * kFew + lane]);
+                }
+                live &= quarter == 0;
+                warp_live &= quarter == 0;
+            }
             const bool whole = c->whole();
             const bool nan = c->bad || c->bad_page;
             auto finish = [&]() {                            // the factor that ends the quotient
@@ -1235,7 +1372,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     p.part + (size_t)(2 * blockIdx.x + (c->lo > 0 ? 0 : 1)) * part_floats(D) +
                     (size_t)(pair ? w : 0) * BM * (D + 2));
                 const long long out_row = ((long long)c->t0 + sub0 + row_token) * p.q_heads +
-                                          c->h * p.g + (row - row_token * p.g);
+                                          c->h * p.g + ((few ? lane : row) - row_token * p.g);
                 uint16_t* out = static_cast<uint16_t*>(p.out) + out_row * D;
                 // The rows whose output this lane stores: 16-byte pieces pass through groups of four
                 // lanes, so that a store covers 8 rows x 64 bytes and not 32 rows x 16.
@@ -1444,16 +1581,19 @@ cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a
     });
     if (attr_err[dev.device] != cudaSuccess) return attr_err[dev.device];
     const KvCache& c = a.cache;
-    CUtensorMap map_q, map_k, map_v;
+    CUtensorMap map_q, map_few, map_k, map_v;
+    const int few = std::max(1, kFew / p.g);
     const int box = std::min(c.page_size, BN);
     if (!encode_4d(&map_q, a.dtype, a.query, {D, p.g, c.kv_heads, a.T},
                    {a.q_head_stride, p.g * a.q_head_stride, a.q_token_stride}, p.g, p.tpt) ||
+        !encode_4d(&map_few, a.dtype, a.query, {D, p.g, c.kv_heads, a.T},
+                   {a.q_head_stride, p.g * a.q_head_stride, a.q_token_stride}, p.g, few) ||
         !encode_4d(&map_k, c.dtype, c.key, {D, c.page_size, c.kv_heads, c.num_pages},
                    {c.token_stride, c.head_stride, c.page_stride}, box, 1) ||
         !encode_4d(&map_v, c.dtype, c.value, {D, c.page_size, c.kv_heads, c.num_pages},
                    {c.token_stride, c.head_stride, c.page_stride}, box, 1))
         return cudaErrorInvalidValue;
-    kernel<<<p.G, kThreads, smem, stream>>>(map_q, map_k, map_v, p, status);
+    kernel<<<p.G, kThreads, smem, stream>>>(map_q, map_few, map_k, map_v, p, status);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.join) return e;
     // The join may be set up before the attention has ended, and waits for it before it reads.

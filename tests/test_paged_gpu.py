@@ -263,6 +263,22 @@ def test_attention_long_contexts(dev, dtype, cache, D):
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_mixed_batch(dev, dtype, cache, D):
+    """Single tokens, blocks and prompt chunks in one batch of many requests, in every order, so that
+    one SM takes items of all kinds one after another."""
+    rng = np.random.default_rng(15)
+    new = rng.choice([1, 1, 2, 8, 16, 40, 130, 300], 160)
+    ctx = rng.integers(0, 600, 160)
+    b = paged.Batch(ctx, new, 4, 1, D, 16, dtype, cache, seed=15)
+    want = check(b)
+    for _ in range(10):
+        for g, w in zip(ds.dflash_paged_attention(*b.args(), **b.scales()), want):
+            assert torch.equal(g, w)
+    check(b, left=150, right=4, softcap=15.0)
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
 def test_attention_many_steps(dev, dtype, cache):
     """Single tokens over contexts long enough that each part of a split has many key tiles, from
     pages all over a large pool: right, and the same bits every time."""
