@@ -21,7 +21,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(OUT_DIR, "libdflash_gb300.so")
 SOURCES = ["api.cu", "topk.cu", "projection.cu", "edges.cu", "lmhead.cu", "path.cu",
-           "kvcache.cu", "attention.cu", "attention_e4m3.cu", "attention_rows.cu"]
+           "kvcache.cu", "attention.cu", "attention_16bit.cu", "attention_e4m3.cu",
+           "attention_rows.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -77,10 +77,15 @@ struct AttentionProblem {
     bool join;                          // items may be cut
 };
 
-// The call with an e4m3 cache (attention_e4m3.cu).
+// The call with a 16-bit cache (attention_16bit.cu) and with an e4m3 cache (attention_e4m3.cu). few:
+// the build for row tiles of few rows.
+cudaError_t launch_attention_16bit(const DeviceInfo& dev, const AttentionArgs& a,
+                                   const AttentionProblem& p, bool few, uint32_t* status,
+                                   cudaStream_t stream);
 cudaError_t launch_attention_e4m3(const DeviceInfo& dev, const AttentionArgs& a,
-                                  const AttentionProblem& p, uint32_t* status,
+                                  const AttentionProblem& p, bool few, uint32_t* status,
                                   cudaStream_t stream);
+
 namespace {
 
 using namespace ptx;
@@ -611,7 +616,7 @@ __device__ __forceinline__ void turn_pieces(uint32_t (&piece)[4][4], int lane) {
     }
 }
 
-template <int D, bool kHalf, bool kCap, bool kSmall>
+template <int D, bool kHalf, bool kCap, bool kSmall, bool kFewRows>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_few,
                  const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Problem p,
@@ -777,7 +782,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     if (nq > 0) wait(q_empty, (nq - 1) & 1);
                     if (!(ok = __all_sync(kFull, tries != 0))) break;
                     ++nq;
-                    const bool few = c->few(p), pair = c->pair(p);
+                    const bool few = kFewRows && c->few(p), pair = c->pair(p);
                     if (pair && few_before) {
                         // The second row tile lies where P of the few rows before it has been.
                         wait(p_free + 8 * ((nq - 2) & 1), ((nq - 2) >> 1) & 1);
@@ -853,7 +858,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 const int steps = __shfl_sync(kFull, c->hi - c->lo, 0);
                 if (steps > 0) {
                     const bool pair = __shfl_sync(kFull, c->pair(p) ? 1 : 0, 0) != 0;
-                    const bool few = __shfl_sync(kFull, c->few(p) ? 1 : 0, 0) != 0;
+                    const bool few = kFewRows && __shfl_sync(kFull, c->few(p) ? 1 : 0, 0) != 0;
                     // Steps whose values need no look.
                     const int from = __shfl_sync(kFull, c->from - c->begin - c->lo, 0);
                     const int to = __shfl_sync(kFull, c->to - c->begin - c->lo, 0);
@@ -1083,7 +1088,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const bool pair = c->pair(p);
             const int sub0 = c->tok0 + (pair ? w : 0) * p.tpt;   // the row tile's first token
             const int nsub = min(p.tpt, c->n - sub0);            // and its tokens
-            const bool few = c->few(p);
+            const bool few = kFewRows && c->few(p);
             const int row_token = (few ? lane : row) / p.g;
             bool live = row_token < nsub;
             const int pos = c->L - c->n + sub0 + row_token;
@@ -1563,17 +1568,14 @@ bool encode_4d(CUtensorMap* map, int dtype, const void* base, const long long (&
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-using Launch = cudaError_t (*)(const DeviceInfo&, const AttentionArgs&, const Problem&, uint32_t*,
-                               cudaStream_t);
-
-template <int D, bool kHalf, bool kCap, bool kSmall>
+template <int D, bool kHalf, bool kCap, bool kSmall, bool kFewRows>
 cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a, const Problem& p,
                                    uint32_t* status, cudaStream_t stream) {
     static std::once_flag once[64];
     static cudaError_t attr_err[64];
     if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
     using L = Layout<D, kSmall>;
-    auto kernel = attention_kernel<D, kHalf, kCap, kSmall>;
+    auto kernel = attention_kernel<D, kHalf, kCap, kSmall, kFewRows>;
     const size_t smem = 1024 + L::total;
     std::call_once(once[dev.device], [&] {
         attr_err[dev.device] = cudaFuncSetAttribute(
@@ -1607,6 +1609,27 @@ cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, kHalf);
+}
+
+template <int D, bool kHalf, bool kSmall>
+cudaError_t launch_build(const DeviceInfo& dev, const AttentionArgs& a, const Problem& p, bool few,
+                         uint32_t* status, cudaStream_t stream) {
+    if (a.softcap > 0.f)
+        return few ? launch_on_tensor_cores<D, kHalf, true, kSmall, true>(dev, a, p, status, stream)
+                   : launch_on_tensor_cores<D, kHalf, true, kSmall, false>(dev, a, p, status, stream);
+    return few ? launch_on_tensor_cores<D, kHalf, false, kSmall, true>(dev, a, p, status, stream)
+               : launch_on_tensor_cores<D, kHalf, false, kSmall, false>(dev, a, p, status, stream);
+}
+
+template <bool kSmall>
+cudaError_t launch_for_cache(const DeviceInfo& dev, const AttentionArgs& a, const Problem& p, bool few,
+                             uint32_t* status, cudaStream_t stream) {
+    const bool half_type = a.dtype == kFp16;
+    if (p.D == 64)
+        return half_type ? launch_build<64, true, kSmall>(dev, a, p, few, status, stream)
+                         : launch_build<64, false, kSmall>(dev, a, p, few, status, stream);
+    return half_type ? launch_build<128, true, kSmall>(dev, a, p, few, status, stream)
+                     : launch_build<128, false, kSmall>(dev, a, p, few, status, stream);
 }
 
 }  // namespace
