@@ -37,7 +37,6 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     p.q_heads = a.q_heads;
     p.kv_heads = c.kv_heads;
     p.g = a.q_heads / c.kv_heads;
-    p.tpt = BM / p.g;
     p.R = a.R;
     p.max_pages = a.max_pages;
     p.num_pages = c.num_pages;
@@ -62,17 +61,20 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     w += align256((size_t)(dev.sm_count + 1) * sizeof(int4));
     p.part = reinterpret_cast<float*>(w);
     p.G = dev.sm_count;
+    // Two builds. Where a request has few rows of a key head on average, the one whose row tiles
+    // have few rows and use all softmax warps (windowed, capped blocks of 32 rows: 228 us, 389 us
+    // without; a longer request among them takes more items); the others are spared its code
+    // (16001-token prompt: 820 us, 890 us with both).
+    const bool few = p.g <= kFew && (long long)a.T * p.g <= (long long)kFew * a.R;
+    p.tpt = (few ? kFew : BM) / p.g;
+    p.tpi = few ? p.tpt : 2 * p.tpt;
     // Nothing is cut, and no join is launched, where the table's width and the number of tokens alone
     // say that plan_ranges will take whole items (about 2 us of a short call).
     const long long steps = ((long long)a.max_pages * c.page_size + BN - 1) / BN;
-    const long long per_request = ((long long)a.T + 2 * p.tpt - 1) / (2 * p.tpt);
-    const long long items = (a.R + (long long)a.T / (2 * p.tpt)) * c.kv_heads;
-    p.join = p.G > 1 && ((a.T > p.tpt ? 2 : 1) * (1 + steps) > 1 + kWholeSteps ||
+    const long long per_request = ((long long)a.T + p.tpi - 1) / p.tpi;
+    const long long items = (a.R + (long long)a.T / p.tpi) * c.kv_heads;
+    p.join = p.G > 1 && ((a.T > p.tpt && !few ? 2 : 1) * (1 + steps) > 1 + kWholeSteps ||
                          per_request > kSerialItems || items > p.G);
-    // Two builds. Where a request has few rows of a key head on average, the one whose row tiles of
-    // few rows use all softmax warps (windowed, capped blocks of 32 rows: 278 us, 389 us without);
-    // the others are spared its code (16001-token prompt: 822 us, 890 us with it).
-    const bool few = (long long)a.T * p.g <= (long long)kFew * a.R;
     return (c.dtype == kE4m3 ? launch_attention_e4m3 : launch_attention_16bit)(dev, a, p, few,
                                                                               status_word, stream);
 }

@@ -13,11 +13,13 @@
 // tiles of 128 tokens, or, where a request has no more than tpt tokens left, one row tile whose
 // even and odd key tiles go to the two halves of the CTA.
 //
-// Few rows. A row tile of at most 32 rows (single tokens, small blocks) would keep one softmax warp
-// of each half busy and the others idle. Its queries go into all four quarters of the tile's lanes
-// instead: S then has four copies, and each warp takes 32 of the 128 keys of every row. The warps
-// agree on a row's maximum through shared memory, and P meets there too: it is the A operand from
-// shared memory in place of tensor memory.
+// Few rows. Row tiles of at most 32 rows (single tokens, small blocks) would keep one softmax warp
+// of each half busy and the others idle. They have a build of their own, with tpt = floor(32 / g)
+// and one row tile an item. The queries go into all four quarters of the tile's lanes: S then has
+// four copies, and each warp takes 32 of the 128 keys of every row. The warps agree on a row's
+// maximum through shared memory, and P meets there too: it is the A operand from shared memory in
+// place of tensor memory. S is free again once it is in registers, so the next scores are taken
+// while the weights are.
 //
 // One CTA per SM, 16 warps (13-15 work for 8-bit caches only):
 //   * warps 0 and 12: TMA producers, of keys (and queries) and of values. Each lane looks up one page
@@ -60,7 +62,8 @@ namespace dflash {
 
 // A call of the tensor-core kernel.
 struct AttentionProblem {
-    int D, T, q_heads, kv_heads, g, tpt;   // tpt: tokens per row tile
+    int D, T, q_heads, kv_heads, g;
+    int tpt, tpi;                       // tokens per row tile, per item
     int R, max_pages, num_pages, page_size;
     int left, right;
     float softcap, scale, v_scale;      // scale includes the keys' scale
@@ -127,14 +130,14 @@ __device__ __forceinline__ void key_tiles(const Problem& p, int n, int L, int to
 }
 
 __device__ __forceinline__ int item_count(const Problem& p, int n) {
-    return (n + 2 * p.tpt - 1) / (2 * p.tpt);
+    return (n + p.tpi - 1) / p.tpi;
 }
 
 // Cost of an item in half steps of the two-tile kind, which is what the split makes equal.
 __device__ __forceinline__ int step_cost(const Problem& p, int ntok) { return ntok > p.tpt ? 2 : 1; }
 
 __device__ __forceinline__ int item_cost(const Problem& p, int n, int L, int t) {
-    const int tok0 = t * 2 * p.tpt, ntok = min(2 * p.tpt, n - tok0);
+    const int tok0 = t * p.tpi, ntok = min(p.tpi, n - tok0);
     int b, e;
     key_tiles(p, n, L, tok0, ntok, b, e);
     return step_cost(p, ntok) * (1 + e - b);
@@ -205,7 +208,7 @@ __device__ __forceinline__ int4 range_start(const Problem& p, const long long* c
         const int ck = __shfl_sync(kFull, c, k);
         off -= __shfl_sync(kFull, upto, k) - ck;
         const int tk = t0 + k;
-        const int w = step_cost(p, min(2 * p.tpt, q.n - tk * 2 * p.tpt));
+        const int w = step_cost(p, min(p.tpi, q.n - tk * p.tpi));
         const int step = max(0, (w == 2 ? ((int)off + 1) >> 1 : (int)off) - 1);
         at = make_int4(lo, h, tk, step);
         if (step * w >= ck - w && step > 0) {                // past the last step: the next item
@@ -325,7 +328,6 @@ struct __align__(16) Item {
     int v_odd;           // a value that is not finite was cleared
     int bad_page;        // a page id outside the pool was met
     __device__ __forceinline__ bool pair(const Problem& p) const { return ntok > p.tpt; }
-    __device__ __forceinline__ bool few(const Problem& p) const { return ntok * p.g <= kFew; }
     __device__ __forceinline__ bool whole() const { return lo == 0 && hi == steps; }
 };
 
@@ -349,7 +351,7 @@ __device__ __forceinline__ bool count_past(const volatile uint32_t* count, uint3
     return true;
 }
 
-template <int D, bool kSmall>
+template <int D, bool kSmall, bool kFewRows>
 struct Layout {
     static constexpr int kReaders = kSmall ? 15 : 12;            // warps that wait for items
     static constexpr uint32_t kChunk = BN * 128;                 // 128 rows x 64 values
@@ -358,12 +360,12 @@ struct Layout {
     static constexpr int kRawStages = kSmall ? (D == 128 ? 2 : 8) : 0;
     static constexpr int kK = kSmall ? (D == 128 ? 2 : 3) : (D == 128 ? 2 : 5);   // key stages
     static constexpr int kV = kSmall ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 5);   // value stages
-    static constexpr uint32_t q = 0;                             // two row tiles
-    // P of few rows, in the place of the second row tile: 16 KB for each half, 4 KB for 64 keys
-    // and a row's maxima and sums behind them.
+    // Two row tiles; or four copies of one of few rows, and behind them for each half P, 4 KB for 64
+    // keys, and a row's maxima and sums. (The MMA reads on behind P for the lanes of no row.)
+    static constexpr uint32_t q = 0;
+    static constexpr uint32_t pKeys = kFew * 128, pShare = 2 * pKeys, pHalf = pShare + 2 * 4 * kFew * 4;
     static constexpr uint32_t p = kTile;
-    static constexpr uint32_t pHalf = 16384, pKeys = kFew * 128, pShare = 2 * pKeys;
-    static constexpr uint32_t keys = p + (kTile > 2 * pHalf ? kTile : 2 * pHalf);
+    static constexpr uint32_t keys = p + (kFewRows ? 2 * pHalf : kTile);
     static constexpr uint32_t values = keys + kK * kTile;
     static constexpr uint32_t raw = values + kV * kTile;
     static constexpr uint32_t bars = raw + kRawStages * kRaw;
@@ -401,7 +403,7 @@ __device__ __forceinline__ uint32_t odd_halves(uint32_t w) {
 // cached token (one of the first `cached` rows of the tile). By one warp.
 template <int D, bool kHalf>
 __device__ __forceinline__ bool clear_odd(uint8_t* tile, int lane, int cached) {
-    constexpr int kVecs = (int)(Layout<D, false>::kTile / 16), kRun = 8;
+    constexpr int kVecs = (int)(Layout<D, false, false>::kTile / 16), kRun = 8;
     uint4* v = reinterpret_cast<uint4*>(tile);
     bool found = false;
     for (int i0 = lane; i0 < kVecs; i0 += 32 * kRun) {
@@ -446,7 +448,7 @@ __device__ __forceinline__ bool clear_odd(uint8_t* tile, int lane, int cached) {
             }
             if (!hit) continue;
             v[at] = make_uint4(word[0], word[1], word[2], word[3]);
-            found |= (at * 16 % (int)Layout<D, false>::kChunk) / 128 < cached;
+            found |= (at * 16 % (int)Layout<D, false, false>::kChunk) / 128 < cached;
         }
     }
     return found;
@@ -618,10 +620,10 @@ __device__ __forceinline__ void turn_pieces(uint32_t (&piece)[4][4], int lane) {
 
 template <int D, bool kHalf, bool kCap, bool kSmall, bool kFewRows>
 __global__ void __launch_bounds__(kThreads, 1)
-attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_few,
-                 const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Problem p,
+attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Problem p,
                  uint32_t* status) {
-    using L = Layout<D, kSmall>;
+    using L = Layout<D, kSmall, kFewRows>;
     constexpr bool kMmaHalf = kHalf || kSmall;               // the tensor cores' operands are fp16
     constexpr bool kScaleQ = kSmall && !kHalf;               // bf16 queries are scaled to fp16
     constexpr int kChunks = kSmall ? 1 : D / 64;             // boxes across a row
@@ -645,7 +647,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     const uint32_t o_done = q_full + 64;
     const uint32_t ml_there = q_full + 80, ml_back = q_full + 88, halves_done = q_full + 96;
     const uint32_t drained = q_full + 104, q_ready = q_full + 120;   // drained: [2]
-    const uint32_t p_free = q_full + 128, share = q_full + 144;          // [2] by turns, [2] by half
+    const uint32_t s_read = q_full + 128, share = q_full + 144;          // by half
     const uint32_t item_full = q_full + 160, item_empty = item_full + 8 * kItems;
     const uint32_t raw_full = item_empty + 8 * kItems, raw_empty = raw_full + 8 * L::kRawStages;
     float2* ml = reinterpret_cast<float2*>(smem + L::ml);
@@ -658,9 +660,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         // Landings: the producer, or the four widening warps. Releases: both halves' warps.
         for (uint32_t s = 0; s < 2 * kK; ++s) mbar_init(k_full + 8 * s, kSmall ? 4 : 1);
         for (uint32_t s = 0; s < 2 * kV; ++s) mbar_init(v_full + 8 * s, kSmall ? 4 : 1);
-        for (uint32_t s = 0; s < kK; ++s) mbar_init(k_empty + 8 * s, 2);
+        for (uint32_t s = 0; s < kK; ++s) mbar_init(k_empty + 8 * s, kFewRows ? 1 : 2);
         for (uint32_t s = 0; s < kV; ++s) {
-            mbar_init(v_empty + 8 * s, 2);
+            mbar_init(v_empty + 8 * s, kFewRows ? 1 : 2);
             mbar_init(v_fix + 8 * s, 1);
         }
         mbar_init(q_full, 1);
@@ -678,7 +680,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(drained + 8, 1);
         mbar_init(q_ready, 8);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(p_free + 8 * i, 2);
+            mbar_init(s_read + 8 * i, 4);
             mbar_init(share + 8 * i, 4);
         }
         for (int s = 0; s < L::kRawStages; ++s) {
@@ -771,7 +773,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (warp == 0) {
             // ---- TMA producer of queries and keys; of an 8-bit cache's raw tiles, keys and values
             uint32_t g = 0, nq = 0;      // tiles issued, items with steps
-            bool few_before = false;     // P of few rows may still be in use
             auto free_stage = [&](uint32_t empty, uint32_t n) {
                 if (g >= n) wait(empty + 8 * (g % n), (g / n - 1) & 1);
                 return ok = __all_sync(kFull, tries != 0);
@@ -782,24 +783,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     if (nq > 0) wait(q_empty, (nq - 1) & 1);
                     if (!(ok = __all_sync(kFull, tries != 0))) break;
                     ++nq;
-                    const bool few = kFewRows && c->few(p), pair = c->pair(p);
-                    if (pair && few_before) {
-                        // The second row tile lies where P of the few rows before it has been.
-                        wait(p_free + 8 * ((nq - 2) & 1), ((nq - 2) >> 1) & 1);
-                        if (!(ok = __all_sync(kFull, tries != 0))) break;
-                        few_before = false;
-                    }
-                    few_before |= few;
+                    const bool pair = c->pair(p);
                     if (lane == 0) {
-                        const int tiles = few ? 4 : (pair ? 2 : 1);
-                        const uint32_t apart = few ? kFew * 128 : L::kTile;
-                        mbar_expect_tx(q_full,
-                                       (uint32_t)(tiles * p.g * (few ? kFew / p.g : p.tpt)) * D * 2);
+                        const int tiles = kFewRows ? 4 : (pair ? 2 : 1);
+                        constexpr uint32_t apart = kFewRows ? kFew * 128 : L::kTile;
+                        mbar_expect_tx(q_full, (uint32_t)(tiles * p.g * p.tpt) * D * 2);
                         for (int s = 0; s < tiles; ++s)
                             for (int i = 0; i < D / 64; ++i)
-                                tma_load_4d(base + L::q + s * apart + i * L::kChunk,
-                                            few ? &map_few : &map_q, q_full, i * 64, 0, h,
-                                            c->t0 + c->tok0 + (pair ? s * p.tpt : 0));
+                                tma_load_4d(base + L::q + s * apart + i * L::kChunk, &map_q, q_full,
+                                            i * 64, 0, h, c->t0 + c->tok0 + (pair ? s * p.tpt : 0));
                     }
                     __syncwarp();
                     if constexpr (kSmall) {
@@ -852,13 +844,13 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             const uint64_t dp = sw128_desc(ubase + L::p + w * L::pHalf);
             const uint32_t acc = utmem + 256 + w * 128, st = utmem + w * BN, pt = st + 64;
             uint32_t g = 0, nq = 0;      // steps of earlier items; items with steps
-            uint32_t np = 0, nl = 0;     // P tiles waited for, their lower halves
+            uint32_t np = 0;             // P tiles waited for
             uint32_t fixed = 0;          // phase bit of each stage's v_fix
             while (const Item* c = get_item()) {
                 const int steps = __shfl_sync(kFull, c->hi - c->lo, 0);
                 if (steps > 0) {
-                    const bool pair = __shfl_sync(kFull, c->pair(p) ? 1 : 0, 0) != 0;
-                    const bool few = kFewRows && __shfl_sync(kFull, c->few(p) ? 1 : 0, 0) != 0;
+                    const bool pair =
+                        !kFewRows && __shfl_sync(kFull, c->pair(p) ? 1 : 0, 0) != 0;
                     // Steps whose values need no look.
                     const int from = __shfl_sync(kFull, c->from - c->begin - c->lo, 0);
                     const int to = __shfl_sync(kFull, c->to - c->begin - c->lo, 0);
@@ -868,7 +860,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     // A tile of a pair is freed by both halves, another by its half alone.
                     auto release = [&](uint32_t empty) {
                         umma_commit_warp(empty);
-                        if (!pair) umma_commit_warp(empty);
+                        if (!kFewRows && !pair) umma_commit_warp(empty);
                     };
                     const int stride = pair ? 1 : 2, j0 = pair ? 0 : w;
                     auto scores = [&](int j) {               // S of step j; its keys have landed
@@ -902,12 +894,20 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             const int next = j + stride;
                             const uint64_t b = dv + s * (L::kTile >> 4);
                             const uint32_t more = j != j0;
+                            if constexpr (kFewRows) {
+                                // The next scores start once these are in the softmax's registers.
+                                if (next < steps) {
+                                    k_landed(next);
+                                    wait(s_read + 8 * w, np & 1);
+                                    scores(next);
+                                }
+                            }
                             // The values have landed, and been looked through where they must be.
                             wait(v_full + 8 * (t % (2 * kV)), (t / (2 * kV)) & 1);
                             if (look) wait(v_fix + 8 * s, (fixed >> s) & 1);
                             wait(p_up + 8 * w, np & 1);
                             tc_fence_after();
-                            if (few) {
+                            if constexpr (kFewRows) {
 #pragma unroll
                                 for (int x = 0; x < 8; ++x)
                                     umma_f16_warp(acc, dp + (((x / 4) * L::pKeys + (x % 4) * 32) >> 4),
@@ -917,10 +917,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                 for (int x = 4; x < 8; ++x)
                                     umma_f16_tmem_a_warp(acc, pt + x * 8, b + x * (2048 >> 4), idesc_o,
                                                          x > 4 ? 1u : more);
-                            }
-                            if (next < steps) k_landed(next);
-                            if (!few) {
-                                wait(p_low + 8 * w, nl++ & 1);
+                                if (next < steps) k_landed(next);
+                                wait(p_low + 8 * w, np & 1);
                                 tc_fence_after();
 #pragma unroll
                                 for (int x = 0; x < 4; ++x)
@@ -930,11 +928,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             ++np;
                             umma_commit_warp(o_done + 8 * w);
                             release(v_empty + 8 * s);
-                            if (next < steps) scores(next);
+                            if (!kFewRows && next < steps) scores(next);
                         }
                         if (look) fixed ^= 1u << s;
                     }
-                    umma_commit_warp(p_free + 8 * ((nq - 1) & 1));
                     g += steps;
                 }
                 done_with();
@@ -964,8 +961,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     c.r = over ? -1 : at.x;
                     if (!over) {
                         c.h = at.y;
-                        c.tok0 = at.z * 2 * p.tpt;
-                        c.ntok = min(2 * p.tpt, q.n - c.tok0);
+                        c.tok0 = at.z * p.tpi;
+                        c.ntok = min(p.tpi, q.n - c.tok0);
                         c.t0 = q.t0;
                         c.n = q.n;
                         c.L = q.L;
@@ -1083,13 +1080,17 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const float cap = p.softcap * kLog2e;
         // S tiles of this half; items of one row tile, with steps; times that few rows were shared
         uint32_t ns = 0, nb = 0, nq = 0, nshare = 0;
+        bool both = false;                                   // halves_done is still to be waited for
+        auto settle = [&]() {
+            if (both) wait(halves_done, (nb - 1) & 1);
+            both = false;
+        };
         while (const Item* c = get_item()) {
             const int steps = c->hi - c->lo;
-            const bool pair = c->pair(p);
+            const bool pair = !kFewRows && c->pair(p);
             const int sub0 = c->tok0 + (pair ? w : 0) * p.tpt;   // the row tile's first token
             const int nsub = min(p.tpt, c->n - sub0);            // and its tokens
-            const bool few = kFewRows && c->few(p);
-            const int row_token = (few ? lane : row) / p.g;
+            const int row_token = (kFewRows ? lane : row) / p.g;
             bool live = row_token < nsub;
             const int pos = c->L - c->n + sub0 + row_token;
             const int row_lo = first_key(p, pos);
@@ -1107,6 +1108,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 // which leaves the factors for half 1.
                 if (steps > 0) {
                     wait(q_full, nq++ & 1);
+                    settle();                            // the factors there have been read
                     if (pair || w == 0) {
                         const float undo = widen_query_row<D>(smem + L::q + w * L::kTile, row);
                         if (!pair) ml[row].x = undo;
@@ -1129,14 +1131,20 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                 }
                 ++ns;
-                any = true;
-                if (few) {
+                if (!any) {
+                    // Neither half's O is written again before both halves have read it.
+                    settle();
+                    any = true;
+                }
+                if constexpr (kFewRows) {
                     // This warp's 32 keys of all rows, which lie in every quarter's lanes.
                     uint32_t v[32];
                     const uint32_t shared = base + L::p + w * L::pHalf;
                     tc_fence_after();
                     tmem_ld_issue_x32(ts + 32 * quarter, v);
                     tmem_ld_wait_x32(v);
+                    tc_fence_before();
+                    mbar_arrive_warp(s_read + 8 * w);
                     if constexpr (kCap) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = capped(v[i], cap_in, cap);
@@ -1156,7 +1164,9 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             top[x] = fmaxf(fmaxf(top[x], __uint_as_float(v[i + 2 * x])),
                                            __uint_as_float(v[i + 2 * x + 1]));
                     // The tile's maximum of the row, from all four warps.
-                    float* maxima = reinterpret_cast<float*>(smem + L::p + w * L::pHalf + L::pShare);
+                    // In two buffers by turns: P of the tile before the last has been waited for by all.
+                    float* maxima = reinterpret_cast<float*>(smem + L::p + w * L::pHalf + L::pShare) +
+                                    (ns & 1) * 4 * kFew;
                     maxima[quarter * kFew + lane] = fmaxf(top[0], top[1]);
                     mbar_arrive_warp(share + 8 * w);
                     wait(share + 8 * w, nshare++ & 1);
@@ -1166,11 +1176,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     const bool grown = most > m + kGrowth;
                     const float keep = grown && m > -INFINITY ? ex2(m - most) : 1.f;
                     if (grown) m = most;
+                    // The tile before this one is in O, and its P has been read.
+                    wait(o_done + 8 * w, ns & 1);
                     if (__any_sync(kFull, keep != 1.f)) {
                         l *= keep;
-                        // The scores are here, so the MMAs before them are over; O lies in the first
-                        // quarter's lanes.
-                        if (quarter == 0) {
+                        if (quarter == 0) {              // O lies in the first quarter's lanes
+                            tc_fence_after();
 #pragma unroll 1
                             for (int d = 0; d < D; d += 16) scale_columns(to_ + d, keep);
                         }
@@ -1203,118 +1214,119 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive_warp(p_up + 8 * w);
-                    continue;
-                }
-                if (!warp_live) {
-                    mbar_arrive_warp(p_up + 8 * w);
-                    mbar_arrive_warp(p_low + 8 * w);
-                    continue;
-                }
-                tc_fence_after();
-                uint32_t va[32], vb[32];
-                const bool masked = j < from || j >= to;
-                if (kCap || masked) {
-                    // Caps and masks first, in tensor memory, in quarters of 32 keys: the steps that
-                    // every tile takes stay short.
-                    const int k0 = (first + j) * BN;
-                    auto prepare = [&](uint32_t (&v)[32], int c0) {
-                        if constexpr (kCap) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) v[i] = capped(v[i], cap_in, cap);
-                        }
-                        if (masked) {
-                            const uint32_t seen =
-                                below(row_hi - k0 - c0) & ~below(row_lo - k0 - c0);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                if (!(seen & (1u << i))) v[i] = 0xFF800000u;
-                        }
-                        tmem_st_x32(ts + c0, v);
-                    };
-#pragma unroll 1
-                    for (int c0 = 0; c0 < BN; c0 += 64) {
-                        tmem_ld_issue_x32(ts + c0, va);
-                        tmem_ld_issue_x32(ts + c0 + 32, vb);
-                        tmem_ld_wait_x32(va);
-                        tmem_ld_wait_x32(vb);
-                        prepare(va, c0);
-                        prepare(vb, c0 + 32);
+                } else {
+                    if (!warp_live) {
+                        mbar_arrive_warp(p_up + 8 * w);
+                        mbar_arrive_warp(p_low + 8 * w);
+                        continue;
                     }
-                    tmem_st_wait();
-                }
-                // S in quarters, first for the maximum, then, from the top, for the weights. P of a
-                // quarter overwrites S that has been read for good: quarter c goes to columns
-                // 64 + 16 c.
-                float top[2] = {-INFINITY, -INFINITY};
-                auto raise = [&](const uint32_t (&v)[32]) {
-#pragma unroll
-                    for (int i = 0; i < 32; i += 4)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            top[x] = fmaxf(fmaxf(top[x], __uint_as_float(v[i + 2 * x])),
-                                           __uint_as_float(v[i + 2 * x + 1]));
-                };
-                tmem_ld_issue_x32(ts, va);
-                tmem_ld_issue_x32(ts + 32, vb);
-                tmem_ld_wait_x32(va);
-                tmem_ld_wait_x32(vb);
-                raise(va);
-                tmem_ld_issue_x32(ts + 64, va);
-                raise(vb);
-                tmem_ld_issue_x32(ts + 96, vb);
-                tmem_ld_wait_x32(va);
-                tmem_ld_wait_x32(vb);
-                raise(va);
-                raise(vb);
-                const float most = fmaxf(top[0], top[1]) * unit;
-                const bool grown = most > m + kGrowth;       // also when m is still -inf
-                const float keep = grown && m > -INFINITY ? ex2(m - most) : 1.f;
-                if (grown) m = most;
-                if (__any_sync(kFull, keep != 1.f)) {
-                    // O holds the tiles before this one: wait for the last of them.
-                    wait(o_done + 8 * w, ns & 1);
                     tc_fence_after();
-                    l *= keep;
-#pragma unroll 1
-                    for (int d = 0; d < D; d += 16) scale_columns(to_ + d, keep);
-                }
-                const float off = m == -INFINITY ? 0.f : m;
-                const uint64_t unit2 = pair_of(unit, unit), off2 = pair_of(-off, -off);
-                uint64_t add[2] = {0, 0};
-                // The weights of one quarter, from its scores.
-                auto weigh = [&](const uint32_t (&v)[32], int quarter) {
-                    uint32_t pk[16];
+                    uint32_t va[32], vb[32];
+                    const bool masked = j < from || j >= to;
+                    if (kCap || masked) {
+                        // Caps and masks first, in tensor memory, in quarters of 32 keys: the steps that
+                        // every tile takes stay short.
+                        const int k0 = (first + j) * BN;
+                        auto prepare = [&](uint32_t (&v)[32], int c0) {
+                            if constexpr (kCap) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float2 x = halves_of(
-                            fma_pair(pair_of(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
-                                     unit2, off2));
-                        const float lo = ex2(x.x), hi = ex2(x.y);
-                        add[i & 1] = add_pair(add[i & 1], pair_of(lo, hi));
-                        pk[i] = pack16(kMmaHalf, lo, hi);
+                                for (int i = 0; i < 32; ++i) v[i] = capped(v[i], cap_in, cap);
+                            }
+                            if (masked) {
+                                const uint32_t seen =
+                                    below(row_hi - k0 - c0) & ~below(row_lo - k0 - c0);
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    if (!(seen & (1u << i))) v[i] = 0xFF800000u;
+                            }
+                            tmem_st_x32(ts + c0, v);
+                        };
+#pragma unroll 1
+                        for (int c0 = 0; c0 < BN; c0 += 64) {
+                            tmem_ld_issue_x32(ts + c0, va);
+                            tmem_ld_issue_x32(ts + c0 + 32, vb);
+                            tmem_ld_wait_x32(va);
+                            tmem_ld_wait_x32(vb);
+                            prepare(va, c0);
+                            prepare(vb, c0 + 32);
+                        }
+                        tmem_st_wait();
                     }
-                    tmem_st_x16(ts + 64 + 16 * quarter, pk);
-                };
-                weigh(vb, 3);
-                tmem_ld_issue_x32(ts + 32, vb);
-                weigh(va, 2);
-                tmem_ld_wait_x32(vb);
-                tmem_ld_issue_x32(ts, va);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive_warp(p_up + 8 * w);
-                weigh(vb, 1);
-                tmem_ld_wait_x32(va);
-                weigh(va, 0);
-                tmem_st_wait();
-                tc_fence_before();
-                mbar_arrive_warp(p_low + 8 * w);
-                const float2 sums = halves_of(add_pair(add[0], add[1]));
-                l += sums.x + sums.y;
+                    // S in quarters, first for the maximum, then, from the top, for the weights. P of a
+                    // quarter overwrites S that has been read for good: quarter c goes to columns
+                    // 64 + 16 c.
+                    float top[2] = {-INFINITY, -INFINITY};
+                    auto raise = [&](const uint32_t (&v)[32]) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x)
+                                top[x] = fmaxf(fmaxf(top[x], __uint_as_float(v[i + 2 * x])),
+                                               __uint_as_float(v[i + 2 * x + 1]));
+                    };
+                    tmem_ld_issue_x32(ts, va);
+                    tmem_ld_issue_x32(ts + 32, vb);
+                    tmem_ld_wait_x32(va);
+                    tmem_ld_wait_x32(vb);
+                    raise(va);
+                    tmem_ld_issue_x32(ts + 64, va);
+                    raise(vb);
+                    tmem_ld_issue_x32(ts + 96, vb);
+                    tmem_ld_wait_x32(va);
+                    tmem_ld_wait_x32(vb);
+                    raise(va);
+                    raise(vb);
+                    const float most = fmaxf(top[0], top[1]) * unit;
+                    const bool grown = most > m + kGrowth;       // also when m is still -inf
+                    const float keep = grown && m > -INFINITY ? ex2(m - most) : 1.f;
+                    if (grown) m = most;
+                    if (__any_sync(kFull, keep != 1.f)) {
+                        // O holds the tiles before this one: wait for the last of them.
+                        wait(o_done + 8 * w, ns & 1);
+                        tc_fence_after();
+                        l *= keep;
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 16) scale_columns(to_ + d, keep);
+                    }
+                    const float off = m == -INFINITY ? 0.f : m;
+                    const uint64_t unit2 = pair_of(unit, unit), off2 = pair_of(-off, -off);
+                    uint64_t add[2] = {0, 0};
+                    // The weights of one quarter, from its scores.
+                    auto weigh = [&](const uint32_t (&v)[32], int quarter) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 x = halves_of(
+                                fma_pair(pair_of(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                         unit2, off2));
+                            const float lo = ex2(x.x), hi = ex2(x.y);
+                            add[i & 1] = add_pair(add[i & 1], pair_of(lo, hi));
+                            pk[i] = pack16(kMmaHalf, lo, hi);
+                        }
+                        tmem_st_x16(ts + 64 + 16 * quarter, pk);
+                    };
+                    weigh(vb, 3);
+                    tmem_ld_issue_x32(ts + 32, vb);
+                    weigh(va, 2);
+                    tmem_ld_wait_x32(vb);
+                    tmem_ld_issue_x32(ts, va);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive_warp(p_up + 8 * w);
+                    weigh(vb, 1);
+                    tmem_ld_wait_x32(va);
+                    weigh(va, 0);
+                    tmem_st_wait();
+                    tc_fence_before();
+                    mbar_arrive_warp(p_low + 8 * w);
+                    const float2 sums = halves_of(add_pair(add[0], add[1]));
+                    l += sums.x + sums.y;
+                }
             }
             // Epilogue, once this half's last tile is in O.
             if (any) wait(o_done + 8 * w, (ns - 1) & 1);
-            if (few) {
+            else settle();
+            if constexpr (kFewRows) {
                 // The four warps' sums; O and the rest of the item are the first one's.
                 if (any) {
                     float* sums = reinterpret_cast<float*>(smem + L::p + w * L::pHalf + L::pShare);
@@ -1377,7 +1389,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     p.part + (size_t)(2 * blockIdx.x + (c->lo > 0 ? 0 : 1)) * part_floats(D) +
                     (size_t)(pair ? w : 0) * BM * (D + 2));
                 const long long out_row = ((long long)c->t0 + sub0 + row_token) * p.q_heads +
-                                          c->h * p.g + ((few ? lane : row) - row_token * p.g);
+                                          c->h * p.g + ((kFewRows ? lane : row) - row_token * p.g);
                 uint16_t* out = static_cast<uint16_t*>(p.out) + out_row * D;
                 // The rows whose output this lane stores: 16-byte pieces pass through groups of four
                 // lanes, so that a store covers 8 rows x 64 bytes and not 32 rows x 16.
@@ -1434,9 +1446,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             }
             tc_fence_before();
             if (!pair) {
-                // Neither half's O is written again before both halves have read it.
                 mbar_arrive_warp(halves_done);
-                wait(halves_done, nb & 1);
+                both = true;
                 ++nb;
             }
             done_with();
@@ -1466,7 +1477,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     if (at.x >= p.R || at.w == 0) return;
     if (before.x == at.x && before.y == at.y && before.z == at.z && before.w > 0) return;
     const Request q = request_of(p, at.x);
-    const int tok0 = at.z * 2 * p.tpt, ntok = min(2 * p.tpt, q.n - tok0);
+    const int tok0 = at.z * p.tpi, ntok = min(p.tpi, q.n - tok0);
     int begin, end;
     key_tiles(p, q.n, q.L, tok0, ntok, begin, end);
     const int steps = end - begin;
@@ -1574,7 +1585,7 @@ cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a
     static std::once_flag once[64];
     static cudaError_t attr_err[64];
     if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
-    using L = Layout<D, kSmall>;
+    using L = Layout<D, kSmall, kFewRows>;
     auto kernel = attention_kernel<D, kHalf, kCap, kSmall, kFewRows>;
     const size_t smem = 1024 + L::total;
     std::call_once(once[dev.device], [&] {
@@ -1583,19 +1594,16 @@ cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a
     });
     if (attr_err[dev.device] != cudaSuccess) return attr_err[dev.device];
     const KvCache& c = a.cache;
-    CUtensorMap map_q, map_few, map_k, map_v;
-    const int few = std::max(1, kFew / p.g);
+    CUtensorMap map_q, map_k, map_v;
     const int box = std::min(c.page_size, BN);
     if (!encode_4d(&map_q, a.dtype, a.query, {D, p.g, c.kv_heads, a.T},
                    {a.q_head_stride, p.g * a.q_head_stride, a.q_token_stride}, p.g, p.tpt) ||
-        !encode_4d(&map_few, a.dtype, a.query, {D, p.g, c.kv_heads, a.T},
-                   {a.q_head_stride, p.g * a.q_head_stride, a.q_token_stride}, p.g, few) ||
         !encode_4d(&map_k, c.dtype, c.key, {D, c.page_size, c.kv_heads, c.num_pages},
                    {c.token_stride, c.head_stride, c.page_stride}, box, 1) ||
         !encode_4d(&map_v, c.dtype, c.value, {D, c.page_size, c.kv_heads, c.num_pages},
                    {c.token_stride, c.head_stride, c.page_stride}, box, 1))
         return cudaErrorInvalidValue;
-    kernel<<<p.G, kThreads, smem, stream>>>(map_q, map_few, map_k, map_v, p, status);
+    kernel<<<p.G, kThreads, smem, stream>>>(map_q, map_k, map_v, p, status);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || !p.join) return e;
     // The join may be set up before the attention has ended, and waits for it before it reads.
