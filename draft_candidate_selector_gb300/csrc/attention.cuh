@@ -35,6 +35,8 @@
 //     shared memory; then looks through the value tiles that some row must not see all of, and
 //     clears what is not finite there (0 x infinity would reach the rows that do not see it). See
 //     Item::v_odd.
+//   * warps 13-15, with 12, for 8-bit caches: widen tiles to fp16. With few rows the softmax warps
+//     widen the values.
 //   * warps 4-7 and 8-11: one softmax each, a thread per row. S comes from tensor memory, P goes
 //     back over it. O stays in tensor memory and is scaled there only when the row's maximum has
 //     grown by more than 2^8 since it was last scaled; until then P is taken relative to the old
@@ -357,9 +359,17 @@ struct Layout {
     static constexpr uint32_t kChunk = BN * 128;                 // 128 rows x 64 values
     static constexpr uint32_t kTile = kChunk * (D / 64);
     static constexpr uint32_t kRaw = BN * D;                     // a tile in 8 bits
-    static constexpr int kRawStages = kSmall ? (D == 128 ? 2 : 8) : 0;
-    static constexpr int kK = kSmall ? (D == 128 ? 2 : 3) : (D == 128 ? 2 : 5);   // key stages
-    static constexpr int kV = kSmall ? (D == 128 ? 2 : 3) : (D == 128 ? 3 : 5);   // value stages
+    // Raw tiles of an 8-bit cache: one ring of keys and values; or, of few rows, one of keys and one
+    // of values, which the softmax warps widen: their half has the tile to itself, and four warps
+    // would take longer over keys and values than everything else (128 single tokens over 200 to
+    // 20000: 226 us, 241 us by four warps).
+    static constexpr bool kSpread = kSmall && kFewRows;
+    static constexpr int kRawStages = kSmall ? (kSpread ? (D == 128 ? 2 : 4) : (D == 128 ? 2 : 8)) : 0;
+    static constexpr int kRawV = kSpread ? (D == 128 ? 2 : 4) : 0;
+    // Stages of keys and values.
+    static constexpr int kK = kSmall ? (D == 128 ? (kSpread ? 1 : 2) : 3) : (D == 128 ? 2 : 5);
+    static constexpr int kV = kSmall ? (D == 128 ? 2 : (kSpread ? 4 : 3)) : (D == 128 ? 3 : 5);
+    static_assert(!kSpread || kV % 2 == 0, "within an item a half's stages are its own");
     // Two row tiles; or four copies of one of few rows, and behind them for each half P, 4 KB for 64
     // keys, and a row's maxima and sums. (The MMA reads on behind P for the lanes of no row.)
     static constexpr uint32_t q = 0;
@@ -368,8 +378,8 @@ struct Layout {
     static constexpr uint32_t keys = p + (kFewRows ? 2 * pHalf : kTile);
     static constexpr uint32_t values = keys + kK * kTile;
     static constexpr uint32_t raw = values + kV * kTile;
-    static constexpr uint32_t bars = raw + kRawStages * kRaw;
-    static constexpr int kBars = 3 * kK + 4 * kV + 2 * kRawStages + 20 + 2 * kItems;
+    static constexpr uint32_t bars = raw + (kRawStages + kRawV) * kRaw;
+    static constexpr int kBars = 3 * kK + 4 * kV + 2 * kRawStages + 3 * kRawV + 20 + 2 * kItems;
     static constexpr uint32_t ml = (bars + kBars * 8 + 15) / 16 * 16;   // [128] float2
     static constexpr uint32_t items = ml + BM * 8;               // [kItems] Item
     static constexpr uint32_t slot = items + kItems * 64;        // tensor memory's base
@@ -628,6 +638,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     constexpr bool kScaleQ = kSmall && !kHalf;               // bf16 queries are scaled to fp16
     constexpr int kChunks = kSmall ? 1 : D / 64;             // boxes across a row
     constexpr uint32_t kK = L::kK, kV = L::kV;
+    constexpr bool kSpread = L::kSpread;                     // the softmax warps widen the values
     extern __shared__ uint8_t smem_raw[];
     __shared__ int4 range[2];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -650,6 +661,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     const uint32_t s_read = q_full + 128, share = q_full + 144;          // by half
     const uint32_t item_full = q_full + 160, item_empty = item_full + 8 * kItems;
     const uint32_t raw_full = item_empty + 8 * kItems, raw_empty = raw_full + 8 * L::kRawStages;
+    const uint32_t rv_full = raw_empty + 8 * L::kRawStages, rv_empty = rv_full + 16 * L::kRawV;   // [2 kRawV]
     float2* ml = reinterpret_cast<float2*>(smem + L::ml);
     Item* items = reinterpret_cast<Item*>(smem + L::items);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::slot);
@@ -687,6 +699,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             mbar_init(raw_full + 8 * s, 1);
             mbar_init(raw_empty + 8 * s, 4);
         }
+        for (int s = 0; s < 2 * L::kRawV; ++s) mbar_init(rv_full + 8 * s, 1);
+        for (int s = 0; s < L::kRawV; ++s) mbar_init(rv_empty + 8 * s, 4);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(item_full + 8 * i, 1);
             mbar_init(item_empty + 8 * i, L::kReaders);
@@ -773,6 +787,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (warp == 0) {
             // ---- TMA producer of queries and keys; of an 8-bit cache's raw tiles, keys and values
             uint32_t g = 0, nq = 0;      // tiles issued, items with steps
+            uint32_t gv = 0;             // value tiles, where they have a ring of their own
             auto free_stage = [&](uint32_t empty, uint32_t n) {
                 if (g >= n) wait(empty + 8 * (g % n), (g / n - 1) & 1);
                 return ok = __all_sync(kFull, tries != 0);
@@ -796,8 +811,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     __syncwarp();
                     if constexpr (kSmall) {
                         // K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1
-                        constexpr uint32_t n = L::kRawStages;
+                        constexpr uint32_t n = L::kRawStages, nv = std::max(L::kRawV, 1);
                         auto load = [&](const CUtensorMap* map, int step, int id) {
+                            if (kSpread && map == &map_v) {
+                                if (gv >= nv) wait(rv_empty + 8 * (gv % nv), (gv / nv - 1) & 1);
+                                if (!(ok = __all_sync(kFull, tries != 0))) return;
+                                issue_tile(map, base + L::raw + (n + gv % nv) * L::kRaw,
+                                           rv_full + 8 * (gv % (2 * nv)), h, row_of(c, step), id);
+                                ++gv;
+                                return;
+                            }
                             if (!free_stage(raw_empty, n)) return;
                             issue_tile(map, base + L::raw + (g % n) * L::kRaw, raw_full + 8 * (g % n),
                                        h, row_of(c, step), id);
@@ -832,6 +855,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             for (uint32_t t = g > n ? g - n : 0; t < g; ++t)
                 (void)(kSmall ? mbar_wait(raw_full + 8 * (t % n), (t / n) & 1)
                               : mbar_wait(k_full + 8 * (t % (2 * n)), (t / (2 * n)) & 1));
+            if constexpr (kSpread) {
+                constexpr uint32_t nv = L::kRawV;
+                for (uint32_t t = gv > nv ? gv - nv : 0; t < gv; ++t)
+                    (void)mbar_wait(rv_full + 8 * (t % (2 * nv)), (t / (2 * nv)) & 1);
+            }
             if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
         } else if (warp <= 2) {
             // ---- MMA issuer of half w: the warp together, an elected lane issues
@@ -1026,10 +1054,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             uint32_t g = 0, raw = 0;     // steps of earlier items; raw tiles taken
             while (const Item* c = get_item()) {
                 const int steps = max(c->hi - c->lo, 0);
-                for (int i = 0; i < 2 * steps; ++i, ++raw) {
+                for (int i = 0; i < (kSpread ? 1 : 2) * steps; ++i, ++raw) {
                     // K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1
-                    const bool value = i == 2 * steps - 1 || (i > 0 && (i & 1) == 0);
-                    const int j = value ? (i - 1) / 2 : (i + 1) / 2;
+                    const bool value = !kSpread && (i == 2 * steps - 1 || (i > 0 && (i & 1) == 0));
+                    const int j = kSpread ? i : (value ? (i - 1) / 2 : (i + 1) / 2);
                     const int tile = c->begin + c->lo + j;
                     const bool look = value && !(tile >= c->from && tile < c->to);
                     const uint32_t n = value ? kV : kK, u = g + j, r = raw % L::kRawStages;
@@ -1080,6 +1108,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         const float cap = p.softcap * kLog2e;
         // S tiles of this half; items of one row tile, with steps; times that few rows were shared
         uint32_t ns = 0, nb = 0, nq = 0, nshare = 0;
+        uint32_t g = 0;                                      // steps of earlier items
         bool both = false;                                   // halves_done is still to be waited for
         auto settle = [&]() {
             if (both) wait(halves_done, (nb - 1) & 1);
@@ -1214,6 +1243,18 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive_warp(p_up + 8 * w);
+                    if constexpr (kSpread) {
+                        const uint32_t u = g + j, r = u % L::kRawV, to_stage = u % kV;
+                        wait(rv_full + 8 * (u % (2 * L::kRawV)), (u / (2 * L::kRawV)) & 1);
+                        if (u >= kV) wait(v_empty + 8 * to_stage, (u / kV - 1) & 1);
+                        if (widen_tile<D>(smem + L::raw + (L::kRawStages + r) * L::kRaw,
+                                          smem + L::values + to_stage * L::kTile, row,
+                                          j < from || j >= to, c->L - (first + j) * BN))
+                            items[k % kItems].v_odd = 1;
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        mbar_arrive_warp(rv_empty + 8 * r);
+                        mbar_arrive_warp(v_full + 8 * (u % (2 * kV)));
+                    }
                 } else {
                     if (!warp_live) {
                         mbar_arrive_warp(p_up + 8 * w);
@@ -1323,6 +1364,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     l += sums.x + sums.y;
                 }
             }
+            g += max(steps, 0);
             // Epilogue, once this half's last tile is in O.
             if (any) wait(o_done + 8 * w, (ns - 1) & 1);
             else settle();
