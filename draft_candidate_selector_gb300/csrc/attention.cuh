@@ -381,7 +381,8 @@ struct Layout {
     static constexpr uint32_t bars = raw + (kRawStages + kRawV) * kRaw;
     static constexpr int kBars = 3 * kK + 4 * kV + 2 * kRawStages + 3 * kRawV + 20 + 2 * kItems;
     static constexpr uint32_t ml = (bars + kBars * 8 + 15) / 16 * 16;   // [128] float2
-    static constexpr uint32_t items = ml + BM * 8;               // [kItems] Item
+    static constexpr uint32_t undo = ml + BM * 8;                // [kItems][kFew] float
+    static constexpr uint32_t items = undo + (kSpread ? kItems * kFew * 4 : 0);               // [kItems] Item
     static constexpr uint32_t slot = items + kItems * 64;        // tensor memory's base
     static constexpr uint32_t issued = slot + 4;                 // value tiles issued
     static constexpr uint32_t total = slot + 16;
@@ -507,8 +508,8 @@ __device__ __noinline__ void refill_values(const Problem& p, const Item& c, int 
 // than 2^-39 of the row's largest value. The inverse goes into the row's score scale.
 
 // This thread's row of a query tile (128-byte rows, 128-byte swizzle): bf16 to scaled fp16, in
-// place. Returns the factor that undoes the scaling.
-template <int D>
+// place and into the copies 32 rows on. Returns the factor that undoes the scaling.
+template <int D, int kCopies>
 __device__ __forceinline__ float widen_query_row(uint8_t* tile, int row) {
     constexpr uint32_t kChunk = BN * 128;
     uint32_t top = 0;                                        // largest |x| of each half, as bits
@@ -534,7 +535,8 @@ __device__ __forceinline__ float widen_query_row(uint8_t* tile, int row) {
         for (int k = 0; k < 4; ++k)
             word[k] = pack16(true, __uint_as_float(word[k] << 16) * by,
                              __uint_as_float(word[k] & 0xFFFF0000u) * by);
-        *at = x;
+#pragma unroll
+        for (int copy = 0; copy < kCopies; ++copy) at[copy * kFew * 128 / 16] = x;
     }
     return __uint_as_float((uint32_t)(127 - shift) << 23);
 }
@@ -663,6 +665,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     const uint32_t raw_full = item_empty + 8 * kItems, raw_empty = raw_full + 8 * L::kRawStages;
     const uint32_t rv_full = raw_empty + 8 * L::kRawStages, rv_empty = rv_full + 16 * L::kRawV;   // [2 kRawV]
     float2* ml = reinterpret_cast<float2*>(smem + L::ml);
+    float* undo_of = reinterpret_cast<float*>(smem + L::undo);
     Item* items = reinterpret_cast<Item*>(smem + L::items);
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::slot);
     volatile uint32_t* issued = reinterpret_cast<volatile uint32_t*>(smem + L::issued);
@@ -690,7 +693,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         mbar_init(halves_done, 8);
         mbar_init(drained, 1);
         mbar_init(drained + 8, 1);
-        mbar_init(q_ready, 8);
+        mbar_init(q_ready, kFewRows ? 1 : 8);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_read + 8 * i, 4);
             mbar_init(share + 8 * i, 4);
@@ -800,7 +803,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     ++nq;
                     const bool pair = c->pair(p);
                     if (lane == 0) {
-                        const int tiles = kFewRows ? 4 : (pair ? 2 : 1);
+                        const int tiles = kFewRows ? (kScaleQ ? 1 : 4) : (pair ? 2 : 1);   // (copies follow)
                         constexpr uint32_t apart = kFewRows ? kFew * 128 : L::kTile;
                         mbar_expect_tx(q_full, (uint32_t)(tiles * p.g * p.tpt) * D * 2);
                         for (int s = 0; s < tiles; ++s)
@@ -1023,12 +1026,22 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                 }
             };
-            uint32_t handed = 0, g = 0;
+            uint32_t handed = 0, g = 0, nq = 0;
             for (;; ++k) {
                 while (!over && handed < k + 3) hand_out(handed++);
                 const Item* c = &items[k % kItems];
                 if (c->r < 0 || !__all_sync(kFull, tries != 0)) break;
                 const int steps = c->hi - c->lo;
+                if constexpr (kScaleQ && kFewRows) {
+                    // The queries, which are few. (By the softmax warps the scores of an item could
+                    // not begin before the item in front of it has ended: 30 us of 226.)
+                    if (steps > 0) {
+                        wait(q_full, nq++ & 1);
+                        undo_of[(k % kItems) * kFew + lane] = widen_query_row<D, 4>(smem + L::q, lane);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        mbar_arrive_warp(q_ready);
+                    }
+                }
                 for (int j = 0; j < steps && !kSmall; ++j) {
                     const int tile = c->begin + c->lo + j;
                     if (tile >= c->from && tile < c->to) continue;
@@ -1132,14 +1145,14 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             to -= first;
             float unit = kCap ? 1.f : p.scale * kLog2e;      // S to log2 of a weight
             float cap_in = kCap ? 2.f * kLog2e * p.scale / p.softcap : 0.f;
-            if constexpr (kScaleQ) {
+            if constexpr (kScaleQ && !kFewRows) {
                 // Half w scales the row tile it will read the scores of; one row tile is half 0's,
                 // which leaves the factors for half 1.
                 if (steps > 0) {
                     wait(q_full, nq++ & 1);
                     settle();                            // the factors there have been read
                     if (pair || w == 0) {
-                        const float undo = widen_query_row<D>(smem + L::q + w * L::kTile, row);
+                        const float undo = widen_query_row<D, 1>(smem + L::q + w * L::kTile, row);
                         if (!pair) ml[row].x = undo;
                         if (kCap) cap_in *= undo;
                         else unit *= undo;
@@ -1153,7 +1166,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 #pragma unroll 1
             for (int j = pair ? 0 : w; j < steps; j += pair ? 1 : 2) {
                 wait(s_full + 8 * w, ns & 1);
-                if constexpr (kScaleQ) {
+                if constexpr (kScaleQ && !kFewRows) {
                     if (!pair && w == 1 && !any) {           // S of half 1 follows the scaling
                         if (kCap) cap_in *= ml[row].x;
                         else unit *= ml[row].x;
@@ -1163,6 +1176,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 if (!any) {
                     // Neither half's O is written again before both halves have read it.
                     settle();
+                    if constexpr (kScaleQ && kFewRows) {
+                        const float undo = undo_of[(k % kItems) * kFew + lane];
+                        if (kCap) cap_in *= undo;
+                        else unit *= undo;
+                    }
                     any = true;
                 }
                 if constexpr (kFewRows) {
