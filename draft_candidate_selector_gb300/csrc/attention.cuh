@@ -553,24 +553,29 @@ template <int D>
 __device__ __forceinline__ bool widen_tile(const uint8_t* raw, uint8_t* tile, int t, bool look,
                                            int cached) {
     constexpr uint32_t kChunk = BN * 128;
-    constexpr int kUnits = BN * D / 16, kRun = 4;
+    constexpr int kAcross = D / 16, kDown = 128 / kAcross, kRounds = BN / kDown, kRun = 4;
+    // Eight lanes that store together: at D = 128 they take the left halves of one row and the right
+    // halves of its neighbour, whose pieces the swizzle puts into other banks.
+    const int c = t % kAcross, row_t = (t / kAcross) ^ (D == 128 ? (t >> 2) & 1 : 0);
+    const uint8_t* from = raw + row_t * D + c * 16;
+    uint8_t* to = tile + (c / 4) * kChunk + row_t * 128;
+    const int at0 = ((2 * c) % 8 ^ (row_t & 7)) * 16, at1 = ((2 * c + 1) % 8 ^ (row_t & 7)) * 16;
     bool found = false;
 #pragma unroll
-    for (int u0 = 0; u0 < kUnits; u0 += 128 * kRun) {
+    for (int n0 = 0; n0 < kRounds; n0 += kRun) {
         uint4 x[kRun];
 #pragma unroll
         for (int r = 0; r < kRun; ++r)
-            x[r] = *reinterpret_cast<const uint4*>(raw + (u0 + 128 * r + t) * 16);
+            x[r] = *reinterpret_cast<const uint4*>(from + (n0 + r) * kDown * D);
 #pragma unroll
         for (int r = 0; r < kRun; ++r) {
-            const int u = u0 + 128 * r + t, row = u / (D / 16), c = u % (D / 16);
             uint32_t* word = reinterpret_cast<uint32_t*>(&x[r]);
             if (look) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint32_t odd = __vcmpeq4(word[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
                     word[i] &= ~odd;
-                    found |= odd != 0 && row < cached;
+                    found |= odd != 0 && row_t + (n0 + r) * kDown < cached;
                 }
             }
             uint4 y[2];
@@ -580,10 +585,8 @@ __device__ __forceinline__ bool widen_tile(const uint8_t* raw, uint8_t* tile, in
                 wide[2 * i] = widen2(word[i] & 0xFFFFu);
                 wide[2 * i + 1] = widen2(word[i] >> 16);
             }
-            uint8_t* to = tile + (c / 4) * kChunk + row * 128;
-            const int at = (2 * c) % 8;
-            *reinterpret_cast<uint4*>(to + ((at ^ (row & 7)) * 16)) = y[0];
-            *reinterpret_cast<uint4*>(to + (((at + 1) ^ (row & 7)) * 16)) = y[1];
+            *reinterpret_cast<uint4*>(to + at0 + (n0 + r) * kDown * 128) = y[0];
+            *reinterpret_cast<uint4*>(to + at1 + (n0 + r) * kDown * 128) = y[1];
         }
     }
     return found;
