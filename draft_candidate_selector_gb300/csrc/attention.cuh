@@ -35,8 +35,8 @@
 //     shared memory; then looks through the value tiles that some row must not see all of, and
 //     clears what is not finite there (0 x infinity would reach the rows that do not see it). See
 //     Item::v_odd.
-//   * warps 13-15, with 12, for 8-bit caches: widen tiles to fp16. With few rows the softmax warps
-//     widen the values.
+//   * warps 12-15, for 8-bit caches: widen tiles to fp16. With few rows they widen the keys, the
+//     softmax warps the values, and warp 3 loads the values and scales bf16 queries to fp16.
 //   * warps 4-7 and 8-11: one softmax each, a thread per row. S comes from tensor memory, P goes
 //     back over it. O stays in tensor memory and is scaled there only when the row's maximum has
 //     grown by more than 2^8 since it was last scaled; until then P is taken relative to the old
@@ -793,7 +793,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         if (warp == 0) {
             // ---- TMA producer of queries and keys; of an 8-bit cache's raw tiles, keys and values
             uint32_t g = 0, nq = 0;      // tiles issued, items with steps
-            uint32_t gv = 0;             // value tiles, where they have a ring of their own
             auto free_stage = [&](uint32_t empty, uint32_t n) {
                 if (g >= n) wait(empty + 8 * (g % n), (g / n - 1) & 1);
                 return ok = __all_sync(kFull, tries != 0);
@@ -816,17 +815,10 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     }
                     __syncwarp();
                     if constexpr (kSmall) {
-                        // K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1
-                        constexpr uint32_t n = L::kRawStages, nv = std::max(L::kRawV, 1);
+                        // K_0, K_1, V_0, K_2, V_1, ..., K_n-1, V_n-2, V_n-1; with few rows warp 3 loads
+                        // the values
+                        constexpr uint32_t n = L::kRawStages;
                         auto load = [&](const CUtensorMap* map, int step, int id) {
-                            if (kSpread && map == &map_v) {
-                                if (gv >= nv) wait(rv_empty + 8 * (gv % nv), (gv / nv - 1) & 1);
-                                if (!(ok = __all_sync(kFull, tries != 0))) return;
-                                issue_tile(map, base + L::raw + (n + gv % nv) * L::kRaw,
-                                           rv_full + 8 * (gv % (2 * nv)), h, row_of(c, step), id);
-                                ++gv;
-                                return;
-                            }
                             if (!free_stage(raw_empty, n)) return;
                             issue_tile(map, base + L::raw + (g % n) * L::kRaw, raw_full + 8 * (g % n),
                                        h, row_of(c, step), id);
@@ -837,7 +829,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         for (int j = lo; j < hi && ok; ++j) {
                             const int id_after = page_of(c, j + 2);
                             if (j + 1 < hi) load(&map_k, j + 1, id_next);
-                            if (ok) load(&map_v, j, id);
+                            if (!kSpread && ok) load(&map_v, j, id);
                             id = id_next;
                             id_next = id_after;
                         }
@@ -861,11 +853,6 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
             for (uint32_t t = g > n ? g - n : 0; t < g; ++t)
                 (void)(kSmall ? mbar_wait(raw_full + 8 * (t % n), (t / n) & 1)
                               : mbar_wait(k_full + 8 * (t % (2 * n)), (t / (2 * n)) & 1));
-            if constexpr (kSpread) {
-                constexpr uint32_t nv = L::kRawV;
-                for (uint32_t t = gv > nv ? gv - nv : 0; t < gv; ++t)
-                    (void)mbar_wait(rv_full + 8 * (t % (2 * nv)), (t / (2 * nv)) & 1);
-            }
             if (nq > 0) (void)mbar_wait(q_full, (nq - 1) & 1);
         } else if (warp <= 2) {
             // ---- MMA issuer of half w: the warp together, an elected lane issues
@@ -1045,6 +1032,21 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         mbar_arrive_warp(q_ready);
                     }
                 }
+                if constexpr (kSpread) {
+                    // The raw value tiles, as warp 12 loads those of 16-bit caches (pages of 64
+                    // tokens 183 us, 187 us by the warp that loads the keys; of 16, 192 and 239).
+                    constexpr uint32_t n = L::kRawV;
+                    int id = steps > 0 ? page_of(c, c->lo) : -1;
+                    for (int j = c->lo; j < c->hi; ++j, ++g) {
+                        const int id_next = page_of(c, j + 1);
+                        if (g >= n) wait(rv_empty + 8 * (g % n), (g / n - 1) & 1);
+                        if (!__all_sync(kFull, tries != 0)) break;
+                        issue_tile(&map_v, base + L::raw + (L::kRawStages + g % n) * L::kRaw,
+                                   rv_full + 8 * (g % (2 * n)), c->h, row_of(c, j), id);
+                        id = id_next;
+                    }
+                    continue;
+                }
                 for (int j = 0; j < steps && !kSmall; ++j) {
                     const int tile = c->begin + c->lo + j;
                     if (tile >= c->from && tile < c->to) continue;
@@ -1061,6 +1063,11 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 g += max(steps, 0);
             }
             if (!__all_sync(kFull, tries != 0) && lane == 0) atomicOr(status, kStatusTimeout);
+            if constexpr (kSpread) {                         // the last loads land
+                constexpr uint32_t n = L::kRawV;
+                for (uint32_t t = g > n ? g - n : 0; t < g; ++t)
+                    (void)mbar_wait(rv_full + 8 * (t % (2 * n)), (t / (2 * n)) & 1);
+            }
         }
     } else if (warp >= 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
