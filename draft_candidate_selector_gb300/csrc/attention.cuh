@@ -29,8 +29,8 @@
 //     16.
 //   * warps 1 and 2, one for each half: issue the tcgen05.mma: S = Q K^T into tensor memory, and
 //     O += P V with P in tensor memory (over S, in 16 bits) and V transposed by its descriptor.
-//     Two warps, because the tensor cores idle through the waits of one (16001-token prompt: 833 us
-//     with one).
+//     Two warps, because the tensor cores idle through the waits of one (16001-token prompt: 810 us,
+//     833 us with one).
 //   * warp 3: walks the items of this CTA's range and hands them to the others through a ring in
 //     shared memory; then looks through the value tiles that some row must not see all of, and
 //     clears what is not finite there (0 x infinity would reach the rows that do not see it). See
@@ -40,8 +40,22 @@
 //   * warps 4-7 and 8-11: one softmax each, a thread per row. S comes from tensor memory, P goes
 //     back over it. O stays in tensor memory and is scaled there only when the row's maximum has
 //     grown by more than 2^8 since it was last scaled; until then P is taken relative to the old
-//     maximum, which changes nothing but the common factor of P, l and O.
+//     maximum, which changes nothing but the common factor of P, l and O. With few rows it is scaled
+//     whenever the maximum has grown: the largest weight is 1 then, which no rounding changes.
 // While one half's softmax runs, the tensor cores work for the other half.
+//
+// What bounds it. Single tokens and small blocks read each cached key and value once: 96 single
+// tokens over 500 to 16000 (16-bit, 8 key heads of 128) take 288 us, 6.2 TB/s. From an 8-bit cache
+// it is shared memory: per value a byte lands, is read, is written as two and read by the MMA (128
+// tokens over 200 to 20000: 183 us, 3.1 TB/s). Long prompts are bound by the tensor cores and the
+// softmax between two products (16001 tokens, 16 heads of 128, causal: 820 us, 1.28 PFLOP/s). A
+// call's plan, launch and first loads take some 20 us (one token over 332, with the join skipped).
+//
+// Rounding. P is rounded to the type of V (fp16 over an 8-bit cache), since one MMA's operands have
+// one type; S, m, l and O are fp32. Where many keys weigh alike that adds as much error as the
+// rounding of the output does; where few keys do, a largest weight of exactly 1 keeps it smaller
+// (two single tokens over 142 to 428, bf16: 1.3 times the output's rounding, 1.5 with the maximum
+// left behind; 1% of the time).
 //
 // Work split. The flat list of (request, key head, item, key tile) is cut into one equal range
 // per SM, wherever that falls. Every CTA takes the running cost over the requests itself (their
@@ -386,6 +400,7 @@ struct Layout {
     static constexpr uint32_t slot = items + kItems * 64;        // tensor memory's base
     static constexpr uint32_t issued = slot + 4;                 // value tiles issued
     static constexpr uint32_t total = slot + 16;
+    static_assert(bars - keys >= (kMaxTableRequests + 1) * 8, "the plan's running costs lie in the rings");
     static_assert(total + 1024 + 288 <= 232448, "a block's shared memory, with its alignment and the plan's own");
 };
 
@@ -1230,7 +1245,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     const float most = fmaxf(fmaxf(maxima[lane], maxima[kFew + lane]),
                                              fmaxf(maxima[2 * kFew + lane], maxima[3 * kFew + lane])) *
                                        unit;
-                    const bool grown = most > m + kGrowth;
+                    const bool grown = live && most > m;
                     const float keep = grown && m > -INFINITY ? ex2(m - most) : 1.f;
                     if (grown) m = most;
                     // The tile before this one is in O, and its P has been read.

@@ -422,13 +422,17 @@ dflash_status dflash_store_kv(const void* key, const void* value, int dtype, con
  * A token that sees no key gets zeros and lse = -inf. What the cache holds at keys that a
  * token does not see has no effect on it, infinities and NaN included. Scores, maxima and sums
  * are fp32; the products exp(s_j) v_j take exp(s_j) relative to a running maximum, rounded to
- * the query's type, and are summed in fp32.
+ * the query's type (to fp16 over an e4m3 cache), and are summed in fp32. Over an e4m3 cache bf16
+ * queries are taken as fp16 times a power of two for each row: what that loses is less than 2^-39
+ * of the row's largest value.
  * Page ids outside the pool are never followed: the request's outputs are NaN and the status
  * word records DFLASH_DEVICE_BAD_ID. A request whose kv_lens does not fit max_pages, or
  * whose query_start is out of order or past T, is refused with DFLASH_DEVICE_BAD_LENGTH: its
  * rows are NaN or not written. Rows of out at and behind query_start[R] are not written.
  * head_dim is a multiple of 8 up to 256 (16 for e4m3). A result does not depend on what else
- * is in the batch beyond the rounding of its sums' order, and equal calls give equal bits.
+ * is in the batch beyond the rounding of its sums and of their order, and equal calls give equal
+ * bits. head_dim 64 and 128 with pages of a power of two from 8 tokens on, q_heads / kv_heads up
+ * to 128 and R up to 16384 run on the tensor cores, all others on the CUDA cores.
  * ---------------------------------------------------------------------------------- */
 size_t dflash_paged_attention_workspace_bytes(int R, int T, int q_heads, int kv_heads,
                                               int head_dim);

@@ -518,3 +518,21 @@ def test_steps_together(dev, small):
             ctx = ctx - 11
             kept = [tuple([torch.cat(x)[:int(c)]] for x in k) for k, c in zip(kept, ctx)]
     clean()
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (10, 2), (16, 1)])
+def test_attention_few_rows_on_average(dev, dtype, cache, D, Hq, Hkv):
+    """Few rows a request on average, among them requests of many row tiles, of no new tokens and
+    of one cached token: all take the build for few rows, whose tiles hold 32 // g tokens."""
+    rng = np.random.default_rng(16)
+    new = np.where(rng.random(150) < 0.05, rng.integers(5, 60, 150), rng.integers(0, 2, 150))
+    assert new.sum() * (Hq // Hkv) <= 32 * len(new) and new.max() * (Hq // Hkv) > 128
+    ctx = np.where(rng.random(150) < 0.3, 0, rng.integers(0, 900, 150))
+    b = paged.Batch(ctx, new, Hq, Hkv, D, 16, dtype, cache, seed=16)
+    want = check(b)
+    for _ in range(5):
+        for g, w in zip(ds.dflash_paged_attention(*b.args(), **b.scales()), want):
+            assert torch.equal(g, w)
+    check(b, left=150, right=4, softcap=15.0)
