@@ -80,6 +80,7 @@ namespace dflash {
 struct AttentionProblem {
     int D, T, q_heads, kv_heads, g;
     int tpt, tpi;                       // tokens per row tile, per item
+    int over;                           // an item's fixed cost, in its steps
     int R, max_pages, num_pages, page_size;
     int left, right;
     float softcap, scale, v_scale;      // scale includes the keys' scale
@@ -156,7 +157,7 @@ __device__ __forceinline__ int item_cost(const Problem& p, int n, int L, int t) 
     const int tok0 = t * p.tpi, ntok = min(p.tpi, n - tok0);
     int b, e;
     key_tiles(p, n, L, tok0, ntok, b, e);
-    return step_cost(p, ntok) * (1 + e - b);
+    return step_cost(p, ntok) * (p.over + e - b);
 }
 
 // A request's new and cached tokens; n = 0 where query_start is refused, bad where kv_lens is.
@@ -225,9 +226,9 @@ __device__ __forceinline__ int4 range_start(const Problem& p, const long long* c
         off -= __shfl_sync(kFull, upto, k) - ck;
         const int tk = t0 + k;
         const int w = step_cost(p, min(p.tpi, q.n - tk * p.tpi));
-        const int step = max(0, (w == 2 ? ((int)off + 1) >> 1 : (int)off) - 1);
+        const int step = max(0, (w == 2 ? ((int)off + 1) >> 1 : (int)off) - p.over);
         at = make_int4(lo, h, tk, step);
-        if (step * w >= ck - w && step > 0) {                // past the last step: the next item
+        if (step * w >= ck - p.over * w && step > 0) {       // past the last step: the next item
             at.w = 0;
             if (++at.z == items) {
                 at.z = 0;
@@ -264,7 +265,7 @@ __device__ __forceinline__ void plan_ranges(const Problem& p, long long* cost, i
             c = 0;
             for (int t = 0; t < items; ++t) {
                 const int k = item_cost(p, q.n, q.L, t);
-                is_long |= k > 1 + kWholeSteps;
+                is_long |= k > p.over + kWholeSteps;
                 c += k;
             }
         } else {
