@@ -60,7 +60,7 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     p.bound = reinterpret_cast<int4*>(w);
     w += align256((size_t)(dev.sm_count + 1) * sizeof(int4));
     p.part = reinterpret_cast<float*>(w);
-    p.G = dev.sm_count;
+    p.G = std::min(dev.sm_count, kMaxRanges);
     // Two builds. Where a request has few rows of a key head on average, the one whose row tiles
     // have few rows and use all softmax warps (windowed, capped blocks of 32 rows: 228 us, 389 us
     // without; a longer request among them takes more items); the others are spared its code

@@ -116,6 +116,7 @@ constexpr int BM = 128;                 // rows of a row tile: tensor-memory lan
 constexpr int BN = 128;                 // keys of a key tile
 constexpr int kThreads = 512;
 constexpr int kJoinThreads = 256;
+constexpr int kMaxRanges = 1024;
 constexpr int kJoinSlices = 8;          // CTAs that share one cut item's join
 constexpr int kFew = 32;                // rows of a tile that is copied to all quarters
 constexpr int kItems = 4;               // slots of the item ring
@@ -1061,22 +1062,22 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                                    rv_full + 8 * (g % (2 * n)), c->h, row_of(c, j), id);
                         id = id_next;
                     }
-                    continue;
+                } else if constexpr (!kSmall) {
+                    for (int j = 0; j < steps; ++j) {
+                        const int tile = c->begin + c->lo + j;
+                        if (tile >= c->from && tile < c->to) continue;
+                        const uint32_t t = g + j, s = t % kV;
+                        // This warp may be any number of tiles ahead: only once the tile is issued does a
+                        // parity say which use has landed.
+                        if (!__all_sync(kFull, count_past(issued, t))) tries = 0;
+                        wait(v_full + 8 * (t % (2 * kV)), (t / (2 * kV)) & 1);
+                        if (clear_odd<D, kMmaHalf>(smem + L::values + s * L::kTile, lane, c->L - tile * BN))
+                            items[k % kItems].v_odd = 1;
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        mbar_arrive_warp(v_fix + 8 * s);
+                    }
+                    g += max(steps, 0);
                 }
-                for (int j = 0; j < steps && !kSmall; ++j) {
-                    const int tile = c->begin + c->lo + j;
-                    if (tile >= c->from && tile < c->to) continue;
-                    const uint32_t t = g + j, s = t % kV;
-                    // This warp may be any number of tiles ahead: only once the tile is issued does a
-                    // parity say which use has landed.
-                    if (!__all_sync(kFull, count_past(issued, t))) tries = 0;
-                    wait(v_full + 8 * (t % (2 * kV)), (t / (2 * kV)) & 1);
-                    if (clear_odd<D, kMmaHalf>(smem + L::values + s * L::kTile, lane, c->L - tile * BN))
-                        items[k % kItems].v_odd = 1;
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    mbar_arrive_warp(v_fix + 8 * s);
-                }
-                g += max(steps, 0);
             }
             if (!__all_sync(kFull, tries != 0) && lane == 0) atomicOr(status, kStatusTimeout);
             if constexpr (kSpread) {                         // the last loads land
@@ -1554,11 +1555,16 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 //
 // For each range start that cuts an item, and is the first to: out = sum_i w_i O_i / sum_i w_i l_i
 // over the item's pieces, w_i = 2^(m_i - max m). blockIdx.x: the range start - 1; blockIdx.y: a
-// slice of the item's rows and columns.
+// slice of the item's rows and columns. Bound by latency, so pieces are found by all threads at
+// once, `ways` threads share an element's pieces, and each loads four at a time (one token over
+// 6775 keys, 53 pieces: a call of 86 us with one thread walking them, 27 us so).
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Problem p, bool half_type) {
+    __shared__ int slot[kMaxRanges + 1];                     // each piece's place, -1: no steps
+    __shared__ float2 sum_ml[kJoinThreads];
+    __shared__ float4 sum_o[kJoinThreads];
     grid_dependency_wait();
-    const int b = blockIdx.x + 1;
+    const int b = blockIdx.x + 1, tid = threadIdx.x;
     const int4 at = p.bound[b], before = p.bound[b - 1];
     if (at.x >= p.R || at.w == 0) return;
     if (before.x == at.x && before.y == at.y && before.z == at.z && before.w > 0) return;
@@ -1567,44 +1573,76 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
     int begin, end;
     key_tiles(p, q.n, q.L, tok0, ntok, begin, end);
     const int steps = end - begin;
-    // The ranges whose pieces follow the first one's (range b - 1, from step 0).
-    int last = b;
-    for (; last + 1 <= p.G; ++last) {
-        const int4 n = p.bound[last + 1];
-        if (!(n.x == at.x && n.y == at.y && n.z == at.z)) break;
+    // The item's pieces: range b - 1 from step 0, and the ranges that start in it.
+    int pieces = 1;
+    for (int m0 = b; m0 <= p.G; m0 += kJoinThreads) {
+        const int m = m0 + tid;
+        const int4 x = p.bound[min(m, p.G)];
+        const int4 next = p.bound[min(m + 1, p.G)];
+        const bool in = m <= p.G && x.x == at.x && x.y == at.y && x.z == at.z;
+        const bool ends = !(m < p.G && next.x == at.x && next.y == at.y && next.z == at.z);
+        if (in) slot[m - b + 1] = x.w < (ends ? steps : next.w) ? 2 * m : -1;
+        pieces += __syncthreads_count(in);
     }
-    auto piece = [&](int m) -> const float* {                // null: no steps
-        if (m < b) return p.part + (size_t)(2 * m + 1) * part_floats(D);
-        const int lo = p.bound[m].w, hi = m == last ? steps : p.bound[m + 1].w;
-        return lo < hi ? p.part + (size_t)(2 * m) * part_floats(D) : nullptr;
-    };
+    if (tid == 0) slot[0] = 2 * (b - 1) + 1;
+    __syncthreads();
+    const int ways = pieces >= 32 ? 8 : (pieces >= 8 ? 4 : (pieces >= 4 ? 2 : 1));
+    const int per = kJoinThreads / ways, way = tid / per;
     const int rows = ntok * p.g;                             // of both row tiles
-    const int in_tile = p.tpt * p.g;
-    for (int e = blockIdx.y * kJoinThreads + threadIdx.x; e < rows * (D / 4);
-         e += kJoinSlices * kJoinThreads) {
+    const int in_tile = p.tpt * p.g, total = rows * (D / 4);
+    for (int e0 = blockIdx.y * per; e0 < total; e0 += kJoinSlices * per) {
+        const int e = min(e0 + tid % per, total - 1);
         const int col = e / rows, row = e - col * rows;
         const int sub = row >= in_tile ? 1 : 0, r = row - sub * in_tile;
-        const size_t tile_at = (size_t)sub * BM * (D + 2);
-        float top = -INFINITY;
-        for (int m = b - 1; m <= last; ++m) {
-            const float* o_ml = piece(m);
-            if (o_ml) top = fmaxf(top, reinterpret_cast<const float2*>(o_ml + tile_at + BM * D)[r].x);
-        }
-        const float ref = top == -INFINITY ? 0.f : top;
-        float l = 0.f;
+        const float* tile = p.part + (size_t)sub * BM * (D + 2);
+        float top = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int m = b - 1; m <= last; ++m) {
-            const float* o_ml = piece(m);
-            if (!o_ml) continue;
-            const float2 s = reinterpret_cast<const float2*>(o_ml + tile_at + BM * D)[r];
-            const float4 x = reinterpret_cast<const float4*>(o_ml + tile_at)[col * BM + r];
+        auto add = [&](float2 s, float4 x, float ref) {
             const float wt = ex2(s.x - ref);
             l = fmaf(s.y, wt, l);
             o.x = fmaf(x.x, wt, o.x);
             o.y = fmaf(x.y, wt, o.y);
             o.z = fmaf(x.z, wt, o.z);
             o.w = fmaf(x.w, wt, o.w);
+        };
+        auto follow = [&](float most) -> float {             // the reference from here on
+            const float ref = most == -INFINITY ? 0.f : most, by = ex2(top - ref);
+            top = most;
+            l *= by;
+            o = make_float4(o.x * by, o.y * by, o.z * by, o.w * by);
+            return ref;
+        };
+        for (int i = way; i < pieces; i += 4 * ways) {
+            float2 s[4];
+            float4 x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int at_slot = i + u * ways < pieces ? slot[i + u * ways] : -1;
+                s[u] = make_float2(-INFINITY, 0.f);
+                x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (at_slot >= 0) {
+                    const float* o_ml = tile + (size_t)at_slot * part_floats(D);
+                    s[u] = reinterpret_cast<const float2*>(o_ml + BM * D)[r];
+                    x[u] = reinterpret_cast<const float4*>(o_ml)[col * BM + r];
+                }
+            }
+            const float ref = follow(fmaxf(top, fmaxf(fmaxf(s[0].x, s[1].x), fmaxf(s[2].x, s[3].x))));
+#pragma unroll
+            for (int u = 0; u < 4; ++u) add(s[u], x[u], ref);
         }
+        if (ways > 1) {
+            sum_ml[tid] = make_float2(top, l);
+            sum_o[tid] = o;
+            __syncthreads();
+            if (way == 0) {
+                for (int y = 1; y < ways; ++y) {
+                    const float2 s = sum_ml[tid + y * per];
+                    add(s, sum_o[tid + y * per], follow(fmaxf(top, s.x)));
+                }
+            }
+            __syncthreads();
+        }
+        if (way > 0 || e0 + tid >= total) continue;
         const float norm = l == 0.f ? 0.f : p.v_scale / l;
         const long long out_row = ((long long)q.t0 + tok0 + row / p.g) * p.q_heads + at.y * p.g +
                                   row % p.g;
@@ -1612,7 +1650,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             make_uint2(pack16(half_type, o.x * norm, o.y * norm),
                        pack16(half_type, o.z * norm, o.w * norm));
         if (col == 0 && p.lse)
-            p.lse[out_row] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
+            p.lse[out_row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
     }
 }
 
