@@ -68,12 +68,12 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     const bool few = p.g <= kFew && (long long)a.T * p.g <= (long long)kFew * a.R;
     p.tpt = (few ? kFew : BM) / p.g;
     p.tpi = few ? p.tpt : 2 * p.tpt;
-    // What an item costs besides its steps: more steps' worth where a step is short, that is with few
-    // rows, and above all with 32 KB or less of keys and values a step. Microseconds at 1 / 2 / 3:
-    // windowed blocks of D = 64 231 / 213 / 199, single tokens from an 8-bit cache 187 / 172 / 159,
-    // 16-bit ones of D = 128 over 100 to 5000 356 / 346 / 356.
+    // What an item costs besides its steps, in steps: more where a step is short, which it is with few
+    // rows and 32 KB or less of keys and values. Microseconds at 1 / 2 / 3: windowed blocks of
+    // D = 64 231 / 213 / 199, single tokens from an 8-bit cache 187 / 172 / 159; 16-bit ones of
+    // D = 128 over 100 to 5000 356 / 346 / 356, a 16001-token prompt 806 / 781 / 783.
     const long long step_bytes = 2LL * BN * D * (c.dtype == kE4m3 ? 1 : 2);
-    p.over = !few ? 1 : (step_bytes > 32768 ? 2 : 3);
+    p.over = few && step_bytes <= 32768 ? 3 : 2;
     // Nothing is cut, and no join is launched, where the table's width and the number of tokens alone
     // say that plan_ranges will take whole items (about 2 us of a short call).
     const long long steps = ((long long)a.max_pages * c.page_size + BN - 1) / BN;
