@@ -62,9 +62,9 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     p.part = reinterpret_cast<float*>(w);
     p.G = std::min(dev.sm_count, kMaxRanges);
     // Two builds. Where a request has few rows of a key head on average, the one whose row tiles
-    // have few rows and use all softmax warps (windowed, capped blocks of 32 rows: 228 us, 389 us
+    // have few rows and use all softmax warps (windowed, capped blocks of 32 rows: 199 us, 389 us
     // without; a longer request among them takes more items); the others are spared its code
-    // (16001-token prompt: 820 us, 890 us with both).
+    // (16001-token prompt: 806 us, 890 us with both).
     const bool few = p.g <= kFew && (long long)a.T * p.g <= (long long)kFew * a.R;
     p.tpt = (few ? kFew : BM) / p.g;
     p.tpi = few ? p.tpt : 2 * p.tpt;

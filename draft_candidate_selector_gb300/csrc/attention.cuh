@@ -45,10 +45,10 @@
 // While one half's softmax runs, the tensor cores work for the other half.
 //
 // What bounds it. Single tokens and small blocks read each cached key and value once: 96 single
-// tokens over 500 to 16000 (16-bit, 8 key heads of 128) take 288 us, 6.2 TB/s. From an 8-bit cache
+// tokens over 500 to 16000 (16-bit, 8 key heads of 128) take 285 us, 6.2 TB/s. From an 8-bit cache
 // it is shared memory: per value a byte lands, is read, is written as two and read by the MMA (128
-// tokens over 200 to 20000: 183 us, 3.1 TB/s). Long prompts are bound by the tensor cores and the
-// softmax between two products (16001 tokens, 16 heads of 128, causal: 820 us, 1.28 PFLOP/s). A
+// tokens over 200 to 20000: 156 us, 3.7 TB/s). Long prompts are bound by the tensor cores and the
+// softmax between two products (16001 tokens, 16 heads of 128, causal: 806 us, 1.3 PFLOP/s). A
 // call's plan, launch and first loads take some 20 us (one token over 332, with the join skipped).
 //
 // Rounding. P is rounded to the type of V (fp16 over an 8-bit cache), since one MMA's operands have
