@@ -187,8 +187,9 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(BlockTableA
 // A thread moves 8 elements of a key or value row at a time: 16 bytes in, 16 or 8 out. The threads of
 // a block lie along a token's vectors and over tokens, so that a thread keeps its head and vector
 // and finds a token's place in the cache once for several, with all of their loads in flight. The
-// rows are streamed once; bound by HBM: 40001 tokens of 8 heads of 128 from bf16 to e4m3 take 53 us,
-// 4.6 TB/s (90 us with one token in flight).
+// rows are streamed once; bound by HBM: 40001 tokens of 8 heads of 128 from bf16 to e4m3 take 43 us,
+// 5.7 TB/s (with 256 threads a block, one vector of a token's 256 each, 53 us; 90 us with one token
+// in flight besides).
 
 template <typename T>
 __device__ __forceinline__ float to_float(T x);
@@ -228,7 +229,7 @@ struct StoreArgs {
     KvCache cache;
 };
 
-constexpr int kStoreThreads = 256;
+constexpr int kStoreThreads = 128;
 constexpr int kStoreTokens = 4;    // tokens a thread has in flight
 
 template <typename T, bool kSmall, bool kDivide>
