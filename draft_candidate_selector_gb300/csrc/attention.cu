@@ -79,7 +79,11 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     const long long steps = ((long long)a.max_pages * c.page_size + BN - 1) / BN;
     const long long per_request = ((long long)a.T + p.tpi - 1) / p.tpi;
     const long long items = (a.R + (long long)a.T / p.tpi) * c.kv_heads;
-    p.join = p.G > 1 && ((a.T > p.tpt && !few ? 2 : 1) * (p.over + steps) > p.over + kWholeSteps ||
+    // Single tokens of few requests gain from SMs that have no item of their own (a call in a graph, 8
+    // items of 9 tiles: 14 us cut, 20 us whole); 100 tokens over 500 are joined dearly (32 us, 20 us
+    // whole), and so are items that nearly fill the SMs (128 items of 11 tiles: 31 us, 27 us whole).
+    p.whole = few && 2 * items <= p.G ? 4 : 12;
+    p.join = p.G > 1 && ((a.T > p.tpt && !few ? 2 : 1) * (p.over + steps) > p.over + p.whole ||
                          per_request > kSerialItems || items > p.G);
     return (c.dtype == kE4m3 ? launch_attention_e4m3 : launch_attention_16bit)(dev, a, p, few,
                                                                               status_word, stream);

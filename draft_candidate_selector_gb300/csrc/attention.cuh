@@ -81,6 +81,7 @@ struct AttentionProblem {
     int D, T, q_heads, kv_heads, g;
     int tpt, tpi;                       // tokens per row tile, per item
     int over;                           // an item's fixed cost, in its steps
+    int whole;                          // key tiles up to which items are not worth cutting
     int R, max_pages, num_pages, page_size;
     int left, right;
     float softcap, scale, v_scale;      // scale includes the keys' scale
@@ -121,7 +122,6 @@ constexpr int kJoinSlices = 8;          // CTAs that share one cut item's join
 constexpr int kFew = 32;                // rows of a tile that is copied to all quarters
 constexpr int kItems = 4;               // slots of the item ring
 constexpr int kSerialItems = 8;         // items of a request that one thread adds up
-constexpr int kWholeSteps = 8;          // key tiles up to which an item is not worth cutting
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrowth = 8.f;          // log2 growth of a maximum before O is scaled
@@ -266,7 +266,7 @@ __device__ __forceinline__ void plan_ranges(const Problem& p, long long* cost, i
             c = 0;
             for (int t = 0; t < items; ++t) {
                 const int k = item_cost(p, q.n, q.L, t);
-                is_long |= k > p.over + kWholeSteps;
+                is_long |= k > p.over + p.whole;
                 c += k;
             }
         } else {
