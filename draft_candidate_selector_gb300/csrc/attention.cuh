@@ -1442,18 +1442,20 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 f0 = finish();
             } else {
                 // One row tile: half 1 passes (m, l) over, half 0 returns the factors of both
-                // halves' O, and each half writes half of the columns.
+                // halves' O, and each half writes half of the columns. A half 1 without a tile has
+                // nothing to pass, and must not: it has not waited for the scores, which follow half
+                // 0's factors in ml, so its write could land on either side of theirs.
                 has0 = steps > 0;
                 has1 = steps > 1;
                 if (w == 1) {
-                    ml[row] = make_float2(m, l);
+                    if (has1) ml[row] = make_float2(m, l);
                     mbar_arrive_warp(ml_there);
                     wait(ml_back, nb & 1);
                     f0 = ml[row].x;
                     f1 = ml[row].y;
                 } else {
                     wait(ml_there, nb & 1);
-                    const float2 other = ml[row];
+                    const float2 other = has1 ? ml[row] : make_float2(-INFINITY, 0.f);
                     const float top = fmaxf(m, other.x);
                     const float at = top == -INFINITY ? 0.f : top;
                     f0 = ex2(m - at);
