@@ -3,7 +3,10 @@
 This is the Python binding of libdflash_gb300.so, whose C ABI is in include/dflash.h.
 The functions here marshal torch CUDA tensors into pointers and sizes and allocate any
 outputs the caller did not pass. Every step of the method runs in the library's
-sm_103a kernels, on the current CUDA stream of the tensors' device.
+sm_103a kernels, on the current CUDA stream of the tensors' device or on the stream passed
+as `stream`. What a call allocates belongs to the stream it runs on. To order that stream
+behind the work that makes the inputs, and to keep the inputs until it has read them, is the
+caller's part.
 
 Method (page "vllm.models.beam.nvidia.dflash2"): for request r and step p,
   1. cand_ids, unary = top-K of logits[r, p]        (compute_candidates)
@@ -80,11 +83,32 @@ def dflash_selector_lmhead_workspace_bytes(R: int, S: int, V: int, K: int) -> in
     return int(_native.load().dflash_selector_lmhead_workspace_bytes(R, S, V, K))
 
 
-def _workspace(nbytes: int, dev: torch.device, workspace: torch.Tensor | None) -> torch.Tensor:
+def _empty(shape: tuple, dtype: torch.dtype, dev: torch.device, stream,
+           handed_out: bool = True) -> torch.Tensor:
+    """An output (or, not handed_out, a workspace) of a call on `stream`, None being the current one.
+
+    It comes from the memory of that stream: the allocator takes it back when its last reference
+    goes, and must not give it to work that runs beside the call's kernels, nor take it from work
+    that still runs on the current stream. What is handed out is kept from that stream, too, until
+    the work that the current stream has been given by then is done.
+    """
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    if handed_out:
+        t.record_stream(torch.cuda.current_stream(dev))
+    return t
+
+
+def _workspace(nbytes: int, dev: torch.device, workspace: torch.Tensor | None,
+               stream) -> torch.Tensor:
     if nbytes <= 0:
         _native.check(_native.DFLASH_INVALID_ARGUMENT)
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        workspace = _empty((nbytes,), torch.uint8, dev, stream, handed_out=False)
     return workspace
 
 
@@ -105,12 +129,12 @@ def dflash_topk_candidates(logits: torch.Tensor, K: int, cand_ids: torch.Tensor 
     dev = logits.device
     with torch.cuda.device(dev):
         if cand_ids is None:
-            cand_ids = torch.empty((R, S, K), dtype=torch.int32, device=dev)
+            cand_ids = _empty((R, S, K), torch.int32, dev, stream)
         if unary is None:
-            unary = torch.empty((R, S, K), dtype=torch.float32, device=dev)
+            unary = _empty((R, S, K), torch.float32, dev, stream)
         _need(cand_ids, "cand_ids", torch.int32, (R, S, K))
         _need(unary, "unary", torch.float32, (R, S, K))
-        ws = _workspace(lib.dflash_topk_workspace_bytes(R, S, V, K), dev, workspace)
+        ws = _workspace(lib.dflash_topk_workspace_bytes(R, S, V, K), dev, workspace, stream)
         _native.check(lib.dflash_topk_candidates(
             _ptr(logits), R, S, V, K, float(softcap), float(scale), _ptr(cand_ids), _ptr(unary),
             _ptr(ws), ws.numel(), _stream(dev, stream)))
@@ -132,12 +156,12 @@ def dflash_lmhead_topk(hidden: torch.Tensor, lm_head: torch.Tensor, K: int,
     dev = hidden.device
     with torch.cuda.device(dev):
         if cand_ids is None:
-            cand_ids = torch.empty((R, S, K), dtype=torch.int32, device=dev)
+            cand_ids = _empty((R, S, K), torch.int32, dev, stream)
         if unary is None:
-            unary = torch.empty((R, S, K), dtype=torch.float32, device=dev)
+            unary = _empty((R, S, K), torch.float32, dev, stream)
         _need(cand_ids, "cand_ids", torch.int32, (R, S, K))
         _need(unary, "unary", torch.float32, (R, S, K))
-        ws = _workspace(lib.dflash_lmhead_topk_workspace_bytes(R, S, V, K), dev, workspace)
+        ws = _workspace(lib.dflash_lmhead_topk_workspace_bytes(R, S, V, K), dev, workspace, stream)
         _native.check(lib.dflash_lmhead_topk(
             _ptr(hidden), _ptr(lm_head), R, S, H, V, K, float(softcap), float(scale),
             _ptr(cand_ids), _ptr(unary), _ptr(ws), ws.numel(), _stream(dev, stream)))
@@ -157,7 +181,7 @@ def dflash_hidden_projection(hidden: torch.Tensor, w_proj: torch.Tensor,
     dev = hidden.device
     with torch.cuda.device(dev):
         if h_out is None:
-            h_out = torch.empty((R, S, rank), dtype=torch.bfloat16, device=dev)
+            h_out = _empty((R, S, rank), torch.bfloat16, dev, stream)
         _need(h_out, "h_out", torch.bfloat16, (R, S, rank))
         _native.check(lib.dflash_hidden_projection(
             _ptr(hidden), _ptr(w_proj), R, S, H, rank, _ptr(h_out), _stream(dev, stream)))
@@ -183,7 +207,7 @@ def dflash_candidate_edges(pred_cb: torch.Tensor, succ_cb: torch.Tensor,
     dev = cand_ids.device
     with torch.cuda.device(dev):
         if edges is None:
-            edges = torch.empty((R, S, K, K), dtype=torch.float32, device=dev)
+            edges = _empty((R, S, K, K), torch.float32, dev, stream)
         _need(edges, "edges", torch.float32, (R, S, K, K))
         _native.check(lib.dflash_candidate_edges(
             _ptr(pred_cb), _ptr(succ_cb), _ptr(cand_ids), _ptr(unary), _ptr(h), _ptr(anchors),
@@ -216,18 +240,18 @@ def dflash_selector(logits: torch.Tensor, hidden: torch.Tensor, w_proj: torch.Te
     dev = logits.device
     with torch.cuda.device(dev):
         if cand_ids is None:
-            cand_ids = torch.empty((R, S, K), dtype=torch.int32, device=dev)
+            cand_ids = _empty((R, S, K), torch.int32, dev, stream)
         if unary is None:
-            unary = torch.empty((R, S, K), dtype=torch.float32, device=dev)
+            unary = _empty((R, S, K), torch.float32, dev, stream)
         if h_out is None:
-            h_out = torch.empty((R, S, rank), dtype=torch.bfloat16, device=dev)
+            h_out = _empty((R, S, rank), torch.bfloat16, dev, stream)
         if edges is None:
-            edges = torch.empty((R, S, K, K), dtype=torch.float32, device=dev)
+            edges = _empty((R, S, K, K), torch.float32, dev, stream)
         _need(cand_ids, "cand_ids", torch.int32, (R, S, K))
         _need(unary, "unary", torch.float32, (R, S, K))
         _need(h_out, "h_out", torch.bfloat16, (R, S, rank))
         _need(edges, "edges", torch.float32, (R, S, K, K))
-        ws = _workspace(lib.dflash_selector_workspace_bytes(R, S, V, K), dev, workspace)
+        ws = _workspace(lib.dflash_selector_workspace_bytes(R, S, V, K), dev, workspace, stream)
         _native.check(lib.dflash_selector(
             _ptr(logits), _ptr(hidden), _ptr(w_proj), _ptr(pred_cb), _ptr(succ_cb),
             _ptr(anchors), R, S, K, V, H, rank, float(softcap), float(scale), _ptr(cand_ids),
@@ -261,9 +285,9 @@ def dflash_selector_forward(cand_ids: torch.Tensor, unary: torch.Tensor, hidden:
     dev = hidden.device
     with torch.cuda.device(dev):
         if h_out is None:
-            h_out = torch.empty((R, S, rank), dtype=torch.bfloat16, device=dev)
+            h_out = _empty((R, S, rank), torch.bfloat16, dev, stream)
         if edges is None:
-            edges = torch.empty((R, S, K, K), dtype=torch.float32, device=dev)
+            edges = _empty((R, S, K, K), torch.float32, dev, stream)
         _need(h_out, "h_out", torch.bfloat16, (R, S, rank))
         _need(edges, "edges", torch.float32, (R, S, K, K))
         _native.check(lib.dflash_selector_forward(
@@ -299,18 +323,18 @@ def dflash_selector_lmhead(hidden: torch.Tensor, lm_head: torch.Tensor, w_proj: 
     dev = hidden.device
     with torch.cuda.device(dev):
         if cand_ids is None:
-            cand_ids = torch.empty((R, S, K), dtype=torch.int32, device=dev)
+            cand_ids = _empty((R, S, K), torch.int32, dev, stream)
         if unary is None:
-            unary = torch.empty((R, S, K), dtype=torch.float32, device=dev)
+            unary = _empty((R, S, K), torch.float32, dev, stream)
         if h_out is None:
-            h_out = torch.empty((R, S, rank), dtype=torch.bfloat16, device=dev)
+            h_out = _empty((R, S, rank), torch.bfloat16, dev, stream)
         if edges is None:
-            edges = torch.empty((R, S, K, K), dtype=torch.float32, device=dev)
+            edges = _empty((R, S, K, K), torch.float32, dev, stream)
         _need(cand_ids, "cand_ids", torch.int32, (R, S, K))
         _need(unary, "unary", torch.float32, (R, S, K))
         _need(h_out, "h_out", torch.bfloat16, (R, S, rank))
         _need(edges, "edges", torch.float32, (R, S, K, K))
-        ws = _workspace(lib.dflash_selector_lmhead_workspace_bytes(R, S, V, K), dev, workspace)
+        ws = _workspace(lib.dflash_selector_lmhead_workspace_bytes(R, S, V, K), dev, workspace, stream)
         _native.check(lib.dflash_selector_lmhead(
             _ptr(hidden), _ptr(lm_head), _ptr(w_proj), _ptr(pred_cb), _ptr(succ_cb),
             _ptr(anchors), R, S, K, V, H, rank, float(softcap), float(scale), _ptr(cand_ids),
@@ -332,11 +356,11 @@ def dflash_best_path(edges: torch.Tensor, cand_ids: torch.Tensor, path: torch.Te
     dev = edges.device
     with torch.cuda.device(dev):
         if path is None:
-            path = torch.empty((R, S), dtype=torch.int32, device=dev)
+            path = _empty((R, S), torch.int32, dev, stream)
         if tokens is None:
-            tokens = torch.empty((R, S), dtype=torch.int32, device=dev)
+            tokens = _empty((R, S), torch.int32, dev, stream)
         if score is None:
-            score = torch.empty((R,), dtype=torch.float32, device=dev)
+            score = _empty((R,), torch.float32, dev, stream)
         _need(path, "path", torch.int32, (R, S))
         _need(tokens, "tokens", torch.int32, (R, S))
         _need(score, "score", torch.float32, (R,))
@@ -405,17 +429,17 @@ def dflash_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor,
     given = (query_start, kv_lens, held_out, positions, pages_needed)
     names = ("query_start", "kv_lens", "held_out", "positions", "pages_needed")
     if given == (None, None, None, None, None):
-        room = torch.empty((3 * R + T + 2,), dtype=i32, device=dev)
+        room = _empty((3 * R + T + 2,), i32, dev, stream)
         out = room.split_with_sizes(sizes)
         at = room.data_ptr()
         ptrs = (at, at + 4 * (R + 1), at + 4 * (2 * R + 1), at + 4 * (3 * R + 1),
                 at + 4 * (3 * R + 1 + T))
     else:
-        out = tuple(torch.empty((n,), dtype=i32, device=dev) if t is None else t
+        out = tuple(_empty((n,), i32, dev, stream) if t is None else t
                     for t, n in zip(given, sizes))
         ptrs = tuple(_checked(t, name, i32, (n,)) for t, name, n in zip(out, names, sizes))
     if slots is None:
-        slots = torch.empty((T,), dtype=torch.int64, device=dev)
+        slots = _empty((T,), torch.int64, dev, stream)
         slots_at = slots.data_ptr()
     else:
         slots_at = _checked(slots, "slots", torch.int64, (T,))
@@ -539,17 +563,18 @@ def dflash_paged_attention(query: torch.Tensor, key_cache: torch.Tensor,
     kv = _checked(kv_lens, "kv_lens", torch.int32, (R,))
     dev = query.device
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=query.dtype, device=dev)
+        out = _empty((T, Hq, D), query.dtype, dev, stream)
         out_at = out.data_ptr()
     else:
         out_at = _checked(out, "out", query.dtype, (T, Hq, D))
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = _empty((T, Hq), torch.float32, dev, stream)
         lse_at = lse.data_ptr()
     else:
         lse_at = _checked(lse, "lse", torch.float32, (T, Hq))
     if workspace is None:
-        workspace = torch.empty(_attention_workspace(dev, D), dtype=torch.uint8, device=dev)
+        workspace = _empty((_attention_workspace(dev, D),), torch.uint8, dev, stream,
+                           handed_out=False)
     _launch(lib.dflash_paged_attention, dev, stream, query.data_ptr(), code, T, Hq, qs[0], qs[1],
             cache, table, R, max_pages, start, kv, D ** -0.5 if scale is None else scale,
             window_left, window_right, softcap, out_at, lse_at, workspace.data_ptr(),
