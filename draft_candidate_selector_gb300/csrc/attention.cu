@@ -44,7 +44,9 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     while ((1 << p.page_shift) < c.page_size) ++p.page_shift;
     p.left = a.window_left;
     p.right = a.window_right;
-    p.softcap = a.softcap;
+    // Beyond 2^64 a cap changes no score that fp32 tells from its neighbours, below 2^-64 it makes all
+    // of them 0; between, nothing in the cap's arithmetic overflows.
+    p.softcap = a.softcap > 0.f ? std::min(std::max(a.softcap, 0x1p-64f), 0x1p64f) : 0.f;
     p.scale = a.scale * c.k_scale;
     p.v_scale = c.v_scale;
     p.block_table = a.block_table;

@@ -615,8 +615,37 @@ __device__ __forceinline__ uint32_t below(int n) {
 }
 
 // cap tanh(s / cap) = cap - 2 cap / (1 + e^(2 s / cap)), in log2 units; in = 2 log2(e) scale / cap.
+// Two nearly equal numbers meet in it where s is small beside the cap, so it is off by up to 2^-21
+// cap: taken for caps up to kQuickCap, where that is 3e-5, less than an fp32 dot product is sure of.
+constexpr float kQuickCap = 64.f;
 __device__ __forceinline__ uint32_t capped(uint32_t s, float in, float cap) {
     return __float_as_uint(fmaf(rcp(1.f + ex2(__uint_as_float(s) * in)), -2.f * cap, cap));
+}
+
+// The same for any cap, to 2^-19 of the result: below s / cap = 1/4 by tanh's series, whose next term
+// is 2^-26 of it there. With y = s in, tanh's argument is y ln 2 / 2, and half the cap times y is
+// the uncapped score.
+__device__ __forceinline__ uint32_t capped_wide(uint32_t s, float in, float cap) {
+    const float y = __uint_as_float(s) * in, x = y * (0.5f * kLn2), x2 = x * x;
+    float t = fmaf(x2, 62.f / 2835.f, -17.f / 315.f);
+    t = fmaf(x2, t, 2.f / 15.f);
+    t = fmaf(x2, t, -1.f / 3.f);
+    t = fmaf(x2, t, 1.f);
+    const float low = y * (0.5f * kLn2 * cap) * t;
+    const float high = fmaf(rcp(1.f + ex2(y)), -2.f * cap, cap);
+    return __float_as_uint(fabsf(x) < 0.25f ? low : high);
+}
+
+// `n` scores through the cap. (One branch for all: caps that models have take the quick form.)
+template <int n>
+__device__ __forceinline__ void cap_scores(uint32_t (&v)[n], float in, float cap) {
+    if (cap <= kQuickCap * kLog2e) {
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = capped(v[i], in, cap);
+    } else {
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = capped_wide(v[i], in, cap);
+    }
 }
 
 // 16 columns of this thread's lane times `by`.
@@ -1219,10 +1248,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     tmem_ld_wait_x32(v);
                     tc_fence_before();
                     mbar_arrive_warp(s_read + 8 * w);
-                    if constexpr (kCap) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = capped(v[i], cap_in, cap);
-                    }
+                    if constexpr (kCap) cap_scores(v, cap_in, cap);
                     if (j < from || j >= to) {
                         const int k0 = (first + j) * BN + 32 * quarter;
                         const uint32_t seen = below(row_hi - k0) & ~below(row_lo - k0);
@@ -1314,10 +1340,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         // every tile takes stay short.
                         const int k0 = (first + j) * BN;
                         auto prepare = [&](uint32_t (&v)[32], int c0) {
-                            if constexpr (kCap) {
-#pragma unroll
-                                for (int i = 0; i < 32; ++i) v[i] = capped(v[i], cap_in, cap);
-                            }
+                            if constexpr (kCap) cap_scores(v, cap_in, cap);
                             if (masked) {
                                 const uint32_t seen =
                                     below(row_hi - k0 - c0) & ~below(row_lo - k0 - c0);

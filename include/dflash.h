@@ -421,10 +421,11 @@ dflash_status dflash_store_kv(const void* key, const void* value, int dtype, con
  *   out = sum_j exp(s_j) v_j / sum_j exp(s_j),   lse = log sum_j exp(s_j)  (natural).
  * A token that sees no key gets zeros and lse = -inf. What the cache holds at keys that a
  * token does not see has no effect on it, infinities and NaN included. Scores, maxima and sums
- * are fp32; the products exp(s_j) v_j take exp(s_j) relative to a running maximum, rounded to
- * the query's type (to fp16 over an e4m3 cache), and are summed in fp32. Over an e4m3 cache bf16
- * queries are taken as fp16 times a power of two for each row: what that loses is less than 2^-39
- * of the row's largest value.
+ * are fp32. The cap adds at most 2^-19 of a score, or 2^-21 softcap where softcap <= 64, to a score's
+ * rounding; a softcap outside [2^-64, 2^64] counts as the nearer end. The products exp(s_j) v_j
+ * take exp(s_j) relative to a running maximum, rounded to the query's type (to fp16 over an e4m3
+ * cache), and are summed in fp32. Over an e4m3 cache bf16 queries are taken as fp16 times a power
+ * of two for each row: what that loses is less than 2^-39 of the row's largest value.
  * Page ids outside the pool are never followed: the request's outputs are NaN and the status
  * word records DFLASH_DEVICE_BAD_ID. A request whose kv_lens does not fit max_pages, or
  * whose query_start is out of order or past T, is refused with DFLASH_DEVICE_BAD_LENGTH: its

@@ -71,3 +71,62 @@ def test_scores_far_below_zero(dev, dtype, cache, D, loud):
     assert want[1].max() < -90
     for _ in range(5):
         paged.assert_attention(attend(b), want)
+
+
+def reference(b, left=-1, right=0, softcap=0.0, quick=0.0, step=0.0):
+    """fp64 (out, lse) and bounds, with the unit roundoffs of paged.attention, but a score bound that
+    is relative: a score's fp32 sum of D products is off by at most (D + 8) 2^-23 sum|q k| scale,
+    which the cap (of slope 1 at most) does not enlarge; the cap itself adds 2^-19 of the capped
+    score and `quick`, and rounding 2^-22 of it. `step`: half the smallest step of a weight, of the
+    largest."""
+    u = 2.0 ** -8 if b.dtype == BF else 2.0 ** -11
+    g = b.Hq // b.Hkv
+    out = torch.zeros((b.T, b.Hq, b.D), dtype=torch.float64)
+    lse = torch.zeros((b.T, b.Hq), dtype=torch.float64)
+    tol, tol_lse = torch.zeros_like(out), torch.zeros_like(lse)
+    t0 = 0
+    for r in range(len(b.ctx)):
+        n, L = int(b.new[r]), int(b.kv[r])
+        kr, vr = b.k[r].double() * b.k_scale, b.v[r].double() * b.v_scale
+        pos, j = torch.arange(L - n, L)[:, None], torch.arange(L)[None, :]
+        see = torch.ones((n, L), dtype=torch.bool)
+        if right >= 0:
+            see &= j <= pos + right
+        if left >= 0:
+            see &= j >= pos - left
+        for h in range(b.Hq):
+            q, k, v = b.qkv[t0:t0 + n, h].double(), kr[:, h // g], vr[:, h // g]
+            s = q @ k.T * b.D ** -0.5
+            ds_ = (b.D + 8) * 2.0 ** -23 * (q.abs() @ k.abs().T) * b.D ** -0.5
+            if softcap > 0:
+                s = softcap * torch.tanh(s / softcap)
+                ds_ = ds_ + 2.0 ** -19 * s.abs() + quick
+            ds_ = (ds_ + 2.0 ** -22 * s.abs()).masked_fill(~see, 0.0).amax(1, keepdim=True)
+            s = s.masked_fill(~see, -torch.inf)
+            m = s.amax(1, keepdim=True)
+            p = torch.exp(s - m)
+            tot = p.sum(1, keepdim=True)
+            o, A = p @ v / tot, p @ v.abs() / tot
+            sums = (L + 64) * 2.0 ** -22
+            at = slice(t0, t0 + n)
+            out[at, h], lse[at, h] = o, (m + torch.log(tot))[:, 0]
+            tol[at, h] = (u * o.abs() + (u + 2 * ds_ + sums) * A
+                          + step * (see.double() @ v.abs()) / tot + 1e-30)
+            tol_lse[at, h] = ds_[:, 0] + sums + 2.0 ** -22 * lse[at, h].abs()
+        t0 += n
+    return out, lse, tol, tol_lse
+
+
+@pytest.mark.parametrize("softcap", [0.5, 64.0, 65.0, 1e3, 1e4, 1e6, 1e30, 3.4e38])
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("D,few", [(64, True), (128, True), (64, False), (128, False), (80, True)])
+def test_caps_of_any_height(dev, softcap, dtype, cache, D, few):
+    """A cap costs a score no more than its own rounding, or 2^-21 of a cap up to 64: single keys,
+    whose log-sum-exp is the score, and more."""
+    new = [1] * 50 + [2, 1] if few else [40, 17, 33]
+    ctx = [0] * 50 + [3, 300] if few else [0, 5, 290]
+    b = paged.Batch(ctx, new, 4, 2, D, 16, dtype, cache, seed=D, spread=3.0)
+    # fp16 weights have 2^-24 as their smallest step, and are taken of a maximum that is at most 1
+    step = 0.0 if dtype == BF and cache is None else 2.0 ** -25
+    want = reference(b, softcap=softcap, quick=2.0 ** -21 * softcap if softcap <= 64 else 0.0, step=step)
+    paged.assert_attention(attend(b, softcap=softcap), want)
