@@ -41,7 +41,8 @@
 //     back over it. O stays in tensor memory and is scaled there only when the row's maximum has
 //     grown by more than 2^8 since it was last scaled; until then P is taken relative to the old
 //     maximum, which changes nothing but the common factor of P, l and O. With few rows it is scaled
-//     whenever the maximum has grown: the largest weight is 1 then, which no rounding changes.
+//     whenever the maximum has grown: the largest weight is a power of two then, which no rounding
+//     changes.
 // While one half's softmax runs, the tensor cores work for the other half.
 //
 // What bounds it. Single tokens and small blocks read each cached key and value once: 96 single
@@ -53,7 +54,7 @@
 //
 // Rounding. P is rounded to the type of V (fp16 over an 8-bit cache), since one MMA's operands have
 // one type; S, m, l and O are fp32. Where many keys weigh alike that adds as much error as the
-// rounding of the output does; where few keys do, a largest weight of exactly 1 keeps it smaller
+// rounding of the output does; where few keys do, a largest weight that is exact keeps it smaller
 // (two single tokens over 142 to 428, bf16: 1.3 times the output's rounding, 1.5 with the maximum
 // left behind; 1% of the time).
 //
@@ -126,6 +127,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kGrowth = 8.f;          // log2 growth of a maximum before O is scaled
 
+// fp16 weights are taken times 2^lift: the largest is then 2^14 with few rows, 2^15 at most otherwise
+// (by 2^kGrowth above a maximum left behind), and weights of 2^-38, or 2^-31, of it still count. (At
+// 1, a key 18 above 20000 others would lose them all.) P, l and O have the factor in common; only
+// the log-sum-exp takes it out. bf16 weights have fp32's range and none.
+__host__ __device__ constexpr float weight_lift(bool half_weights, bool few_rows) {
+    return !half_weights ? 0.f : (few_rows ? 14.f : 15.f - kGrowth);
+}
 
 __host__ __device__ inline size_t part_floats(int D) { return 2 * (size_t)BM * (D + 2); }
 
@@ -690,6 +698,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
     constexpr int kChunks = kSmall ? 1 : D / 64;             // boxes across a row
     constexpr uint32_t kK = L::kK, kV = L::kV;
     constexpr bool kSpread = L::kSpread;                     // the softmax warps widen the values
+    constexpr float kLift = weight_lift(kMmaHalf, kFewRows);
     extern __shared__ uint8_t smem_raw[];
     __shared__ int4 range[2];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -1286,8 +1295,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                             for (int d = 0; d < D; d += 16) scale_columns(to_ + d, keep);
                         }
                     }
-                    const float off = m == -INFINITY ? 0.f : m;
-                    const uint64_t unit2 = pair_of(unit, unit), off2 = pair_of(-off, -off);
+                    const float off = m == -INFINITY ? 0.f : kLift - m;
+                    const uint64_t unit2 = pair_of(unit, unit), off2 = pair_of(off, off);
                     uint64_t add[2] = {0, 0};
                     const uint32_t to_p = shared + (quarter >> 1) * L::pKeys + lane * 128;
 #pragma unroll
@@ -1397,8 +1406,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 #pragma unroll 1
                         for (int d = 0; d < D; d += 16) scale_columns(to_ + d, keep);
                     }
-                    const float off = m == -INFINITY ? 0.f : m;
-                    const uint64_t unit2 = pair_of(unit, unit), off2 = pair_of(-off, -off);
+                    const float off = m == -INFINITY ? 0.f : kLift - m;
+                    const uint64_t unit2 = pair_of(unit, unit), off2 = pair_of(off, off);
                     uint64_t add[2] = {0, 0};
                     // The weights of one quarter, from its scores.
                     auto weigh = [&](const uint32_t (&v)[32], int quarter) {
@@ -1553,7 +1562,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     if (!whole)
                         reinterpret_cast<float2*>(part + BM * (D / 4))[row] = make_float2(m, l);
                     else if (p.lse)
-                        p.lse[out_row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                        p.lse[out_row] = l == 0.f ? -INFINITY : (m + (log2f(l) - kLift)) * kLn2;
                 }
             }
             tc_fence_before();
@@ -1584,7 +1593,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
 // once, `ways` threads share an element's pieces, and each loads four at a time (one token over
 // 6775 keys, 53 pieces: a call of 86 us with one thread walking them, 27 us so).
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Problem p, bool half_type) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ Problem p, bool half_type, float lift) {
     __shared__ int slot[kMaxRanges + 1];                     // each piece's place, -1: no steps
     __shared__ float2 sum_ml[kJoinThreads];
     __shared__ float4 sum_o[kJoinThreads];
@@ -1675,7 +1684,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
             make_uint2(pack16(half_type, o.x * norm, o.y * norm),
                        pack16(half_type, o.z * norm, o.w * norm));
         if (col == 0 && p.lse)
-            p.lse[out_row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+            p.lse[out_row] = l == 0.f ? -INFINITY : (top + (log2f(l) - lift)) * kLn2;
     }
 }
 
@@ -1765,7 +1774,7 @@ cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, kHalf);
+    return cudaLaunchKernelEx(&cfg, join_kernel<D>, p, kHalf, weight_lift(kHalf || kSmall, kFewRows));
 }
 
 template <int D, bool kHalf, bool kSmall>

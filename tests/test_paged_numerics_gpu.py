@@ -130,3 +130,31 @@ def test_caps_of_any_height(dev, softcap, dtype, cache, D, few):
     step = 0.0 if dtype == BF and cache is None else 2.0 ** -25
     want = reference(b, softcap=softcap, quick=2.0 ** -21 * softcap if softcap <= 64 else 0.0, step=step)
     paged.assert_attention(attend(b, softcap=softcap), want)
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES[1:])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 40])
+def test_small_weights_keep_their_mass(dev, dtype, cache, D, n):
+    """One key 18 nats above 20000 others, which hold all of the output: weights of 2^-26 in fp16."""
+    b = paged.Batch([20000], [n], 4, 1, D, 64, dtype, cache, seed=2)
+    L = 20000 + n
+    q = torch.zeros((n, 4, D))
+    q[:, :, 0] = D ** 0.5
+    keys, values = torch.zeros((L, 1, D)), torch.ones((L, 1, D))
+    keys[5, 0, 0] = 18.0
+    values[5] = 0.0
+    set_queries(b, q)
+    put(b, 0, keys / b.k_scale, values / b.v_scale)
+    # Equal requests over the same pages, in whole items of one SM each: parts of a long item have
+    # maxima of their own, and only the first would meet the small weights.
+    R = 304 if n == 1 else 152
+    args = (b.query.repeat(R, 1, 1), b.key_cache, b.value_cache, b.block_table.repeat(R, 1),
+            torch.arange(R + 1, dtype=torch.int32, device=dev) * n, b.kv_lens.repeat(R))
+    out, lse = ds.dflash_paged_attention(*args, **b.scales())
+    # Of the largest weight at the least: 2^-39 where it is 2^14 (few rows), 2^-32 where it is 2^7.
+    want = reference(b, step=2.0 ** -39 if n == 1 else 2.0 ** -32)
+    assert want[0].max() < 1e-3
+    for r in range(0, R, 19):
+        paged.assert_attention((out[r * n:(r + 1) * n], lse[r * n:(r + 1) * n]), want, f"copy {r}")
+    assert ds.dflash_device_status(clear=True) == 0
