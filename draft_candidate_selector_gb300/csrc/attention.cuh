@@ -352,7 +352,7 @@ struct __align__(16) Item {
     int lo, hi;          // this CTA's steps
     int from, to;        // key tiles that every row of the item sees all of
     int v_odd;           // a value that is not finite was cleared
-    int bad_page;        // a page id outside the pool was met
+    int bad_page;        // some row sees a key in a page whose id lies outside the pool
     __device__ __forceinline__ bool pair(const Problem& p) const { return ntok > p.tpt; }
     __device__ __forceinline__ bool whole() const { return lo == 0 && hi == steps; }
 };
@@ -523,6 +523,30 @@ __device__ __noinline__ void refill_values(const Problem& p, const Item& c, int 
             }
         }
     }
+}
+
+// An id outside the pool for an item's keys tok .. tok + box - 1: recorded if some row sees one of
+// them.
+__device__ __noinline__ void note_bad_page(const Problem& p, Item& c, int tok, int box,
+                                           uint32_t* status) {
+    const int first = c.L - c.n + c.tok0;
+    if (tok > first_key(p, first) - box && tok < keys_end(p, c.L, first + c.ntok - 1)) {
+        c.bad_page = 1;
+        atomicOr(status, kStatusBadId);
+    }
+}
+
+// Whether a row that sees the keys [row_lo, row_hi) sees one, among this CTA's tiles of the item,
+// in a page whose id lies outside the pool. Taken only by items that have met such a page.
+__device__ __noinline__ bool sees_bad_page(const Problem& p, const Item& c, int row_lo, int row_hi) {
+    const int start = (c.begin + c.lo) * BN;
+    const int a = max(row_lo, start), b = min(row_hi - start, (c.hi - c.lo) * BN) + start;
+    if (a >= b) return false;
+    for (int page = a >> p.page_shift; page <= (b - 1) >> p.page_shift; ++page) {
+        const int id = p.block_table[(long long)c.r * p.max_pages + page];
+        if (id < 0 || id >= p.num_pages) return true;
+    }
+    return false;
 }
 
 // ---------------------------------------------------------------- 8-bit caches
@@ -824,15 +848,15 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
         }
     };
     // This lane's page of an item's tile: -1 behind the last token. Ids outside the pool are not
-    // followed: page 0 takes their place, and the item's result is NaN.
+    // followed: page 0 takes their place, and rows that see a key there become NaN. Where no row
+    // does (a window has left the page, and it may have been given back), nothing is wrong.
     auto page_of = [&](const Item* c, int step) -> int {
         const int box = min(p.page_size, BN);
         const unsigned tok = (unsigned)(c->begin + step) * BN + lane * box;
         if (lane >= BN / box || step >= c->hi || tok >= (unsigned)c->L) return -1;
         int id = p.block_table[(long long)c->r * p.max_pages + (tok >> p.page_shift)];
         if (id < 0 || id >= p.num_pages) {
-            items[k % kItems].bad_page = 1;
-            atomicOr(status, kStatusBadId);
+            note_bad_page(p, items[k % kItems], (int)tok, box, status);
             id = 0;
         }
         return id;
@@ -1458,7 +1482,7 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 warp_live &= quarter == 0;
             }
             const bool whole = c->whole();
-            const bool nan = c->bad || c->bad_page;
+            const bool nan = c->bad || (c->bad_page && sees_bad_page(p, *c, row_lo, row_hi));
             auto finish = [&]() {                            // the factor that ends the quotient
                 if (nan) {
                     m = 0.f;

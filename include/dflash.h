@@ -426,8 +426,9 @@ dflash_status dflash_store_kv(const void* key, const void* value, int dtype, con
  * take exp(s_j) relative to a running maximum, rounded to the query's type (to fp16 over an e4m3
  * cache), and are summed in fp32. Over an e4m3 cache bf16 queries are taken as fp16 times a power
  * of two for each row: what that loses is less than 2^-39 of the row's largest value.
- * Page ids outside the pool are never followed: the request's outputs are NaN and the status
- * word records DFLASH_DEVICE_BAD_ID. A request whose kv_lens does not fit max_pages, or
+ * Page ids outside the pool are never followed: tokens that see a key of such a page get NaN, the
+ * others what they would get without it, and the status word records DFLASH_DEVICE_BAD_ID. Pages of
+ * which no token sees a key (a window may have left them) can have any id. A request whose kv_lens does not fit max_pages, or
  * whose query_start is out of order or past T, is refused with DFLASH_DEVICE_BAD_LENGTH: its
  * rows are NaN or not written. Rows of out at and behind query_start[R] are not written.
  * head_dim is a multiple of 8 up to 256 (16 for e4m3). A result does not depend on what else

@@ -158,3 +158,35 @@ def test_small_weights_keep_their_mass(dev, dtype, cache, D, n):
     for r in range(0, R, 19):
         paged.assert_attention((out[r * n:(r + 1) * n], lse[r * n:(r + 1) * n]), want, f"copy {r}")
     assert ds.dflash_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("D", [64, 128, 80])
+@pytest.mark.parametrize("ctx,new", [(600, 3), (600, 40), (20000, 3), (5000, 300)])
+def test_bad_pages_reach_only_rows_that_see_them(dev, dtype, cache, D, ctx, new):
+    """Pages that a window has left may be taken back (id -1): nothing is recorded and nothing
+    changes. A bad page that some rows see makes NaN of those rows alone."""
+    left = 50
+    b = paged.Batch([ctx, 70], [new, 9], 4, 2, D, 16, dtype, cache, seed=3)
+    kw = dict(window_left=left, window_right=0, **b.scales())
+    want = ds.dflash_paged_attention(*b.args(), **kw)
+    assert ds.dflash_device_status(clear=True) == 0
+    table = b.block_table.clone()
+    hidden = (ctx - left) // 16                      # pages of which no row sees a key
+    b.block_table[0, :hidden] = torch.tensor([-1, 2 ** 31 - 1], dtype=torch.int32,
+                                             device=dev).repeat(hidden)[:hidden]
+    for g, w in zip(ds.dflash_paged_attention(*b.args(), **kw), want):
+        assert torch.equal(g, w)
+    assert ds.dflash_device_status(clear=True) == 0
+    for page in sorted({hidden, hidden + 1, ctx // 16, (ctx + new - 1) // 16}):
+        b.block_table.copy_(table)
+        b.block_table[0, page] = -1
+        got = ds.dflash_paged_attention(*b.args(), **kw)
+        assert ds.dflash_device_status(clear=True) == ds.DEVICE_BAD_ID
+        pos = torch.arange(ctx, ctx + new, device=dev)
+        sees = torch.cat([(pos - left < 16 * page + 16) & (pos >= 16 * page),
+                          torch.zeros(9, dtype=torch.bool, device=dev)])
+        assert sees.any()
+        for g, w in zip(got, want):
+            assert torch.isnan(g[sees]).all()
+            assert torch.equal(g[~sees], w[~sees])
