@@ -668,17 +668,9 @@ __device__ __forceinline__ uint32_t capped_wide(uint32_t s, float in, float cap)
     return __float_as_uint(fabsf(x) < 0.25f ? low : high);
 }
 
-// `n` scores through the cap. (One branch for all: caps that models have take the quick form.)
-template <int n>
-__device__ __forceinline__ void cap_scores(uint32_t (&v)[n], float in, float cap) {
-    if (cap <= kQuickCap * kLog2e) {
-#pragma unroll
-        for (int i = 0; i < n; ++i) v[i] = capped(v[i], in, cap);
-    } else {
-#pragma unroll
-        for (int i = 0; i < n; ++i) v[i] = capped_wide(v[i], in, cap);
-    }
-}
+// Builds without a cap, with one up to kQuickCap, and with any. (A branch between the two forms in
+// one build costs windowed blocks with a cap of 50 8 us of 205.)
+enum : int { kNoCap = 0, kQuick = 1, kWide = 2 };
 
 // 16 columns of this thread's lane times `by`.
 __device__ __forceinline__ void scale_columns(uint32_t taddr, float by) {
@@ -711,7 +703,7 @@ __device__ __forceinline__ void turn_pieces(uint32_t (&piece)[4][4], int lane) {
     }
 }
 
-template <int D, bool kHalf, bool kCap, bool kSmall, bool kFewRows>
+template <int D, bool kHalf, int kCap, bool kSmall, bool kFewRows>
 __global__ void __launch_bounds__(kThreads, 1)
 attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const __grid_constant__ Problem p,
@@ -1281,7 +1273,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                     tmem_ld_wait_x32(v);
                     tc_fence_before();
                     mbar_arrive_warp(s_read + 8 * w);
-                    if constexpr (kCap) cap_scores(v, cap_in, cap);
+                    if constexpr (kCap != kNoCap) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[i] = kCap == kWide ? capped_wide(v[i], cap_in, cap)
+                                                 : capped(v[i], cap_in, cap);
+                    }
                     if (j < from || j >= to) {
                         const int k0 = (first + j) * BN + 32 * quarter;
                         const uint32_t seen = below(row_hi - k0) & ~below(row_lo - k0);
@@ -1373,7 +1370,12 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                         // every tile takes stay short.
                         const int k0 = (first + j) * BN;
                         auto prepare = [&](uint32_t (&v)[32], int c0) {
-                            if constexpr (kCap) cap_scores(v, cap_in, cap);
+                            if constexpr (kCap != kNoCap) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    v[i] = kCap == kWide ? capped_wide(v[i], cap_in, cap)
+                                                         : capped(v[i], cap_in, cap);
+                            }
                             if (masked) {
                                 const uint32_t seen =
                                     below(row_hi - k0 - c0) & ~below(row_lo - k0 - c0);
@@ -1761,7 +1763,7 @@ bool encode_4d(CUtensorMap* map, int dtype, const void* base, const long long (&
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool kHalf, bool kCap, bool kSmall, bool kFewRows>
+template <int D, bool kHalf, int kCap, bool kSmall, bool kFewRows>
 cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a, const Problem& p,
                                    uint32_t* status, cudaStream_t stream) {
     static std::once_flag once[64];
@@ -1804,11 +1806,14 @@ cudaError_t launch_on_tensor_cores(const DeviceInfo& dev, const AttentionArgs& a
 template <int D, bool kHalf, bool kSmall>
 cudaError_t launch_build(const DeviceInfo& dev, const AttentionArgs& a, const Problem& p, bool few,
                          uint32_t* status, cudaStream_t stream) {
-    if (a.softcap > 0.f)
-        return few ? launch_on_tensor_cores<D, kHalf, true, kSmall, true>(dev, a, p, status, stream)
-                   : launch_on_tensor_cores<D, kHalf, true, kSmall, false>(dev, a, p, status, stream);
-    return few ? launch_on_tensor_cores<D, kHalf, false, kSmall, true>(dev, a, p, status, stream)
-               : launch_on_tensor_cores<D, kHalf, false, kSmall, false>(dev, a, p, status, stream);
+    if (p.softcap == 0.f)
+        return few ? launch_on_tensor_cores<D, kHalf, kNoCap, kSmall, true>(dev, a, p, status, stream)
+                   : launch_on_tensor_cores<D, kHalf, kNoCap, kSmall, false>(dev, a, p, status, stream);
+    if (p.softcap <= kQuickCap)
+        return few ? launch_on_tensor_cores<D, kHalf, kQuick, kSmall, true>(dev, a, p, status, stream)
+                   : launch_on_tensor_cores<D, kHalf, kQuick, kSmall, false>(dev, a, p, status, stream);
+    return few ? launch_on_tensor_cores<D, kHalf, kWide, kSmall, true>(dev, a, p, status, stream)
+               : launch_on_tensor_cores<D, kHalf, kWide, kSmall, false>(dev, a, p, status, stream);
 }
 
 template <bool kSmall>
