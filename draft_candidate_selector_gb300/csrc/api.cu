@@ -683,6 +683,8 @@ size_t dflash_paged_attention_workspace_bytes(int R, int T, int q_heads, int kv_
     }
     dflash::DeviceInfo dev;
     if (current_device(&dev, nullptr) != DFLASH_OK) return 0;
+    // The kernel for other head sizes and groups writes its outputs at once.
+    if (!dflash::attention_may_use_tensor_cores(head_dim, q_heads / kv_heads, R)) return 256;
     return dflash::attention_workspace_bytes(dev, head_dim);
 }
 

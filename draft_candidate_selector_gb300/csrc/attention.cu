@@ -14,14 +14,17 @@ size_t attention_workspace_bytes(const DeviceInfo& dev, int D) {
            2 * (size_t)dev.sm_count * part_floats(D) * sizeof(float);
 }
 
+bool attention_may_use_tensor_cores(int head_dim, int g, int R) {
+    return (head_dim == 64 || head_dim == 128) && g <= BM && R <= kMaxTableRequests;
+}
+
 bool attention_on_tensor_cores(const AttentionArgs& a) {
     const KvCache& c = a.cache;
     const auto fits = [](long long stride, long long dim) {   // a tensor map's stride
         return dim == 1 || (stride > 0 && stride < (1LL << 38));
     };
-    const long long g = a.q_heads / c.kv_heads;
-    return (c.head_dim == 64 || c.head_dim == 128) && c.page_size >= 8 &&
-           (c.page_size & (c.page_size - 1)) == 0 && g <= BM && a.R <= kMaxTableRequests &&
+    return attention_may_use_tensor_cores(c.head_dim, a.q_heads / c.kv_heads, a.R) &&
+           c.page_size >= 8 && (c.page_size & (c.page_size - 1)) == 0 &&
            fits(c.token_stride, c.page_size) && fits(c.head_stride, c.kv_heads) &&
            fits(c.page_stride, c.num_pages) && fits(a.q_head_stride, a.q_heads) &&
            fits(a.q_token_stride, a.T);

@@ -203,9 +203,11 @@ struct AttentionArgs {
     float* lse;                      // may be null
 };
 
-// Whether the tensor-core kernel takes these arguments: head_dim 64 or 128, pages of a power of two of 8 or more tokens, at most 128 query heads per key
-// head, strides that a tensor map can hold.
+// Whether the tensor-core kernel takes these arguments: head_dim 64 or 128, pages of a power of two
+// of 8 or more tokens, at most 128 query heads per key head, strides that a tensor map can hold;
+// and whether it can by head_dim, query heads per key head and requests alone.
 bool attention_on_tensor_cores(const AttentionArgs& a);
+bool attention_may_use_tensor_cores(int head_dim, int g, int R);
 size_t attention_workspace_bytes(const DeviceInfo& dev, int head_dim);
 cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void* workspace,
                              uint32_t* status_word, cudaStream_t stream);

@@ -411,8 +411,9 @@ dflash_status dflash_store_kv(const void* key, const void* value, int dtype, con
  *              dflash_block_tables writes them
  * out          [T, q_heads, head_dim] of type dtype, contiguous
  * lse          [T, q_heads] float, contiguous, or NULL
- * workspace    at least dflash_paged_attention_workspace_bytes(...) bytes; its contents on
- *              entry do not matter
+ * workspace    at least dflash_paged_attention_workspace_bytes(...) bytes (a token amount where
+ *              head_dim, q_heads / kv_heads or R rule the tensor cores out); its contents on entry
+ *              do not matter
  *
  * Token i of request r, of its n = query_start[r+1] - query_start[r], has position
  * p = kv_lens[r] - n + i and sees the keys j with max(0, p - window_left) <= j <=
