@@ -1484,9 +1484,8 @@ attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constan
                 warp_live &= quarter == 0;
             }
             const bool whole = c->whole();
-            const bool nan = c->bad || (c->bad_page && sees_bad_page(p, *c, row_lo, row_hi));
             auto finish = [&]() {                            // the factor that ends the quotient
-                if (nan) {
+                if (c->bad || (c->bad_page && sees_bad_page(p, *c, row_lo, row_hi))) {
                     m = 0.f;
                     l = NAN;
                 }
