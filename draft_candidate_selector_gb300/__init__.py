@@ -480,8 +480,11 @@ def _kv_cache(key_cache: torch.Tensor, value_cache: torch.Tensor, k_scale: float
                          "head_dim contiguous")
     if dtype not in _DTYPES:
         raise ValueError(f"key_cache must be bf16, fp16 or float8_e4m3fn, got {dtype}")
+    # A dimension of one element may have any stride.
     if (value_cache.shape != shape or value_cache.dtype != dtype
-            or value_cache.stride() != strides):
+            or (value_cache.stride() != strides
+                and any(n != 1 and x != y
+                        for n, x, y in zip(shape, strides, value_cache.stride())))):
         raise ValueError("key_cache and value_cache must have one shape, type and strides")
     return _native.KvCache(key_cache.data_ptr(), value_cache.data_ptr(), strides[0], strides[1],
                            strides[2], shape[0], shape[1], shape[2], shape[3], _DTYPES[dtype],

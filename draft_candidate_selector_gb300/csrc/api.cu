@@ -177,8 +177,10 @@ dflash_status check_ptr8(const void* p, const char* name) {
         if (_s != DFLASH_OK) return _s;      \
     } while (0)
 
-// A stride in elements that keeps rows aligned for loads of 8 elements.
-dflash_status check_stride(long long stride, int multiple, const char* name) {
+// A stride in elements that keeps rows aligned for loads of 8 elements. A dimension of one element
+// is never stepped along, whatever its stride.
+dflash_status check_stride(long long stride, int dim, int multiple, const char* name) {
+    if (dim == 1) return DFLASH_OK;
     if (stride < 0) return fail(DFLASH_INVALID_ARGUMENT, "%s=%lld must be >= 0", name, stride);
     if (stride % multiple != 0)
         return fail(DFLASH_UNSUPPORTED, "%s=%lld: must be a multiple of %d elements", name, stride,
@@ -202,9 +204,9 @@ dflash_status check_cache(const dflash_kv_cache* c, int dtype, dflash::KvCache* 
     if (c->head_dim % mult != 0 || c->head_dim > 256)
         return fail(DFLASH_UNSUPPORTED, "head_dim=%d: must be a multiple of %d up to 256",
                     c->head_dim, mult);
-    DFLASH_TRY(check_stride(c->page_stride, mult, "page_stride"));
-    DFLASH_TRY(check_stride(c->token_stride, mult, "token_stride"));
-    DFLASH_TRY(check_stride(c->head_stride, mult, "head_stride"));
+    DFLASH_TRY(check_stride(c->page_stride, c->num_pages, mult, "page_stride"));
+    DFLASH_TRY(check_stride(c->token_stride, c->page_size, mult, "token_stride"));
+    DFLASH_TRY(check_stride(c->head_stride, c->kv_heads, mult, "head_stride"));
     if (!(c->k_scale > 0.f) || isinf(c->k_scale) || !(c->v_scale > 0.f) || isinf(c->v_scale))
         return fail(DFLASH_INVALID_ARGUMENT, "k_scale=%g and v_scale=%g must be finite and > 0",
                     (double)c->k_scale, (double)c->v_scale);
@@ -657,10 +659,10 @@ dflash_status dflash_store_kv(const void* key, const void* value, int dtype, con
     if (T < 0) return fail(DFLASH_INVALID_ARGUMENT, "T=%d must be >= 0", T);
     dflash::KvCache c;
     DFLASH_TRY(check_cache(cache, dtype, &c));
-    DFLASH_TRY(check_stride(key_token_stride, 8, "key_token_stride"));
-    DFLASH_TRY(check_stride(key_head_stride, 8, "key_head_stride"));
-    DFLASH_TRY(check_stride(value_token_stride, 8, "value_token_stride"));
-    DFLASH_TRY(check_stride(value_head_stride, 8, "value_head_stride"));
+    DFLASH_TRY(check_stride(key_token_stride, T, 8, "key_token_stride"));
+    DFLASH_TRY(check_stride(key_head_stride, c.kv_heads, 8, "key_head_stride"));
+    DFLASH_TRY(check_stride(value_token_stride, T, 8, "value_token_stride"));
+    DFLASH_TRY(check_stride(value_head_stride, c.kv_heads, 8, "value_head_stride"));
     if (T == 0) return ok();
     DFLASH_TRY(check_ptr(key, "key"));
     DFLASH_TRY(check_ptr(value, "value"));
@@ -717,8 +719,8 @@ dflash_status dflash_paged_attention(const void* query, int dtype, int T, int q_
     if (!(softcap >= 0.f) || isinf(softcap))
         return fail(DFLASH_INVALID_ARGUMENT, "softcap=%g must be finite and >= 0 (0 = no cap)",
                     (double)softcap);
-    DFLASH_TRY(check_stride(q_token_stride, 8, "q_token_stride"));
-    DFLASH_TRY(check_stride(q_head_stride, 8, "q_head_stride"));
+    DFLASH_TRY(check_stride(q_token_stride, T, 8, "q_token_stride"));
+    DFLASH_TRY(check_stride(q_head_stride, q_heads, 8, "q_head_stride"));
     if (T == 0) return ok();
     DFLASH_TRY(check_ptr(query, "query"));
     DFLASH_TRY(check_ptr4(block_table, "block_table"));

@@ -319,8 +319,9 @@ typedef enum {
 
 /* One layer's cache: key and value hold [num_pages, page_size, kv_heads, head_dim] elements
  * of type dtype, at the same strides (in elements; the innermost is 1), so both orders of
- * page rows and heads, and caches with keys and values interleaved, can be passed. Row
- * addresses must be 16-byte aligned. With DFLASH_E4M3 an element stands for itself times
+ * page rows and heads, and caches with keys and values interleaved, can be passed. (Here and in
+ * the calls below a dimension of one element may have any stride.) Row addresses must be 16-byte
+ * aligned. With DFLASH_E4M3 an element stands for itself times
  * k_scale or v_scale; with the other types both scales must be 1. A host struct; the calls read
  * it before they return. */
 typedef struct {
