@@ -108,7 +108,17 @@ def _workspace(nbytes: int, dev: torch.device, workspace: torch.Tensor | None,
     if nbytes <= 0:
         _native.check(_native.DFLASH_INVALID_ARGUMENT)
     if workspace is None:
-        workspace = _empty((nbytes,), torch.uint8, dev, stream, handed_out=False)
+        return _empty((nbytes,), torch.uint8, dev, stream, handed_out=False)
+    return _check_workspace(workspace, dev)
+
+
+def _check_workspace(workspace: torch.Tensor, dev: torch.device) -> torch.Tensor:
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if workspace.device != dev:
+        raise ValueError(f"workspace must be a CUDA tensor on {dev}, not {workspace.device}")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     return workspace
 
 
@@ -137,7 +147,7 @@ def dflash_topk_candidates(logits: torch.Tensor, K: int, cand_ids: torch.Tensor 
         ws = _workspace(lib.dflash_topk_workspace_bytes(R, S, V, K), dev, workspace, stream)
         _native.check(lib.dflash_topk_candidates(
             _ptr(logits), R, S, V, K, float(softcap), float(scale), _ptr(cand_ids), _ptr(unary),
-            _ptr(ws), ws.numel(), _stream(dev, stream)))
+            _ptr(ws), ws.nbytes, _stream(dev, stream)))
     return cand_ids, unary
 
 
@@ -164,7 +174,7 @@ def dflash_lmhead_topk(hidden: torch.Tensor, lm_head: torch.Tensor, K: int,
         ws = _workspace(lib.dflash_lmhead_topk_workspace_bytes(R, S, V, K), dev, workspace, stream)
         _native.check(lib.dflash_lmhead_topk(
             _ptr(hidden), _ptr(lm_head), R, S, H, V, K, float(softcap), float(scale),
-            _ptr(cand_ids), _ptr(unary), _ptr(ws), ws.numel(), _stream(dev, stream)))
+            _ptr(cand_ids), _ptr(unary), _ptr(ws), ws.nbytes, _stream(dev, stream)))
     return cand_ids, unary
 
 
@@ -255,7 +265,7 @@ def dflash_selector(logits: torch.Tensor, hidden: torch.Tensor, w_proj: torch.Te
         _native.check(lib.dflash_selector(
             _ptr(logits), _ptr(hidden), _ptr(w_proj), _ptr(pred_cb), _ptr(succ_cb),
             _ptr(anchors), R, S, K, V, H, rank, float(softcap), float(scale), _ptr(cand_ids),
-            _ptr(unary), _ptr(h_out), _ptr(edges), _ptr(ws), ws.numel(), _stream(dev, stream)))
+            _ptr(unary), _ptr(h_out), _ptr(edges), _ptr(ws), ws.nbytes, _stream(dev, stream)))
     return cand_ids, unary, h_out, edges
 
 
@@ -338,7 +348,7 @@ def dflash_selector_lmhead(hidden: torch.Tensor, lm_head: torch.Tensor, w_proj: 
         _native.check(lib.dflash_selector_lmhead(
             _ptr(hidden), _ptr(lm_head), _ptr(w_proj), _ptr(pred_cb), _ptr(succ_cb),
             _ptr(anchors), R, S, K, V, H, rank, float(softcap), float(scale), _ptr(cand_ids),
-            _ptr(unary), _ptr(h_out), _ptr(edges), _ptr(ws), ws.numel(), _stream(dev, stream)))
+            _ptr(unary), _ptr(h_out), _ptr(edges), _ptr(ws), ws.nbytes, _stream(dev, stream)))
     return cand_ids, unary, h_out, edges
 
 
@@ -374,15 +384,20 @@ def dflash_best_path(edges: torch.Tensor, cand_ids: torch.Tensor, path: torch.Te
 # by _need; addresses go to the library as integers; outputs the caller did not pass are not
 # checked, and those of one type share an allocation.
 
-def _checked(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple) -> int:
-    """The address of a contiguous CUDA tensor of this type and shape."""
+def _checked(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, index: int) -> int:
+    """The address of a contiguous tensor of this type and shape on CUDA device `index`."""
     try:
-        if t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        if (t.dtype is dtype and t.get_device() == index and t.shape == shape
+                and t.is_contiguous()):
             return t.data_ptr()
     except AttributeError:
         pass
     _need(t, name, dtype, shape)
-    return t.data_ptr()
+    raise _elsewhere(t, name, index)
+
+
+def _elsewhere(t: torch.Tensor, name: str, index: int) -> ValueError:
+    return ValueError(f"{name} is on {t.device}, the call's first tensor on cuda:{index}")
 
 
 def _launch(fn, dev: torch.device, stream, *args) -> None:
@@ -419,12 +434,15 @@ def dflash_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor,
     if context_lens.dim() != 1 or free_pages.dim() != 1 or block_table.dim() != 2:
         raise ValueError("context_lens must be [R], free_pages [n], block_table [R, max_pages]")
     (R,), max_pages, n_free = context_lens.shape, block_table.shape[1], free_pages.shape[0]
-    ctx = _checked(context_lens, "context_lens", i32, (R,))
-    new = _checked(new_lens, "new_lens", i32, (R,))
-    held = _checked(held_pages, "held_pages", i32, (R,))
-    free = _checked(free_pages, "free_pages", i32, (n_free,))
-    table = _checked(block_table, "block_table", i32, (R, max_pages))
     dev = context_lens.device
+    index = context_lens.get_device()
+    if index < 0:
+        _need(context_lens, "context_lens", i32)                 # raises
+    ctx = _checked(context_lens, "context_lens", i32, (R,), index)
+    new = _checked(new_lens, "new_lens", i32, (R,), index)
+    held = _checked(held_pages, "held_pages", i32, (R,), index)
+    free = _checked(free_pages, "free_pages", i32, (n_free,), index)
+    table = _checked(block_table, "block_table", i32, (R, max_pages), index)
     sizes = (R + 1, R, R, T, 1)
     given = (query_start, kv_lens, held_out, positions, pages_needed)
     names = ("query_start", "kv_lens", "held_out", "positions", "pages_needed")
@@ -437,12 +455,13 @@ def dflash_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor,
     else:
         out = tuple(_empty((n,), i32, dev, stream) if t is None else t
                     for t, n in zip(given, sizes))
-        ptrs = tuple(_checked(t, name, i32, (n,)) for t, name, n in zip(out, names, sizes))
+        ptrs = tuple(_checked(t, name, i32, (n,), index)
+                     for t, name, n in zip(out, names, sizes))
     if slots is None:
         slots = _empty((T,), torch.int64, dev, stream)
         slots_at = slots.data_ptr()
     else:
-        slots_at = _checked(slots, "slots", torch.int64, (T,))
+        slots_at = _checked(slots, "slots", torch.int64, (T,), index)
     _launch(lib.dflash_block_tables, dev, stream, ctx, new, held, free, R, n_free, page_size,
             max_pages, T, table, ptrs[0], ptrs[1], ptrs[2], ptrs[3], slots_at, ptrs[4])
     return out[0], out[1], out[2], out[3], slots, out[4]
@@ -468,12 +487,12 @@ def _rows(t: torch.Tensor, name: str, dtype: torch.dtype | None = None):
 
 
 def _kv_cache(key_cache: torch.Tensor, value_cache: torch.Tensor, k_scale: float,
-              v_scale: float) -> _native.KvCache:
+              v_scale: float, index: int) -> _native.KvCache:
     for t, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != index:
+            raise _elsewhere(t, name, index)
     shape, strides, dtype = key_cache.shape, key_cache.stride(), key_cache.dtype
     if len(shape) != 4 or (strides[3] != 1 and shape[3] != 1):
         raise ValueError("key_cache must be [pages, page_size, kv_heads, head_dim], "
@@ -501,13 +520,16 @@ def dflash_store_kv(key: torch.Tensor, value: torch.Tensor, slots: torch.Tensor,
     lib = _native._lib or _native.load()
     code, ks = _rows(key, "key")
     _, vs = _rows(value, "value", key.dtype)
-    cache = _kv_cache(key_cache, value_cache, k_scale, v_scale)
+    index = key.get_device()
+    if value.get_device() != index:
+        raise _elsewhere(value, "value", index)
+    cache = _kv_cache(key_cache, value_cache, k_scale, v_scale, index)
     shape = key.shape
     T = shape[0]
     if shape != (T, cache.kv_heads, cache.head_dim) or value.shape != shape:
         raise ValueError(f"key and value must be [T, {cache.kv_heads}, {cache.head_dim}], got "
                          f"{tuple(key.shape)} and {tuple(value.shape)}")
-    at = _checked(slots, "slots", torch.int64, (T,))
+    at = _checked(slots, "slots", torch.int64, (T,), index)
     _launch(lib.dflash_store_kv, key.device, stream, key.data_ptr(), value.data_ptr(), code, at, T,
             ks[0], ks[1], vs[0], vs[1], cache)
     return key_cache, value_cache
@@ -554,34 +576,37 @@ def dflash_paged_attention(query: torch.Tensor, key_cache: torch.Tensor,
     """
     lib = _native._lib or _native.load()
     code, qs = _rows(query, "query")
-    cache = _kv_cache(key_cache, value_cache, k_scale, v_scale)
+    index = query.get_device()
+    cache = _kv_cache(key_cache, value_cache, k_scale, v_scale, index)
     T, Hq, D = query.shape
     if D != cache.head_dim:
         raise ValueError(f"query has head_dim {D}, the cache {cache.head_dim}")
     if block_table.dim() != 2 or kv_lens.dim() != 1:
         raise ValueError("block_table must be [R, max_pages] and kv_lens [R]")
     R, max_pages = block_table.shape
-    table = _checked(block_table, "block_table", torch.int32, (R, max_pages))
-    start = _checked(query_start, "query_start", torch.int32, (R + 1,))
-    kv = _checked(kv_lens, "kv_lens", torch.int32, (R,))
+    table = _checked(block_table, "block_table", torch.int32, (R, max_pages), index)
+    start = _checked(query_start, "query_start", torch.int32, (R + 1,), index)
+    kv = _checked(kv_lens, "kv_lens", torch.int32, (R,), index)
     dev = query.device
     if out is None:
         out = _empty((T, Hq, D), query.dtype, dev, stream)
         out_at = out.data_ptr()
     else:
-        out_at = _checked(out, "out", query.dtype, (T, Hq, D))
+        out_at = _checked(out, "out", query.dtype, (T, Hq, D), index)
     if lse is None:
         lse = _empty((T, Hq), torch.float32, dev, stream)
         lse_at = lse.data_ptr()
     else:
-        lse_at = _checked(lse, "lse", torch.float32, (T, Hq))
+        lse_at = _checked(lse, "lse", torch.float32, (T, Hq), index)
     if workspace is None:
         workspace = _empty((_attention_workspace(dev, D),), torch.uint8, dev, stream,
                            handed_out=False)
+    else:
+        _check_workspace(workspace, dev)
     _launch(lib.dflash_paged_attention, dev, stream, query.data_ptr(), code, T, Hq, qs[0], qs[1],
             cache, table, R, max_pages, start, kv, D ** -0.5 if scale is None else scale,
             window_left, window_right, softcap, out_at, lse_at, workspace.data_ptr(),
-            workspace.numel())
+            workspace.nbytes)
     return out, lse
 
 
