@@ -29,6 +29,15 @@ sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 import draft_candidate_selector_gb300 as ds   # noqa: E402
 
 
+def check_status() -> None:
+    """Raises if a kernel of the calls so far has set a bit of the device status."""
+    status = ds.dflash_device_status()
+    if status & ds.DEVICE_NO_PAGES:
+        raise RuntimeError("the cache is out of pages")
+    if status:
+        raise RuntimeError(f"device status {status:#x}")
+
+
 class Drafter:
     """Weights, the paged cache and the requests' state. All tensors live on `device`."""
 
@@ -73,10 +82,10 @@ class Drafter:
         the context of each; their keys and values are cached, the context is not moved on."""
         start, kv_lens, self.held, positions, slots, taken = ds.dflash_block_tables(
             self.context, new_lens, self.held, self.free, self.table, self.page_size, len(tokens))
-        # The number of pages taken is the step's one value that the host reads.
+        # The host reads two values a step: the number of pages taken, and the status word, which
+        # holds what the kernels have met since it was last read (here, or after the last step).
         self.free = self.free[int(taken):].contiguous()
-        if ds.dflash_device_status() & ds.DEVICE_NO_PAGES:
-            raise RuntimeError("the cache is out of pages")
+        check_status()
         hq, hkv, d = self.heads
         x = self.embedded(tokens, positions)
         q, k, v = (x @ self.w_qkv.t()).view(len(tokens), hq + 2 * hkv, d).split([hq, hkv, hkv], 1)
@@ -133,6 +142,7 @@ def run(requests=8, prompt=400, steps=4, page_size=16, cache_dtype=torch.bfloat1
             torch.cuda.synchronize()
             print(f"step {step}: {1e3 * (time.perf_counter() - t0):.2f} ms, contexts "
                   f"{drafter.context.tolist()}, request 0 drafts {drafted[0].tolist()}")
+    check_status()
     return torch.stack(tokens), torch.stack(scores)
 
 

@@ -76,3 +76,14 @@ def test_out_of_pages(loop):
     with pytest.raises(RuntimeError, match="out of pages"):
         d.prompts([torch.zeros(40, dtype=torch.long, device="cuda")] * 2)
     ds.dflash_device_status(clear=True)
+
+
+def test_earlier_faults_are_not_passed_over(loop):
+    """A device status set in front of a step's tables (here by a store to a slot outside the cache)
+    is an error of the loop, not cleared and forgotten."""
+    d = loop.Drafter(2, 30, 16, 400)
+    x = torch.zeros((1, 4, 64), dtype=torch.bfloat16, device="cuda")
+    ds.dflash_store_kv(x, x, torch.tensor([30 * 16], device="cuda"), d.k_cache, d.v_cache)
+    with pytest.raises(RuntimeError, match="status"):
+        d.prompts([torch.zeros(40, dtype=torch.long, device="cuda")] * 2)
+    assert ds.dflash_device_status(clear=True) == 0
