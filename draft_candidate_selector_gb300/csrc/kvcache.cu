@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(kTableThreads) block_tables_kernel(BlockTableA
         a.kv_lens[r] = granted ? a.context_lens[r] + n : 0;
         a.held_out[r] = a.held_pages[r] + (granted ? need : 0);
     }
-    for (int j = at; j < min(fresh, a.n_free); j += stride) {
-        const int r = owner_of(first, a.R, j);
+    for (long long j = at; j < min(fresh, a.n_free); j += stride) {   // 64 bits: j + stride may pass 2^31
+        const int r = owner_of(first, a.R, (int)j);
         if (first[r + 1] > a.n_free) continue;               // refused: the list ends inside it
         a.block_table[(long long)r * a.max_pages + a.held_pages[r] + (j - first[r])] =
             a.free_pages[j];

@@ -171,3 +171,21 @@ def test_tables_into_given_outputs(dev, given):
     with pytest.raises(ValueError, match="positions"):
         ds.dflash_block_tables(*args(), positions=torch.zeros(54, dtype=torch.int32, device=dev))
     assert ds.dflash_device_status(clear=True) == 0
+
+
+@pytest.mark.gpu
+def test_tables_of_nearly_two_to_the_31_pages(dev):
+    """Fresh pages up to the end of 31 bits: a table and a free list of 8.6 GB each."""
+    R, width = 16384, 131071
+    if torch.cuda.mem_get_info(dev)[0] < 40 * 2 ** 30:
+        pytest.skip("needs 40 GB of device memory")
+    i32 = dict(dtype=torch.int32, device=dev)
+    free = torch.arange(R * width, **i32)
+    table = torch.full((R, width), -1, **i32)
+    zero, new = torch.zeros(R, **i32), torch.full((R,), width, **i32)
+    start, kv, held, _, _, needed = ds.dflash_block_tables(zero, new, zero.clone(), free, table, 1, 0)
+    # there is no room for the tokens, which only positions and slots need
+    assert ds.dflash_device_status(clear=True) == ds.DEVICE_BAD_LENGTH
+    assert int(needed) == R * width and (kv == width).all() and (held == width).all()
+    assert torch.equal(start.long(), torch.arange(R + 1, device=dev) * width)
+    assert torch.equal(table.view(-1), free)
