@@ -396,6 +396,9 @@ def _checked(t: torch.Tensor, name: str, dtype: torch.dtype, shape: tuple, index
     raise _elsewhere(t, name, index)
 
 
+_INT_MAX = 2 ** 31 - 1      # ctypes passes the low 32 bits of a larger number, without an error
+
+
 def _elsewhere(t: torch.Tensor, name: str, index: int) -> ValueError:
     return ValueError(f"{name} is on {t.device}, the call's first tensor on cuda:{index}")
 
@@ -434,6 +437,8 @@ def dflash_block_tables(context_lens: torch.Tensor, new_lens: torch.Tensor,
     if context_lens.dim() != 1 or free_pages.dim() != 1 or block_table.dim() != 2:
         raise ValueError("context_lens must be [R], free_pages [n], block_table [R, max_pages]")
     (R,), max_pages, n_free = context_lens.shape, block_table.shape[1], free_pages.shape[0]
+    if page_size > _INT_MAX or T > _INT_MAX or n_free > _INT_MAX or max_pages > _INT_MAX:
+        raise ValueError("page_size, T, max_pages and the number of free pages must be below 2^31")
     dev = context_lens.device
     index = context_lens.get_device()
     if index < 0:
@@ -584,6 +589,10 @@ def dflash_paged_attention(query: torch.Tensor, key_cache: torch.Tensor,
     if block_table.dim() != 2 or kv_lens.dim() != 1:
         raise ValueError("block_table must be [R, max_pages] and kv_lens [R]")
     R, max_pages = block_table.shape
+    if window_left > _INT_MAX:                                   # sees all there is
+        window_left = -1
+    if window_right > _INT_MAX:
+        window_right = -1
     table = _checked(block_table, "block_table", torch.int32, (R, max_pages), index)
     start = _checked(query_start, "query_start", torch.int32, (R + 1,), index)
     kv = _checked(kv_lens, "kv_lens", torch.int32, (R,), index)

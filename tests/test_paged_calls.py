@@ -189,3 +189,21 @@ def test_tables_of_nearly_two_to_the_31_pages(dev):
     assert int(needed) == R * width and (kv == width).all() and (held == width).all()
     assert torch.equal(start.long(), torch.arange(R + 1, device=dev) * width)
     assert torch.equal(table.view(-1), free)
+
+
+def test_integers_past_31_bits(monkeypatch):
+    """A window wider than any context has no bound; sizes that do not fit the C interface are
+    refused. (ctypes would pass the low 32 bits: a window of 2^32 as 0.)"""
+    launched = []
+    monkeypatch.setattr(ds, "_launch", lambda fn, dev, stream, *a: launched.append(a))
+    ds.dflash_paged_attention(**attention_arguments(), window_left=12345, window_right=2 ** 31 - 1)
+    at = launched[0].index(12345)
+    for wide in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1):
+        ds.dflash_paged_attention(**attention_arguments(), window_left=wide, window_right=wide)
+        assert launched[-1][at:at + 2] == (-1, -1)
+    assert launched[0][at:at + 2] == (12345, 2 ** 31 - 1)
+    n = len(launched)
+    for name in ("page_size", "T"):
+        with pytest.raises(ValueError, match=name):
+            ds.dflash_block_tables(**{**table_arguments(), name: 2 ** 32 + 16})
+    assert len(launched) == n
