@@ -75,8 +75,9 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     p.tpi = few ? p.tpt : 2 * p.tpt;
     // What an item costs besides its steps, in steps: more where a step is short, which it is with few
     // rows and 32 KB or less of keys and values. Microseconds at 1 / 2 / 3: windowed blocks of
-    // D = 64 231 / 213 / 199, single tokens from an 8-bit cache 187 / 172 / 159; 16-bit ones of
-    // D = 128 over 100 to 5000 356 / 346 / 356, a 16001-token prompt 806 / 781 / 783.
+    // D = 64 233 / 215 / 203 (uncapped 209 / 195 / 184), single tokens from an 8-bit cache 191 / 176 /
+    // 164 at D = 128, 147 / 137 / 129 at 64, windowed blocks over one 80 / 76 / 70; 16-bit single tokens
+    // of D = 128 299 / 297 / 297, of D = 64 246 / 245 / 247, a 16001-token prompt 819 / 792 / 797.
     const long long step_bytes = 2LL * BN * D * (c.dtype == kE4m3 ? 1 : 2);
     p.over = few && step_bytes <= 32768 ? 3 : 2;
     // Nothing is cut, and no join is launched, where the table's width and the number of tokens alone
@@ -85,8 +86,9 @@ cudaError_t launch_attention(const DeviceInfo& dev, const AttentionArgs& a, void
     const long long per_request = ((long long)a.T + p.tpi - 1) / p.tpi;
     const long long items = (a.R + (long long)a.T / p.tpi) * c.kv_heads;
     // Single tokens of few requests gain from SMs that have no item of their own (a call in a graph, 8
-    // items of 9 tiles: 14 us cut, 20 us whole); 100 tokens over 500 are joined dearly (32 us, 20 us
-    // whole), and so are items that nearly fill the SMs (128 items of 11 tiles: 31 us, 27 us whole).
+    // items of 9 tiles: 14 us cut, 20 us whole; cold, 22 and 28, and 16 items of 8 tiles 24 and 26); 100
+    // tokens over 400 are joined dearly (35 us, 26 us whole), and so are items that nearly fill the SMs
+    // (128 items of 6 tiles: 33 us, 27 us whole; 144 of 11: 43 and 39).
     p.whole = few && 2 * items <= p.G ? 4 : 12;
     p.join = p.G > 1 && ((a.T > p.tpt && !few ? 2 : 1) * (p.over + steps) > p.over + p.whole ||
                          per_request > kSerialItems || items > p.G);

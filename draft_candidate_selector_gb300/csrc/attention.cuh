@@ -53,7 +53,8 @@
 // call's plan, launch and first loads take some 20 us (one token over 332, with the join skipped).
 //
 // Rounding. P is rounded to the type of V (fp16 over an 8-bit cache), since one MMA's operands have
-// one type; S, m, l and O are fp32. Where many keys weigh alike that adds as much error as the
+// one type; S, m, l and O are fp32. fp16 weights are lifted by a power of two (weight_lift), so that
+// many small ones still count. Where many keys weigh alike that adds as much error as the
 // rounding of the output does; where few keys do, a largest weight that is exact keeps it smaller
 // (two single tokens over 142 to 428, bf16: 1.3 times the output's rounding, 1.5 with the maximum
 // left behind; 1% of the time).
@@ -554,7 +555,8 @@ __device__ __noinline__ bool sees_bad_page(const Problem& p, const Item& c, int 
 // An e4m3 value is an fp16 value, so tiles of an 8-bit cache are widened to fp16 in shared memory,
 // and queries of either type meet them as fp16. A bf16 query row is scaled by a power of two so
 // that its largest value lies in [2^14, 2^15); what that pushes below fp16's smallest step is less
-// than 2^-39 of the row's largest value. The inverse goes into the row's score scale.
+// than 2^-39 of the row's largest value. (The power stops at 2^100, so that its inverse is a normal
+// number: rows below 2^-86 lose more.) The inverse goes into the row's score scale.
 
 // This thread's row of a query tile (128-byte rows, 128-byte swizzle): bf16 to scaled fp16, in
 // place and into the copies 32 rows on. Returns the factor that undoes the scaling.

@@ -231,7 +231,7 @@ __device__ __forceinline__ uint32_t pack_bf16x2(uint32_t lo_bits, uint32_t hi_bi
 // tries to 0 in its lane: later waits do not wait, and whoever looks at tries learns of it. The hot
 // waits of a kernel are long chains of short ones, so nothing else is done here: reading the clock,
 // agreeing on the result after each wait, or polling with one lane each cost the attention kernel 5
-// to 50% of its time.
+// to 50% of its time. (A try on a barrier that does not move takes about 4 us: 17 s in all.)
 constexpr uint32_t kWaitTries = 1u << 22;
 __device__ __forceinline__ void mbar_wait_tries(uint32_t bar, uint32_t parity, uint32_t& tries) {
     bool done = false;

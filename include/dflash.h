@@ -427,7 +427,8 @@ dflash_status dflash_store_kv(const void* key, const void* value, int dtype, con
  * rounding; a softcap outside [2^-64, 2^64] counts as the nearer end. The products exp(s_j) v_j
  * take exp(s_j) relative to a running maximum, rounded to the query's type (to fp16 over an e4m3
  * cache), and are summed in fp32. Over an e4m3 cache bf16 queries are taken as fp16 times a power
- * of two for each row: what that loses is less than 2^-39 of the row's largest value.
+ * of two for each row: what that loses is less than 2^-39 of the row's largest value (of one of
+ * 2^-86 or more; smaller queries may be taken as 0).
  * Page ids outside the pool are never followed: tokens that see a key of such a page get NaN, the
  * others what they would get without it, and the status word records DFLASH_DEVICE_BAD_ID. Pages of
  * which no token sees a key (a window may have left them) can have any id. A request whose kv_lens does not fit max_pages, or
