@@ -92,14 +92,22 @@ def _empty(shape: tuple, dtype: torch.dtype, dev: torch.device, stream,
     that still runs on the current stream. What is handed out is kept from that stream, too, until
     the work that the current stream has been given by then is done.
     """
-    if stream is None:
+    if stream is None or stream.cuda_stream == torch._C._cuda_getCurrentRawStream(dev.index):
         return torch.empty(shape, dtype=dtype, device=dev)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(stream.cuda_stream, device=dev)
-    with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=dev)
+    here = torch.cuda.current_stream(dev)
+    if dev.index == torch.cuda.current_device():
+        torch.cuda.set_stream(stream)          # half of what the context manager costs
+        try:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        finally:
+            torch.cuda.set_stream(here)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(shape, dtype=dtype, device=dev)
     if handed_out:
-        t.record_stream(torch.cuda.current_stream(dev))
+        t.record_stream(here)
     return t
 
 

@@ -129,3 +129,44 @@ def test_any_object_with_a_stream_handle(dev):
     s.synchronize()
     for g, w in zip(got, want):
         assert torch.equal(g, w)
+
+
+def test_the_current_stream_by_name(dev, monkeypatch):
+    """The current stream passed as `stream` is no other stream: nothing is switched or recorded."""
+    call, s = calls(dev)["attention"], torch.cuda.Stream()
+    want = call()
+    torch.cuda.synchronize()
+
+    def refuse(*a, **k):
+        raise AssertionError("the call switched streams")
+
+    with torch.cuda.stream(s):
+        with monkeypatch.context() as m:
+            m.setattr(torch.cuda, "stream", refuse)
+            m.setattr(torch.cuda, "set_stream", refuse)
+            m.setattr(torch.Tensor, "record_stream", refuse)
+            got = call(stream=s)
+    got2 = call(stream=torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    for g, g2, w in zip(got, got2, want):
+        assert torch.equal(g, w) and torch.equal(g2, w)
+
+
+@pytest.mark.parametrize("name", ["selector", "attention", "tables"])
+def test_another_stream_in_a_graph(dev, name):
+    """A call on a stream that a capture has forked to."""
+    call = calls(dev)[name]
+    want = [t.clone() for t in call()]
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        s.wait_stream(torch.cuda.current_stream())
+        got = call(stream=s)
+        torch.cuda.current_stream().wait_stream(s)
+    for _ in range(2):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
