@@ -23,14 +23,16 @@ import ctypes
 import torch
 
 from . import _native
-from ._native import (DEVICE_BAD_ID, DEVICE_BAD_LENGTH, DEVICE_NO_PAGES,  # noqa: F401
-                      DEVICE_TIMEOUT, DflashError)
+from ._native import (DEVICE_BAD_ID, DEVICE_BAD_LENGTH, DEVICE_BAD_LOGITS,  # noqa: F401
+                      DEVICE_NO_PAGES, DEVICE_TIMEOUT, DflashError)
 
 __all__ = [
     "dflash_topk_candidates", "dflash_hidden_projection", "dflash_candidate_edges",
     "dflash_selector", "dflash_selector_forward", "dflash_lmhead_topk", "dflash_selector_lmhead",
     "dflash_best_path", "dflash_block_tables", "dflash_store_kv", "dflash_paged_attention",
     "dflash_paged_attention_workspace_bytes",
+    "dflash_rope_frequencies", "dflash_qk_norm_rope", "dflash_qk_norm_rope_store",
+    "dflash_sample_path", "dflash_verify_drafts", "dflash_verify_drafts_workspace_bytes",
     "dflash_topk_workspace_bytes",
     "dflash_selector_workspace_bytes", "dflash_lmhead_topk_workspace_bytes",
     "dflash_selector_lmhead_workspace_bytes",
@@ -625,6 +627,286 @@ def dflash_paged_attention(query: torch.Tensor, key_cache: torch.Tensor,
             window_left, window_right, softcap, out_at, lse_at, workspace.data_ptr(),
             workspace.nbytes)
     return out, lse
+
+
+def dflash_rope_frequencies(rotary_dim: int, base: float = 10000.0, factor: float = 1.0,
+                            original_len: float = 0.0, turns_slow: float = 1.0,
+                            turns_fast: float = 32.0, inv_freq: torch.Tensor | None = None,
+                            device="cuda") -> torch.Tensor:
+    """Rotation frequencies int64 [rotary_dim / 2] for dflash_qk_norm_rope: the turns of each pair
+    between two positions, as whole numbers of 2^-64.
+
+    inv_freq [rotary_dim / 2] gives radians per position; without it they are
+    base^(-2 j / rotary_dim). For long contexts they are divided by factor: all of them if
+    original_len is 0, else those that make at most turns_slow turns over original_len positions,
+    those with turns_fast or more not at all, and the others in between.
+    """
+    lib = _native._lib or _native.load()
+    out = torch.empty((max(rotary_dim, 0) // 2,), dtype=torch.int64)
+    given = None
+    if inv_freq is not None:
+        given = inv_freq.detach().to("cpu", torch.float64).contiguous()
+        if given.shape != out.shape:
+            raise ValueError(f"inv_freq must have shape {tuple(out.shape)}, got {tuple(given.shape)}")
+    _native.check(lib.dflash_rope_frequencies(
+        rotary_dim, base, factor, original_len, turns_slow, turns_fast,
+        None if given is None else given.data_ptr(), out.data_ptr()))
+    return out.to(device)
+
+
+def _norm_rope(dtype: torch.dtype, head_dim: int, index: int, frequencies, q_weight, k_weight,
+               eps: float, interleaved: bool, rope_scale: float) -> _native.NormRope:
+    at, w_dtype = [None, None], dtype
+    if q_weight is not None or k_weight is not None:
+        w_dtype = (q_weight if q_weight is not None else k_weight).dtype
+        if w_dtype != torch.float32:
+            w_dtype = dtype
+        if q_weight is not None:
+            at[0] = _checked(q_weight, "q_weight", w_dtype, (head_dim,), index)
+        if k_weight is not None:
+            at[1] = _checked(k_weight, "k_weight", w_dtype, (head_dim,), index)
+    freq, rotary = None, 0
+    if frequencies is not None:
+        rotary = 2 * frequencies.shape[0]
+        freq = _checked(frequencies, "frequencies", torch.int64, (rotary // 2,), index)
+    return _native.NormRope(at[0], at[1], _DTYPES.get(w_dtype, _native.FP32), eps, freq, rotary,
+                            interleaved, rope_scale)
+
+
+def _heads_out(out, name: str, like: torch.Tensor, index: int, stream):
+    """An output of the shape and type of `like`, new or given (strided as a query may be), its address
+    and its strides."""
+    shape = like.shape
+    if out is None:
+        out = _empty(shape, like.dtype, like.device, stream)
+        return out, out.data_ptr(), (shape[1] * shape[2], shape[2])
+    _, strides = _rows(out, name, like.dtype)
+    if out.get_device() != index:
+        raise _elsewhere(out, name, index)
+    if out.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(out.shape)}")
+    return out, out.data_ptr(), strides
+
+
+def dflash_qk_norm_rope(query: torch.Tensor | None, key: torch.Tensor | None,
+                        positions: torch.Tensor | None, frequencies: torch.Tensor | None = None,
+                        q_weight: torch.Tensor | None = None,
+                        k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                        interleaved: bool = False, rope_scale: float = 1.0,
+                        query_out: torch.Tensor | None = None,
+                        key_out: torch.Tensor | None = None, stream=None):
+    """RMS norm of each query and key head, then its rotation by position, in one pass: returns
+    (query_out, key_out).
+
+    query [T, q_heads, head_dim] and key [T, kv_heads, head_dim], bf16 or fp16, strided views
+    allowed; one of them may be None. positions int32 [T]; frequencies as dflash_rope_frequencies
+    gives them, for the first 2 * len(frequencies) values of a head (None: no rotation); weights
+    [head_dim] of their type or fp32 (None: no norm). interleaved pairs values 2j and 2j + 1, else
+    j and j + rotary_dim / 2. An output may be its own input.
+    """
+    lib = _native._lib or _native.load()
+    first = query if query is not None else key
+    if first is None:
+        raise ValueError("query and key must not both be None")
+    code, strides = _rows(first, "query" if query is not None else "key")
+    index, dtype = first.get_device(), first.dtype
+    T, heads, D = first.shape
+    q_heads = kv_heads = q_at = k_at = q_out = k_out = None
+    qs = ks = qos = kos = (0, 0)
+    if query is not None:
+        q_heads, q_at, qs = heads, query.data_ptr(), strides
+    if key is not None:
+        if query is not None:
+            _, ks = _rows(key, "key", dtype)
+            if key.get_device() != index:
+                raise _elsewhere(key, "key", index)
+            if key.shape[0] != T or key.shape[2] != D:
+                raise ValueError(f"key must be [{T}, heads, {D}], got {tuple(key.shape)}")
+        else:
+            ks = strides
+        kv_heads, k_at = key.shape[1], key.data_ptr()
+    how = _norm_rope(dtype, D, index, frequencies, q_weight, k_weight, eps, interleaved, rope_scale)
+    pos = None if how.rotary_dim == 0 else _checked(positions, "positions", torch.int32, (T,), index)
+    if query is not None:
+        query_out, q_out, qos = _heads_out(query_out, "query_out", query, index, stream)
+    if key is not None:
+        key_out, k_out, kos = _heads_out(key_out, "key_out", key, index, stream)
+    _launch(lib.dflash_qk_norm_rope, first.device, stream, q_at, k_at, code, pos, T, q_heads or 0,
+            kv_heads or 0, D, qs[0], qs[1], ks[0], ks[1], how, q_out, k_out, qos[0], qos[1], kos[0],
+            kos[1])
+    return query_out, key_out
+
+
+def dflash_qk_norm_rope_store(query: torch.Tensor | None, key: torch.Tensor, value: torch.Tensor,
+                              positions: torch.Tensor | None, slots: torch.Tensor,
+                              key_cache: torch.Tensor, value_cache: torch.Tensor,
+                              frequencies: torch.Tensor | None = None,
+                              q_weight: torch.Tensor | None = None,
+                              k_weight: torch.Tensor | None = None, eps: float = 1e-6,
+                              interleaved: bool = False, rope_scale: float = 1.0,
+                              k_scale: float = 1.0, v_scale: float = 1.0,
+                              query_out: torch.Tensor | None = None, stream=None):
+    """dflash_qk_norm_rope with the keys, and value [T, kv_heads, head_dim], stored at slots int64 [T]
+    of the caches as dflash_store_kv does: returns (query_out, key_cache, value_cache). query may be
+    None.
+    """
+    lib = _native._lib or _native.load()
+    code, ks = _rows(key, "key")
+    dtype, index = key.dtype, key.get_device()
+    _, vs = _rows(value, "value", dtype)
+    if value.get_device() != index:
+        raise _elsewhere(value, "value", index)
+    cache = _kv_cache(key_cache, value_cache, k_scale, v_scale, index)
+    shape = key.shape
+    T, D = shape[0], shape[2]
+    if shape != (T, cache.kv_heads, cache.head_dim) or value.shape != shape:
+        raise ValueError(f"key and value must be [T, {cache.kv_heads}, {cache.head_dim}], got "
+                         f"{tuple(key.shape)} and {tuple(value.shape)}")
+    at = _checked(slots, "slots", torch.int64, (T,), index)
+    q_heads, q_at, q_out, qs, qos = 0, None, None, (0, 0), (0, 0)
+    if query is not None:
+        _, qs = _rows(query, "query", dtype)
+        if query.get_device() != index:
+            raise _elsewhere(query, "query", index)
+        if query.shape[0] != T or query.shape[2] != D:
+            raise ValueError(f"query must be [{T}, heads, {D}], got {tuple(query.shape)}")
+        q_heads, q_at = query.shape[1], query.data_ptr()
+    how = _norm_rope(dtype, D, index, frequencies, q_weight, k_weight, eps, interleaved, rope_scale)
+    pos = None if how.rotary_dim == 0 else _checked(positions, "positions", torch.int32, (T,), index)
+    if query is not None:
+        query_out, q_out, qos = _heads_out(query_out, "query_out", query, index, stream)
+    _launch(lib.dflash_qk_norm_rope_store, key.device, stream, q_at, key.data_ptr(),
+            value.data_ptr(), code, pos, at, T, q_heads, qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], how,
+            cache, q_out, qos[0], qos[1])
+    return query_out, key_cache, value_cache
+
+
+def _temperatures(temperature, R: int, index: int):
+    """The address of a temperature for each request (or None), and the one for all."""
+    if isinstance(temperature, torch.Tensor):
+        return _checked(temperature, "temperature", torch.float32, (R,), index), 1.0
+    return None, temperature
+
+
+def dflash_sample_path(edges: torch.Tensor, cand_ids: torch.Tensor, uniforms: torch.Tensor,
+                       temperature: float | torch.Tensor = 1.0, path: torch.Tensor | None = None,
+                       tokens: torch.Tensor | None = None, probs: torch.Tensor | None = None,
+                       stream=None):
+    """A path drawn through edge scores [R, S, K, K]: returns (path int32 [R, S], tokens int32
+    [R, S], probs fp32 [R, S, K]).
+
+    Each step's candidate is drawn from the softmax of edges / temperature in the row of the one
+    before, by its number of uniforms fp32 [R, S]; probs are the distributions drawn from.
+    temperature is one for all or fp32 [R]; 0 takes the largest score.
+    """
+    lib = _native._lib or _native.load()
+    if edges.dim() != 4 or edges.shape[2] != edges.shape[3]:
+        raise ValueError("edges must be [R, S, K, K]")
+    R, S, K, _ = edges.shape
+    index = edges.get_device()
+    i32, f32 = torch.int32, torch.float32
+    if index < 0:
+        _need(edges, "edges", f32)                               # raises
+    at = (_checked(edges, "edges", f32, (R, S, K, K), index),
+          _checked(cand_ids, "cand_ids", i32, (R, S, K), index),
+          _checked(uniforms, "uniforms", f32, (R, S), index),
+          *_temperatures(temperature, R, index))
+    dev = edges.device
+    if path is None and tokens is None:
+        room = _empty((2, R, S), i32, dev, stream)
+        path, tokens = room.unbind(0)
+        out = (room.data_ptr(), room.data_ptr() + 4 * R * S)
+    else:
+        path = _empty((R, S), i32, dev, stream) if path is None else path
+        tokens = _empty((R, S), i32, dev, stream) if tokens is None else tokens
+        out = (_checked(path, "path", i32, (R, S), index),
+               _checked(tokens, "tokens", i32, (R, S), index))
+    if probs is None:
+        probs = _empty((R, S, K), f32, dev, stream)
+        probs_at = probs.data_ptr()
+    else:
+        probs_at = _checked(probs, "probs", f32, (R, S, K), index)
+    _launch(lib.dflash_sample_path, dev, stream, *at, R, S, K, *out, probs_at)
+    return path, tokens, probs
+
+
+def dflash_verify_drafts_workspace_bytes(R: int, T: int, V: int) -> int:
+    return int(_native.load().dflash_verify_drafts_workspace_bytes(R, T, V))
+
+
+_LOGITS = {torch.bfloat16: _native.BF16, torch.float16: _native.FP16, torch.float32: _native.FP32}
+
+
+def dflash_verify_drafts(logits: torch.Tensor, query_start: torch.Tensor,
+                         draft_tokens: torch.Tensor, accept_uniforms: torch.Tensor,
+                         sample_uniforms: torch.Tensor, cand_ids: torch.Tensor | None = None,
+                         draft_probs: torch.Tensor | None = None,
+                         temperature: float | torch.Tensor = 1.0,
+                         tokens: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                         logprobs: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None, stream=None):
+    """Drafts taken or rejected against the target's logits: returns (tokens int32 [R, S + 1], counts
+    int32 [R], logprobs fp32 [R, S + 1]).
+
+    logits [T, V] bf16, fp16 or fp32 (rows may be strided) hold a row for each request's last token
+    and one for each of its drafts, at query_start int32 [R + 1] as dflash_block_tables gives it;
+    draft_tokens int32 [R, S]. cand_ids and draft_probs [R, S, K] are what dflash_sample_path drew them
+    from; without them each draft was certain. accept_uniforms fp32 [R, S] and sample_uniforms fp32 [R]
+    are drawn from [0, 1). temperature is one for all or fp32 [R]; 0 is greedy. A row of tokens holds the
+    drafts that were taken, one more token, then -1; logprobs are their log-probabilities.
+    """
+    lib = _native._lib or _native.load()
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits must be a torch.Tensor")
+    if not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor")
+    if logits.dim() != 2 or draft_tokens.dim() != 2 or (logits.stride(1) != 1 and logits.shape[1] != 1):
+        raise ValueError("logits must be [T, V], V contiguous, and draft_tokens [R, S]")
+    code = _LOGITS.get(logits.dtype)
+    if code is None:
+        raise ValueError(f"logits must be bf16, fp16 or fp32, got {logits.dtype}")
+    T, V = logits.shape
+    R, S = draft_tokens.shape
+    if T > _INT_MAX or V > _INT_MAX or R > _INT_MAX:
+        raise ValueError("T, V and R must be below 2^31")
+    index = logits.get_device()
+    i32, f32 = torch.int32, torch.float32
+    start = _checked(query_start, "query_start", i32, (R + 1,), index)
+    drafts = _checked(draft_tokens, "draft_tokens", i32, (R, S), index)
+    accept = _checked(accept_uniforms, "accept_uniforms", f32, (R, S), index)
+    sample = _checked(sample_uniforms, "sample_uniforms", f32, (R,), index)
+    ids_at = probs_at = None
+    K = 0
+    if cand_ids is not None or draft_probs is not None:
+        if cand_ids is None or draft_probs is None or cand_ids.dim() != 3:
+            raise ValueError("cand_ids and draft_probs must be given together, both [R, S, K]")
+        K = cand_ids.shape[2]
+        ids_at = _checked(cand_ids, "cand_ids", i32, (R, S, K), index)
+        probs_at = _checked(draft_probs, "draft_probs", f32, (R, S, K), index)
+    temps, temp = _temperatures(temperature, R, index)
+    dev = logits.device
+    if tokens is None and counts is None:
+        room = _empty((R * (S + 2),), i32, dev, stream)
+        tokens, counts = room[:R * (S + 1)].view(R, S + 1), room[R * (S + 1):]
+        out = (room.data_ptr(), room.data_ptr() + 4 * R * (S + 1))
+    else:
+        tokens = _empty((R, S + 1), i32, dev, stream) if tokens is None else tokens
+        counts = _empty((R,), i32, dev, stream) if counts is None else counts
+        out = (_checked(tokens, "tokens", i32, (R, S + 1), index),
+               _checked(counts, "counts", i32, (R,), index))
+    if logprobs is None:
+        logprobs = _empty((R, S + 1), f32, dev, stream)
+        logprobs_at = logprobs.data_ptr()
+    else:
+        logprobs_at = _checked(logprobs, "logprobs", f32, (R, S + 1), index)
+    if workspace is None:
+        workspace = _workspace(lib.dflash_verify_drafts_workspace_bytes(R, T, V), dev, None, stream)
+    else:
+        _check_workspace(workspace, dev)
+    _launch(lib.dflash_verify_drafts, dev, stream, logits.data_ptr(), code, T, V, logits.stride(0),
+            start, drafts, R, S, ids_at, probs_at, K, accept, sample, temps, temp, *out, logprobs_at,
+            workspace.data_ptr(), workspace.nbytes)
+    return tokens, counts, logprobs
 
 
 def dflash_device_status(clear: bool = True) -> int:

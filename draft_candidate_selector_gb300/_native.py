@@ -23,8 +23,9 @@ DEVICE_BAD_ID = 0x1
 DEVICE_TIMEOUT = 0x2
 DEVICE_BAD_LENGTH = 0x4
 DEVICE_NO_PAGES = 0x8
+DEVICE_BAD_LOGITS = 0x10
 
-BF16, FP16, E4M3 = 0, 1, 2   # dflash_dtype
+BF16, FP16, E4M3, FP32 = 0, 1, 2, 3   # dflash_dtype
 
 HEADER = os.path.join(_build.ROOT, "include", "dflash.h")
 
@@ -40,7 +41,16 @@ class KvCache(ctypes.Structure):
                 ("head_dim", _i), ("dtype", _i), ("k_scale", _f), ("v_scale", _f)]
 
 
+class NormRope(ctypes.Structure):
+    """dflash_norm_rope."""
+
+    _fields_ = [("q_weight", _p), ("k_weight", _p), ("weight_dtype", _i), ("eps", _f),
+                ("frequencies", _p), ("rotary_dim", _i), ("interleaved", _i), ("rope_scale", _f)]
+
+
 _cache = ctypes.POINTER(KvCache)
+_how = ctypes.POINTER(NormRope)
+_d = ctypes.c_double
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -69,6 +79,15 @@ SIGNATURES = {
     "dflash_paged_attention_workspace_bytes": (_sz, [_i, _i, _i, _i, _i]),
     "dflash_paged_attention": (_i, [_p, _i, _i, _i, _ll, _ll, _cache, _p, _i, _i, _p, _p, _f, _i,
                                     _i, _f, _p, _p, _p, _sz, _p]),
+    "dflash_rope_frequencies": (_i, [_i, _d, _d, _d, _d, _d, _p, _p]),
+    "dflash_qk_norm_rope": (_i, [_p, _p, _i, _p, _i, _i, _i, _i, _ll, _ll, _ll, _ll, _how, _p, _p,
+                                 _ll, _ll, _ll, _ll, _p]),
+    "dflash_qk_norm_rope_store": (_i, [_p, _p, _p, _i, _p, _p, _i, _i, _ll, _ll, _ll, _ll, _ll, _ll,
+                                       _how, _cache, _p, _ll, _ll, _p]),
+    "dflash_sample_path": (_i, [_p, _p, _p, _p, _f, _i, _i, _i, _p, _p, _p, _p]),
+    "dflash_verify_drafts_workspace_bytes": (_sz, [_i, _i, _i]),
+    "dflash_verify_drafts": (_i, [_p, _i, _i, _i, _ll, _p, _p, _i, _i, _p, _p, _i, _p, _p, _p, _f, _p,
+                                  _p, _p, _p, _sz, _p]),
     "dflash_device_status": (_i, [ctypes.POINTER(ctypes.c_uint32), _i]),
     "dflash_selftest_wait_timeout": (_i, []),
     "dflash_trace_begin": (_i, [_i]),

@@ -9,6 +9,7 @@
 
 #include <nvtx3/nvToolsExt.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -217,6 +218,78 @@ dflash_status check_cache(const dflash_kv_cache* c, int dtype, dflash::KvCache* 
     *out = dflash::KvCache{c->key, c->value, c->page_stride, c->token_stride, c->head_stride,
                            c->num_pages, c->page_size, c->kv_heads, c->head_dim, c->dtype,
                            c->k_scale, c->v_scale};
+    return DFLASH_OK;
+}
+
+// Checks a dflash_norm_rope and the sizes and strides of the calls that take one; fills in what it says.
+dflash_status check_norm_rope(const dflash_norm_rope* how, dflash::NormRopeArgs* a) {
+    if (!how) return fail(DFLASH_INVALID_ARGUMENT, "how is NULL");
+    if (a->dtype != DFLASH_BF16 && a->dtype != DFLASH_FP16)
+        return fail(DFLASH_INVALID_ARGUMENT, "dtype=%d: must be DFLASH_BF16 or DFLASH_FP16", a->dtype);
+    if (a->T < 0) return fail(DFLASH_INVALID_ARGUMENT, "T=%d must be >= 0", a->T);
+    if (a->head_dim < 1) return fail(DFLASH_INVALID_ARGUMENT, "head_dim=%d must be >= 1", a->head_dim);
+    if (a->head_dim % 8 != 0 || a->head_dim > 256)
+        return fail(DFLASH_UNSUPPORTED, "head_dim=%d: must be a multiple of 8 up to 256", a->head_dim);
+    if (a->q_heads + 2LL * a->kv_heads > (1 << 24) ||
+        a->T * (a->q_heads + 2LL * a->kv_heads) > (1LL << 31) - 1)
+        return fail(DFLASH_INVALID_ARGUMENT, "T=%d tokens of %d and %d heads are more than 2^31-1 rows",
+                    a->T, a->q_heads, a->kv_heads);
+    if (how->rotary_dim < 0 || how->rotary_dim % 2 != 0 || how->rotary_dim > a->head_dim)
+        return fail(DFLASH_INVALID_ARGUMENT, "rotary_dim=%d must be even, from 0 to head_dim=%d",
+                    how->rotary_dim, a->head_dim);
+    if (!(how->eps >= 0.f) || isinf(how->eps))
+        return fail(DFLASH_INVALID_ARGUMENT, "eps=%g must be finite and >= 0", (double)how->eps);
+    if (!isfinite(how->rope_scale))
+        return fail(DFLASH_INVALID_ARGUMENT, "rope_scale=%g must be finite", (double)how->rope_scale);
+    if ((how->q_weight || how->k_weight) && how->weight_dtype != a->dtype &&
+        how->weight_dtype != DFLASH_FP32)
+        return fail(DFLASH_INVALID_ARGUMENT, "weight_dtype=%d: must be dtype=%d or DFLASH_FP32",
+                    how->weight_dtype, a->dtype);
+    if (a->q_heads > 0) {
+        DFLASH_TRY(check_stride(a->qt, a->T, 8, "q_token_stride"));
+        DFLASH_TRY(check_stride(a->qh, a->q_heads, 8, "q_head_stride"));
+        DFLASH_TRY(check_stride(a->qot, a->T, 8, "q_out_token_stride"));
+        DFLASH_TRY(check_stride(a->qoh, a->q_heads, 8, "q_out_head_stride"));
+    }
+    if (a->kv_heads > 0) {
+        DFLASH_TRY(check_stride(a->kt, a->T, 8, "k_token_stride"));
+        DFLASH_TRY(check_stride(a->kh, a->kv_heads, 8, "k_head_stride"));
+    }
+    a->q_weight = how->q_weight;
+    a->k_weight = how->k_weight;
+    a->weight_dtype = how->weight_dtype;
+    a->eps = how->eps;
+    a->frequencies = how->frequencies;
+    a->rotary_dim = how->rotary_dim;
+    a->interleaved = how->interleaved != 0;
+    a->rope_scale = how->rope_scale;
+    return DFLASH_OK;
+}
+
+// The pointers of such a call with any tokens.
+dflash_status check_norm_rope_pointers(const dflash::NormRopeArgs& a) {
+    if (a.q_heads > 0) {
+        DFLASH_TRY(check_ptr(a.query, "query"));
+        DFLASH_TRY(check_ptr(a.query_out, "query_out"));
+    }
+    if (a.kv_heads > 0) DFLASH_TRY(check_ptr(a.key, "key"));
+    const uintptr_t size = a.weight_dtype == DFLASH_FP32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(a.q_weight) % size != 0 ||
+        reinterpret_cast<uintptr_t>(a.k_weight) % size != 0)
+        return fail(DFLASH_INVALID_ARGUMENT, "q_weight or k_weight is not aligned to its elements");
+    if (a.rotary_dim > 0) {
+        DFLASH_TRY(check_ptr4(a.positions, "positions"));
+        DFLASH_TRY(check_ptr8(a.frequencies, "frequencies"));
+    }
+    return DFLASH_OK;
+}
+
+// One temperature for all requests; with one for each it is not looked at.
+dflash_status check_temperature(const float* temperatures, float temperature) {
+    if (temperatures) return check_ptr4(temperatures, "temperatures");
+    if (!(temperature >= 0.f) || isinf(temperature))
+        return fail(DFLASH_INVALID_ARGUMENT, "temperature=%g must be finite and >= 0",
+                    (double)temperature);
     return DFLASH_OK;
 }
 
@@ -744,6 +817,211 @@ dflash_status dflash_paged_attention(const void* query, int dtype, int T, int q_
                         ? dflash::launch_attention(dev, a, workspace, status, st)
                         : dflash::launch_attention_rows(dev, a, status, st);
     if (e != cudaSuccess) return cuda_fail(e, "paged attention launch");
+    return ok();
+}
+
+dflash_status dflash_rope_frequencies(int rotary_dim, double base, double factor,
+                                      double original_len, double turns_slow, double turns_fast,
+                                      const double* inv_freq, int64_t* frequencies) {
+    if (rotary_dim < 0 || rotary_dim % 2 != 0)
+        return fail(DFLASH_INVALID_ARGUMENT, "rotary_dim=%d must be even and >= 0", rotary_dim);
+    if (rotary_dim > 0 && !frequencies) return fail(DFLASH_INVALID_ARGUMENT, "frequencies is NULL");
+    if (!inv_freq) {
+        if (!(base > 0) || std::isinf(base))
+            return fail(DFLASH_INVALID_ARGUMENT, "base=%g must be finite and > 0", base);
+        if (!(factor > 0) || std::isinf(factor))
+            return fail(DFLASH_INVALID_ARGUMENT, "factor=%g must be finite and > 0", factor);
+        if (!(original_len >= 0) || std::isinf(original_len))
+            return fail(DFLASH_INVALID_ARGUMENT, "original_len=%g must be finite and >= 0",
+                        original_len);
+        if (original_len > 0 && !(turns_slow < turns_fast && std::isfinite(turns_slow) &&
+                                  std::isfinite(turns_fast)))
+            return fail(DFLASH_INVALID_ARGUMENT,
+                        "turns_slow=%g and turns_fast=%g must be finite, the first below the second",
+                        turns_slow, turns_fast);
+    }
+    const double two_pi = 6.283185307179586476925;
+    for (int j = 0; j < rotary_dim / 2; ++j) {
+        double f;
+        if (inv_freq) {
+            f = inv_freq[j];
+            if (!std::isfinite(f))
+                return fail(DFLASH_INVALID_ARGUMENT, "inv_freq[%d]=%g must be finite", j, f);
+        } else {
+            f = std::pow(base, -2.0 * j / rotary_dim);
+            double keep = 0.0;
+            if (original_len > 0)
+                keep = std::min(1.0, std::max(0.0, (original_len * f / two_pi - turns_slow) /
+                                                       (turns_fast - turns_slow)));
+            if (factor != 1.0) f = f / factor * (1.0 - keep) + f * keep;
+        }
+        double turns = f / two_pi;
+        turns -= std::floor(turns);                          // whole turns do not show
+        // Two halves of 32 bits, each exact.
+        const double high = std::floor(turns * 4294967296.0);
+        const double low = std::floor((turns * 4294967296.0 - high) * 4294967296.0 + 0.5);
+        frequencies[j] = (int64_t)(((uint64_t)high << 32) + (uint64_t)low);
+    }
+    return ok();
+}
+
+dflash_status dflash_qk_norm_rope(const void* query, const void* key, int dtype,
+                                  const int32_t* positions, int T, int q_heads, int kv_heads,
+                                  int head_dim, long long q_token_stride, long long q_head_stride,
+                                  long long k_token_stride, long long k_head_stride,
+                                  const dflash_norm_rope* how, void* query_out, void* key_out,
+                                  long long q_out_token_stride, long long q_out_head_stride,
+                                  long long k_out_token_stride, long long k_out_head_stride,
+                                  dflash_stream_t stream) {
+    NvtxRange range("dflash_qk_norm_rope");
+    dflash::NormRopeArgs a{};
+    a.query = query; a.key = key; a.dtype = dtype; a.T = T; a.q_heads = q_heads;
+    a.kv_heads = kv_heads; a.head_dim = head_dim; a.positions = positions;
+    a.qt = q_token_stride; a.qh = q_head_stride; a.kt = k_token_stride; a.kh = k_head_stride;
+    a.query_out = query_out; a.key_out = key_out;
+    a.qot = q_out_token_stride; a.qoh = q_out_head_stride;
+    a.kot = k_out_token_stride; a.koh = k_out_head_stride;
+    a.cache.k_scale = a.cache.v_scale = 1.f;
+    if (q_heads < 0 || kv_heads < 0 || q_heads + (long long)kv_heads < 1)
+        return fail(DFLASH_INVALID_ARGUMENT,
+                    "q_heads=%d and kv_heads=%d must be >= 0, and one of them >= 1", q_heads, kv_heads);
+    DFLASH_TRY(check_norm_rope(how, &a));
+    if (kv_heads > 0) {
+        DFLASH_TRY(check_stride(k_out_token_stride, T, 8, "k_out_token_stride"));
+        DFLASH_TRY(check_stride(k_out_head_stride, kv_heads, 8, "k_out_head_stride"));
+    }
+    if (T == 0) return ok();
+    if (kv_heads > 0) DFLASH_TRY(check_ptr(key_out, "key_out"));
+    DFLASH_TRY(check_norm_rope_pointers(a));
+    dflash::DeviceInfo dev;
+    uint32_t* status = nullptr;
+    DFLASH_TRY(current_device(&dev, &status));
+    cudaError_t e = dflash::launch_norm_rope(dev, a, status, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");
+    return ok();
+}
+
+dflash_status dflash_qk_norm_rope_store(
+    const void* query, const void* key, const void* value, int dtype, const int32_t* positions,
+    const int64_t* slots, int T, int q_heads, long long q_token_stride, long long q_head_stride,
+    long long k_token_stride, long long k_head_stride, long long v_token_stride,
+    long long v_head_stride, const dflash_norm_rope* how, const dflash_kv_cache* cache,
+    void* query_out, long long q_out_token_stride, long long q_out_head_stride,
+    dflash_stream_t stream) {
+    NvtxRange range("dflash_qk_norm_rope_store");
+    dflash::NormRopeArgs a{};
+    DFLASH_TRY(check_cache(cache, dtype, &a.cache));
+    a.query = query; a.key = key; a.value = value; a.dtype = dtype; a.T = T; a.q_heads = q_heads;
+    a.kv_heads = a.cache.kv_heads; a.head_dim = a.cache.head_dim; a.positions = positions;
+    a.qt = q_token_stride; a.qh = q_head_stride; a.kt = k_token_stride; a.kh = k_head_stride;
+    a.vt = v_token_stride; a.vh = v_head_stride;
+    a.query_out = query_out; a.qot = q_out_token_stride; a.qoh = q_out_head_stride;
+    a.slots = slots;
+    if (q_heads < 0) return fail(DFLASH_INVALID_ARGUMENT, "q_heads=%d must be >= 0", q_heads);
+    DFLASH_TRY(check_norm_rope(how, &a));
+    DFLASH_TRY(check_stride(v_token_stride, T, 8, "v_token_stride"));
+    DFLASH_TRY(check_stride(v_head_stride, a.kv_heads, 8, "v_head_stride"));
+    if (T == 0) return ok();
+    DFLASH_TRY(check_ptr(value, "value"));
+    DFLASH_TRY(check_ptr8(slots, "slots"));
+    DFLASH_TRY(check_norm_rope_pointers(a));
+    dflash::DeviceInfo dev;
+    uint32_t* status = nullptr;
+    DFLASH_TRY(current_device(&dev, &status));
+    cudaError_t e = dflash::launch_norm_rope(dev, a, status, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "norm, rotation and store launch");
+    return ok();
+}
+
+dflash_status dflash_sample_path(const float* edges, const int32_t* cand_ids, const float* uniforms,
+                                 const float* temperatures, float temperature, int R, int S, int K,
+                                 int32_t* path, int32_t* tokens, float* probs,
+                                 dflash_stream_t stream) {
+    NvtxRange range("dflash_sample_path");
+    if (R < 1 || S < 1 || K < 1)
+        return fail(DFLASH_INVALID_ARGUMENT, "R, S and K must be >= 1 (got R=%d S=%d K=%d)", R, S, K);
+    if (K > 32) return fail(DFLASH_UNSUPPORTED, "K=%d: a path supports K <= 32", K);
+    if (S > dflash::kMaxPathSteps)
+        return fail(DFLASH_UNSUPPORTED, "S=%d: a path supports S <= %d", S, dflash::kMaxPathSteps);
+    DFLASH_TRY(check_temperature(temperatures, temperature));
+    DFLASH_TRY(check_ptr4(edges, "edges"));
+    DFLASH_TRY(check_ptr4(cand_ids, "cand_ids"));
+    DFLASH_TRY(check_ptr4(uniforms, "uniforms"));
+    DFLASH_TRY(check_ptr4(path, "path"));
+    DFLASH_TRY(check_ptr4(tokens, "tokens"));
+    DFLASH_TRY(check_ptr4(probs, "probs"));
+    DFLASH_TRY(current_device(nullptr, nullptr));
+    const dflash::SamplePathArgs a{edges, cand_ids, uniforms, temperatures, temperature, R, S, K,
+                                   path, tokens, probs};
+    cudaError_t e = dflash::launch_sample_path(a, reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "sampled path launch");
+    return ok();
+}
+
+size_t dflash_verify_drafts_workspace_bytes(int R, int T, int V) {
+    if (R < 1 || T < 0 || V < 1) {
+        fail(DFLASH_INVALID_ARGUMENT, "R and V must be >= 1, T >= 0 (got R=%d T=%d V=%d)", R, T, V);
+        return 0;
+    }
+    return dflash::verify_workspace_bytes(R, T, V);
+}
+
+dflash_status dflash_verify_drafts(const void* logits, int dtype, int T, int V, long long row_stride,
+                                   const int32_t* query_start, const int32_t* draft_tokens, int R,
+                                   int S, const int32_t* cand_ids, const float* draft_probs, int K,
+                                   const float* accept_uniforms, const float* sample_uniforms,
+                                   const float* temperatures, float temperature, int32_t* tokens,
+                                   int32_t* counts, float* logprobs, void* workspace,
+                                   size_t workspace_bytes, dflash_stream_t stream) {
+    NvtxRange range("dflash_verify_drafts");
+    if (dtype != DFLASH_BF16 && dtype != DFLASH_FP16 && dtype != DFLASH_FP32)
+        return fail(DFLASH_INVALID_ARGUMENT, "dtype=%d: must be DFLASH_BF16, DFLASH_FP16 or DFLASH_FP32",
+                    dtype);
+    if (T < 0 || V < 1 || R < 1 || S < 0)
+        return fail(DFLASH_INVALID_ARGUMENT, "V and R must be >= 1, T and S >= 0 (got V=%d R=%d T=%d S=%d)",
+                    V, R, T, S);
+    if (S > dflash::kMaxDrafts)
+        return fail(DFLASH_UNSUPPORTED, "S=%d: the verification supports S <= %d", S, dflash::kMaxDrafts);
+    if (T > 1 && row_stride < V)
+        return fail(DFLASH_INVALID_ARGUMENT, "row_stride=%lld must be >= V=%d", row_stride, V);
+    if ((cand_ids == nullptr) != (draft_probs == nullptr) && S > 0)
+        return fail(DFLASH_INVALID_ARGUMENT, "cand_ids and draft_probs must be given together");
+    if (cand_ids && K < 1) return fail(DFLASH_INVALID_ARGUMENT, "K=%d must be >= 1", K);
+    if (cand_ids && K > 32) return fail(DFLASH_UNSUPPORTED, "K=%d: the verification supports K <= 32", K);
+    DFLASH_TRY(check_temperature(temperatures, temperature));
+    DFLASH_TRY(check_ptr4(query_start, "query_start"));
+    DFLASH_TRY(check_ptr4(sample_uniforms, "sample_uniforms"));
+    if (S > 0) {
+        DFLASH_TRY(check_ptr4(draft_tokens, "draft_tokens"));
+        DFLASH_TRY(check_ptr4(accept_uniforms, "accept_uniforms"));
+        if (cand_ids) {
+            DFLASH_TRY(check_ptr4(cand_ids, "cand_ids"));
+            DFLASH_TRY(check_ptr4(draft_probs, "draft_probs"));
+        }
+    }
+    DFLASH_TRY(check_ptr4(tokens, "tokens"));
+    DFLASH_TRY(check_ptr4(counts, "counts"));
+    if (logprobs) DFLASH_TRY(check_ptr4(logprobs, "logprobs"));
+    DFLASH_TRY(check_ptr(workspace, "workspace"));
+    if (T > 0) {
+        if (!logits) return fail(DFLASH_INVALID_ARGUMENT, "logits is NULL");
+        const unsigned size = dtype == DFLASH_FP32 ? 4 : 2;
+        if (reinterpret_cast<uintptr_t>(logits) % size != 0)
+            return fail(DFLASH_INVALID_ARGUMENT, "logits is not %u-byte aligned", size);
+    }
+    const size_t need = dflash::verify_workspace_bytes(R, T, V);
+    if (workspace_bytes < need)
+        return fail(DFLASH_WORKSPACE_TOO_SMALL, "workspace of %zu bytes; %zu needed",
+                    workspace_bytes, need);
+    dflash::DeviceInfo dev;
+    uint32_t* status = nullptr;
+    DFLASH_TRY(current_device(&dev, &status));
+    const dflash::VerifyArgs a{logits, dtype, T, V, row_stride, query_start, draft_tokens, R, S,
+                               cand_ids, draft_probs, K, accept_uniforms, sample_uniforms,
+                               temperatures, temperature, tokens, counts, logprobs};
+    cudaError_t e = dflash::launch_verify(dev, a, workspace, status,
+                                          reinterpret_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "verification launch");
     return ok();
 }
 

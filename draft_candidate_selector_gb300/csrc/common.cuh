@@ -14,6 +14,7 @@ constexpr uint32_t kStatusBadId = 0x1u;     // matches DFLASH_DEVICE_BAD_ID
 constexpr uint32_t kStatusTimeout = 0x2u;   // matches DFLASH_DEVICE_TIMEOUT
 constexpr uint32_t kStatusBadLength = 0x4u; // matches DFLASH_DEVICE_BAD_LENGTH
 constexpr uint32_t kStatusNoPages = 0x8u;   // matches DFLASH_DEVICE_NO_PAGES
+constexpr uint32_t kStatusBadLogits = 0x10u; // matches DFLASH_DEVICE_BAD_LOGITS
 
 // Per-device facts the launchers size their grids with.
 struct DeviceInfo {
@@ -154,6 +155,42 @@ constexpr int kMaxPathSteps = 256;   // steps per request the best path supports
 cudaError_t launch_best_path(const float* edges, const int32_t* cand_ids, int R, int S, int K,
                              int32_t* path, int32_t* tokens, float* score, cudaStream_t stream);
 
+struct SamplePathArgs {
+    const float* edges;
+    const int32_t* cand_ids;
+    const float *uniforms, *temperatures;   // temperatures may be null: `temperature` for all
+    float temperature;
+    int R, S, K;
+    int32_t *path, *tokens;
+    float* probs;
+};
+
+// One CTA per request: a path drawn through E, step by step (K <= 32, S <= kMaxPathSteps).
+cudaError_t launch_sample_path(const SamplePathArgs& a, cudaStream_t stream);
+
+// ---------------------------------------------------------------- verification (verify.cu)
+
+constexpr int kMaxDrafts = 255;      // drafts per request the verification supports
+
+struct VerifyArgs {
+    const void* logits;
+    int dtype, T, V;
+    long long row_stride;
+    const int32_t *query_start, *draft_tokens;
+    int R, S;
+    const int32_t* cand_ids;         // null: each draft was certain
+    const float* draft_probs;
+    int K;
+    const float *accept_uniforms, *sample_uniforms, *temperatures;   // temperatures may be null
+    float temperature;
+    int32_t *tokens, *counts;
+    float* logprobs;                 // may be null
+};
+
+size_t verify_workspace_bytes(int R, int T, int V);
+cudaError_t launch_verify(const DeviceInfo& dev, const VerifyArgs& a, void* workspace,
+                          uint32_t* status_word, cudaStream_t stream);
+
 // ---------------------------------------------------------------- paged cache (kvcache.cu)
 
 constexpr int kMaxTableRequests = 16384;   // requests whose running sums fit in shared memory
@@ -170,7 +207,7 @@ cudaError_t launch_block_tables(const DeviceInfo& dev, const BlockTableArgs& a,
                                 uint32_t* status_word, cudaStream_t stream);
 
 // Element types, as in dflash_dtype.
-enum : int { kBf16 = 0, kFp16 = 1, kE4m3 = 2 };
+enum : int { kBf16 = 0, kFp16 = 1, kE4m3 = 2, kFp32 = 3 };
 
 // A cache as in dflash_kv_cache (strides in elements).
 struct KvCache {
@@ -185,6 +222,29 @@ cudaError_t launch_store_kv(const DeviceInfo& dev, const void* key, const void* 
                             long long key_head_stride, long long value_token_stride,
                             long long value_head_stride, const KvCache& cache,
                             uint32_t* status_word, cudaStream_t stream);
+
+// ---------------------------------------------------------------- norm and rotation (rope.cu)
+
+struct NormRopeArgs {
+    const void *query, *key, *value;                 // value: only with slots
+    int dtype, T, q_heads, kv_heads, head_dim;
+    long long qt, qh, kt, kh, vt, vh;                // strides in elements
+    const int32_t* positions;
+    const void *q_weight, *k_weight;                 // null: not normed
+    int weight_dtype;
+    float eps;
+    const int64_t* frequencies;                      // [rotary_dim / 2] turns, as 2^-64ths
+    int rotary_dim;
+    bool interleaved;
+    float rope_scale;
+    void *query_out, *key_out;
+    long long qot, qoh, kot, koh;
+    const int64_t* slots;                            // null: keys go to key_out, there are no values
+    KvCache cache;                                   // with slots
+};
+
+cudaError_t launch_norm_rope(const DeviceInfo& dev, const NormRopeArgs& a, uint32_t* status_word,
+                             cudaStream_t stream);
 
 // ---------------------------------------------------------------- attention (attention*.cu)
 

@@ -1,4 +1,4 @@
-// path.cu: the best path through each request's edge scores.
+// path.cu: paths through each request's edge scores: the best one, and one drawn at random.
 //
 // Reading (the pages show no consumer of the edge scores): page
 // "vllm.models.beam.nvidia.dflash2", module docstring: the selector rescores the top-k tokens
@@ -24,7 +24,13 @@
 // takes the last step's choice and walks the kept predecessors back; the threads then write
 // the path and its token ids in parallel. Reads R*S*K*K*4 bytes of E once. No waits on other
 // CTAs.
+//
+// The drawn path takes the edge scores as the drafter's own distribution of each token given the
+// one before it, softmax over c of E[r,p,c_{p-1},c] / T, and inverts its running sum at a number that
+// the caller drew. Staged through the same ring; one warp follows the path while the others copy.
 #include "common.cuh"
+
+#include <cmath>
 
 namespace dflash {
 namespace {
@@ -193,7 +199,113 @@ best_path_kernel(const float* __restrict__ edges, const int32_t* __restrict__ ca
     }
 }
 
+// ---------------------------------------------------------------- a drawn path
+//
+//   w_c = exp((E[p, c_{p-1}, c] - max) / T),  c_p = the smallest c with sum_{j<=c} w_j > u_p sum_j w_j
+//
+// The choice is the one that exact sums give. Sums are taken in fp32 first, and where u_p sum_j w_j
+// lies within kSlack of the sum from one of the borders, again in fp64. The fp32 error: exponents are
+// sums of two floats, expf is within 2^-23, its product with the lower part and the scan's five
+// additions 6 * 2^-24; the border's product 2^-24: in all below 2^-20 of the sum. A few choices in a
+// hundred thousand are taken again.
+//
+// Bound by latency: S dependent choices of a warp, each a maximum, an exponential and a scan.
+constexpr float kSlack = 0x1p-19f;
+
+// The order of floats as unsigned numbers; NaN lowest.
+__device__ __forceinline__ uint32_t order_of(float x) {
+    const uint32_t b = __float_as_uint(x);
+    return x != x ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+
+// The first lane whose running sum of w passes u times the sum of all; the last with w > 0 if none does.
+template <typename F>
+__device__ __forceinline__ int invert(F w, F u, int lane, F& total, F& run) {
+    run = w;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const F other = __shfl_up_sync(kFull, run, d);
+        if (lane >= d) run += other;
+    }
+    total = __shfl_sync(kFull, run, 31);
+    const unsigned past = __ballot_sync(kFull, run > u * total), any = __ballot_sync(kFull, w > F(0));
+    return past ? __ffs(past) - 1 : 31 - __clz(any | 1u);
+}
+
+__global__ void __launch_bounds__(kThreads) sample_path_kernel(SamplePathArgs a) {
+    extern __shared__ __align__(16) uint8_t path_smem[];
+    const int tid = threadIdx.x, lane = tid & 31, K = a.K, S = a.S;
+    const long long r = blockIdx.x;
+    float* ring = reinterpret_cast<float*>(path_smem);                        // [kDepth][K*K]
+    float* u = reinterpret_cast<float*>(path_smem + path_ring_bytes(K));      // [S]
+    uint8_t* chosen = reinterpret_cast<uint8_t*>(u + S);                      // [S]
+    const float* E = a.edges + (size_t)r * S * K * K;
+    const bool wide = (K & 1) == 0 && (reinterpret_cast<uintptr_t>(a.edges) & 15) == 0;
+    for (int p = 0; p < kDepth; ++p) {
+        if (p < S) stage_step(ring, E, p, K, tid, wide);
+        cp_async_commit();
+    }
+    for (int p = tid; p < S; p += kThreads) u[p] = fminf(fmaxf(a.uniforms[(size_t)r * S + p], 0.f), 1.f - 0x1p-24f);
+    float t = a.temperatures ? a.temperatures[r] : a.temperature;
+    const bool greedy = !(t > 0.f);                      // NaN too
+    t = fmaxf(t, 0x1p-100f);
+    // 1 / T in two floats.
+    const float inv_t = greedy ? 0.f : 1.f / t;
+    const float inv_low = t < 0x1p60f ? inv_t * fmaf(-t, inv_t, 1.f) : 0.f;
+    int before = 0;                                      // the row of step 0 is q = 0
+    for (int p = 0; p < S; ++p) {
+        cp_async_wait_ring();
+        __syncthreads();
+        if (p >= 1) {
+            if (p - 1 + kDepth < S) stage_step(ring, E, p - 1 + kDepth, K, tid, wide);
+            cp_async_commit();
+        }
+        if (tid >= 32) continue;
+        const float e = lane < K ? ring[(size_t)(p % kDepth) * K * K + before * K + lane] + 0.f : NAN;   // no -0
+        const uint32_t order = order_of(e), top = __reduce_max_sync(kFull, order);
+        // the largest score (of a row with one): its first lane
+        const int first = __ffs(__ballot_sync(kFull, order == top)) - 1;
+        const float m = __shfl_sync(kFull, e, first);
+        float prob = lane == first ? 1.f : 0.f;
+        int pick = first;
+        if (!greedy && fabsf(m) < INFINITY) {            // else nothing to draw from: the largest
+            float w = 0.f;
+            if (e > -INFINITY) {
+                // z in two floats; exp(z_low) = 1 + z_low
+                const float d = __fsub_rn(e, m), back = __fsub_rn(d, e);
+                const float d_low = __fsub_rn(__fsub_rn(e, __fsub_rn(d, back)), __fadd_rn(m, back));
+                const float z = __fmul_rn(d, inv_t);
+                const float z_low = fmaf(d, inv_low, fmaf(d_low, inv_t, fmaf(d, inv_t, -z)));
+                w = expf(z);
+                if (z > -100.f) w = fmaf(w, z_low, w);
+            }
+            float total, run;
+            pick = invert(w, u[p], lane, total, run);
+            prob = w / total;
+            if (__any_sync(kFull, lane < K && fabsf(run - u[p] * total) <= kSlack * total)) {
+                double wd = e > -INFINITY ? exp(((double)e - (double)m) / (double)t) : 0.0, td, rd;
+                pick = invert(wd, (double)u[p], lane, td, rd);
+            }
+        }
+        if (lane < K) a.probs[((size_t)r * S + p) * K + lane] = prob;
+        if (lane == 0) chosen[p] = (uint8_t)pick;
+        before = pick;
+    }
+    __syncthreads();
+    for (int p = tid; p < S; p += kThreads) {
+        const int c = chosen[p];
+        a.path[(size_t)r * S + p] = c;
+        a.tokens[(size_t)r * S + p] = a.cand_ids[((size_t)r * S + p) * K + c];
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_sample_path(const SamplePathArgs& a, cudaStream_t stream) {
+    const size_t smem = path_ring_bytes(a.K) + (((size_t)a.S * 5 + 15) & ~(size_t)15);
+    sample_path_kernel<<<(unsigned)a.R, kThreads, smem, stream>>>(a);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_best_path(const float* edges, const int32_t* cand_ids, int R, int S, int K,
                              int32_t* path, int32_t* tokens, float* score, cudaStream_t stream) {

@@ -11,9 +11,12 @@
  *      E[r,p,q,c] = unary[r,p,c] + <pred_cb[cand[r,p-1,q]] * h_p, succ_cb[cand[r,p,c]]>,
  *      where the predecessor at p = 0 is the request's anchor token.
  *                                        DFlash2BeamCandidateSelector (class docstring)
- * Before them, the paged key-value cache of the draft step's attention: its block tables
- * (dflash_block_tables), its store (dflash_store_kv) and the attention over it
- * (dflash_paged_attention).
+ * Before them, the norm and rotation of queries and keys (dflash_qk_norm_rope) and the paged
+ * key-value cache of the draft step's attention: its block tables (dflash_block_tables), its store
+ * (dflash_store_kv, or in one pass with the norm and rotation, dflash_qk_norm_rope_store) and the
+ * attention over it (dflash_paged_attention). Behind them, drafts drawn from the edge scores
+ * (dflash_sample_path) and their verification against the target model's logits
+ * (dflash_verify_drafts).
  * Around these: step 1 straight from the LM head without logits in memory
  * (dflash_lmhead_topk, dflash_selector_lmhead), steps 2 and 3 on given candidates
  * (dflash_selector_forward), and the best path through E (dflash_best_path, a reading: the
@@ -71,6 +74,7 @@ typedef enum {
 #define DFLASH_DEVICE_BAD_LENGTH 0x4u   /* a request's lengths contradict each other or  */
                                         /* do not fit its row of the block table         */
 #define DFLASH_DEVICE_NO_PAGES 0x8u     /* the list of free pages was too short          */
+#define DFLASH_DEVICE_BAD_LOGITS 0x10u  /* a row of logits has a NaN or +inf, or only -inf */
 
 /* A static string naming a status code. Never NULL. */
 const char* dflash_status_string(int status);
@@ -301,6 +305,83 @@ dflash_status dflash_best_path(const float* edges, const int32_t* cand_ids, int 
                                dflash_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
+ * A path through the edge scores drawn at random: the drafter's own distribution of each token,
+ * given the one before it, is the softmax of that token's row of edge scores.
+ * Reading: as for dflash_best_path, the pages do not show what consumes the scores; sampled drafts
+ * need a distribution, which the verification of drafts then takes away.
+ *
+ * edges, cand_ids  as in dflash_best_path
+ * uniforms     [R, S]    float  numbers drawn evenly from [0, 1), one for each choice
+ * temperatures [R]       float  each request's T; or NULL, and `temperature` is T for all
+ * path         [R, S]    int32  out: the chosen candidate index c_p at each step
+ * tokens       [R, S]    int32  out: cand_ids[r, p, c_p]
+ * probs        [R, S, K] float  out: the distribution that c_p was drawn from
+ *
+ * With the row E[r, p, c_{p-1}, :] (at p = 0: q = 0), probs[c] = w_c / sum_j w_j, w_c =
+ * exp((E_c - max E) / T), and c_p is the smallest c with sum_{j<=c} w_j > u sum_j w_j. The choice is
+ * made as with exact sums (it may differ where a sum is within 2^-45 of the border); probs are fp32.
+ * T below 2^-100 counts as 2^-100.
+ * T = 0 takes the largest score (so do T < 0 and NaN), the first of equals, with probability 1; a row
+ * whose largest score is +inf, or which has none but -inf and NaN, is taken the same way. In other rows
+ * NaN scores have no weight. A uniform outside [0, 1) counts as the nearer end, NaN as 0. Weights
+ * below 2^-126 of the largest may count as 0. Requires 1 <= K <= 32 and S <= 256
+ * (DFLASH_UNSUPPORTED beyond). No workspace.
+ * ---------------------------------------------------------------------------------- */
+dflash_status dflash_sample_path(const float* edges, const int32_t* cand_ids, const float* uniforms,
+                                 const float* temperatures, float temperature, int R, int S, int K,
+                                 int32_t* path, int32_t* tokens, float* probs,
+                                 dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Verification of drafted tokens against the target model's logits.
+ * Source: DFlashSpeculator.propose hands its draft tokens to the target model; how that one takes or
+ * leaves them is not on the pages. This is the standard rule, which keeps the target's distribution
+ * whatever the drafter's is.
+ *
+ * logits       [T, V] of type dtype (DFLASH_BF16, DFLASH_FP16 or DFLASH_FP32), rows at row_stride
+ *              elements: the target's logits of a step's new tokens. Natural alignment suffices.
+ * query_start  [R + 1] int32, as dflash_block_tables writes it: request r has the rows from
+ *              query_start[r] to query_start[r + 1] - 1, one for its last token and one for each of its
+ *              drafts, n_r rows for n_r - 1 <= S drafts. No rows: nothing is done for the request.
+ * draft_tokens [R, S] int32: draft i was made for row i's place, token i + 1 of the request's step
+ * cand_ids     [R, S, K] int32 and draft_probs [R, S, K] float: the distribution q that each draft was
+ *              drawn from, as dflash_sample_path gives it (an id that occurs twice has the sum); both
+ *              NULL: each draft was certain
+ * accept_uniforms [R, S], sample_uniforms [R] float  numbers drawn evenly from [0, 1)
+ * temperatures [R] float  each request's T; or NULL, and `temperature` is T for all
+ * tokens       [R, S + 1] int32  out: the drafts that were taken, one token behind them, then -1
+ * counts       [R] int32         out: how many tokens that is, 0 for a request without rows
+ * logprobs     [R, S + 1] float  out: log p of each token under the target (0 behind them), or NULL
+ * workspace    at least dflash_verify_drafts_workspace_bytes(R, T, V) bytes; its contents on entry do
+ *              not matter
+ *
+ * With p = softmax(logits / T) of row i, draft x is taken iff u q(x) < p(x). In the row of the first that
+ * is not, a token is drawn from max(p - q, 0), normalised (from p, should nothing be left); if all
+ * are taken, from p of the last row. Drawn: the smallest v with sum_{j<=v} weight_j > u sum_j weight_j.
+ * Tokens are those of exact arithmetic; only where a border is within about 2^-40 of a row's sum may
+ * they differ. T = 0 (so T < 0 and NaN): p is 1 at the first of the row's largest logits; T counts as at least 2^-99 and at
+ * most 2^100. Masked
+ * logits may be -inf or the type's lowest value; weights below 2^-126 of the largest may count as 0.
+ * A sample uniform outside [0, 1) counts as the nearer end, NaN as 0.
+ * A row that is reached and has a NaN, +inf or nothing but -inf ends its request without a token
+ * (DFLASH_DEVICE_BAD_LOGITS). A draft that is reached and is outside [0, V) is not taken, a candidate
+ * that is outside is left out of q, and DFLASH_DEVICE_BAD_ID is set. A request whose rows are out of
+ * order, past T or more than S + 1 is refused: count 0, tokens -1 (DFLASH_DEVICE_BAD_LENGTH). Rows
+ * behind a request's first rejected draft have no effect. Rows at and behind query_start[R] are not read.
+ * 0 <= S <= 255, K <= 32 (DFLASH_UNSUPPORTED beyond). Equal calls give equal bits. It can be captured
+ * in a CUDA graph.
+ * ---------------------------------------------------------------------------------- */
+size_t dflash_verify_drafts_workspace_bytes(int R, int T, int V);
+
+dflash_status dflash_verify_drafts(const void* logits, int dtype, int T, int V, long long row_stride,
+                                   const int32_t* query_start, const int32_t* draft_tokens, int R,
+                                   int S, const int32_t* cand_ids, const float* draft_probs, int K,
+                                   const float* accept_uniforms, const float* sample_uniforms,
+                                   const float* temperatures, float temperature, int32_t* tokens,
+                                   int32_t* counts, float* logprobs, void* workspace,
+                                   size_t workspace_bytes, dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
  * The paged key-value cache that the drafter and the target model attend to. A cache is a
  * pool of pages of page_size token rows; a request owns the pages that its row of the block
  * table lists, and token j of it lives in row j % page_size of its page j / page_size. A slot
@@ -314,7 +395,8 @@ dflash_status dflash_best_path(const float* edges, const int32_t* cand_ids, int 
 typedef enum {
     DFLASH_BF16 = 0,
     DFLASH_FP16 = 1,
-    DFLASH_E4M3 = 2    /* 8-bit floating point, 4 exponent bits, no infinities (cache only) */
+    DFLASH_E4M3 = 2,   /* 8-bit floating point, 4 exponent bits, no infinities (cache only) */
+    DFLASH_FP32 = 3    /* norm weights and logits only */
 } dflash_dtype;
 
 /* One layer's cache: key and value hold [num_pages, page_size, kv_heads, head_dim] elements
@@ -397,6 +479,80 @@ dflash_status dflash_store_kv(const void* key, const void* value, int dtype, con
                               int T, long long key_token_stride, long long key_head_stride,
                               long long value_token_stride, long long value_head_stride,
                               const dflash_kv_cache* cache, dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Rotation frequencies, as the calls below take them: the turns that pair j of a head makes from
+ * one position to the next, f_j / (2 pi) modulo 1, as a whole number of 2^-64. Angles are then exact
+ * modulo one turn at every position of 32 bits.
+ *
+ * inv_freq     host, [rotary_dim / 2] radians per position; or NULL, and then
+ *              f_j = base^(-2 j / rotary_dim), for long contexts divided by factor: every pair if
+ *              original_len is 0; else a pair that makes at most turns_slow turns over original_len
+ *              positions is, one that makes turns_fast or more is not, and in between f_j goes over
+ *              linearly in the number of turns from the one to the other.
+ * frequencies  host, [rotary_dim / 2] out: copy them to device memory
+ * A host function: no device is needed, and nothing is launched.
+ * ---------------------------------------------------------------------------------- */
+dflash_status dflash_rope_frequencies(int rotary_dim, double base, double factor,
+                                      double original_len, double turns_slow, double turns_fast,
+                                      const double* inv_freq, int64_t* frequencies);
+
+/* What is done to queries and keys. A host struct; the calls read it before they return. */
+typedef struct {
+    const void* q_weight;       /* [head_dim], or NULL: queries are not normed              */
+    const void* k_weight;       /* [head_dim], or NULL: keys are not normed                 */
+    int weight_dtype;           /* the type of queries and keys, or DFLASH_FP32             */
+    float eps;                  /* >= 0                                                     */
+    const int64_t* frequencies; /* device, [rotary_dim / 2]; not read if rotary_dim is 0    */
+    int rotary_dim;             /* even, 0 (no rotation) to head_dim                        */
+    int interleaved;            /* pairs (2j, 2j + 1); 0: pairs (j, j + rotary_dim / 2)     */
+    float rope_scale;           /* factor of the rotated values (1: a plain rotation)       */
+} dflash_norm_rope;
+
+/* ------------------------------------------------------------------------------------
+ * Norm of each query and key head, then its rotation by position, in one pass.
+ * Source: beam_qk_norm_rope (DFlash2BeamAttention): RMS norm of queries and keys for each head, then
+ * their rotation. The pages show the call; the arithmetic is the standard one:
+ *   y = x w / sqrt(mean(x^2) + eps) over a head's head_dim values (no norm where the weight is NULL),
+ *   (a, b) -> rope_scale (a cos t - b sin t, b cos t + a sin t), t = positions[token] f_j,
+ * for the pairs j of the first rotary_dim values; the others stay as they are (normed).
+ *
+ * query, key  [T, q_heads, head_dim], [T, kv_heads, head_dim] of type dtype (DFLASH_BF16 or
+ *             DFLASH_FP16) at the given strides (elements, multiples of 8). Either may have no heads.
+ * positions   [T] int32, of any sign; not read if rotary_dim is 0
+ * query_out, key_out  out, of the same shapes and type at their own strides. Each may be its own input
+ *             (the same address and strides); else outputs must not overlap inputs.
+ * Sums and products are fp32, rounded once at the end. head_dim is a multiple of 8 up to 256. A head
+ * whose sum of squares passes fp32's range is taken 2^-72 as large (eps then counts as 0). T = 0
+ * does nothing. One launch, no workspace.
+ * ---------------------------------------------------------------------------------- */
+dflash_status dflash_qk_norm_rope(const void* query, const void* key, int dtype,
+                                  const int32_t* positions, int T, int q_heads, int kv_heads,
+                                  int head_dim, long long q_token_stride, long long q_head_stride,
+                                  long long k_token_stride, long long k_head_stride,
+                                  const dflash_norm_rope* how, void* query_out, void* key_out,
+                                  long long q_out_token_stride, long long q_out_head_stride,
+                                  long long k_out_token_stride, long long k_out_head_stride,
+                                  dflash_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * The same, with keys and values stored in the paged cache in the same pass.
+ * Source: beam_qk_norm_rope with a slot mapping; and precompute_and_store_context_kv, which norms,
+ * rotates and stores the context's keys without queries (q_heads = 0).
+ *
+ * value, slots, cache  as in dflash_store_kv. Keys go to the cache rounded once: what a call of
+ *                      dflash_qk_norm_rope and one of dflash_store_kv give, but into an e4m3 cache
+ *                      without a rounding to dtype before that to e4m3.
+ * query, positions, how, query_out  as in dflash_qk_norm_rope
+ * Queries of tokens whose slot is negative or outside the cache are written as any others.
+ * ---------------------------------------------------------------------------------- */
+dflash_status dflash_qk_norm_rope_store(
+    const void* query, const void* key, const void* value, int dtype, const int32_t* positions,
+    const int64_t* slots, int T, int q_heads, long long q_token_stride, long long q_head_stride,
+    long long k_token_stride, long long k_head_stride, long long v_token_stride,
+    long long v_head_stride, const dflash_norm_rope* how, const dflash_kv_cache* cache,
+    void* query_out, long long q_out_token_stride, long long q_out_head_stride,
+    dflash_stream_t stream);
 
 /* ------------------------------------------------------------------------------------
  * Attention of new tokens over the paged cache, which holds their own keys and values too.
