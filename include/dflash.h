@@ -356,12 +356,12 @@ dflash_status dflash_sample_path(const float* edges, const int32_t* cand_ids, co
  *              not matter
  *
  * With p = softmax(logits / T) of row i, draft x is taken iff u q(x) < p(x). In the row of the first that
- * is not, a token is drawn from max(p - q, 0), normalised (from p, should nothing be left); if all
+ * is not, a token is drawn from max(p - q, 0), normalised (from p, should less than 2^-36 be left); if all
  * are taken, from p of the last row. Drawn: the smallest v with sum_{j<=v} weight_j > u sum_j weight_j.
- * Tokens are those of exact arithmetic; only where a border is within about 2^-40 of a row's sum may
+ * Tokens are those of exact arithmetic; only where a border is within about 2^-38 of a row's sum may
  * they differ. T = 0 (so T < 0 and NaN): p is 1 at the first of the row's largest logits; T counts as at least 2^-99 and at
  * most 2^100. Masked
- * logits may be -inf or the type's lowest value; weights below 2^-126 of the largest may count as 0.
+ * logits may be -inf or the type's lowest value; weights below 2^-125 of the largest may count as 0.
  * A sample uniform outside [0, 1) counts as the nearer end, NaN as 0.
  * A row that is reached and has a NaN, +inf or nothing but -inf ends its request without a token
  * (DFLASH_DEVICE_BAD_LOGITS). A draft that is reached and is outside [0, V) is not taken, a candidate

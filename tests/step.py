@@ -154,7 +154,7 @@ def verify(logits, query_start, drafts, accept, sample, ids, probs, temperatures
                     counts[r] = i + 1
                     continue
                 rest = np.maximum(p - q, 0)
-                if math.fsum(rest) > 2.0 ** -40:
+                if math.fsum(rest) > 2.0 ** -36:
                     p = rest
             u = clamp_uniform(sample[r].double())
             so_far = np.cumsum(p)
