@@ -28,6 +28,7 @@
 // its draft is surely rejected, and later rows of that request are passed over.
 // Bound by HBM: the rows up to the first rejected draft are read once.
 #include "common.cuh"
+#include "ptx.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -36,6 +37,7 @@
 #include <cfloat>
 #include <climits>
 #include <cmath>
+#include <mutex>
 #include <type_traits>
 
 namespace dflash {
@@ -88,13 +90,6 @@ __device__ __forceinline__ float to_float(float x) { return x; }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 
-// 2^x, within 2^-22 of it; results below 2^-126 are 0.
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // A row's tiles. The row starts `head` elements before its first 16-byte boundary; tile 0 also has
 // those, and tile t has the elements from first(t) to first(t + 1), so every other tile starts on one.
 constexpr int kVecs = 8;                         // 16-byte vectors of a tile a lane holds
@@ -115,23 +110,38 @@ struct Row {
     // the tile of element v
     __device__ __forceinline__ int tile_of(int v) const { return v < head ? 0 : (v - head) / kTile; }
 
-    // Tile t's whole vectors, a warp's lanes side by side, -inf where there are none; and of the elements
-    // at its ends that are in none, at most one a lane, or -inf.
-    __device__ __forceinline__ void load(int t, int lane, uint4 (&v)[kVecs], float& edge) const {
-        const int hi = first(t + 1), body = t == 0 ? min(head, hi) : first(t), n = hi - body;
-        const uint32_t low = sizeof(T) == 4 ? 0xff800000u
-                                            : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
-        const T* base = x + body;
+    // Elements of tile t that start on a boundary: from, and how many.
+    __device__ __forceinline__ int body(int t, int& n) const {
+        const int hi = first(t + 1), from = t == 0 ? min(head, hi) : first(t);
+        n = hi - from;
+        return from;
+    }
+    // Tile t's whole vectors, a warp's lanes side by side, -inf where there are none. from: the first, in
+    // the row or in a copy of it.
+    __device__ __forceinline__ void load(int t, int lane, const uint4* from, uint4 (&v)[kVecs]) const {
+        constexpr uint32_t low = sizeof(T) == 4 ? 0xff800000u
+                                                : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+        int n;
+        body(t, n);
+        from += lane;
+        if (n == kTile) {
+#pragma unroll
+            for (int k = 0; k < kVecs; ++k) v[k] = from[32 * k];
+            return;
+        }
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            const int e = (k * 32 + lane) * kN;
             v[k] = make_uint4(low, low, low, low);
-            if (e + kN <= n) v[k] = __ldcs(reinterpret_cast<const uint4*>(base + e));
+            if ((k * 32 + lane) * kN + kN <= n) v[k] = from[32 * k];
         }
-        edge = -INFINITY;
-        const int rest = n & (kN - 1);
-        if (t == 0 && lane < head && lane < hi) edge = to_float(x[lane]);
-        if (lane >= 16 && lane - 16 < rest) edge = to_float(base[n - rest + lane - 16]);
+    }
+    // Of the elements of tile t that are in no whole vector, at most one a lane, or -inf.
+    __device__ __forceinline__ float edge(int t, int lane) const {
+        int n;
+        const int from = body(t, n), rest = n & (kN - 1);
+        if (t == 0 && lane < head && lane < from) return to_float(x[lane]);
+        if (lane >= 16 && lane - 16 < rest) return to_float(x[from + n - rest + lane - 16]);
+        return -INFINITY;
     }
 };
 
@@ -160,20 +170,39 @@ struct Unsettled {
     unsigned arrived;  // CTAs that are done with their tiles
 };
 
+// Quotients by a fixed divisor, of numbers below 2^31: with l = ceil(log2 d) and m = floor(2^32 (2^l - d)
+// / d) + 1, n / d is the upper half of m n, plus n, shifted by l.
+struct Divisor {
+    unsigned m;
+    int l;
+    Divisor(unsigned d = 1) {
+        for (l = 0; (1ull << l) < d;) ++l;
+        m = (unsigned)(((1ull << 32) * ((1ull << l) - d)) / d + 1);
+    }
+    __device__ __forceinline__ unsigned of(unsigned n) const { return (__umulhi(m, n) + n) >> l; }
+};
+
 struct VerifyPlan {
     VerifyArgs a;
     int tiles;                // of a row
-    float2* sums;             // [T][tiles]: the largest logit, the sum of exp((x - it) / T); settle: a double
+    int chunks;               // items of a row: kSumWarps tiles each
+    float2* sums;             // [T][tiles]: the largest logit, the sum of exp((x - it) / T); a listed row's: a double
     Unsettled* list;          // [R]
     unsigned* listed;         // how many
-    uint32_t* dead;           // [R] a row at and before the first rejected; null: rows are not left out
-    uint32_t* arrived;        // [T] tiles of the row that are done, less one (as a wrapped number)
+    // Where rows may be passed over (else null), by position and request, [S + 1][padded]:
+    int* alive;               // [padded] the request's last row that may be needed, -1: none
+    int* handed;              // groups of items that were handed out, less one
+    int padded;               // R, to a multiple of 4
+    int group, groups;        // items that are handed out at a time, and such groups in a row
+    int window;               // rows that items are taken of at a time
+    Divisor by_chunks, by_R, by_padded;
 };
 
+// NaN is passed over.
 __device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, d));
-    return x;
+    float y;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+    return y;
 }
 template <typename F>
 __device__ __forceinline__ F warp_sum(F x) {
@@ -183,29 +212,28 @@ __device__ __forceinline__ F warp_sum(F x) {
 }
 
 // The largest logit of a row and the sum of its weights relative to it, from the tiles' sums, by a
-// warp. The sum is NaN where the row has a NaN or +inf, and 0 where all of it is -inf.
-__device__ __forceinline__ void join_tiles(const float2* sums, int tiles, float c, int lane, float& M,
+// warp. The sum is NaN where the row has a NaN or +inf, and 0 where all of it is -inf. False if a tile's
+// is not there yet.
+__device__ __forceinline__ bool join_tiles(const float2* sums, int tiles, float c, int lane, float& M,
                                            float& Z) {
-    constexpr int kHeld = 8;
-    float2 s[kHeld];
+    bool there = true;
     M = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-        s[k] = make_float2(-INFINITY, 0.f);
-        if (k * 32 + lane < tiles) s[k] = __ldcg(&sums[k * 32 + lane]);
+#pragma unroll 4
+    for (int t = lane; t < tiles; t += 32) {
+        const float m = __ldcg(&sums[t]).x;
+        there &= __float_as_uint(m) != 0xffffffffu;
+        M = fmaxf(M, m);
     }
-    for (int t = kHeld * 32 + lane; t < tiles; t += 32) M = fmaxf(M, __ldcg(&sums[t].x));
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) M = fmaxf(M, s[k].x);
+    if (!__all_sync(kFull, there)) return false;
     M = warp_max(M);
     Z = 0.f;
-    auto part = [&](float2 x) {
-        return x.y * (x.x == -INFINITY ? (x.y == x.y ? 0.f : 1.f) : exp2_fast((x.x - M) * c));
-    };
-#pragma unroll
-    for (int k = 0; k < kHeld; ++k) Z += part(s[k]);
-    for (int t = kHeld * 32 + lane; t < tiles; t += 32) Z += part(__ldcg(&sums[t]));
+#pragma unroll 4
+    for (int t = lane; t < tiles; t += 32) {
+        const float2 x = __ldcg(&sums[t]);
+        Z += x.y * (x.x == -INFINITY ? (x.y == x.y ? 0.f : 1.f) : ptx::ex2((x.x - M) * c));
+    }
     Z = warp_sum(Z);
+    return true;
 }
 
 // q of token x in row (r, i), by a warp.
@@ -225,8 +253,11 @@ __device__ __forceinline__ F draft_probability(const VerifyArgs& a, long long at
 // an exponential, additions) no more than that again. In all below 2^-17 for V < 2^31.
 constexpr float kSlack = 0x1p-16f;
 
-constexpr int kSumThreads = 256;
-constexpr int kSumWarps = kSumThreads / 32;
+enum : int { kTaken = 0, kRejected = 1, kUnsure = 2, kBad = 3 };   // drafts
+
+constexpr int kSumWarps = 8;
+constexpr int kSumBlocks = 2;                    // CTAs of an SM
+constexpr int kSumThreads = 32 * (kSumWarps + 2);
 
 template <typename T>
 __device__ __forceinline__ float largest(const uint4 (&v)[kVecs]);
@@ -263,116 +294,326 @@ __device__ __forceinline__ float largest<__half>(const uint4 (&v)[kVecs]) {
 template <typename T>
 __device__ __forceinline__ float weight_sum(const uint4 (&v)[kVecs], float m, float c) {
     constexpr int kN = Vec<T>::kN;
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
     const float mc = __fmul_rn(m, c);
     if (fabsf(mc) < 0x1p60f) {
-        // x c - mc in one rounding; mc's own is taken back at the end.
+        // x c - mc in one rounding, two at a time; mc's own is taken back at the end.
+        const uint64_t cc = ptx::pair_of(c, c), mm = ptx::pair_of(-mc, -mc);
+        uint64_t s[2] = {0, 0};
 #pragma unroll
         for (int i = 0; i < kVecs; ++i) {
             float x[kN];
             Vec<T>::widen(v[i], x);
 #pragma unroll
-            for (int e = 0; e < kN; ++e) s[e & 3] += exp2_fast(fmaf(x[e], c, -mc));
+            for (int e = 0; e < kN; e += 2) {
+                const float2 z = ptx::halves_of(ptx::fma_pair(ptx::pair_of(x[e], x[e + 1]), cc, mm));
+                s[e / 2 & 1] = ptx::add_pair(s[e / 2 & 1], ptx::pair_of(ptx::ex2(z.x), ptx::ex2(z.y)));
+            }
         }
-        return ((s[0] + s[1]) + (s[2] + s[3])) * exp2_fast(-fmaf(m, c, -mc));
+        const float2 both = ptx::halves_of(ptx::add_pair(s[0], s[1]));
+        return (both.x + both.y) * ptx::ex2(-fmaf(m, c, -mc));
     }
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
     const float ref = fmaxf(m, -FLT_MAX);
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
         float x[kN];
         Vec<T>::widen(v[i], x);
 #pragma unroll
-        for (int e = 0; e < kN; ++e) s[e & 3] += exp2_fast((x[e] - ref) * c);
+        for (int e = 0; e < kN; ++e) s[e & 3] += ptx::ex2((x[e] - ref) * c);
     }
     return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
-// Whether draft i of request r, in a row whose tiles are all done, is surely rejected. A warp.
+// Whether draft i of request r is surely rejected; kUnsure if not all of its row's sums are there. A warp.
+// Sums are 8 bytes, written at once, and are all ones before: each tells by itself that it is there, and no
+// order between them is needed.
 template <typename T>
-__device__ __noinline__ bool surely_rejected(const VerifyPlan& p, int r, int i, long long row) {
+__device__ __noinline__ int judge(const VerifyPlan& p, int r, int i, long long row) {
     const VerifyArgs& a = p.a;
     const int lane = threadIdx.x & 31;
     const Temperature temp(a, r);
+    const float2* sums = p.sums + row * p.tiles;
     float M, Z;
-    join_tiles(p.sums + row * p.tiles, p.tiles, temp.c, lane, M, Z);
-    if (!(Z > 0.f)) return true;                     // no distribution: the request ends here
+    if (!join_tiles(sums, p.tiles, temp.c, lane, M, Z)) return kUnsure;
+    if (!(Z > 0.f)) return kRejected;                // no distribution: the request ends here
     const long long draft = (long long)r * a.S + i;
     const int token = a.draft_tokens[draft];
-    if ((unsigned)token >= (unsigned)a.V) return true;
+    if ((unsigned)token >= (unsigned)a.V) return kRejected;
     const float l = to_float(Row<T>(a, row).x[token]);
-    if (temp.greedy) return l < M;
+    if (temp.greedy) return l < M ? kRejected : kTaken;
     const float q = draft_probability<float>(a, draft, token, lane);
     const float z = (l - M) * temp.c;
-    const float w = exp2_fast(z), uq = a.accept_uniforms[draft] * q * Z;
-    return uq > w * (1.f + kSlack - z * 0x1p-20f) + kSlack * uq;
+    const float w = ptx::ex2(z), uq = a.accept_uniforms[draft] * q * Z;
+    return uq > w * (1.f + kSlack - z * 0x1p-20f) + kSlack * uq ? kRejected : kTaken;
 }
 
-// A warp takes tiles at the distance of all warps, rows of the requests' first drafts first. Whether a
-// tile completed its row is looked at a tile later, when the count has long come back.
-template <typename T>
-__global__ void __launch_bounds__(kSumThreads, 4) row_sums_kernel(const __grid_constant__ VerifyPlan p) {
-    const VerifyArgs& a = p.a;
-    if (blockIdx.x == 0 && threadIdx.x == 0) *p.listed = 0;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31;
-    const int warps = gridDim.x * kSumWarps;
-    const int step_t = warps % p.tiles, step_at = warps / p.tiles;
-    const int w = blockIdx.x * kSumWarps + (threadIdx.x >> 5);
-    int t = w % p.tiles, i = w / p.tiles / a.R, r = w / p.tiles - i * a.R;
-    long long judge = -1;                            // the row before: its last arrival is under way
-    int judge_r = 0, judge_i = 0;
-    unsigned arrival = 0;
-    auto judge_last = [&]() {
-        if (judge < 0) return;
-        const long long row = judge;
-        judge = -1;
-        if (__shfl_sync(kFull, arrival, 0) + 2u != (uint32_t)p.tiles) return;
-        __syncwarp();
-        const bool rejected = surely_rejected<T>(p, judge_r, judge_i, row);
-        if (rejected && lane == 0) atomicMin(&p.dead[judge_r], (uint32_t)judge_i);
-    };
-    while (i <= a.S) {
-        const int start = a.query_start[r], end = a.query_start[r + 1];
-        // lengths that the choice refuses, and rows that the request does not have
-        bool here = !bad_rows(a, start, end) && i < end - start;
-        if (here && p.dead) here = __shfl_sync(kFull, lane == 0 ? __ldcg(&p.dead[r]) : 0u, 0) >= (uint32_t)i;
-        if (here) {
-            const long long row = start + i;
-            const Row<T> x(a, row);
-            uint4 v[kVecs];
-            float edge;
-            x.load(t, lane, v, edge);
-            const float c = Temperature(a, r).c;
-            const float m = warp_max(fmaxf(edge, largest<T>(v)));
-            float s = weight_sum<T>(v, m, c);
-            s += exp2_fast((edge - fmaxf(m, -FLT_MAX)) * c);
-            s = warp_sum(s);
-            judge_last();
-            if (lane == 0) __stcg(&p.sums[row * p.tiles + t], make_float2(m, s));
-            if (p.dead && i < end - start - 1) {
-                if (lane == 0)
-                    asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
-                                 : "=r"(arrival) : "l"(&p.arrived[row]) : "memory");
-                judge = row;
-                judge_r = r;
-                judge_i = i;
-            }
-        } else {
-            judge_last();
-        }
-        t += step_t;
-        r += step_at;
-        if (t >= p.tiles) {
-            t -= p.tiles;
-            ++r;
-        }
-        if (r >= a.R) {
-            const int q = r / a.R;
-            i += q;
-            r -= q * a.R;
+// An item is kSumWarps tiles of a row, 32 KB in one piece, and goes through a ring of kSlots in shared memory.
+// A CTA has a warp that finds the next item and starts its copy, eight that take a tile of it each, and one
+// that judges rows' drafts.
+//
+// Rows go by position in the requests, then by request. Where rows may be passed over, a CTA looks at the
+// next 256 of them, and takes items of one that is alive and has some left; of several such rows not all CTAs
+// take the first, which would have them all ask at one address. (In a fixed assignment, CTAs that pass over
+// many rows run ahead, into rows that nothing is known of yet: a batch of 64 x 16 rows of 1 MB read 683 MB, of
+// which it needed 414. With one counter of items for all it read 479 MB, at half of the bandwidth.)
+struct Item {
+    long long row;
+    int r, i, chunk;
+    bool drafted;       // not the request's last row
+};
+
+struct Handout {
+    const VerifyPlan& p;
+    const int lane;
+    long long at;       // rows are not passed over: the next item; else the first row with anything left
+    int turn;
+    int more = 0;       // items in hand behind the last
+    Item last;
+    int4 alive[2], handed[2];   // of the 8 rows that this lane looks at from `at` on
+
+    __device__ Handout(const VerifyPlan& plan)
+        : p(plan), lane(threadIdx.x & 31), at(plan.alive ? 0 : blockIdx.x), turn(blockIdx.x) {
+        if (p.alive) ask();
+    }
+
+    // Asks for the rows from `at` on; the answers are first needed when the next item is.
+    __device__ __forceinline__ void ask() {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            const int x = (int)at + 128 * g + 4 * lane;
+            alive[g] = handed[g] = make_int4(-1, -1, -1, -1);
+            if (x >= (p.a.S + 1) * p.padded) continue;
+            alive[g] = __ldcg(reinterpret_cast<const int4*>(p.alive + (x - (int)p.by_padded.of(x) * p.padded)));
+            handed[g] = __ldcg(reinterpret_cast<const int4*>(p.handed + x));
         }
     }
-    judge_last();
+
+    // The next item, chunk -1 if there is none. One warp.
+    __device__ Item next() {
+        if (more > 0) {
+            --more;
+            ++last.chunk;
+        } else if (p.alive) {
+            of_the_living();
+        } else {
+            in_order();
+        }
+        return last;
+    }
+
+    __device__ void in_order() {
+        const VerifyArgs& a = p.a;
+        const long long items = (long long)(a.S + 1) * a.R * p.chunks;
+        const bool narrow = items < 1ll << 31;
+        last.chunk = -1;
+        for (; at < items && last.chunk < 0; at += gridDim.x) {
+            const long long x = narrow ? p.by_chunks.of((unsigned)at) : at / p.chunks;
+            const int i = narrow ? (int)p.by_R.of((unsigned)x) : (int)(x / a.R), r = (int)(x - (long long)i * a.R);
+            const int start = a.query_start[r], end = a.query_start[r + 1];
+            if (bad_rows(a, start, end) || i >= end - start) continue;
+            last = Item{(long long)start + i, r, i, (int)(at - x * p.chunks), false};
+        }
+    }
+
+    // Looks at 256 rows, 8 a lane; takes of the turn-th of the first `window` that have anything left.
+    __device__ void of_the_living() {
+        const int rows = (p.a.S + 1) * p.padded;
+        last.chunk = -1;
+        for (; at < rows; ask()) {
+            unsigned left = 0;                                       // a bit for each of the lane's rows
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+                const int i = (int)p.by_padded.of((int)at + 128 * g + 4 * lane);
+                left |= ((alive[g].x >= i && handed[g].x + 1 < p.groups) |
+                         (alive[g].y >= i && handed[g].y + 1 < p.groups) << 1 |
+                         (alive[g].z >= i && handed[g].z + 1 < p.groups) << 2 |
+                         (alive[g].w >= i && handed[g].w + 1 < p.groups) << 3) << 4 * g;
+            }
+            // How many such rows lanes below have, of the first 128 and of the others.
+            const int n0 = __popc(left & 15u), n1 = __popc(left >> 4);
+            int below0 = 0, below1 = 0, total0 = 0, total1 = 0;
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                const unsigned b0 = __ballot_sync(kFull, n0 >> k & 1), b1 = __ballot_sync(kFull, n1 >> k & 1);
+                const unsigned lower = (1u << lane) - 1;
+                below0 += __popc(b0 & lower) << k;
+                below1 += __popc(b1 & lower) << k;
+                total0 += __popc(b0) << k;
+                total1 += __popc(b1) << k;
+            }
+            if (total0 + total1 == 0) {
+                at += 256;
+                continue;
+            }
+            const int pick = turn % min(total0 + total1, p.window);
+            ++turn;
+            int row = -1, count = 0, start = 0, end = 0;
+            if (pick < total0 ? pick >= below0 && pick < below0 + n0
+                              : pick - total0 >= below1 && pick - total0 < below1 + n1) {
+                const int g = pick < total0 ? 0 : 1;
+                unsigned bits = g ? left >> 4 : left & 15u;
+                for (int k = g ? pick - total0 - below1 : pick - below0; k > 0; --k) bits &= bits - 1;
+                row = (int)at + 128 * g + 4 * lane + __ffs(bits) - 1;
+                count = (int)(atomicAdd(&p.handed[row], 1) + 1);
+                const int r = row - (int)p.by_padded.of(row) * p.padded;
+                start = p.a.query_start[r];
+                end = p.a.query_start[r + 1];
+            }
+            const int from = __ffs(__ballot_sync(kFull, row >= 0)) - 1;
+            if (total0 == 0) at += 128;
+            count = __shfl_sync(kFull, count, from);
+            if (count >= p.groups) continue;                         // others were quicker
+            row = __shfl_sync(kFull, row, from);
+            start = __shfl_sync(kFull, start, from);
+            end = __shfl_sync(kFull, end, from);
+            const int i = (int)p.by_padded.of(row), r = row - i * p.padded;
+            last = Item{(long long)start + i, r, i, count * p.group, i < end - start - 1};
+            more = min(p.group, p.chunks - last.chunk) - 1;
+            ask();
+            return;
+        }
+    }
+};
+
+constexpr int kSlots = 3;
+constexpr int kSlotBytes = kSumWarps * kVecs * 32 * 16;
+
+constexpr int kQueue = 32;
+
+struct SumShared {
+    uint64_t full[kSlots];     // the item's copy has landed
+    uint64_t done[kSlots];     // its tiles' sums are written
+    Item items[kSlots];
+    // Rows whose last item this CTA has, to be judged.
+    Item queue[kQueue];
+    volatile unsigned pushed, popped;
+    volatile bool over;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kSumThreads, kSumBlocks)
+row_sums_kernel(const __grid_constant__ VerifyPlan p, uint32_t* status) {
+    extern __shared__ __align__(128) uint8_t ring[];                 // [kSlots][kSlotBytes]
+    __shared__ SumShared sh;
+    constexpr int kN = Vec<T>::kN;
+    const VerifyArgs& a = p.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        if (blockIdx.x == 0 && !p.alive) *p.listed = 0;
+        for (int k = 0; k < kSlots; ++k) {
+            ptx::mbar_init(ptx::smem_u32(&sh.full[k]), 1);
+            ptx::mbar_init(ptx::smem_u32(&sh.done[k]), kSumWarps);
+        }
+        sh.pushed = sh.popped = 0;
+        sh.over = false;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    ptx::grid_dependents_launch();
+    if (p.alive) ptx::grid_dependency_wait();
+    __syncthreads();
+    int slot = 0;
+    uint32_t parity = 0;
+    auto advance = [&]() {
+        if (++slot == kSlots) {
+            slot = 0;
+            parity ^= 1;
+        }
+    };
+    auto await = [&](uint64_t* bar, uint32_t phase) {
+        if (ptx::mbar_wait(ptx::smem_u32(bar), phase)) return true;
+        if (lane == 0) atomicOr(status, kStatusTimeout);
+        return false;
+    };
+    if (warp == kSumWarps) {                                         // finds and copies
+        Handout handout(p);
+        for (int n = 0;; ++n) {
+            if (n >= kSlots && !await(&sh.done[slot], parity ^ 1)) break;
+            const Item item = handout.next();
+            if (lane == 0) {
+                sh.items[slot] = item;
+                const uint32_t bar = ptx::smem_u32(&sh.full[slot]);
+                uint32_t bytes = 0;
+                if (item.chunk >= 0) {
+                    const Row<T> x(a, item.row);
+                    const int t = item.chunk * kSumWarps;
+                    const int hi = x.first(min(t + kSumWarps, p.tiles));
+                    const int body = t == 0 ? min(x.head, hi) : x.first(t);
+                    bytes = (uint32_t)((hi - body) / kN) * 16;
+                    if (bytes) {
+                        ptx::mbar_expect_tx(bar, bytes);
+                        ptx::bulk_load(ptx::smem_u32(ring + slot * kSlotBytes), x.x + body, bytes, bar);
+                    }
+                }
+                if (!bytes) ptx::mbar_arrive(bar);
+                // (With a full queue nobody looks at the row, and the next ones are read.)
+                if (p.alive && item.drafted && item.chunk == p.chunks - 1 && sh.pushed - sh.popped < kQueue) {
+                    sh.queue[sh.pushed % kQueue] = item;
+                    __threadfence_block();
+                    sh.pushed = sh.pushed + 1;
+                }
+            }
+            if (item.chunk < 0) break;
+            advance();
+        }
+        if (lane == 0) sh.over = true;
+        return;
+    }
+    if (warp > kSumWarps) {                                          // judges
+        // Looks at a row until all of its sums are there. Ends with the warp that finds items, which ends.
+        if (!p.alive) return;
+        for (;;) {
+            if (__any_sync(kFull, sh.over)) return;                  // what is left decides nothing any more
+            const unsigned popped = sh.popped;
+            if (!__any_sync(kFull, sh.pushed != popped)) {
+                __nanosleep(200);
+                continue;
+            }
+            __threadfence_block();
+            const Item row = sh.queue[popped % kQueue];
+            const int state = judge<T>(p, row.r, row.i, row.row);
+            if (state == kRejected && lane == 0) atomicMin(&p.alive[row.r], row.i);
+            __syncwarp();
+            if (lane == 0 && state != kUnsure) sh.popped = popped + 1;
+            __syncwarp();
+        }
+    }
+    for (;; advance()) {                                             // sums
+        if (!await(&sh.full[slot], parity)) return;
+        const Item now = sh.items[slot];
+        if (now.chunk < 0) return;
+        const int t = now.chunk * kSumWarps + warp;
+        if (t < p.tiles) {
+            const Row<T> x(a, now.row);
+            uint4 v[kVecs];
+            const float edge = x.edge(t, lane);
+            x.load(t, lane, reinterpret_cast<const uint4*>(ring + slot * kSlotBytes) + warp * kVecs * 32, v);
+            const float c = Temperature(a, now.r).c;
+            const float m = warp_max(fmaxf(edge, largest<T>(v)));
+            float s = weight_sum<T>(v, m, c);
+            if (__any_sync(kFull, edge > -INFINITY || edge != edge)) s += ptx::ex2((edge - fmaxf(m, -FLT_MAX)) * c);
+            s = warp_sum(s);
+            if (lane == 0) __stcg(&p.sums[now.row * p.tiles + t], make_float2(m, s));
+        }
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.done[slot]));
+    }
+}
+
+// What row_sums starts from where rows may be passed over.
+constexpr int kStartThreads = 256;
+__global__ void __launch_bounds__(kStartThreads) start_kernel(const __grid_constant__ VerifyPlan p) {
+    const VerifyArgs& a = p.a;
+    ptx::grid_dependents_launch();
+    const long long at = (long long)blockIdx.x * kStartThreads + threadIdx.x, step = (long long)gridDim.x * kStartThreads;
+    if (at == 0) *p.listed = 0;
+    for (long long r = at; r < p.padded; r += step) {
+        const int start = r < a.R ? a.query_start[r] : 0, end = r < a.R ? a.query_start[r + 1] : 0;
+        p.alive[r] = bad_rows(a, start, end) ? -1 : end - start - 1;
+    }
+    for (long long k = at; k < (long long)(a.S + 1) * p.padded; k += step) p.handed[k] = -1;
+    const uint4 ones = make_uint4(~0u, ~0u, ~0u, ~0u);
+    uint4* sums = reinterpret_cast<uint4*>(p.sums);                  // room for a whole number of these
+    for (long long k = at; k < ((long long)a.T * p.tiles + 1) / 2; k += step) sums[k] = ones;
 }
 
 // ---------------------------------------------------------------- sums of twice the precision
@@ -442,32 +683,37 @@ __device__ __forceinline__ Two exp_two(float x, float M, Two inv_t, const Two* p
     return {some ? h * scale : 0.f, some ? l * scale : 0.f};
 }
 
-// The sum of a tile's weights, by a warp.
+// The sum of a tile's weights, by a warp. stage: room for it in shared memory.
 template <typename T>
-__device__ __noinline__ double exact_tile(const Row<T>& x, int t, float M, Two inv_t, const Two* powers) {
-    constexpr int kN = Vec<T>::kN;
+__device__ __noinline__ double exact_tile(const Row<T>& x, int t, float M, Two inv_t, const Two* powers,
+                                          uint4* stage) {
     const int lane = threadIdx.x & 31;
-    const int hi = x.first(t + 1), body = t == 0 ? min(x.head, hi) : x.first(t), n = hi - body;
-    const T* base = x.x + body;
-    Two sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-    auto add = [&](float f, int to) {
-        const Two w = exp_two(f, M, inv_t, powers), s = two_sum(sum[to].h, w.h);
-        sum[to] = {s.h, sum[to].l + (s.l + w.l)};
-    };
-    const int rest = n & (kN - 1);
-    if (t == 0 && lane < x.head && lane < hi) add(to_float(x.x[lane]), 0);
-    if (lane >= 16 && lane - 16 < rest) add(to_float(base[n - rest + lane - 16]), 0);
-    uint4 next = make_uint4(0, 0, 0, 0);
-    if (lane * kN + kN <= n) next = *reinterpret_cast<const uint4*>(base + lane * kN);
-#pragma unroll 1
-    for (int e = lane * kN; e + kN <= n; e += 32 * kN) {
-        float f[kN];
-        Vec<T>::widen(next, f);
-        if (e + 33 * kN <= n) next = *reinterpret_cast<const uint4*>(base + e + 32 * kN);
+    int n;
+    const uint4* from = reinterpret_cast<const uint4*>(x.x + x.body(t, n));
+    uint4 v[kVecs];
+    const float edge = x.edge(t, lane);
+    x.load(t, lane, from, v);
+    __syncwarp();
 #pragma unroll
-        for (int k = 0; k < kN; ++k) add(f[k], k & 1);
+    for (int k = 0; k < kVecs; ++k) stage[32 * k + lane] = v[k];
+    __syncwarp();
+    const T* f = reinterpret_cast<const T*>(stage);
+    Two sum[4] = {exp_two(edge, M, inv_t, powers), {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+    // (Not unrolled further: the code runs once or twice, and is fetched from far.)
+#pragma unroll 1
+    for (int e = lane; e < Row<T>::kTile; e += 128) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const Two w = exp_two(to_float(f[e + 32 * k]), M, inv_t, powers), to = two_sum(sum[k].h, w.h);
+            sum[k] = {to.h, sum[k].l + (to.l + w.l)};
+        }
     }
-    return warp_sum(((double)sum[0].h + (double)sum[1].h) + ((double)sum[0].l + (double)sum[1].l));
+#pragma unroll
+    for (int k = 1; k < 4; ++k) {
+        const Two to = two_sum(sum[0].h, sum[k].h);
+        sum[0] = {to.h, (sum[0].l + sum[k].l) + to.l};
+    }
+    return warp_sum((double)sum[0].h + (double)sum[0].l);
 }
 
 // ---------------------------------------------------------------- the choice
@@ -475,9 +721,10 @@ __device__ __noinline__ double exact_tile(const Row<T>& x, int t, float M, Two i
 constexpr int kChooseThreads = 256;
 constexpr int kWarps = kChooseThreads / 32;
 constexpr int kMaxK = 32;
-enum : int { kTaken = 0, kRejected = 1, kUnsure = 2, kBad = 3 };
+constexpr int kRoom = kWarps * kVecs * 32 * 16;      // a tile for each warp, or a tile's weights
 
 struct ChooseShared {
+    uint4 room[kRoom / 16];
     Two powers[64];
     float M[kMaxDrafts + 1], Z[kMaxDrafts + 1], logprob[kMaxDrafts + 1];
     uint8_t state[kMaxDrafts + 1];
@@ -556,7 +803,12 @@ struct Chooser {
             const Two w = exp_two(x, M, inverse(temp.t), sh.powers);
             return (F)w.h + (F)w.l;
         }
-        return (F)exp2_fast((x - M) * temp.c);
+        return (F)ptx::ex2((x - M) * temp.c);
+    }
+
+    template <typename F>
+    __device__ __forceinline__ F weight_of(float x, float M) const {
+        return x > -INFINITY ? weight<F>(x, M) : (F)0;
     }
 
     // Weight of a tile.
@@ -565,7 +817,7 @@ struct Chooser {
         const float2* sums = p.sums + row * p.tiles;
         if (sizeof(F) == 8) return (F)__ldcg(reinterpret_cast<const double*>(sums) + t);
         const float2 s = __ldcg(&sums[t]);
-        return s.x == -INFINITY ? (F)0 : (F)(s.y * exp2_fast((s.x - M) * temp.c));
+        return s.x == -INFINITY ? (F)0 : (F)(s.y * ptx::ex2((s.x - M) * temp.c));
     }
 
     __device__ __forceinline__ float uniform() const {
@@ -664,26 +916,42 @@ struct Chooser {
             *reinterpret_cast<F*>(&sh.before) = before;
         }
         __syncthreads();
-        // Inside the tile: each thread a run of its elements.
-        constexpr int kEach = (Row<T>::kTile + Row<T>::kN - 1 + kChooseThreads - 1) / kChooseThreads;
+        // Inside the tile: its elements' weights, what the candidates lose taken away, then each thread a
+        // run of them.
+        constexpr int kMost = Row<T>::kTile + Row<T>::kN - 1;
+        constexpr int kEach = ((kMost + kChooseThreads - 1) / kChooseThreads) | 1;   // odd: no bank conflicts
+        static_assert(kEach * kChooseThreads * sizeof(F) <= kRoom, "a tile's weights fit");
+        F* w = reinterpret_cast<F*>(sh.room);
         const int tile = sh.tile;
         const F before = *reinterpret_cast<F*>(&sh.before);
-        const int lo = x.first(tile), n = x.first(tile + 1) - lo, e0 = tid * kEach;
-        float l[kEach];
-        F w[kEach];
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            l[e] = -INFINITY;
-            if (e0 + e < n) l[e] = to_float(x.x[lo + e0 + e]);
+        const int lo = x.first(tile), n = x.first(tile + 1) - lo;
+        {
+            int whole;
+            const int skip = x.body(tile, whole) - lo;               // elements before the first vector
+            const uint4* from = reinterpret_cast<const uint4*>(x.x + lo + skip);
+            float l[Row<T>::kN];
+            const bool full = (tid + 1) * Row<T>::kN <= whole;
+            if (full) Vec<T>::widen(from[tid], l);
+            for (int e = tid; e < kEach * kChooseThreads; e += kChooseThreads) {
+                const bool outside = e < skip || (e >= skip + (whole & -Row<T>::kN) && e < n);
+                if (outside || e >= n) w[e] = outside ? weight_of<F>(to_float(x.x[lo + e]), M) : (F)0;
+            }
+            if (full) {
+#pragma unroll 2
+                for (int k = 0; k < Row<T>::kN; ++k)
+                    w[skip + tid * Row<T>::kN + k] = weight_of<F>(l[k], M);
+            }
         }
+        __syncthreads();
+        if (tid < taken) {
+            const int e = sh.less_at[tid] - lo;
+            if (e >= 0 && e < n) w[e] = w[e] > less[tid] ? w[e] - less[tid] : (F)0;
+        }
+        __syncthreads();
+        const F* own = w + tid * kEach;
         run = 0;
-#pragma unroll
-        for (int e = 0; e < kEach; ++e) {
-            w[e] = l[e] > -INFINITY ? weight<F>(l[e], M) : (F)0;
-            for (int k = 0; k < taken; ++k)
-                if (sh.less_at[k] == lo + e0 + e) w[e] = w[e] > less[k] ? w[e] - less[k] : (F)0;
-            run += w[e];
-        }
+#pragma unroll 1
+        for (int e = 0; e < kEach; ++e) run += own[e];
         F in_tile;
         const F here = before + block_scan(run, sh, in_tile);
         int holder = first_thread(here > border, sh);
@@ -700,15 +968,14 @@ struct Chooser {
         if (tid == holder) {
             F at = here - run, after = at;
             int pick = -1;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-                if (pick >= 0 && after > border) continue;
-                if (!(w[e] > (F)0)) continue;
+#pragma unroll 1
+            for (int e = 0; e < kEach && !(pick >= 0 && after > border); ++e) {
+                if (!(own[e] > (F)0)) continue;
                 if (pick >= 0) at = after;
                 pick = e;
-                after = at + w[e];
+                after = at + own[e];
             }
-            if (pick >= 0) sh.found = lo + e0 + pick;
+            if (pick >= 0) sh.found = lo + tid * kEach + pick;
             const F slack = (F)kSlack * Z;
             sh.unsure = pick < 0 || border - at < slack || after - border < slack;
         }
@@ -737,9 +1004,10 @@ struct Chooser {
         }
         if (tile == INT_MAX) return -1;                              // no tile has it (not so for a row's M)
         uint4 v[kVecs];
-        float edge;
-        x.load((int)tile, lane, v, edge);
-        const int hi = x.first(tile + 1), body = tile == 0 ? min(x.head, hi) : x.first(tile);
+        int n;
+        const int body = x.body((int)tile, n);
+        const float edge = x.edge((int)tile, lane);
+        x.load((int)tile, lane, reinterpret_cast<const uint4*>(x.x + body), v);
         unsigned best = UINT_MAX;
         constexpr int kN = Vec<T>::kN;
 #pragma unroll
@@ -750,7 +1018,7 @@ struct Chooser {
             for (int e = kN - 1; e >= 0; --e)
                 if (f[e] == M) best = min(best, (unsigned)(body + (k * 32 + lane) * kN + e));
         }
-        if (edge == M) best = min(best, (unsigned)(lane < 16 ? lane : hi - ((hi - body) & (kN - 1)) + lane - 16));
+        if (edge == M) best = min(best, (unsigned)(lane < 16 ? lane : body + n - (n & (kN - 1)) + lane - 16));
         return (int)__reduce_min_sync(kFull, best);
     }
 
@@ -775,7 +1043,7 @@ struct Chooser {
             if (temp.greedy) {
                 state = l == M && argmax(row, M) == token ? kTaken : kRejected;
             } else {
-                const float z = (l - M) * temp.c, w = exp2_fast(z), uq = u * q * Z;
+                const float z = (l - M) * temp.c, w = ptx::ex2(z), uq = u * q * Z;
                 const float slack = kSlack * uq + (kSlack - z * 0x1p-20f) * w;
                 state = fabsf(uq - w) <= slack ? kUnsure : uq < w ? kTaken : kRejected;
                 logprob = (l - M) / temp.t - logf(Z);
@@ -799,7 +1067,7 @@ struct Chooser {
         __syncthreads();
         double mine = 0.0, Z;
         for (int t = warp; t < p.tiles; t += kWarps) {
-            const double s = exact_tile<T>(x, t, M, inverse(temp.t), sh.powers);
+            const double s = exact_tile<T>(x, t, M, inverse(temp.t), sh.powers, sh.room + warp * kVecs * 32);
             if (lane == 0) mine += s;
         }
         block_scan(mine, sh, Z);
@@ -818,8 +1086,7 @@ struct Chooser {
         float* logprobs = a.logprobs ? a.logprobs + (long long)r * (a.S + 1) : nullptr;
         const bool bad = bad_rows(a, start, end);
         const int n = bad ? 0 : end - start;
-        const uint32_t dead = p.dead ? p.dead[r] : 0xffffffffu;
-        const int rows = dead < (uint32_t)n ? (int)dead + 1 : n;
+        const int rows = p.alive && n > 0 ? p.alive[r] + 1 : n;
         for (int i = warp; i < rows; i += kWarps) look(start + i, i, n);
         __syncthreads();
         // The drafts in order.
@@ -885,8 +1152,8 @@ template <typename T>
 __global__ void __launch_bounds__(kChooseThreads)
 choose_kernel(const __grid_constant__ VerifyPlan p, uint32_t* status) {
     __shared__ ChooseShared sh;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    ptx::grid_dependents_launch();
+    ptx::grid_dependency_wait();
     const int r = blockIdx.x;
     Chooser<T> chooser{p, sh, r, Temperature(p.a, r)};
     chooser.run(status);
@@ -896,7 +1163,7 @@ choose_kernel(const __grid_constant__ VerifyPlan p, uint32_t* status) {
 template <typename T>
 __global__ void __launch_bounds__(kChooseThreads) settle_kernel(const __grid_constant__ VerifyPlan p) {
     __shared__ ChooseShared sh;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    ptx::grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31;
     const unsigned n = __ldcg(p.listed);
     if (n == 0) return;
@@ -909,7 +1176,8 @@ __global__ void __launch_bounds__(kChooseThreads) settle_kernel(const __grid_con
         const long long row = p.a.query_start[u.r] + u.i;
         __syncthreads();
         if (t < p.tiles) {
-            const double s = exact_tile<T>(Row<T>(p.a, row), t, u.M, inverse(temp.t), sh.powers);
+            const double s = exact_tile<T>(Row<T>(p.a, row), t, u.M, inverse(temp.t), sh.powers,
+                                           sh.room + (tid >> 5) * kVecs * 32);
             if (lane == 0) __stcg(reinterpret_cast<double*>(p.sums + row * p.tiles) + t, s);
         }
         __syncthreads();
@@ -926,26 +1194,32 @@ __global__ void __launch_bounds__(kChooseThreads) settle_kernel(const __grid_con
     }
 }
 
-// The workspace: the list's length and the rows' counters, the list, the tiles' sums.
-size_t counter_bytes(int R, int T) { return (16 + ((size_t)R + T) * 4 + 255) & ~(size_t)255; }
-size_t list_bytes(int R) { return ((size_t)R * sizeof(Unsettled) + 255) & ~(size_t)255; }
+// The workspace: the list's length, the list, requests' and rows' counters, the tiles' sums.
+size_t padded_bytes(size_t n) { return (n + 255) & ~(size_t)255; }
+size_t list_bytes(int R) { return padded_bytes(16 + (size_t)R * sizeof(Unsettled)); }
+// (Rows that are all of one request's leave R others without any: no more than T + R counters are needed, but
+// by position and request there are (S + 1) R. Batches for which that is more than 4 (T + R) are not worth it.)
+size_t counter_bytes(int R, int T) { return padded_bytes((4 * ((size_t)T + R) + R + 8) * 4); }
 
 int tiles_of(int V, int size) {
     const int tile = kVecs * 32 * 16 / size;
     return (int)(((long long)V + tile - 1) / tile);
 }
 
+// dependent: as the programmatic dependent of the kernel before it.
 template <typename Kernel, typename... Args>
-cudaError_t launch_dependent(Kernel kernel, unsigned blocks, int threads, cudaStream_t stream, Args... args) {
+cudaError_t launch_kernel(Kernel kernel, unsigned blocks, int threads, int smem, bool dependent,
+                          cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = dependent ? 1 : 0;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -955,33 +1229,53 @@ cudaError_t launch(const DeviceInfo& dev, const VerifyArgs& a, void* workspace, 
     VerifyPlan p{};
     p.a = a;
     p.tiles = tiles_of(a.V, (int)sizeof(T));
+    p.chunks = (p.tiles + kSumWarps - 1) / kSumWarps;
+    p.padded = (a.R + 3) & ~3;
+    p.by_chunks = Divisor((unsigned)p.chunks);
+    p.by_R = Divisor((unsigned)a.R);
+    p.by_padded = Divisor((unsigned)p.padded);
     char* at = static_cast<char*>(workspace);
     p.listed = reinterpret_cast<unsigned*>(at);
-    p.list = reinterpret_cast<Unsettled*>(at + counter_bytes(a.R, a.T));
-    p.sums = reinterpret_cast<float2*>(at + counter_bytes(a.R, a.T) + list_bytes(a.R));
-    const long long items = (long long)(a.S + 1) * a.R * p.tiles;
-    const long long most = 4LL * dev.sm_count;
-    if (items > 2 * most * kSumWarps && a.S > 0) {
-        p.dead = reinterpret_cast<uint32_t*>(at + 16);
-        p.arrived = p.dead + a.R;
-        const cudaError_t e = cudaMemsetAsync(p.dead, 0xff, ((size_t)a.R + a.T) * 4, stream);
+    p.list = reinterpret_cast<Unsettled*>(at + 16);
+    p.sums = reinterpret_cast<float2*>(at + list_bytes(a.R) + counter_bytes(a.R, a.T));
+    const long long items = (long long)(a.S + 1) * a.R * p.chunks;
+    const long long most = (long long)kSumBlocks * dev.sm_count;
+    const long long rows = (long long)(a.S + 1) * p.padded;
+    const bool pass_over = items > 2 * most && a.S > 0 && rows <= 4 * ((long long)a.T + a.R) && rows < 1 << 30;
+    if (pass_over) {
+        p.alive = reinterpret_cast<int*>(at + list_bytes(a.R));
+        p.handed = p.alive + p.padded;
+        p.group = (int)std::min(8LL, std::max(1LL, (long long)a.R * p.chunks / (4 * most)));
+        p.groups = (p.chunks + p.group - 1) / p.group;
+        p.window = (int)std::min(256LL, std::max(1LL, 2 * most / p.groups));
+        const long long most_start = (long long)a.T * p.tiles / (2 * 8 * kStartThreads) + 1;
+        start_kernel<<<(unsigned)std::min(most_start, 4LL * dev.sm_count), kStartThreads, 0, stream>>>(p);
+        const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
-    const unsigned blocks = (unsigned)std::min((items + kSumWarps - 1) / kSumWarps, most);
-    row_sums_kernel<T><<<blocks, kSumThreads, 0, stream>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const unsigned blocks = (unsigned)std::min(items, most);
+    constexpr int smem = kSlots * kSlotBytes;
+    static std::once_flag once[64];
+    static cudaError_t attr_err[64];
+    if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
+    std::call_once(once[dev.device], [&] {
+        attr_err[dev.device] =
+            cudaFuncSetAttribute(row_sums_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    });
+    if (attr_err[dev.device] != cudaSuccess) return attr_err[dev.device];
+    cudaError_t e = launch_kernel(row_sums_kernel<T>, blocks, kSumThreads, smem, pass_over, stream, p, status);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(choose_kernel<T>, (unsigned)a.R, kChooseThreads, stream, p, status);
+    e = launch_kernel(choose_kernel<T>, (unsigned)a.R, kChooseThreads, 0, true, stream, p, status);
     if (e != cudaSuccess) return e;
     const long long chunks = (long long)a.R * ((p.tiles + kWarps - 1) / kWarps);
-    return launch_dependent(settle_kernel<T>, (unsigned)std::min(chunks, 3LL * dev.sm_count), kChooseThreads,
-                            stream, p);
+    return launch_kernel(settle_kernel<T>, (unsigned)std::min(chunks, 3LL * dev.sm_count), kChooseThreads, 0,
+                         true, stream, p);
 }
 
 }  // namespace
 
 size_t verify_workspace_bytes(int R, int T, int V) {
-    return counter_bytes(R, T) + list_bytes(R) + (size_t)T * tiles_of(V, 4) * sizeof(float2);
+    return list_bytes(R) + counter_bytes(R, T) + padded_bytes((size_t)T * tiles_of(V, 4) * sizeof(float2));
 }
 
 cudaError_t launch_verify(const DeviceInfo& dev, const VerifyArgs& a, void* workspace,
