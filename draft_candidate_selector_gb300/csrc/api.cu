@@ -10,6 +10,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include <algorithm>
+#include <climits>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -221,6 +222,17 @@ dflash_status check_cache(const dflash_kv_cache* c, int dtype, dflash::KvCache* 
     return DFLASH_OK;
 }
 
+// The strides of queries, keys or values, or of their outputs.
+dflash_status check_row_strides(long long token, int T, long long head, int heads, const char* token_name,
+                                const char* head_name) {
+    DFLASH_TRY(check_stride(token, T, 8, token_name));
+    DFLASH_TRY(check_stride(head, heads, 8, head_name));
+    if ((T != 1 && token > INT_MAX) || (heads != 1 && head > INT_MAX))
+        return fail(DFLASH_UNSUPPORTED, "%s=%lld and %s=%lld must be below 2^31", token_name, token, head_name,
+                    head);
+    return DFLASH_OK;
+}
+
 // Checks a dflash_norm_rope and the sizes and strides of the calls that take one; fills in what it says.
 dflash_status check_norm_rope(const dflash_norm_rope* how, dflash::NormRopeArgs* a) {
     if (!how) return fail(DFLASH_INVALID_ARGUMENT, "how is NULL");
@@ -246,15 +258,12 @@ dflash_status check_norm_rope(const dflash_norm_rope* how, dflash::NormRopeArgs*
         return fail(DFLASH_INVALID_ARGUMENT, "weight_dtype=%d: must be dtype=%d or DFLASH_FP32",
                     how->weight_dtype, a->dtype);
     if (a->q_heads > 0) {
-        DFLASH_TRY(check_stride(a->qt, a->T, 8, "q_token_stride"));
-        DFLASH_TRY(check_stride(a->qh, a->q_heads, 8, "q_head_stride"));
-        DFLASH_TRY(check_stride(a->qot, a->T, 8, "q_out_token_stride"));
-        DFLASH_TRY(check_stride(a->qoh, a->q_heads, 8, "q_out_head_stride"));
+        DFLASH_TRY(check_row_strides(a->qt, a->T, a->qh, a->q_heads, "q_token_stride", "q_head_stride"));
+        DFLASH_TRY(check_row_strides(a->qot, a->T, a->qoh, a->q_heads, "q_out_token_stride",
+                                     "q_out_head_stride"));
     }
-    if (a->kv_heads > 0) {
-        DFLASH_TRY(check_stride(a->kt, a->T, 8, "k_token_stride"));
-        DFLASH_TRY(check_stride(a->kh, a->kv_heads, 8, "k_head_stride"));
-    }
+    if (a->kv_heads > 0)
+        DFLASH_TRY(check_row_strides(a->kt, a->T, a->kh, a->kv_heads, "k_token_stride", "k_head_stride"));
     a->q_weight = how->q_weight;
     a->k_weight = how->k_weight;
     a->weight_dtype = how->weight_dtype;
@@ -273,10 +282,8 @@ dflash_status check_norm_rope_pointers(const dflash::NormRopeArgs& a) {
         DFLASH_TRY(check_ptr(a.query_out, "query_out"));
     }
     if (a.kv_heads > 0) DFLASH_TRY(check_ptr(a.key, "key"));
-    const uintptr_t size = a.weight_dtype == DFLASH_FP32 ? 4 : 2;
-    if (reinterpret_cast<uintptr_t>(a.q_weight) % size != 0 ||
-        reinterpret_cast<uintptr_t>(a.k_weight) % size != 0)
-        return fail(DFLASH_INVALID_ARGUMENT, "q_weight or k_weight is not aligned to its elements");
+    if (a.q_weight) DFLASH_TRY(check_ptr(a.q_weight, "q_weight"));
+    if (a.k_weight) DFLASH_TRY(check_ptr(a.k_weight, "k_weight"));
     if (a.rotary_dim > 0) {
         DFLASH_TRY(check_ptr4(a.positions, "positions"));
         DFLASH_TRY(check_ptr8(a.frequencies, "frequencies"));
@@ -886,10 +893,9 @@ dflash_status dflash_qk_norm_rope(const void* query, const void* key, int dtype,
         return fail(DFLASH_INVALID_ARGUMENT,
                     "q_heads=%d and kv_heads=%d must be >= 0, and one of them >= 1", q_heads, kv_heads);
     DFLASH_TRY(check_norm_rope(how, &a));
-    if (kv_heads > 0) {
-        DFLASH_TRY(check_stride(k_out_token_stride, T, 8, "k_out_token_stride"));
-        DFLASH_TRY(check_stride(k_out_head_stride, kv_heads, 8, "k_out_head_stride"));
-    }
+    if (kv_heads > 0)
+        DFLASH_TRY(check_row_strides(k_out_token_stride, T, k_out_head_stride, kv_heads,
+                                     "k_out_token_stride", "k_out_head_stride"));
     if (T == 0) return ok();
     if (kv_heads > 0) DFLASH_TRY(check_ptr(key_out, "key_out"));
     DFLASH_TRY(check_norm_rope_pointers(a));
@@ -919,8 +925,8 @@ dflash_status dflash_qk_norm_rope_store(
     a.slots = slots;
     if (q_heads < 0) return fail(DFLASH_INVALID_ARGUMENT, "q_heads=%d must be >= 0", q_heads);
     DFLASH_TRY(check_norm_rope(how, &a));
-    DFLASH_TRY(check_stride(v_token_stride, T, 8, "v_token_stride"));
-    DFLASH_TRY(check_stride(v_head_stride, a.kv_heads, 8, "v_head_stride"));
+    DFLASH_TRY(check_row_strides(v_token_stride, T, v_head_stride, a.kv_heads, "v_token_stride",
+                                 "v_head_stride"));
     if (T == 0) return ok();
     DFLASH_TRY(check_ptr(value, "value"));
     DFLASH_TRY(check_ptr8(slots, "slots"));

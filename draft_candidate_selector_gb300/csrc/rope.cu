@@ -15,6 +15,7 @@
 // the low 64 bits of an integer product: what is left of f_j's own rounding is 2^-33 of a turn at
 // position 2^31.
 #include "common.cuh"
+#include "ptx.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -22,23 +23,25 @@
 
 #include <algorithm>
 #include <cfloat>
+#include <climits>
 #include <cmath>
-#include <mutex>
 
 namespace dflash {
 namespace {
 
-// A head row (one head of one token) belongs to a group of kLanes threads, the power of two at or
-// above head_dim / 16; a thread holds 16 values of it, as two 16-byte vectors a and b, chosen so
-// that both values of a pair are in one thread: vectors j and j + rotary_dim / 16 of the halves, or
-// 2j and 2j + 1. Its eight pairs are 8j to 8j + 7 either way. (Halves that are no multiple of 8
-// values long exchange the normed row through shared memory instead.)
+// A head row (one head of one token) belongs to a group of `lanes` threads, the power of two at or
+// above head_dim / 16; a thread holds 16 values of it, eight a and eight b, chosen so that both values of a
+// pair are in one thread: its pairs are 8j to 8j + 7. Interleaved, those are the 16 values from 16 j on. Else
+// they come in units of kUnit pairs, kUnit the largest of 8, 4, 2, 1 that divides the halves: a unit is kUnit
+// values of the first half and the same of the second, or two such pieces of what is not rotated. Pieces are
+// loaded and stored at once: 16 bytes where the halves are multiples of 8 values.
 //
-// A CTA takes a run of consecutive head rows (query, key and value heads of one token, then of the
-// next), kRows of them a thread, all loaded before anything else; while they travel, its threads take
-// the cosines and sines of the tokens that the run touches, once each, into shared memory.
+// A CTA takes a run of tokens: all of their query rows, then key rows, then value rows, so that addresses
+// and weights are found once for a kind. A row is loaded while the one before is worked on, the first ones
+// while the threads take the tokens' cosines and sines, once each, into shared memory.
 constexpr int kThreads = 256;
-enum : int { kHalves = 0, kInterleaved = 1, kOddHalves = 2 };
+constexpr int kBlocks = 3;          // CTAs of an SM
+enum : int { kQuery = 0, kKey = 1, kValue = 2, kNone = 3 };
 
 template <typename T>
 __device__ __forceinline__ float2 widen(uint32_t v);
@@ -64,244 +67,327 @@ __device__ __forceinline__ uint32_t narrow<__half>(float x, float y) {
     return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// Eight values at dst (element address), as T or as e4m3 of x / scale (mul: its exact inverse, or 0).
-template <typename T>
-__device__ __forceinline__ void put(void* base, long long at, const float* x, bool small, float scale,
-                                    float mul) {
-    if (small) {
-        uint32_t o[4];
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            float2 f = make_float2(x[2 * w], x[2 * w + 1]);
-            f.x = mul != 0.f ? f.x * mul : __fdiv_rn(f.x, scale);
-            f.y = mul != 0.f ? f.y * mul : __fdiv_rn(f.y, scale);
-            o[w] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
-        }
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + at) =
-            make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+// kN 16-bit values at p, as kN / 2 words (one, its lower half, for a single value), and back.
+template <int kN>
+__device__ __forceinline__ void get(const uint16_t* p, uint32_t* w) {
+    if constexpr (kN == 8) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else if constexpr (kN == 4) {
+        const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+        w[0] = v.x, w[1] = v.y;
+    } else if constexpr (kN == 2) {
+        w[0] = __ldcs(reinterpret_cast<const uint32_t*>(p));
     } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) =
-            make_uint4(narrow<T>(x[0], x[1]), narrow<T>(x[2], x[3]), narrow<T>(x[4], x[5]),
-                       narrow<T>(x[6], x[7]));
+        w[0] = __ldcs(p);
     }
 }
+template <int kN>
+__device__ __forceinline__ void set(uint16_t* p, const uint32_t* w) {
+    if constexpr (kN == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else if constexpr (kN == 4) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+    else if constexpr (kN == 2) *reinterpret_cast<uint32_t*>(p) = w[0];
+    else *p = (uint16_t)w[0];
+}
+
+// Quotients by a fixed divisor d, of n with n d < 2^32: by the divisor's reciprocal, rounded up, in 32 bits.
+struct Divisor {
+    uint32_t m, d;
+    Divisor(uint32_t divisor = 1) : m((uint32_t)((0x100000000ull + divisor - 1) / divisor)), d(divisor) {}
+    __device__ __forceinline__ int of(int n) const { return d == 1 ? n : (int)__umulhi(m, (uint32_t)n); }
+};
 
 struct RopePlan {
     NormRopeArgs a;
-    long long rows;      // T * heads
-    int heads;           // query, key and value heads of a token
-    int vecs;            // vectors of 8 in a head
-    int per;             // threads of a group that hold any: ceil(vecs / 2)
+    int per;             // threads of a group that hold any of a head: ceil(head_dim / 16)
     int lanes;           // the group
-    int run;             // head rows a CTA
-    int tokens;          // tokens that a run touches at most
+    int tokens;          // of a CTA
     int page_shift;      // -1: page_size is no power of two
     float k_mul, v_mul;  // inverses of the scales, where a product with them is exact; else 0
+    Divisor by_q, by_kv;
 };
 
-// Vector of a thread j's first (b: second) half; vecs or more if there is none.
-template <int kMode>
-__device__ __forceinline__ int vector_of(int j, int b, int rotary_dim) {
-    if (kMode != kHalves) return 2 * j + b;
-    const int half = rotary_dim / 16;
-    return j < half ? j + b * half : 2 * j + b;
-}
+template <typename T, bool kInterleaved, int kUnit>
+struct Rows {
+    static constexpr int kUnits = 8 / kUnit;             // of a thread
+    static constexpr int kWords = (kUnit + 1) / 2;       // of a piece
+    const RopePlan& p;
+    uint32_t* status;
+    const float4* table;       // [tokens][4][per] chunks of two pairs: (cos, cos, sin, sin)
+    long long token0;
+    int tokens, j, group, groups;
+    int dim[2][kUnits];        // first value of each of the thread's pieces; head_dim or more: none
 
-template <typename T, int kMode, int kRows>
-__global__ void __launch_bounds__(kThreads) norm_rope_kernel(RopePlan p, uint32_t* status) {
-    extern __shared__ __align__(16) float rope_smem[];
-    const NormRopeArgs& a = p.a;
-    // [tokens][4][per] chunks of two (cos, sin), [2][4][per] chunks of four weights, odd halves: rows
-    float4* table = reinterpret_cast<float4*>(rope_smem);
-    float4* weights = table + (size_t)p.tokens * 4 * p.per;
-    float* exchange = reinterpret_cast<float*>(weights + 8 * p.per);
-    const int tid = threadIdx.x;
-    const int j = tid & (p.lanes - 1), group = tid / p.lanes, groups = kThreads / p.lanes;
-    const long long row0 = (long long)blockIdx.x * p.run;
-    const int token0 = (int)(row0 / p.heads), head0 = (int)(row0 - (long long)token0 * p.heads);
-    const int rows = (int)min((long long)p.run, p.rows - row0);
-    const int va = vector_of<kMode>(j, 0, a.rotary_dim), vb = vector_of<kMode>(j, 1, a.rotary_dim);
-    const bool has_a = j < p.per, has_b = has_a && vb < p.vecs;
-
-    uint4 xa[kRows], xb[kRows];
-    long long slot[kRows];
+    __device__ __forceinline__ Rows(const RopePlan& plan, uint32_t* word, const float4* cs)
+        : p(plan), status(word), table(cs) {
+        j = threadIdx.x & (p.lanes - 1);
+        group = threadIdx.x / p.lanes;
+        groups = kThreads / p.lanes;
+        token0 = (long long)blockIdx.x * p.tokens;
+        tokens = (int)min((long long)p.tokens, p.a.T - token0);
+        const int half = p.a.rotary_dim / 2;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int local = i * groups + group;
-        xa[i] = xb[i] = make_uint4(0, 0, 0, 0);
-        slot[i] = -1;
-        if (local >= rows) continue;
-        const unsigned at = head0 + local;
-        const unsigned skip = at / p.heads;
-        const int h = (int)(at - skip * p.heads);
-        const long long t = token0 + (long long)skip;
-        const uint16_t* src;
-        if (h < a.q_heads)
-            src = static_cast<const uint16_t*>(a.query) + t * a.qt + h * a.qh;
-        else if (h < a.q_heads + a.kv_heads)
-            src = static_cast<const uint16_t*>(a.key) + t * a.kt + (h - a.q_heads) * a.kh;
-        else
-            src = static_cast<const uint16_t*>(a.value) + t * a.vt + (h - a.q_heads - a.kv_heads) * a.vh;
-        if (has_a) xa[i] = *reinterpret_cast<const uint4*>(src + 8 * va);
-        if (has_b) xb[i] = *reinterpret_cast<const uint4*>(src + 8 * vb);
-        if (a.slots && h >= a.q_heads) slot[i] = a.slots[t];
+        for (int k = 0; k < kUnits; ++k) {
+            const int pair = 8 * j + k * kUnit;
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+                dim[b][k] = kInterleaved || pair >= half ? 2 * pair + b * kUnit : pair + b * half;
+        }
     }
 
-    // Cosines and sines; pairs past rotary_dim stay as they are.
-    const int pairs = 8 * p.per;
-    const int touched = (head0 + rows - 1) / p.heads + 1;
-    for (int e = tid; e < touched * pairs; e += kThreads) {
-        const int skip = e / pairs, pair = e - skip * pairs;
-        float c = 1.f, s = 0.f;
-        if (pair < a.rotary_dim / 2) {
-            const unsigned long long turn = (unsigned long long)a.frequencies[pair] *
-                                            (unsigned long long)(long long)a.positions[token0 + skip];
-            // The nearest quarter turn, and the rest, at most an eighth, in half turns to fp32's precision.
-            const unsigned long long near = turn + (1ull << 61);
-            const int rest = (int)((long long)(turn - (near & (3ull << 62))) >> 30);
-            float sn, cs;
-            sincospif((float)rest * 0x1p-33f, &sn, &cs);
-            const int quarter = (int)(near >> 62);
-            c = quarter & 1 ? sn : cs;
-            s = quarter & 1 ? cs : sn;
-            c = (quarter + 1) & 2 ? -c : c;
-            s = quarter & 2 ? -s : s;
-            c *= a.rope_scale;
-            s *= a.rope_scale;
-        }
-        // thread pair / 8, chunk (pair % 8) / 2: threads of a group read neighbouring chunks
-        float2* to = reinterpret_cast<float2*>(table + ((size_t)skip * 4 + (pair & 7) / 2) * p.per +
-                                               (pair >> 3));
-        to[pair & 1] = make_float2(c, s);
+    template <int kKind>
+    __device__ __forceinline__ int heads() const {
+        return kKind == kQuery ? p.a.q_heads : p.a.kv_heads;
     }
-    for (int e = tid; e < 2 * 16 * p.per; e += kThreads) {
-        const int of = e / (16 * p.per), x = e - of * 16 * p.per;
-        const int chunk = x / (4 * p.per), y = x - chunk * 4 * p.per;
-        const int dim = 8 * vector_of<kMode>(y >> 2, chunk >> 1, a.rotary_dim) + 4 * (chunk & 1) + (y & 3);
-        const void* w = of ? a.k_weight : a.q_weight;
-        float v = 1.f;
-        if (w && dim < a.head_dim)
-            v = a.weight_dtype == kFp32 ? static_cast<const float*>(w)[dim]
-                                        : widen<T>(static_cast<const uint16_t*>(w)[dim]).x;
-        reinterpret_cast<float*>(weights)[e] = v;
+    template <int kKind>
+    __device__ __forceinline__ int rows() const {
+        if (kKind == kNone || (kKind == kValue && !p.a.slots)) return 0;
+        return tokens * heads<kKind>();
     }
-    __syncthreads();
+    // (Runs of several tokens have at most 2048 rows of a kind.)
+    template <int kKind>
+    __device__ __forceinline__ int token_of(int row) const {
+        return p.tokens == 1 ? 0 : (kKind == kQuery ? p.by_q : p.by_kv).of(row);
+    }
+    __device__ __forceinline__ bool has(int b, int k) const { return dim[b][k] < p.a.head_dim; }
 
+    // The thread's 16 values of a row, as they are: eight a, eight b.
+    template <int kKind>
+    __device__ __forceinline__ void load(int row, uint32_t (&x)[2][kUnits][kWords]) const {
+        const NormRopeArgs& a = p.a;
+        const bool live = row < rows<kKind>();
+        const int t = live ? token_of<kKind>(row) : 0, h = row - t * heads<kKind>();
+        const void* from = kKind == kQuery ? a.query : kKind == kKey ? a.key : a.value;
+        const int ts = (int)(kKind == kQuery ? a.qt : kKind == kKey ? a.kt : a.vt);
+        const int hs = (int)(kKind == kQuery ? a.qh : kKind == kKey ? a.kh : a.vh);
+        const uint16_t* src = static_cast<const uint16_t*>(from) + token0 * ts + (long long)t * ts + (long long)h * hs;
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-        const int local = i * groups + group;
-        const unsigned at = head0 + local;
-        const unsigned skip = at / p.heads;
-        const int h = (int)(at - skip * p.heads);
-        const long long t = token0 + (long long)skip;
-        const bool live = local < rows;
-        const bool is_key = h >= a.q_heads, is_value = h >= a.q_heads + a.kv_heads;
-        float x[16];
-        const uint32_t raw[8] = {xa[i].x, xa[i].y, xa[i].z, xa[i].w, xb[i].x, xb[i].y, xb[i].z, xb[i].w};
+        for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int w = 0; w < 8; ++w) {
-            const float2 f = widen<T>(raw[w]);
-            x[2 * w] = f.x;
-            x[2 * w + 1] = f.y;
+            for (int k = 0; k < kUnits; ++k) {
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) x[b][k][w] = 0;
+                if (live && has(b, k)) get<kUnit>(src + dim[b][k], x[b][k]);
+            }
+    }
+
+    // The same as pairs of floats: 0 to 3 are the a, 4 to 7 the b.
+    __device__ __forceinline__ void widened(const uint32_t (&raw)[2][kUnits][kWords], uint64_t (&x)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int b = k >> 2, at = 2 * (k & 3);                  // values at, at + 1
+            float2 f;
+            if constexpr (kUnit == 1) f = make_float2(widen<T>(raw[b][at][0]).x, widen<T>(raw[b][at + 1][0]).x);
+            else f = widen<T>(raw[b][at / kUnit][at % kUnit / 2]);
+            x[k] = ptx::pair_of(f.x, f.y);
         }
-        const bool normed = !is_value && (is_key ? a.k_weight : a.q_weight) != nullptr;
-        if (a.q_weight || a.k_weight) {                      // every lane takes part in the exchanges
-            float sum = 0.f;
+    }
+
+    // The thread's 16 weights.
+    __device__ __forceinline__ void weights(const void* from, uint64_t (&w)[8]) const {
+        if (p.a.weight_dtype == kFp32) {
+            float f[16];
 #pragma unroll
-            for (int w = 0; w < 16; ++w) sum = fmaf(x[w], x[w], sum);
-            for (int d = p.lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-            // Squares past fp32's range (bf16 values from 2^60 on): once more, 2^-72 as large.
-            if (__any_sync(0xffffffffu, sum > FLT_MAX && normed)) {
-                const float down = sum > FLT_MAX && normed ? 0x1p-72f : 1.f;
-                sum = 0.f;
-#pragma unroll
-                for (int w = 0; w < 16; ++w) {
-                    x[w] *= down;
-                    sum = fmaf(x[w], x[w], sum);
-                }
-                for (int d = p.lanes / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+            for (int k = 0; k < 16; ++k) {
+                const int b = k >> 3, unit = (k & 7) / kUnit;
+                f[k] = has(b, unit) ? static_cast<const float*>(from)[dim[b][unit] + (k & 7) % kUnit] : 0.f;
             }
-            if (normed) {
-                const float r = rsqrtf(sum / (float)a.head_dim + a.eps);
-                const float4* w4 = weights + (is_key ? 4 * p.per : 0) + (has_a ? j : 0);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const float4 w = w4[c * p.per];
-                    x[4 * c] *= r * w.x;
-                    x[4 * c + 1] *= r * w.y;
-                    x[4 * c + 2] *= r * w.z;
-                    x[4 * c + 3] *= r * w.w;
+            for (int k = 0; k < 8; ++k) w[k] = ptx::pair_of(f[2 * k], f[2 * k + 1]);
+        } else {
+            uint32_t raw[2][kUnits][kWords];
+#pragma unroll
+            for (int k = 0; k < 2 * kUnits; ++k) {
+                const int b = k / kUnits, unit = k % kUnits;
+#pragma unroll
+                for (int u = 0; u < kWords; ++u) raw[b][unit][u] = 0;
+                if (has(b, unit)) get<kUnit>(static_cast<const uint16_t*>(from) + dim[b][unit], raw[b][unit]);
+            }
+            widened(raw, w);
+        }
+    }
+
+    // Writes a row's values: as T, or as e4m3 of x / scale (mul: its exact inverse, or 0).
+    __device__ __forceinline__ void put(void* out, long long to, const uint64_t (&x)[8], bool small, float scale,
+                                        float mul) const {
+        if (!small) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int k = 0; k < kUnits; ++k) {
+                    if (!has(b, k)) continue;
+                    uint32_t w[kWords];
+#pragma unroll
+                    for (int u = 0; u < kWords; ++u) {
+                        const int at = k * kUnit + 2 * u;
+                        const float2 f = ptx::halves_of(x[4 * b + at / 2]);
+                        w[u] = kUnit == 1 ? narrow<T>(at & 1 ? f.y : f.x, 0.f) : narrow<T>(f.x, f.y);
+                    }
+                    set<kUnit>(static_cast<uint16_t*>(out) + to + dim[b][k], w);
                 }
+            return;
+        }
+        uint16_t two[8];                                             // two e4m3 values each
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            float2 f = ptx::halves_of(x[k]);
+            f = mul == 0.f ? make_float2(__fdiv_rn(f.x, scale), __fdiv_rn(f.y, scale))
+                           : make_float2(f.x * mul, f.y * mul);
+            two[k] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+        }
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+            for (int k = 0; k < kUnits; ++k) {
+                if (!has(b, k)) continue;
+                uint8_t* dst = static_cast<uint8_t*>(out) + to + dim[b][k];
+                const uint16_t* v = two + 4 * b + k * kUnit / 2;
+                if constexpr (kUnit == 8)
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(v[0] | (uint32_t)v[1] << 16, v[2] | (uint32_t)v[3] << 16);
+                else if constexpr (kUnit == 4) *reinterpret_cast<uint32_t*>(dst) = v[0] | (uint32_t)v[1] << 16;
+                else if constexpr (kUnit == 2) *reinterpret_cast<uint16_t*>(dst) = v[0];
+                else *dst = (uint8_t)(k & 1 ? v[0] >> 8 : v[0]);
+            }
+    }
+
+    // The sum of squares of a group's row. Every lane of the warp takes part.
+    __device__ __forceinline__ float squares(const uint64_t (&x)[8]) const {
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k & 1] = ptx::fma_pair(x[k], x[k], sum[k & 1]);
+        const float2 f = ptx::halves_of(ptx::add_pair(sum[0], sum[1]));
+        float s = f.x + f.y;
+        for (int d = p.lanes / 2; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+        return s;
+    }
+
+    // Norms row x in place, by weights w.
+    __device__ __forceinline__ void norm(uint64_t (&x)[8], const uint64_t (&w)[8]) const {
+        float sum = squares(x);
+        // Squares past fp32's range (bf16 values from 2^60 on): once more, 2^-72 as large.
+        if (__any_sync(0xffffffffu, sum > FLT_MAX)) {
+            const float down = sum > FLT_MAX ? 0x1p-72f : 1.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = ptx::mul_pair(x[k], ptx::pair_of(down, down));
+            sum = squares(x);
+        }
+        const float r = rsqrtf(sum / (float)p.a.head_dim + p.a.eps);
+        const uint64_t rr = ptx::pair_of(r, r);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = ptx::mul_pair(x[k], ptx::mul_pair(w[k], rr));
+    }
+
+    // Rotates row x of token t in place.
+    __device__ __forceinline__ void rotate(uint64_t (&x)[8], int t) const {
+        const float4* cs = table + (size_t)t * 4 * p.per + j;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float4 f = cs[c * p.per];
+            if constexpr (!kInterleaved) {
+                const uint64_t cc = ptx::pair_of(f.x, f.y), ss = ptx::pair_of(f.z, f.w);
+                const uint64_t minus = ptx::pair_of(-f.z, -f.w), u = x[c], v = x[c + 4];
+                x[c] = ptx::fma_pair(v, minus, ptx::mul_pair(u, cc));
+                x[c + 4] = ptx::fma_pair(u, ss, ptx::mul_pair(v, cc));
+            } else {
+                const float2 u = ptx::halves_of(x[2 * c]), v = ptx::halves_of(x[2 * c + 1]);
+                x[2 * c] = ptx::pair_of(u.x * f.x - u.y * f.z, u.y * f.x + u.x * f.z);
+                x[2 * c + 1] = ptx::pair_of(v.x * f.y - v.y * f.w, v.y * f.y + v.x * f.w);
             }
         }
-        if constexpr (kMode == kOddHalves) {
-            float* row = exchange + group * a.head_dim;
-            __syncwarp();
-            if (live && !is_value) {
-                for (int w = 0; w < 8; ++w) {
-                    if (has_a) row[8 * va + w] = x[w];
-                    if (has_b) row[8 * vb + w] = x[8 + w];
-                }
-            }
-            __syncwarp();
-            if (live && !is_value && has_a) {
-                const int half = a.rotary_dim / 2;
-                const float4* cs = table + (size_t)skip * 4 * p.per;
-                for (int w = 0; w < 16; ++w) {
-                    const int dim = 16 * j + w;
-                    if (dim >= a.rotary_dim) continue;
-                    const int pair = dim < half ? dim : dim - half;
-                    const float2 f = reinterpret_cast<const float2*>(
-                        cs + (size_t)((pair & 7) / 2) * p.per + (pair >> 3))[pair & 1];
-                    x[w] = dim < half ? x[w] * f.x - row[dim + half] * f.y
-                                      : x[w] * f.x + row[dim - half] * f.y;
-                }
-            }
-        } else if (live && !is_value && has_a && a.rotary_dim > 0) {
-            const float4* cs = table + (size_t)skip * 4 * p.per + j;
+    }
+
+    // All of the CTA's rows of a kind; next: the thread's first, loaded, and then the next kind's.
+    template <int kKind, int kNext>
+    __device__ __forceinline__ void run(uint32_t (&next)[2][kUnits][kWords]) const {
+        const NormRopeArgs& a = p.a;
+        const int n = rows<kKind>();
+        const void* from = kKind == kQuery ? a.q_weight : a.k_weight;
+        uint64_t w[8];
+        if (kKind != kValue && from) weights(from, w);
+        for (int row0 = 0; row0 < n; row0 += groups) {               // the warp stays together
+            const int row = row0 + group;
+            uint32_t now[2][kUnits][kWords];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float4 f = cs[c * p.per];          // two pairs
-                const int u0 = kMode == kHalves ? 2 * c : 4 * c, u1 = kMode == kHalves ? u0 + 8 : u0 + 1;
-                const int w0 = kMode == kHalves ? u0 + 1 : u0 + 2, w1 = kMode == kHalves ? u1 + 1 : u1 + 2;
-                const float x0 = x[u0], x1 = x[u1], y0 = x[w0], y1 = x[w1];
-                x[u0] = x0 * f.x - x1 * f.y;
-                x[u1] = x1 * f.x + x0 * f.y;
-                x[w0] = y0 * f.z - y1 * f.w;
-                x[w1] = y1 * f.z + y0 * f.w;
-            }
-        }
-        if (!live || !has_a) continue;
-        if (!is_key) {
-            const long long to = t * a.qot + h * a.qoh;
-            put<T>(a.query_out, to + 8 * va, x, false, 1.f, 1.f);
-            if (has_b) put<T>(a.query_out, to + 8 * vb, x + 8, false, 1.f, 1.f);
-        } else if (!a.slots) {
-            const long long to = t * a.kot + (h - a.q_heads) * a.koh;
-            put<T>(a.key_out, to + 8 * va, x, false, 1.f, 1.f);
-            if (has_b) put<T>(a.key_out, to + 8 * vb, x + 8, false, 1.f, 1.f);
-        } else if (slot[i] >= (long long)a.cache.num_pages * a.cache.page_size) {
-            if (j == 0) atomicOr(status, kStatusBadId);
-        } else if (slot[i] >= 0) {
-            const long long page = p.page_shift >= 0 ? slot[i] >> p.page_shift : slot[i] / a.cache.page_size;
-            const int head = is_value ? h - a.q_heads - a.kv_heads : h - a.q_heads;
-            const long long to = page * a.cache.page_stride +
-                                 (slot[i] - page * a.cache.page_size) * a.cache.token_stride +
-                                 head * a.cache.head_stride;
-            const bool small = a.cache.dtype == kE4m3;
-            void* base = is_value ? a.cache.value : a.cache.key;
-            const float scale = is_value ? a.cache.v_scale : a.cache.k_scale;
-            const float mul = is_value ? p.v_mul : p.k_mul;
-            if (is_value && !small) {                        // the bits as they are
-                uint16_t* copy = static_cast<uint16_t*>(base) + to;
-                *reinterpret_cast<uint4*>(copy + 8 * va) = xa[i];
-                if (has_b) *reinterpret_cast<uint4*>(copy + 8 * vb) = xb[i];
+            for (int k = 0; k < 2 * kUnits * kWords; ++k) (&now[0][0][0])[k] = (&next[0][0][0])[k];
+            if (row0 + groups < n) load<kKind>(row + groups, next);
+            else load<kNext>(group, next);
+            const bool live = row < n;
+            const int t = live ? token_of<kKind>(row) : 0, h = row - t * heads<kKind>();
+            long long slot = -1;
+            if (kKind != kQuery && a.slots && live) slot = a.slots[token0 + t];
+            uint64_t x[8];
+            widened(now, x);
+            if (kKind != kValue && from) norm(x, w);
+            if (!live || j >= p.per) continue;
+            if (kKind != kValue && a.rotary_dim > 0) rotate(x, t);
+            if (kKind == kQuery || !a.slots) {
+                const int ts = (int)(kKind == kQuery ? a.qot : a.kot), hs = (int)(kKind == kQuery ? a.qoh : a.koh);
+                put(kKind == kQuery ? a.query_out : a.key_out, token0 * ts + (long long)t * ts + (long long)h * hs, x,
+                    false, 1.f, 1.f);
                 continue;
             }
-            put<T>(base, to + 8 * va, x, small, scale, mul);
-            if (has_b) put<T>(base, to + 8 * vb, x + 8, small, scale, mul);
+            if (slot >= (long long)a.cache.num_pages * a.cache.page_size) {
+                if (j == 0) atomicOr(status, kStatusBadId);
+                continue;
+            }
+            if (slot < 0) continue;
+            const long long page = p.page_shift >= 0 ? slot >> p.page_shift : slot / a.cache.page_size;
+            const long long to = page * a.cache.page_stride +
+                                 (slot - page * a.cache.page_size) * a.cache.token_stride + h * a.cache.head_stride;
+            const bool small = a.cache.dtype == kE4m3;
+            if (kKind == kValue && !small) {                         // the bits as they are
+#pragma unroll
+                for (int b = 0; b < 2; ++b)
+#pragma unroll
+                    for (int k = 0; k < kUnits; ++k)
+                        if (has(b, k)) set<kUnit>(static_cast<uint16_t*>(a.cache.value) + to + dim[b][k], now[b][k]);
+                continue;
+            }
+            put(kKind == kValue ? a.cache.value : a.cache.key, to, x, small,
+                kKind == kValue ? a.cache.v_scale : a.cache.k_scale, kKind == kValue ? p.v_mul : p.k_mul);
         }
     }
+};
+
+template <typename T, bool kInterleaved, int kUnit>
+__global__ void __launch_bounds__(kThreads, kBlocks)
+norm_rope_kernel(const __grid_constant__ RopePlan p, uint32_t* status) {
+    extern __shared__ __align__(16) float4 table[];
+    const NormRopeArgs& a = p.a;
+    Rows<T, kInterleaved, kUnit> rows(p, status, table);
+    uint32_t first[2][8 / kUnit][(kUnit + 1) / 2];
+    if (a.q_heads > 0) rows.template load<kQuery>(rows.group, first);
+    else rows.template load<kKey>(rows.group, first);
+    if (a.rotary_dim > 0) {
+        // Cosines and sines; pairs past rotary_dim stay as they are.
+        const int pairs = 8 * p.per;
+        for (int e = threadIdx.x; e < rows.tokens * pairs; e += kThreads) {
+            const int t = e / pairs, pair = e - t * pairs;
+            float c = 1.f, s = 0.f;
+            if (pair < a.rotary_dim / 2) {
+                const unsigned long long turn = (unsigned long long)a.frequencies[pair] *
+                                                (unsigned long long)(long long)a.positions[rows.token0 + t];
+                // The nearest quarter turn, and the rest, at most an eighth, in half turns to fp32's precision.
+                const unsigned long long near = turn + (1ull << 61);
+                const int rest = (int)((long long)(turn - (near & (3ull << 62))) >> 30);
+                float sn, cs;
+                sincospif((float)rest * 0x1p-33f, &sn, &cs);
+                const int quarter = (int)(near >> 62);
+                c = quarter & 1 ? sn : cs;
+                s = quarter & 1 ? cs : sn;
+                c = ((quarter + 1) & 2 ? -c : c) * a.rope_scale;
+                s = (quarter & 2 ? -s : s) * a.rope_scale;
+            }
+            // thread pair / 8, chunk (pair % 8) / 2: threads of a group read neighbouring chunks
+            float* to = reinterpret_cast<float*>(table + ((size_t)t * 4 + ((pair & 7) >> 1)) * p.per + (pair >> 3));
+            to[pair & 1] = c;
+            to[2 + (pair & 1)] = s;
+        }
+        __syncthreads();
+    }
+    rows.template run<kQuery, kKey>(first);
+    rows.template run<kKey, kValue>(first);
+    rows.template run<kValue, kNone>(first);
 }
 
 // 1 / x where multiplying by it is the same as dividing by x: x a power of two, and 1 / x one too.
@@ -310,38 +396,21 @@ float exact_inverse(float x) {
     return frexpf(x, &e) == 0.5f && e > -120 && e < 120 ? 1.f / x : 0.f;
 }
 
-template <typename T, int kMode, int kRows>
-cudaError_t launch(const DeviceInfo& dev, RopePlan p, uint32_t* status, cudaStream_t stream) {
-    const int groups = kThreads / p.lanes;
-    p.run = groups * kRows;
-    p.tokens = (p.run - 1) / p.heads + 2;
-    const size_t smem = ((size_t)p.tokens * 4 * p.per + 8 * p.per) * sizeof(float4) +
-                        (kMode == kOddHalves ? (size_t)groups * p.a.head_dim * sizeof(float) : 0);
-    static std::once_flag once[64];
-    static cudaError_t err[64];
-    if (dev.device < 0 || dev.device >= 64) return cudaErrorInvalidDevice;
-    std::call_once(once[dev.device], [&] {
-        err[dev.device] = cudaFuncSetAttribute(norm_rope_kernel<T, kMode, kRows>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 100 * 1024);
-    });
-    if (err[dev.device] != cudaSuccess) return err[dev.device];
-    const long long blocks = (p.rows + p.run - 1) / p.run;
-    norm_rope_kernel<T, kMode, kRows><<<(unsigned)blocks, kThreads, smem, stream>>>(p, status);
+template <typename T, bool kInterleaved, int kUnit>
+cudaError_t launch(const RopePlan& p, uint32_t* status, cudaStream_t stream) {
+    const size_t smem = (size_t)p.tokens * 4 * p.per * sizeof(float4);
+    const long long blocks = ((long long)p.a.T + p.tokens - 1) / p.tokens;
+    norm_rope_kernel<T, kInterleaved, kUnit><<<(unsigned)blocks, kThreads, smem, stream>>>(p, status);
     return cudaGetLastError();
 }
 
-template <typename T, int kMode>
-cudaError_t launch_rows(const DeviceInfo& dev, const RopePlan& p, uint32_t* status,
-                        cudaStream_t stream) {
-    return launch<T, kMode, 1>(dev, p, status, stream);
-}
-
 template <typename T>
-cudaError_t launch_mode(const DeviceInfo& dev, const RopePlan& p, uint32_t* status,
-                        cudaStream_t stream) {
-    if (p.a.interleaved) return launch_rows<T, kInterleaved>(dev, p, status, stream);
-    if (p.a.rotary_dim % 16 == 0) return launch_rows<T, kHalves>(dev, p, status, stream);
-    return launch_rows<T, kOddHalves>(dev, p, status, stream);
+cudaError_t launch_pairs(const RopePlan& p, uint32_t* status, cudaStream_t stream) {
+    if (p.a.interleaved) return launch<T, true, 8>(p, status, stream);
+    if (p.a.rotary_dim % 16 == 0) return launch<T, false, 8>(p, status, stream);
+    if (p.a.rotary_dim % 8 == 0) return launch<T, false, 4>(p, status, stream);
+    if (p.a.rotary_dim % 4 == 0) return launch<T, false, 2>(p, status, stream);
+    return launch<T, false, 1>(p, status, stream);
 }
 
 }  // namespace
@@ -350,18 +419,34 @@ cudaError_t launch_norm_rope(const DeviceInfo& dev, const NormRopeArgs& a, uint3
                              cudaStream_t stream) {
     RopePlan p{};
     p.a = a;
-    p.heads = a.q_heads + (a.slots ? 2 : 1) * a.kv_heads;
-    p.rows = (long long)a.T * p.heads;
-    p.vecs = a.head_dim / 8;
-    p.per = (p.vecs + 1) / 2;
+    p.per = (a.head_dim + 15) / 16;
     for (p.lanes = 1; p.lanes < p.per;) p.lanes *= 2;
     p.k_mul = exact_inverse(a.cache.k_scale);
     p.v_mul = exact_inverse(a.cache.v_scale);
+    p.by_q = Divisor((uint32_t)std::max(1, a.q_heads));
+    p.by_kv = Divisor((uint32_t)std::max(1, a.kv_heads));
+    // Tokens of a CTA, up to 16 KB of cosines and sines: the number that makes waves times a CTA's time
+    // least, which is its rounds of rows, each kind's rounded up, and about kFixed rounds for cosines, sines and
+    // weights.
+    constexpr int kFixed = 2;
+    const long long groups = kThreads / p.lanes, resident = (long long)kBlocks * dev.sm_count;
+    long long least = LLONG_MAX;
+    for (int n = 1; n <= std::min(a.T, 256 / p.per); ++n) {
+        const long long blocks = (a.T + (long long)n - 1) / n;
+        const long long rounds = (n * (long long)a.q_heads + groups - 1) / groups +
+                                 (a.slots ? 2 : 1) * ((n * (long long)a.kv_heads + groups - 1) / groups);
+        const long long cost = (blocks + resident - 1) / resident * (rounds + kFixed);
+        if (n > 1 && n * (long long)std::max(a.q_heads, a.kv_heads) > 2048) break;
+        if (cost < least) {
+            least = cost;
+            p.tokens = n;
+        }
+    }
     p.page_shift = -1;
     if (a.slots && (a.cache.page_size & (a.cache.page_size - 1)) == 0)
         for (p.page_shift = 0; (1 << p.page_shift) < a.cache.page_size;) ++p.page_shift;
-    return a.dtype == kBf16 ? launch_mode<__nv_bfloat16>(dev, p, status_word, stream)
-                            : launch_mode<__half>(dev, p, status_word, stream);
+    return a.dtype == kBf16 ? launch_pairs<__nv_bfloat16>(p, status_word, stream)
+                            : launch_pairs<__half>(p, status_word, stream);
 }
 
 }  // namespace dflash

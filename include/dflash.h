@@ -518,7 +518,8 @@ typedef struct {
  * for the pairs j of the first rotary_dim values; the others stay as they are (normed).
  *
  * query, key  [T, q_heads, head_dim], [T, kv_heads, head_dim] of type dtype (DFLASH_BF16 or
- *             DFLASH_FP16) at the given strides (elements, multiples of 8). Either may have no heads.
+ *             DFLASH_FP16) at the given strides (elements, multiples of 8, below 2^31). Either may have no
+ *             heads.
  * positions   [T] int32, of any sign; not read if rotary_dim is 0
  * query_out, key_out  out, of the same shapes and type at their own strides. Each may be its own input
  *             (the same address and strides); else outputs must not overlap inputs.
