@@ -101,13 +101,18 @@ struct RopePlan {
     NormRopeArgs a;
     int per;             // threads of a group that hold any of a head: ceil(head_dim / 16)
     int lanes;           // the group
+    int pairs_shift;     // log2(8 per), where that is a whole number
     int tokens;          // of a CTA
     int page_shift;      // -1: page_size is no power of two
     float k_mul, v_mul;  // inverses of the scales, where a product with them is exact; else 0
+    float inv_dim;       // 1 / head_dim
+    // Of queries, keys and values: strides in bytes, of tokens and of heads; and of the first two's outputs.
+    uint32_t token_bytes[3], head_bytes[3], out_token_bytes[2], out_head_bytes[2];
     Divisor by_q, by_kv;
 };
 
-template <typename T, bool kInterleaved, int kUnit>
+// kFull: head_dim is 16 times a power of two, so that every thread has all of its values.
+template <typename T, bool kInterleaved, int kUnit, bool kFull>
 struct Rows {
     static constexpr int kUnits = 8 / kUnit;             // of a thread
     static constexpr int kWords = (kUnit + 1) / 2;       // of a piece
@@ -149,25 +154,27 @@ struct Rows {
     __device__ __forceinline__ int token_of(int row) const {
         return p.tokens == 1 ? 0 : (kKind == kQuery ? p.by_q : p.by_kv).of(row);
     }
-    __device__ __forceinline__ bool has(int b, int k) const { return dim[b][k] < p.a.head_dim; }
+    __device__ __forceinline__ bool has(int b, int k) const { return kFull || dim[b][k] < p.a.head_dim; }
 
     // The thread's 16 values of a row, as they are: eight a, eight b.
     template <int kKind>
     __device__ __forceinline__ void load(int row, uint32_t (&x)[2][kUnits][kWords]) const {
         const NormRopeArgs& a = p.a;
-        const bool live = row < rows<kKind>();
-        const int t = live ? token_of<kKind>(row) : 0, h = row - t * heads<kKind>();
+        if (rows<kKind>() == 0) return;
+        row = min(row, rows<kKind>() - 1);                           // past the end: anything, it is not used
+        const int t = token_of<kKind>(row), h = row - t * heads<kKind>();
         const void* from = kKind == kQuery ? a.query : kKind == kKey ? a.key : a.value;
-        const int ts = (int)(kKind == kQuery ? a.qt : kKind == kKey ? a.kt : a.vt);
-        const int hs = (int)(kKind == kQuery ? a.qh : kKind == kKey ? a.kh : a.vh);
-        const uint16_t* src = static_cast<const uint16_t*>(from) + token0 * ts + (long long)t * ts + (long long)h * hs;
+        const uint32_t ts = p.token_bytes[kKind % 3], hs = p.head_bytes[kKind % 3];
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(
+            static_cast<const uint8_t*>(from) + (uint64_t)token0 * ts + (uint64_t)(uint32_t)t * ts +
+            (uint64_t)(uint32_t)h * hs);
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
             for (int k = 0; k < kUnits; ++k) {
 #pragma unroll
                 for (int w = 0; w < kWords; ++w) x[b][k][w] = 0;
-                if (live && has(b, k)) get<kUnit>(src + dim[b][k], x[b][k]);
+                if (has(b, k)) get<kUnit>(src + dim[b][k], x[b][k]);
             }
     }
 
@@ -271,7 +278,7 @@ struct Rows {
             for (int k = 0; k < 8; ++k) x[k] = ptx::mul_pair(x[k], ptx::pair_of(down, down));
             sum = squares(x);
         }
-        const float r = rsqrtf(sum / (float)p.a.head_dim + p.a.eps);
+        const float r = rsqrtf(fmaf(sum, p.inv_dim, p.a.eps));
         const uint64_t rr = ptx::pair_of(r, r);
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = ptx::mul_pair(x[k], ptx::mul_pair(w[k], rr));
@@ -306,23 +313,27 @@ struct Rows {
         if (kKind != kValue && from) weights(from, w);
         for (int row0 = 0; row0 < n; row0 += groups) {               // the warp stays together
             const int row = row0 + group;
-            uint32_t now[2][kUnits][kWords];
-#pragma unroll
-            for (int k = 0; k < 2 * kUnits * kWords; ++k) (&now[0][0][0])[k] = (&next[0][0][0])[k];
-            if (row0 + groups < n) load<kKind>(row + groups, next);
-            else load<kNext>(group, next);
             const bool live = row < n;
-            const int t = live ? token_of<kKind>(row) : 0, h = row - t * heads<kKind>();
+            const int t = token_of<kKind>(min(row, n - 1)), h = row - t * heads<kKind>();
             long long slot = -1;
             if (kKind != kQuery && a.slots && live) slot = a.slots[token0 + t];
+            const bool small = a.cache.dtype == kE4m3;
+            uint32_t bits[2][kUnits][kWords];
+            if (kKind == kValue && !small) {
+#pragma unroll
+                for (int k = 0; k < 2 * kUnits * kWords; ++k) (&bits[0][0][0])[k] = (&next[0][0][0])[k];
+            }
             uint64_t x[8];
-            widened(now, x);
+            widened(next, x);
+            if (row0 + groups < n) load<kKind>(row + groups, next);
+            else load<kNext>(group, next);
             if (kKind != kValue && from) norm(x, w);
-            if (!live || j >= p.per) continue;
+            if (!live || (!kFull && j >= p.per)) continue;
             if (kKind != kValue && a.rotary_dim > 0) rotate(x, t);
             if (kKind == kQuery || !a.slots) {
-                const int ts = (int)(kKind == kQuery ? a.qot : a.kot), hs = (int)(kKind == kQuery ? a.qoh : a.koh);
-                put(kKind == kQuery ? a.query_out : a.key_out, token0 * ts + (long long)t * ts + (long long)h * hs, x,
+                const uint32_t ts = p.out_token_bytes[kKind & 1], hs = p.out_head_bytes[kKind & 1];
+                uint8_t* out = static_cast<uint8_t*>(kKind == kQuery ? a.query_out : a.key_out);
+                put(out + (uint64_t)token0 * ts + (uint64_t)(uint32_t)t * ts + (uint64_t)(uint32_t)h * hs, 0, x,
                     false, 1.f, 1.f);
                 continue;
             }
@@ -334,13 +345,12 @@ struct Rows {
             const long long page = p.page_shift >= 0 ? slot >> p.page_shift : slot / a.cache.page_size;
             const long long to = page * a.cache.page_stride +
                                  (slot - page * a.cache.page_size) * a.cache.token_stride + h * a.cache.head_stride;
-            const bool small = a.cache.dtype == kE4m3;
             if (kKind == kValue && !small) {                         // the bits as they are
 #pragma unroll
                 for (int b = 0; b < 2; ++b)
 #pragma unroll
                     for (int k = 0; k < kUnits; ++k)
-                        if (has(b, k)) set<kUnit>(static_cast<uint16_t*>(a.cache.value) + to + dim[b][k], now[b][k]);
+                        if (has(b, k)) set<kUnit>(static_cast<uint16_t*>(a.cache.value) + to + dim[b][k], bits[b][k]);
                 continue;
             }
             put(kKind == kValue ? a.cache.value : a.cache.key, to, x, small,
@@ -349,12 +359,12 @@ struct Rows {
     }
 };
 
-template <typename T, bool kInterleaved, int kUnit>
+template <typename T, bool kInterleaved, int kUnit, bool kFull>
 __global__ void __launch_bounds__(kThreads, kBlocks)
 norm_rope_kernel(const __grid_constant__ RopePlan p, uint32_t* status) {
     extern __shared__ __align__(16) float4 table[];
     const NormRopeArgs& a = p.a;
-    Rows<T, kInterleaved, kUnit> rows(p, status, table);
+    Rows<T, kInterleaved, kUnit, kFull> rows(p, status, table);
     uint32_t first[2][8 / kUnit][(kUnit + 1) / 2];
     if (a.q_heads > 0) rows.template load<kQuery>(rows.group, first);
     else rows.template load<kKey>(rows.group, first);
@@ -362,7 +372,7 @@ norm_rope_kernel(const __grid_constant__ RopePlan p, uint32_t* status) {
         // Cosines and sines; pairs past rotary_dim stay as they are.
         const int pairs = 8 * p.per;
         for (int e = threadIdx.x; e < rows.tokens * pairs; e += kThreads) {
-            const int t = e / pairs, pair = e - t * pairs;
+            const int t = kFull ? e >> p.pairs_shift : e / pairs, pair = e - t * pairs;
             float c = 1.f, s = 0.f;
             if (pair < a.rotary_dim / 2) {
                 const unsigned long long turn = (unsigned long long)a.frequencies[pair] *
@@ -400,7 +410,10 @@ template <typename T, bool kInterleaved, int kUnit>
 cudaError_t launch(const RopePlan& p, uint32_t* status, cudaStream_t stream) {
     const size_t smem = (size_t)p.tokens * 4 * p.per * sizeof(float4);
     const long long blocks = ((long long)p.a.T + p.tokens - 1) / p.tokens;
-    norm_rope_kernel<T, kInterleaved, kUnit><<<(unsigned)blocks, kThreads, smem, stream>>>(p, status);
+    if (p.per == p.lanes && p.a.head_dim % 16 == 0)
+        norm_rope_kernel<T, kInterleaved, kUnit, true><<<(unsigned)blocks, kThreads, smem, stream>>>(p, status);
+    else
+        norm_rope_kernel<T, kInterleaved, kUnit, false><<<(unsigned)blocks, kThreads, smem, stream>>>(p, status);
     return cudaGetLastError();
 }
 
@@ -421,8 +434,15 @@ cudaError_t launch_norm_rope(const DeviceInfo& dev, const NormRopeArgs& a, uint3
     p.a = a;
     p.per = (a.head_dim + 15) / 16;
     for (p.lanes = 1; p.lanes < p.per;) p.lanes *= 2;
+    for (p.pairs_shift = 3; (1 << p.pairs_shift) < 8 * p.per;) ++p.pairs_shift;
     p.k_mul = exact_inverse(a.cache.k_scale);
     p.v_mul = exact_inverse(a.cache.v_scale);
+    p.inv_dim = 1.f / (float)a.head_dim;
+    const long long strides[10] = {a.qt, a.kt, a.vt, a.qh, a.kh, a.vh, a.qot, a.kot, a.qoh, a.koh};
+    uint32_t* const bytes[10] = {&p.token_bytes[0], &p.token_bytes[1], &p.token_bytes[2], &p.head_bytes[0],
+                                 &p.head_bytes[1], &p.head_bytes[2], &p.out_token_bytes[0],
+                                 &p.out_token_bytes[1], &p.out_head_bytes[0], &p.out_head_bytes[1]};
+    for (int k = 0; k < 10; ++k) *bytes[k] = 2u * (uint32_t)strides[k];
     p.by_q = Divisor((uint32_t)std::max(1, a.q_heads));
     p.by_kv = Divisor((uint32_t)std::max(1, a.kv_heads));
     // Tokens of a CTA, up to 16 KB of cosines and sines: the number that makes waves times a CTA's time
