@@ -781,6 +781,14 @@ def dflash_qk_norm_rope_store(query: torch.Tensor | None, key: torch.Tensor, val
     return query_out, key_cache, value_cache
 
 
+def _output(t, name: str, dtype: torch.dtype, shape: tuple, index: int, dev: torch.device, stream):
+    """An output, new or given, and its address."""
+    if t is None:
+        t = _empty(shape, dtype, dev, stream)
+        return t, t.data_ptr()
+    return t, _checked(t, name, dtype, shape, index)
+
+
 def _temperatures(temperature, R: int, index: int):
     """The address of a temperature for each request (or None), and the one for all."""
     if isinstance(temperature, torch.Tensor):
@@ -812,21 +820,10 @@ def dflash_sample_path(edges: torch.Tensor, cand_ids: torch.Tensor, uniforms: to
           _checked(uniforms, "uniforms", f32, (R, S), index),
           *_temperatures(temperature, R, index))
     dev = edges.device
-    if path is None and tokens is None:
-        room = _empty((2, R, S), i32, dev, stream)
-        path, tokens = room.unbind(0)
-        out = (room.data_ptr(), room.data_ptr() + 4 * R * S)
-    else:
-        path = _empty((R, S), i32, dev, stream) if path is None else path
-        tokens = _empty((R, S), i32, dev, stream) if tokens is None else tokens
-        out = (_checked(path, "path", i32, (R, S), index),
-               _checked(tokens, "tokens", i32, (R, S), index))
-    if probs is None:
-        probs = _empty((R, S, K), f32, dev, stream)
-        probs_at = probs.data_ptr()
-    else:
-        probs_at = _checked(probs, "probs", f32, (R, S, K), index)
-    _launch(lib.dflash_sample_path, dev, stream, *at, R, S, K, *out, probs_at)
+    path, path_at = _output(path, "path", i32, (R, S), index, dev, stream)
+    tokens, tokens_at = _output(tokens, "tokens", i32, (R, S), index, dev, stream)
+    probs, probs_at = _output(probs, "probs", f32, (R, S, K), index, dev, stream)
+    _launch(lib.dflash_sample_path, dev, stream, *at, R, S, K, path_at, tokens_at, probs_at)
     return path, tokens, probs
 
 
@@ -885,27 +882,16 @@ def dflash_verify_drafts(logits: torch.Tensor, query_start: torch.Tensor,
         probs_at = _checked(draft_probs, "draft_probs", f32, (R, S, K), index)
     temps, temp = _temperatures(temperature, R, index)
     dev = logits.device
-    if tokens is None and counts is None:
-        room = _empty((R * (S + 2),), i32, dev, stream)
-        tokens, counts = room[:R * (S + 1)].view(R, S + 1), room[R * (S + 1):]
-        out = (room.data_ptr(), room.data_ptr() + 4 * R * (S + 1))
-    else:
-        tokens = _empty((R, S + 1), i32, dev, stream) if tokens is None else tokens
-        counts = _empty((R,), i32, dev, stream) if counts is None else counts
-        out = (_checked(tokens, "tokens", i32, (R, S + 1), index),
-               _checked(counts, "counts", i32, (R,), index))
-    if logprobs is None:
-        logprobs = _empty((R, S + 1), f32, dev, stream)
-        logprobs_at = logprobs.data_ptr()
-    else:
-        logprobs_at = _checked(logprobs, "logprobs", f32, (R, S + 1), index)
+    tokens, tokens_at = _output(tokens, "tokens", i32, (R, S + 1), index, dev, stream)
+    counts, counts_at = _output(counts, "counts", i32, (R,), index, dev, stream)
+    logprobs, logprobs_at = _output(logprobs, "logprobs", f32, (R, S + 1), index, dev, stream)
     if workspace is None:
         workspace = _workspace(lib.dflash_verify_drafts_workspace_bytes(R, T, V), dev, None, stream)
     else:
         _check_workspace(workspace, dev)
     _launch(lib.dflash_verify_drafts, dev, stream, logits.data_ptr(), code, T, V, logits.stride(0),
-            start, drafts, R, S, ids_at, probs_at, K, accept, sample, temps, temp, *out, logprobs_at,
-            workspace.data_ptr(), workspace.nbytes)
+            start, drafts, R, S, ids_at, probs_at, K, accept, sample, temps, temp, tokens_at, counts_at,
+            logprobs_at, workspace.data_ptr(), workspace.nbytes)
     return tokens, counts, logprobs
 
 

@@ -27,9 +27,12 @@
 //
 // The drawn path takes the edge scores as the drafter's own distribution of each token given the
 // one before it, softmax over c of E[r,p,c_{p-1},c] / T, and inverts its running sum at a number that
-// the caller drew. Staged through the same ring; one warp follows the path while the others copy.
+// the caller drew.
 #include "common.cuh"
+#include "ptx.cuh"
 
+#include <algorithm>
+#include <cfloat>
 #include <cmath>
 
 namespace dflash {
@@ -205,12 +208,18 @@ best_path_kernel(const float* __restrict__ edges, const int32_t* __restrict__ ca
 //
 // The choice is the one that exact sums give. Sums are taken in fp32 first, and where u_p sum_j w_j
 // lies within kSlack of the sum from one of the borders, again in fp64. The fp32 error: exponents are
-// sums of two floats, expf is within 2^-23, its product with the lower part and the scan's five
-// additions 6 * 2^-24; the border's product 2^-24: in all below 2^-20 of the sum. A few choices in a
-// hundred thousand are taken again.
+// rounded four times (difference, log2(e) / T twice, product), 2^-22 of |z|, and sum p |z| <= ln 32 + 1; ex2
+// is within 2^-22, 32 additions within 2^-19: in all below 2^-18 of the sum. A choice in about ten thousand is
+// taken again.
 //
-// Bound by latency: S dependent choices of a warp, each a maximum, an exponential and a scan.
-constexpr float kSlack = 0x1p-19f;
+// A CTA a request. Every row's choice is made, a thread a row, whether the path comes through it or not: following
+// the path is then a look-up for each step. (One warp that made the choices along the path, a maximum, an
+// exponential and a scan for each, took 15 us for 15 steps, this 5.) Rows lie in shared memory at a distance that
+// spreads threads over the banks. The distributions are then taken for the path's rows, a warp a step.
+// Bound by latency; 512 requests of 15 steps of 32 also read 31 MB of edges, 4.7 us at the copy rate.
+constexpr float kSlack = 0x1p-17f;
+constexpr int kSampleThreads = 256;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // The order of floats as unsigned numbers; NaN lowest.
 __device__ __forceinline__ uint32_t order_of(float x) {
@@ -219,80 +228,155 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 }
 
 // The first lane whose running sum of w passes u times the sum of all; the last with w > 0 if none does.
-template <typename F>
-__device__ __forceinline__ int invert(F w, F u, int lane, F& total, F& run) {
-    run = w;
+__device__ __forceinline__ int invert(double w, double u, int lane) {
+    double run = w;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const F other = __shfl_up_sync(kFull, run, d);
+        const double other = __shfl_up_sync(kFull, run, d);
         if (lane >= d) run += other;
     }
-    total = __shfl_sync(kFull, run, 31);
-    const unsigned past = __ballot_sync(kFull, run > u * total), any = __ballot_sync(kFull, w > F(0));
+    const double total = __shfl_sync(kFull, run, 31);
+    const unsigned past = __ballot_sync(kFull, run > u * total), any = __ballot_sync(kFull, w > 0.0);
     return past ? __ffs(past) - 1 : 31 - __clz(any | 1u);
 }
 
-__global__ void __launch_bounds__(kThreads) sample_path_kernel(SamplePathArgs a) {
+// T, its inverse in two floats, and whether it is greedy.
+struct PathTemperature {
+    float t, inv, inv_low;
+    bool greedy;
+    __device__ __forceinline__ explicit PathTemperature(float x) {
+        greedy = !(x > 0.f);                             // NaN too
+        t = fmaxf(x, 0x1p-100f);
+        inv = greedy ? 0.f : 1.f / t;
+        inv_low = t < 0x1p60f ? inv * fmaf(-t, inv, 1.f) : 0.f;
+    }
+};
+
+// The choice in a row of K scores at `row`, and 0x80 if fp32 sums do not settle it. One thread. Weights take the
+// scores' place.
+template <int kVec>
+__device__ __forceinline__ uint32_t choose(float* row, int K, float u, const PathTemperature& t) {
+    float m = -INFINITY;
+    int first = -1;
+    auto each = [&](bool back, auto&& f) {
+        for (int c = 0; c < K; c += kVec) {
+            float e[kVec];
+            if constexpr (kVec == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(row + c);
+                e[0] = v.x, e[1] = v.y, e[2] = v.z, e[3] = v.w;
+            } else {
+                e[0] = row[c];
+            }
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) f(c + k, e[k]);
+            if (!back) continue;
+            if constexpr (kVec == 4) *reinterpret_cast<float4*>(row + c) = make_float4(e[0], e[1], e[2], e[3]);
+            else row[c] = e[0];
+        }
+    };
+    each(false, [&](int c, float e) {
+        if (e > m || (first < 0 && e == e)) {            // -0 equals 0
+            m = e;
+            first = c;
+        }
+    });
+    if (t.greedy || !(fabsf(m) < INFINITY)) return max(first, 0);
+    const float scale = kLog2e * t.inv;
+    float total = 0.f;
+    each(true, [&](int, float& e) {
+        e = e > -INFINITY ? ptx::ex2(fmaxf(e - m, -FLT_MAX) * scale) : 0.f;
+        total += e;
+    });
+    const float border = u * total;
+    float run = 0.f, near = INFINITY;
+    int pick = -1, last = 0;
+    each(false, [&](int c, float w) {
+        run += w;
+        near = fminf(near, fabsf(run - border));
+        if (w > 0.f) last = c;
+        if (pick < 0 && run > border) pick = c;
+    });
+    return (uint32_t)(pick < 0 ? last : pick) | (near <= kSlack * total ? 0x80u : 0u);
+}
+
+// chunk: steps that are in shared memory at a time; stride: floats from row to row there.
+template <int kVec>
+__global__ void __launch_bounds__(kSampleThreads) sample_path_kernel(SamplePathArgs a, int chunk, int stride) {
     extern __shared__ __align__(16) uint8_t path_smem[];
     const int tid = threadIdx.x, lane = tid & 31, K = a.K, S = a.S;
     const long long r = blockIdx.x;
-    float* ring = reinterpret_cast<float*>(path_smem);                        // [kDepth][K*K]
-    float* u = reinterpret_cast<float*>(path_smem + path_ring_bytes(K));      // [S]
-    uint8_t* chosen = reinterpret_cast<uint8_t*>(u + S);                      // [S]
+    float* rows = reinterpret_cast<float*>(path_smem);                        // [chunk * K][stride]
+    float* u = rows + (size_t)chunk * K * stride;                             // [S]
+    uint8_t* picks = reinterpret_cast<uint8_t*>(u + S);                       // [chunk * K]
+    uint8_t* chosen = picks + chunk * K;                                      // [S]
     const float* E = a.edges + (size_t)r * S * K * K;
-    const bool wide = (K & 1) == 0 && (reinterpret_cast<uintptr_t>(a.edges) & 15) == 0;
-    for (int p = 0; p < kDepth; ++p) {
-        if (p < S) stage_step(ring, E, p, K, tid, wide);
-        cp_async_commit();
-    }
-    for (int p = tid; p < S; p += kThreads) u[p] = fminf(fmaxf(a.uniforms[(size_t)r * S + p], 0.f), 1.f - 0x1p-24f);
-    float t = a.temperatures ? a.temperatures[r] : a.temperature;
-    const bool greedy = !(t > 0.f);                      // NaN too
-    t = fmaxf(t, 0x1p-100f);
-    // 1 / T in two floats.
-    const float inv_t = greedy ? 0.f : 1.f / t;
-    const float inv_low = t < 0x1p60f ? inv_t * fmaf(-t, inv_t, 1.f) : 0.f;
+    // numbers outside [0, 1) count as the nearer end, NaN as 0
+    for (int p = tid; p < S; p += kSampleThreads)
+        u[p] = fminf(fmaxf(a.uniforms[(size_t)r * S + p], 0.f), 1.f - 0x1p-24f);
+    const PathTemperature t(a.temperatures ? a.temperatures[r] : a.temperature);
     int before = 0;                                      // the row of step 0 is q = 0
-    for (int p = 0; p < S; ++p) {
-        cp_async_wait_ring();
+    for (int p0 = 0; p0 < S; p0 += chunk) {
+        const int steps = min(chunk, S - p0), n = steps * K;
+        const float* from = E + (size_t)p0 * K * K;
+        // A run of threads copies a row.
+        const int across = K / kVec, down = kSampleThreads / across;
+        const int x = tid % across * kVec, y = tid / across;
+        if (y < down)
+            for (int i = y; i < n; i += down) {
+                if constexpr (kVec == 4) cp_async16(rows + i * stride + x, from + (size_t)i * K + x);
+                else cp_async4(rows + i * stride + x, from + (size_t)i * K + x);
+            }
+        asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
-        if (p >= 1) {
-            if (p - 1 + kDepth < S) stage_step(ring, E, p - 1 + kDepth, K, tid, wide);
-            cp_async_commit();
-        }
-        if (tid >= 32) continue;
-        const float e = lane < K ? ring[(size_t)(p % kDepth) * K * K + before * K + lane] + 0.f : NAN;   // no -0
-        const uint32_t order = order_of(e), top = __reduce_max_sync(kFull, order);
-        // the largest score (of a row with one): its first lane
-        const int first = __ffs(__ballot_sync(kFull, order == top)) - 1;
-        const float m = __shfl_sync(kFull, e, first);
-        float prob = lane == first ? 1.f : 0.f;
-        int pick = first;
-        if (!greedy && fabsf(m) < INFINITY) {            // else nothing to draw from: the largest
-            float w = 0.f;
-            if (e > -INFINITY) {
-                // z in two floats; exp(z_low) = 1 + z_low
-                const float d = __fsub_rn(e, m), back = __fsub_rn(d, e);
-                const float d_low = __fsub_rn(__fsub_rn(e, __fsub_rn(d, back)), __fadd_rn(m, back));
-                const float z = __fmul_rn(d, inv_t);
-                const float z_low = fmaf(d, inv_low, fmaf(d_low, inv_t, fmaf(d, inv_t, -z)));
-                w = expf(z);
-                if (z > -100.f) w = fmaf(w, z_low, w);
-            }
-            float total, run;
-            pick = invert(w, u[p], lane, total, run);
-            prob = w / total;
-            if (__any_sync(kFull, lane < K && fabsf(run - u[p] * total) <= kSlack * total)) {
-                double wd = e > -INFINITY ? exp(((double)e - (double)m) / (double)t) : 0.0, td, rd;
-                pick = invert(wd, (double)u[p], lane, td, rd);
+        for (int i = tid; i < n; i += kSampleThreads)
+            if (p0 > 0 || i == 0 || i >= K) picks[i] = (uint8_t)choose<kVec>(rows + i * stride, K, u[p0 + i / K], t);
+        __syncthreads();
+        if (tid < 32) {
+            for (int p = 0; p < steps; ++p) {
+                const int i = p * K + before;
+                int pick = picks[i] & 0x7f;
+                if (picks[i] & 0x80) {
+                    const float e = lane < K ? from[(size_t)i * K + lane] : NAN;
+                    const uint32_t order = order_of(e), top = __reduce_max_sync(kFull, order);
+                    const float m = __shfl_sync(kFull, e, __ffs(__ballot_sync(kFull, order == top)) - 1);
+                    const double w = e > -INFINITY ? exp(((double)e - (double)m) / (double)t.t) : 0.0;
+                    pick = invert(w, (double)u[p0 + p], lane);
+                }
+                if (lane == 0) chosen[p0 + p] = (uint8_t)pick;
+                before = pick;
             }
         }
-        if (lane < K) a.probs[((size_t)r * S + p) * K + lane] = prob;
-        if (lane == 0) chosen[p] = (uint8_t)pick;
-        before = pick;
+        __syncthreads();
+        // The distributions along the path.
+        for (int p = tid >> 5; p < steps; p += kSampleThreads / 32) {
+            const int at = p0 + p, i = p * K + (at > 0 ? chosen[at - 1] : 0);
+            const float e = lane < K ? from[(size_t)i * K + lane] + 0.f : NAN;   // no -0
+            const uint32_t order = order_of(e), top = __reduce_max_sync(kFull, order);
+            // the largest score (of a row with one): its first lane
+            const int first = __ffs(__ballot_sync(kFull, order == top)) - 1;
+            const float m = __shfl_sync(kFull, e, first);
+            float prob = lane == first ? 1.f : 0.f;
+            if (!t.greedy && fabsf(m) < INFINITY) {      // else nothing to draw from: the largest
+                float w = 0.f;
+                if (e > -INFINITY) {
+                    // z in two floats; exp(z_low) = 1 + z_low
+                    const float d = fmaxf(__fsub_rn(e, m), -FLT_MAX), back = __fsub_rn(d, e);
+                    const float d_low = __fsub_rn(__fsub_rn(e, __fsub_rn(d, back)), __fadd_rn(m, back));
+                    const float z = __fmul_rn(d, t.inv);
+                    const float z_low = fmaf(d, t.inv_low, fmaf(d_low, t.inv, fmaf(d, t.inv, -z)));
+                    w = expf(z);
+                    if (z > -100.f) w = fmaf(w, z_low, w);
+                }
+                float total = w;
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) total += __shfl_xor_sync(kFull, total, d);
+                prob = w / total;
+            }
+            if (lane < K) a.probs[((size_t)r * S + at) * K + lane] = prob;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    for (int p = tid; p < S; p += kThreads) {
+    for (int p = tid; p < S; p += kSampleThreads) {
         const int c = chosen[p];
         a.path[(size_t)r * S + p] = c;
         a.tokens[(size_t)r * S + p] = a.cand_ids[((size_t)r * S + p) * K + c];
@@ -302,8 +386,16 @@ __global__ void __launch_bounds__(kThreads) sample_path_kernel(SamplePathArgs a)
 }  // namespace
 
 cudaError_t launch_sample_path(const SamplePathArgs& a, cudaStream_t stream) {
-    const size_t smem = path_ring_bytes(a.K) + (((size_t)a.S * 5 + 15) & ~(size_t)15);
-    sample_path_kernel<<<(unsigned)a.R, kThreads, smem, stream>>>(a);
+    // Rows of whole 16-byte pieces lie 16 bytes apart, which spreads 8 threads' pieces over the banks (K = 4: two
+    // at a time); others at an odd distance.
+    const bool wide = a.K % 4 == 0 && (reinterpret_cast<uintptr_t>(a.edges) & 15) == 0;
+    const int stride = wide ? a.K + 4 : a.K | 1;
+    constexpr int kRoom = 40 * 1024;                     // five CTAs an SM, and no more than 48 KB in all
+    const int most = kRoom / (a.K * stride * 4), chunks = (a.S + most - 1) / most;
+    const int chunk = (a.S + chunks - 1) / chunks;
+    const size_t smem = (size_t)chunk * a.K * stride * 4 + (size_t)a.S * 5 + (size_t)chunk * a.K;
+    if (wide) sample_path_kernel<4><<<(unsigned)a.R, kSampleThreads, smem, stream>>>(a, chunk, stride);
+    else sample_path_kernel<1><<<(unsigned)a.R, kSampleThreads, smem, stream>>>(a, chunk, stride);
     return cudaGetLastError();
 }
 
