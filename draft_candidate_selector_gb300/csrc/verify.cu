@@ -97,6 +97,9 @@ template <typename T>
 struct Row {
     static constexpr int kN = Vec<T>::kN;
     static constexpr int kTile = kVecs * 32 * kN;
+    // -inf
+    static constexpr uint32_t kLow = sizeof(T) == 4 ? 0xff800000u
+                                                    : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
     const T* x;
     int V, head;
     __device__ __forceinline__ Row(const VerifyArgs& a, long long row) {
@@ -119,8 +122,6 @@ struct Row {
     // Tile t's whole vectors, a warp's lanes side by side, -inf where there are none. from: the first, in
     // the row or in a copy of it.
     __device__ __forceinline__ void load(int t, int lane, const uint4* from, uint4 (&v)[kVecs]) const {
-        constexpr uint32_t low = sizeof(T) == 4 ? 0xff800000u
-                                                : std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
         int n;
         body(t, n);
         from += lane;
@@ -131,7 +132,7 @@ struct Row {
         }
 #pragma unroll
         for (int k = 0; k < kVecs; ++k) {
-            v[k] = make_uint4(low, low, low, low);
+            v[k] = make_uint4(kLow, kLow, kLow, kLow);
             if ((k * 32 + lane) * kN + kN <= n) v[k] = from[32 * k];
         }
     }
@@ -186,7 +187,7 @@ struct VerifyPlan {
     VerifyArgs a;
     int tiles;                // of a row
     int chunks;               // items of a row: kSumWarps tiles each
-    float2* sums;             // [T][tiles]: the largest logit, the sum of exp((x - it) / T); a listed row's: a double
+    float2* sums;             // [T][tiles]: the largest logit, the sum of exp((x - it) / T); a listed row's: a Two
     Unsettled* list;          // [R]
     unsigned* listed;         // how many
     // Where rows may be passed over (else null), by position and request, [S + 1][padded]:
@@ -204,8 +205,7 @@ __device__ __forceinline__ float warp_max(float x) {
     asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
     return y;
 }
-template <typename F>
-__device__ __forceinline__ F warp_sum(F x) {
+__device__ __forceinline__ float warp_sum(float x) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(kFull, x, d);
     return x;
@@ -237,10 +237,9 @@ __device__ __forceinline__ bool join_tiles(const float2* sums, int tiles, float 
 }
 
 // q of token x in row (r, i), by a warp.
-template <typename F>
-__device__ __forceinline__ F draft_probability(const VerifyArgs& a, long long at, int x, int lane) {
-    if (!a.cand_ids) return F(1);
-    F q = 0;
+__device__ __forceinline__ float draft_probability(const VerifyArgs& a, long long at, int x, int lane) {
+    if (!a.cand_ids) return 1.f;
+    float q = 0.f;
     if (lane < a.K && a.cand_ids[at * a.K + lane] == x) q = a.draft_probs[at * a.K + lane];
     return warp_sum(q);
 }
@@ -341,7 +340,7 @@ __device__ __noinline__ int judge(const VerifyPlan& p, int r, int i, long long r
     if ((unsigned)token >= (unsigned)a.V) return kRejected;
     const float l = to_float(Row<T>(a, row).x[token]);
     if (temp.greedy) return l < M ? kRejected : kTaken;
-    const float q = draft_probability<float>(a, draft, token, lane);
+    const float q = draft_probability(a, draft, token, lane);
     const float z = (l - M) * temp.c;
     const float w = ptx::ex2(z), uq = a.accept_uniforms[draft] * q * Z;
     return uq > w * (1.f + kSlack - z * 0x1p-20f) + kSlack * uq ? kRejected : kTaken;
@@ -618,13 +617,50 @@ __global__ void __launch_bounds__(kStartThreads) start_kernel(const __grid_const
 
 // ---------------------------------------------------------------- sums of twice the precision
 
-// A value as the sum of two floats.
+// A value as the sum of two floats, the second at most half a step of the first.
 struct Two {
     float h, l;
 };
 __device__ __forceinline__ Two two_sum(float a, float b) {        // exact
     const float s = __fadd_rn(a, b), bb = __fsub_rn(s, a);
     return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb))};
+}
+
+__device__ __forceinline__ Two quick_sum(float a, float b) {      // exact where |a| >= |b|
+    const float s = __fadd_rn(a, b);
+    return {s, __fsub_rn(b, __fsub_rn(s, a))};
+}
+// Sums and products are within about 2^-46 of the larger operand, or of the product. (fp64 would be a few hundred
+// clocks an operation here.)
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    const Two s = two_sum(a.h, b.h);
+    return quick_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
+}
+__device__ __forceinline__ Two operator-(Two a, Two b) { return a + Two{-b.h, -b.l}; }
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    const float p = __fmul_rn(a.h, b.h);
+    return quick_sum(p, __fmaf_rn(a.l, b.h, __fmaf_rn(a.h, b.l, __fmaf_rn(a.h, b.h, -p))));
+}
+__device__ __forceinline__ bool operator>(Two a, Two b) { return a.h > b.h || (a.h == b.h && a.l > b.l); }
+
+// What the choice needs of its numbers, float or Two.
+template <typename F>
+__device__ __forceinline__ F number(float x);
+template <>
+__device__ __forceinline__ float number<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ Two number<Two>(float x) { return {x, 0.f}; }
+__device__ __forceinline__ float rounded(float x) { return x; }
+__device__ __forceinline__ float rounded(Two x) { return x.h; }
+__device__ __forceinline__ float shift_up(float x, int d) { return __shfl_up_sync(kFull, x, d); }
+__device__ __forceinline__ Two shift_up(Two x, int d) {
+    return {__shfl_up_sync(kFull, x.h, d), __shfl_up_sync(kFull, x.l, d)};
+}
+__device__ __forceinline__ Two warp_sum(Two x) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        x = x + Two{__shfl_xor_sync(kFull, x.h, d), __shfl_xor_sync(kFull, x.l, d)};
+    return x;
 }
 
 // 2^(j / 64) in two floats.
@@ -677,43 +713,43 @@ __device__ __forceinline__ Two exp_two(float x, float M, Two inv_t, const Two* p
     const float low = __fadd_rn(__fsub_rn(sh, __fsub_rn(one, 1.f)), tail);
     const Two b = powers[k & 63];
     const float h = __fmul_rn(one, b.h);
-    const float l = __fmaf_rn(low, b.h, __fmaf_rn(one, b.l, __fmaf_rn(one, b.h, -h)));
+    const Two w = quick_sum(h, __fmaf_rn(low, b.h, __fmaf_rn(one, b.l, __fmaf_rn(one, b.h, -h))));
     const float scale = __int_as_float(((k >> 6) + 127) << 23);
     const bool some = p > -87.f;
-    return {some ? h * scale : 0.f, some ? l * scale : 0.f};
+    return {some ? w.h * scale : 0.f, some ? w.l * scale : 0.f};
 }
 
-// The sum of a tile's weights, by a warp. stage: room for it in shared memory.
+// The sum of the weights of half of a tile, by a warp. stage: room for it in shared memory.
 template <typename T>
-__device__ __noinline__ double exact_tile(const Row<T>& x, int t, float M, Two inv_t, const Two* powers,
-                                          uint4* stage) {
+__device__ __noinline__ Two exact_half(const Row<T>& x, int t, int half, float M, Two inv_t, const Two* powers,
+                                       uint4* stage) {
+    constexpr int kHalf = kVecs / 2, kN = Vec<T>::kN;
     const int lane = threadIdx.x & 31;
     int n;
-    const uint4* from = reinterpret_cast<const uint4*>(x.x + x.body(t, n));
-    uint4 v[kVecs];
-    const float edge = x.edge(t, lane);
-    x.load(t, lane, from, v);
+    const uint4* from = reinterpret_cast<const uint4*>(x.x + x.body(t, n)) + half * kHalf * 32 + lane;
+    uint4 v[kHalf];
+#pragma unroll
+    for (int k = 0; k < kHalf; ++k) {
+        v[k] = make_uint4(Row<T>::kLow, Row<T>::kLow, Row<T>::kLow, Row<T>::kLow);
+        if (((half * kHalf + k) * 32 + lane) * kN + kN <= n) v[k] = from[32 * k];
+    }
+    const float edge = half == 0 ? x.edge(t, lane) : -INFINITY;
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) stage[32 * k + lane] = v[k];
+    for (int k = 0; k < kHalf; ++k) stage[32 * k + lane] = v[k];
     __syncwarp();
     const T* f = reinterpret_cast<const T*>(stage);
     Two sum[4] = {exp_two(edge, M, inv_t, powers), {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
     // (Not unrolled further: the code runs once or twice, and is fetched from far.)
 #pragma unroll 1
-    for (int e = lane; e < Row<T>::kTile; e += 128) {
+    for (int e = lane; e < Row<T>::kTile / 2; e += 128) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const Two w = exp_two(to_float(f[e + 32 * k]), M, inv_t, powers), to = two_sum(sum[k].h, w.h);
             sum[k] = {to.h, sum[k].l + (to.l + w.l)};
         }
     }
-#pragma unroll
-    for (int k = 1; k < 4; ++k) {
-        const Two to = two_sum(sum[0].h, sum[k].h);
-        sum[0] = {to.h, (sum[0].l + sum[k].l) + to.l};
-    }
-    return warp_sum((double)sum[0].h + (double)sum[0].l);
+    return warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
 // ---------------------------------------------------------------- the choice
@@ -721,22 +757,23 @@ __device__ __noinline__ double exact_tile(const Row<T>& x, int t, float M, Two i
 constexpr int kChooseThreads = 256;
 constexpr int kWarps = kChooseThreads / 32;
 constexpr int kMaxK = 32;
-constexpr int kRoom = kWarps * kVecs * 32 * 16;      // a tile for each warp, or a tile's weights
+constexpr int kTiles = kWarps / 2;                   // that the block sums exactly at a time
+constexpr int kRoom = 9 * kChooseThreads * 8;        // a tile's weights, or half a tile for each warp
+static_assert(kRoom >= kWarps * kVecs / 2 * 32 * 16, "half a tile for each warp");
 
 struct ChooseShared {
     uint4 room[kRoom / 16];
     Two powers[64];
     float M[kMaxDrafts + 1], Z[kMaxDrafts + 1], logprob[kMaxDrafts + 1];
     uint8_t state[kMaxDrafts + 1];
-    double warp[kWarps];
+    Two warp[kWarps];
     int owner[kWarps];
     // what the draft's distribution takes away: places and probabilities, each token once
     int n_less, less_at[kMaxK];
-    double less_q[kMaxK], less[kMaxK];
+    Two less_q[kMaxK], less[kMaxK];
     // answers that one thread has for all
     int tile, found, unsure;
-    double before;
-    double total;
+    Two before;
     bool last;
 };
 
@@ -747,33 +784,18 @@ __device__ __forceinline__ F block_scan(F x, ChooseShared& sh, F& total) {
     F* warps = reinterpret_cast<F*>(sh.warp);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const F o = __shfl_up_sync(kFull, x, d);
-        if (lane >= d) x += o;
+        const F o = shift_up(x, d);
+        if (lane >= d) x = x + o;
     }
     __syncthreads();
     if (lane == 31) warps[warp] = x;
     __syncthreads();
-    if (sizeof(F) == 8) {                            // fp64 is slow here: one warp takes the warps' sums
-        if (warp == 0) {
-            F s = lane < kWarps ? warps[lane] : F(0);
-#pragma unroll
-            for (int d = 1; d < kWarps; d <<= 1) {
-                const F o = __shfl_up_sync(kFull, s, d);
-                if (lane >= d) s += o;
-            }
-            __syncwarp();
-            if (lane < kWarps) warps[lane] = s;
-        }
-        __syncthreads();
-        total = warps[kWarps - 1];
-        return warp ? warps[warp - 1] + x : x;
-    }
-    F below = 0;
-    total = 0;
-#pragma unroll
+    F below = number<F>(0.f);
+    total = number<F>(0.f);
+#pragma unroll 1
     for (int w = 0; w < kWarps; ++w) {
         if (w == warp) below = total;
-        total += warps[w];
+        total = total + warps[w];
     }
     return below + x;
 }
@@ -798,26 +820,17 @@ struct Chooser {
 
     // Weight of a logit relative to the row's largest, in fp32 (F: float) or twice that.
     template <typename F>
-    __device__ __forceinline__ F weight(float x, float M) const {
-        if (sizeof(F) == 8) {
-            const Two w = exp_two(x, M, inverse(temp.t), sh.powers);
-            return (F)w.h + (F)w.l;
-        }
-        return (F)ptx::ex2((x - M) * temp.c);
-    }
-
-    template <typename F>
-    __device__ __forceinline__ F weight_of(float x, float M) const {
-        return x > -INFINITY ? weight<F>(x, M) : (F)0;
+    __device__ __forceinline__ F weight(float x, float M, Two inv_t) const {
+        if constexpr (std::is_same<F, Two>::value) return exp_two(x, M, inv_t, sh.powers);
+        else return x > -INFINITY ? ptx::ex2((x - M) * temp.c) : 0.f;
     }
 
     // Weight of a tile.
     template <typename F>
     __device__ __forceinline__ F tile_weight(long long row, int t, float M) const {
-        const float2* sums = p.sums + row * p.tiles;
-        if (sizeof(F) == 8) return (F)__ldcg(reinterpret_cast<const double*>(sums) + t);
-        const float2 s = __ldcg(&sums[t]);
-        return s.x == -INFINITY ? (F)0 : (F)(s.y * ptx::ex2((s.x - M) * temp.c));
+        const float2 s = __ldcg(&p.sums[row * p.tiles + t]);
+        if constexpr (std::is_same<F, Two>::value) return Two{s.x, s.y};
+        else return s.x == -INFINITY ? 0.f : s.y * ptx::ex2((s.x - M) * temp.c);
     }
 
     __device__ __forceinline__ float uniform() const {
@@ -845,11 +858,12 @@ struct Chooser {
                 // Lanes of one id; the first of them has the sum of their q.
                 const unsigned same = __match_any_sync(kFull, id);
                 const bool first = in && (int)__ffs(same) - 1 == lane;
-                double sum = q;
+                Two sum = {q, 0.f};
                 if (__any_sync(kFull, in && same != (1u << lane)))
+#pragma unroll 1
                     for (int k = 0; k < 32; ++k) {
                         const float oq = __shfl_sync(kFull, q, k);
-                        if ((same >> k & 1) && k != lane) sum += oq;
+                        if ((same >> k & 1) && k != lane) sum = sum + Two{oq, 0.f};
                     }
                 const unsigned firsts = __ballot_sync(kFull, first);
                 if (first) {
@@ -867,50 +881,63 @@ struct Chooser {
     // Draws a token of the row, into sh.found; whether fp32 sums settle it. Z: the sum of weights.
     template <typename F>
     __device__ bool draw(long long row, float M, F Z) {
-        constexpr bool kExact = sizeof(F) == 8;
+        constexpr bool kExact = std::is_same<F, Two>::value;
+        const F zero = number<F>(0.f);
         const Row<T> x(p.a, row);
         const int tid = threadIdx.x;
+        const Two inv_t = kExact ? inverse(temp.t) : Two{0.f, 0.f};
         F* less = reinterpret_cast<F*>(sh.less);
         const int n_less = sh.n_less;
+        // Tiles: each thread a run of them.
+        const int per = (p.tiles + kChooseThreads - 1) / kChooseThreads;
+        const int t0 = min(tid * per, p.tiles), t1 = min(t0 + per, p.tiles);
+        const float less_x = tid < n_less ? to_float(x.x[sh.less_at[tid]]) : 0.f;
+        F run = zero, total;
+#pragma unroll 1
+        for (int t = t0; t < t1; ++t) run = run + tile_weight<F>(row, t, M);
         // What each candidate loses.
         if (tid < n_less) {
-            const F w = weight<F>(to_float(x.x[sh.less_at[tid]]), M), qz = (F)sh.less_q[tid] * Z;
-            less[tid] = w < qz ? w : qz;
+            const F w = weight<F>(less_x, M, inv_t);
+            F qz;
+            if constexpr (kExact) qz = sh.less_q[tid] * Z;
+            else qz = sh.less_q[tid].h * Z;
+            less[tid] = w > qz ? qz : w;
         }
         if (tid == 0) {
             sh.found = -1;
             sh.unsure = 1;
             sh.tile = p.tiles - 1;
-            sh.before = 0;
+            *reinterpret_cast<F*>(&sh.before) = zero;
         }
         __syncthreads();
-        F lost = 0;
-        for (int k = 0; k < n_less; ++k) lost += less[k];
-        const bool any = n_less == 0 || Z - lost > (kExact ? (F)0x1p-36 : (F)kSlack) * Z;
+        F lost = zero;
+#pragma unroll 1
+        for (int k = 0; k < n_less; ++k) lost = lost + less[k];
+        const bool any = n_less == 0 || rounded(Z - lost) > (kExact ? 0x1p-36f : kSlack) * rounded(Z);
         if (!kExact && !any) return false;
         const int taken = any ? n_less : 0;          // nothing left over: from p itself
-        // Tiles: each thread a run of them; the first whose running sum passes the border has the tile.
-        const int per = (p.tiles + kChooseThreads - 1) / kChooseThreads;
-        const int t0 = min(tid * per, p.tiles), t1 = min(t0 + per, p.tiles);
-        F run = 0, total;
-        for (int t = t0; t < t1; ++t) run += tile_weight<F>(row, t, M);
+#pragma unroll 1
         for (int k = 0; k < taken; ++k) {
             const int t = x.tile_of(sh.less_at[k]);
-            if (t >= t0 && t < t1) run -= less[k];
+            if (t >= t0 && t < t1) run = run - less[k];
         }
+        // The first run whose running sum passes the border has the tile.
         const F upto = block_scan(run, sh, total);
-        const F border = (F)uniform() * total;
+        const F border = number<F>(uniform()) * total;
         const int owner = first_thread(upto > border, sh);
         if (tid == owner) {
             F before = upto - run;
             int pick = t0;
-            for (int t = t0; t < t1; ++t) {
-                F w = tile_weight<F>(row, t, M);
-                for (int k = 0; k < taken; ++k)
-                    if (x.tile_of(sh.less_at[k]) == t) w -= less[k];
-                pick = t;
-                if (before + w > border || t == t1 - 1) break;
-                before += w;
+            if (t1 - t0 > 1) {
+#pragma unroll 1
+                for (int t = t0; t < t1; ++t) {
+                    F w = tile_weight<F>(row, t, M);
+                    for (int k = 0; k < taken; ++k)
+                        if (x.tile_of(sh.less_at[k]) == t) w = w - less[k];
+                    pick = t;
+                    if (before + w > border || t == t1 - 1) break;
+                    before = before + w;
+                }
             }
             sh.tile = pick;
             *reinterpret_cast<F*>(&sh.before) = before;
@@ -918,40 +945,41 @@ struct Chooser {
         __syncthreads();
         // Inside the tile: its elements' weights, what the candidates lose taken away, then each thread a
         // run of them.
-        constexpr int kMost = Row<T>::kTile + Row<T>::kN - 1;
-        constexpr int kEach = ((kMost + kChooseThreads - 1) / kChooseThreads) | 1;   // odd: no bank conflicts
+        constexpr int kN = Row<T>::kN;
+        constexpr int kEach = ((Row<T>::kTile + kN - 1 + kChooseThreads - 1) / kChooseThreads) | 1;   // odd: no bank conflicts
         static_assert(kEach * kChooseThreads * sizeof(F) <= kRoom, "a tile's weights fit");
         F* w = reinterpret_cast<F*>(sh.room);
         const int tile = sh.tile;
         const F before = *reinterpret_cast<F*>(&sh.before);
         const int lo = x.first(tile), n = x.first(tile + 1) - lo;
         {
+            // A vector a thread; what is in none, one by one; 0 behind the end.
             int whole;
             const int skip = x.body(tile, whole) - lo;               // elements before the first vector
-            const uint4* from = reinterpret_cast<const uint4*>(x.x + lo + skip);
-            float l[Row<T>::kN];
-            const bool full = (tid + 1) * Row<T>::kN <= whole;
-            if (full) Vec<T>::widen(from[tid], l);
+            float l[kN];
+            const bool full = (tid + 1) * kN <= whole;
+            if (full) Vec<T>::widen(reinterpret_cast<const uint4*>(x.x + lo + skip)[tid], l);
+#pragma unroll 1
             for (int e = tid; e < kEach * kChooseThreads; e += kChooseThreads) {
-                const bool outside = e < skip || (e >= skip + (whole & -Row<T>::kN) && e < n);
-                if (outside || e >= n) w[e] = outside ? weight_of<F>(to_float(x.x[lo + e]), M) : (F)0;
+                const bool outside = e < skip || (e >= skip + (whole & -kN) && e < n);
+                if (outside) w[e] = weight<F>(to_float(x.x[lo + e]), M, inv_t);
+                else if (e >= n) w[e] = zero;
             }
             if (full) {
-#pragma unroll 2
-                for (int k = 0; k < Row<T>::kN; ++k)
-                    w[skip + tid * Row<T>::kN + k] = weight_of<F>(l[k], M);
+#pragma unroll
+                for (int k = 0; k < kN; ++k) w[skip + tid * kN + k] = weight<F>(l[k], M, inv_t);
             }
         }
         __syncthreads();
         if (tid < taken) {
             const int e = sh.less_at[tid] - lo;
-            if (e >= 0 && e < n) w[e] = w[e] > less[tid] ? w[e] - less[tid] : (F)0;
+            if (e >= 0 && e < n) w[e] = w[e] > less[tid] ? w[e] - less[tid] : zero;
         }
         __syncthreads();
         const F* own = w + tid * kEach;
-        run = 0;
+        run = zero;
 #pragma unroll 1
-        for (int e = 0; e < kEach; ++e) run += own[e];
+        for (int e = 0; e < kEach; ++e) run = run + own[e];
         F in_tile;
         const F here = before + block_scan(run, sh, in_tile);
         int holder = first_thread(here > border, sh);
@@ -959,7 +987,7 @@ struct Chooser {
         if (holder < 0) {
             if (!kExact) return false;
             __syncthreads();
-            const unsigned b = __ballot_sync(kFull, run > (F)0);
+            const unsigned b = __ballot_sync(kFull, run > zero);
             if ((tid & 31) == 0) sh.owner[tid >> 5] = b ? tid + 31 - __clz(b) : -1;
             __syncthreads();
             for (int k = 0; k < kWarps; ++k) holder = max(holder, sh.owner[k]);
@@ -970,14 +998,14 @@ struct Chooser {
             int pick = -1;
 #pragma unroll 1
             for (int e = 0; e < kEach && !(pick >= 0 && after > border); ++e) {
-                if (!(own[e] > (F)0)) continue;
+                if (!(own[e] > zero)) continue;
                 if (pick >= 0) at = after;
                 pick = e;
                 after = at + own[e];
             }
             if (pick >= 0) sh.found = lo + tid * kEach + pick;
-            const F slack = (F)kSlack * Z;
-            sh.unsure = pick < 0 || border - at < slack || after - border < slack;
+            const float slack = kSlack * rounded(Z);
+            sh.unsure = pick < 0 || rounded(border - at) < slack || rounded(after - border) < slack;
         }
         __syncthreads();
         return kExact || !sh.unsure;
@@ -1033,7 +1061,7 @@ struct Chooser {
         const bool in = (unsigned)token < (unsigned)a.V;
         const float l = in ? to_float(Row<T>(a, row).x[token]) : 0.f;
         const float u = drafted ? a.accept_uniforms[at] : 0.f;
-        const float q = drafted ? draft_probability<float>(a, at, token, lane) : 0.f;
+        const float q = drafted ? draft_probability(a, at, token, lane) : 0.f;
         join_tiles(p.sums + row * p.tiles, p.tiles, temp.c, lane, M, Z);
         int state = kRejected;
         float logprob = 0.f;
@@ -1065,17 +1093,22 @@ struct Chooser {
         const float M = sh.M[i];
         for (int k = tid; k < 64; k += kChooseThreads) sh.powers[k] = kPowers[k];
         __syncthreads();
-        double mine = 0.0, Z;
-        for (int t = warp; t < p.tiles; t += kWarps) {
-            const double s = exact_tile<T>(x, t, M, inverse(temp.t), sh.powers, sh.room + warp * kVecs * 32);
-            if (lane == 0) mine += s;
+        const Two inv_t = inverse(temp.t);
+        Two mine = {0.f, 0.f}, Z;
+        for (int t = warp >> 1; t < p.tiles; t += kTiles) {
+            const Two sum = exact_half<T>(x, t, warp & 1, M, inv_t, sh.powers, sh.room + warp * kVecs / 2 * 32);
+            if (lane == 0) mine = mine + sum;
         }
         block_scan(mine, sh, Z);
         const long long at = (long long)r * a.S + i;
         const int token = a.draft_tokens[at];
-        const double w = weight<double>(to_float(x.x[token]), M);
-        const double q = draft_probability<double>(a, at, token, lane);
-        return (double)a.accept_uniforms[at] * q * Z < w;
+        const Two w = weight<Two>(to_float(x.x[token]), M, inv_t);
+        Two q = {1.f, 0.f};
+        if (a.cand_ids) {
+            const bool here = lane < a.K && a.cand_ids[at * a.K + lane] == token;
+            q = warp_sum(Two{here ? a.draft_probs[at * a.K + lane] : 0.f, 0.f});
+        }
+        return w > Two{a.accept_uniforms[at], 0.f} * q * Z;
     }
 
     __device__ void run(uint32_t* status) {
@@ -1134,16 +1167,16 @@ struct Chooser {
         const int tid = threadIdx.x;
         const int start = a.query_start[r], n = a.query_start[r + 1] - start;
         const long long row = start + u.i;
-        double mine = 0.0, Z;
-        for (int t = tid; t < p.tiles; t += kChooseThreads) mine += tile_weight<double>(row, t, u.M);
+        Two mine = {0.f, 0.f}, Z;
+        for (int t = tid; t < p.tiles; t += kChooseThreads) mine = mine + tile_weight<Two>(row, t, u.M);
         block_scan(mine, sh, Z);
         gather_less(u.i, u.i < n - 1, nullptr);
-        draw<double>(row, u.M, Z);
+        draw<Two>(row, u.M, Z);
         if (tid == 0) {
             const long long at = (long long)r * (a.S + 1) + u.i;
             a.tokens[at] = sh.found;
             if (a.logprobs && sh.found >= 0)
-                a.logprobs[at] = (to_float(Row<T>(a, row).x[sh.found]) - u.M) / temp.t - logf((float)Z);
+                a.logprobs[at] = (to_float(Row<T>(a, row).x[sh.found]) - u.M) / temp.t - logf(Z.h);
         }
     }
 };
@@ -1159,28 +1192,34 @@ choose_kernel(const __grid_constant__ VerifyPlan p, uint32_t* status) {
     chooser.run(status);
 }
 
-// Items are kWarps tiles of a listed row; the CTA that finishes a row's last draws its token.
+// Items are kTiles tiles of a listed row, two warps a tile; the CTA that finishes a row's last draws its token.
 template <typename T>
 __global__ void __launch_bounds__(kChooseThreads) settle_kernel(const __grid_constant__ VerifyPlan p) {
     __shared__ ChooseShared sh;
     ptx::grid_dependency_wait();
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x, warp = tid >> 5;
     const unsigned n = __ldcg(p.listed);
     if (n == 0) return;
     if (tid < 64) sh.powers[tid] = kPowers[tid];
-    const int chunks = (p.tiles + kWarps - 1) / kWarps;
+    const int chunks = (p.tiles + kTiles - 1) / kTiles;
     for (long long item = blockIdx.x; item < (long long)n * chunks; item += gridDim.x) {
-        const int at = (int)(item / chunks), t = (int)(item - (long long)at * chunks) * kWarps + (tid >> 5);
+        const int at = (int)(item / chunks), first = (int)(item - (long long)at * chunks) * kTiles;
         const Unsettled u{__ldcg(&p.list[at].r), __ldcg(&p.list[at].i), __ldcg(&p.list[at].M), 0u};
         const Temperature temp(p.a, u.r);
         const long long row = p.a.query_start[u.r] + u.i;
         __syncthreads();
+        const int t = first + (warp >> 1);
         if (t < p.tiles) {
-            const double s = exact_tile<T>(Row<T>(p.a, row), t, u.M, inverse(temp.t), sh.powers,
-                                           sh.room + (tid >> 5) * kVecs * 32);
-            if (lane == 0) __stcg(reinterpret_cast<double*>(p.sums + row * p.tiles) + t, s);
+            const Two half = exact_half<T>(Row<T>(p.a, row), t, warp & 1, u.M, inverse(temp.t), sh.powers,
+                                           sh.room + warp * kVecs / 2 * 32);
+            if ((tid & 31) == 0) sh.warp[warp] = half;
         }
         __syncthreads();
+        if (tid < kTiles && first + tid < p.tiles) {
+            const Two sum = sh.warp[2 * tid] + sh.warp[2 * tid + 1];
+            __stcg(&p.sums[row * p.tiles + first + tid], make_float2(sum.h, sum.l));
+        }
+        __syncwarp();
         if (tid == 0) {
             __threadfence();
             sh.last = atomicAdd(&p.list[at].arrived, 1u) + 1u == (unsigned)chunks;
@@ -1267,7 +1306,7 @@ cudaError_t launch(const DeviceInfo& dev, const VerifyArgs& a, void* workspace, 
     if (e != cudaSuccess) return e;
     e = launch_kernel(choose_kernel<T>, (unsigned)a.R, kChooseThreads, 0, true, stream, p, status);
     if (e != cudaSuccess) return e;
-    const long long chunks = (long long)a.R * ((p.tiles + kWarps - 1) / kWarps);
+    const long long chunks = (long long)a.R * ((p.tiles + kTiles - 1) / kTiles);
     return launch_kernel(settle_kernel<T>, (unsigned)std::min(chunks, 3LL * dev.sm_count), kChooseThreads, 0,
                          true, stream, p);
 }
