@@ -327,13 +327,14 @@ __device__ __forceinline__ float weight_sum(const uint4 (&v)[kVecs], float m, fl
 // Sums are 8 bytes, written at once, and are all ones before: each tells by itself that it is there, and no
 // order between them is needed.
 template <typename T>
-__device__ __noinline__ int judge(const VerifyPlan& p, int r, int i, long long row) {
+__device__ __noinline__ int judge(const VerifyPlan& p, int r, int i, long long row, const volatile bool* over) {
     const VerifyArgs& a = p.a;
     const int lane = threadIdx.x & 31;
+    if (__any_sync(kFull, __ldcg(&p.alive[r]) < i)) return kTaken;   // an earlier draft is rejected: no matter
     const Temperature temp(a, r);
     const float2* sums = p.sums + row * p.tiles;
     float M, Z;
-    if (!join_tiles(sums, p.tiles, temp.c, lane, M, Z)) return kUnsure;
+    if (!join_tiles(sums, p.tiles, temp.c, lane, M, Z) || __any_sync(kFull, *over)) return kUnsure;
     if (!(Z > 0.f)) return kRejected;                // no distribution: the request ends here
     const long long draft = (long long)r * a.S + i;
     const int token = a.draft_tokens[draft];
@@ -569,7 +570,7 @@ row_sums_kernel(const __grid_constant__ VerifyPlan p, uint32_t* status) {
             }
             __threadfence_block();
             const Item row = sh.queue[popped % kQueue];
-            const int state = judge<T>(p, row.r, row.i, row.row);
+            const int state = judge<T>(p, row.r, row.i, row.row, &sh.over);
             if (state == kRejected && lane == 0) atomicMin(&p.alive[row.r], row.i);
             __syncwarp();
             if (lane == 0 && state != kUnsure) sh.popped = popped + 1;
@@ -739,17 +740,18 @@ __device__ __noinline__ Two exact_half(const Row<T>& x, int t, int half, float M
     for (int k = 0; k < kHalf; ++k) stage[32 * k + lane] = v[k];
     __syncwarp();
     const T* f = reinterpret_cast<const T*>(stage);
-    Two sum[4] = {exp_two(edge, M, inv_t, powers), {0.f, 0.f}, {0.f, 0.f}, {0.f, 0.f}};
+    Two sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
     // (Not unrolled further: the code runs once or twice, and is fetched from far.)
 #pragma unroll 1
-    for (int e = lane; e < Row<T>::kTile / 2; e += 128) {
+    for (int e = lane - 64; e < Row<T>::kTile / 2; e += 64) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const Two w = exp_two(to_float(f[e + 32 * k]), M, inv_t, powers), to = two_sum(sum[k].h, w.h);
+        for (int k = 0; k < 2; ++k) {
+            const float v = e < 0 ? (k ? -INFINITY : edge) : to_float(f[e + 32 * k]);
+            const Two w = exp_two(v, M, inv_t, powers), to = two_sum(sum[k].h, w.h);
             sum[k] = {to.h, sum[k].l + (to.l + w.l)};
         }
     }
-    return warp_sum((sum[0] + sum[1]) + (sum[2] + sum[3]));
+    return warp_sum(sum[0] + sum[1]);
 }
 
 // ---------------------------------------------------------------- the choice
