@@ -1286,7 +1286,11 @@ cudaError_t launch(const DeviceInfo& dev, const VerifyArgs& a, void* workspace, 
     if (pass_over) {
         p.alive = reinterpret_cast<int*>(at + list_bytes(a.R));
         p.handed = p.alive + p.padded;
-        p.group = (int)std::min(8LL, std::max(1LL, (long long)a.R * p.chunks / (4 * most)));
+        // To find an item takes about 2500 clocks, much of it waiting for other SMs' counts, and all CTAs ask at few
+        // addresses: up to 8 at a time (256 KB) where a position has two such groups for each CTA. (512 greedy
+        // requests over 151936: 309 us with one at a time, 263, 252 and 240 with 2, 4 and 8. 64 of them: 89, 91, 95
+        // and 99, since more is read that is not needed.)
+        p.group = (int)std::min(8LL, std::max(1LL, (long long)a.R * p.chunks / (2 * most)));
         p.groups = (p.chunks + p.group - 1) / p.group;
         p.window = (int)std::min(256LL, std::max(1LL, 2 * most / p.groups));
         const long long most_start = (long long)a.T * p.tiles / (2 * 8 * kStartThreads) + 1;

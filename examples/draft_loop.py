@@ -13,7 +13,18 @@ context (window_right -1). A step drafts S tokens; a verifier that takes a rando
 stands for the target model. The tokens taken are the context of the next step, so the block's own
 keys and values are written over.
 
+With --temperature the drafts are drawn and a target model verifies them: a second network of random
+weights, whose heads are normed and rotated by position, with a cache of its own. Each step then runs
+
+    dflash_block_tables         as above, of the drafter and of the target
+    dflash_qk_norm_rope_store   in place of the store: norms, positions and the store in one pass
+    dflash_paged_attention      as above
+    dflash_selector_lmhead      as above
+    dflash_sample_path          a drawn token per mask position, and its distribution
+    dflash_verify_drafts        the drafts that the target takes, and one token of its own
+
     python examples/draft_loop.py --requests 8 --prompt 400 --steps 4
+    python examples/draft_loop.py --temperature 0.8
 """
 
 from __future__ import annotations
@@ -43,8 +54,9 @@ class Drafter:
 
     def __init__(self, requests: int, pages: int, page_size: int, max_tokens: int, *,
                  q_heads=16, kv_heads=4, head_dim=64, vocab=4096, rank=64, K=8, S=15, window=1024,
-                 softcap=50.0, cache_dtype=torch.bfloat16, seed=0, device="cuda"):
+                 softcap=50.0, cache_dtype=torch.bfloat16, seed=0, device="cuda", rotary=False):
         self.R, self.page_size, self.S, self.K = requests, page_size, S, K
+        self.rotary = rotary
         self.heads, self.window, self.softcap = (q_heads, kv_heads, head_dim), window, softcap
         hidden = q_heads * head_dim
         g = torch.Generator().manual_seed(seed)
@@ -59,6 +71,10 @@ class Drafter:
         self.w_proj = weight(rank, hidden)
         self.pred_cb, self.succ_cb = weight(vocab, rank), weight(vocab, rank)
         self.mask_token = vocab
+
+        if rotary:
+            self.frequencies = ds.dflash_rope_frequencies(head_dim, device=device)
+            self.q_weight, self.k_weight = (1 + weight(1, head_dim)[0] for _ in range(2))
 
         # The cache: one pool of pages for keys and one for values, and each request's page list.
         self.k_cache = torch.zeros(pages, page_size, kv_heads, head_dim, device=device).to(cache_dtype)
@@ -87,9 +103,14 @@ class Drafter:
         self.free = self.free[int(taken):].contiguous()
         check_status()
         hq, hkv, d = self.heads
-        x = self.embedded(tokens, positions)
+        x = self.embed[tokens] if self.rotary else self.embedded(tokens, positions)
         q, k, v = (x @ self.w_qkv.t()).view(len(tokens), hq + 2 * hkv, d).split([hq, hkv, hkv], 1)
-        ds.dflash_store_kv(k, v, slots, self.k_cache, self.v_cache, self.k_scale, self.v_scale)
+        if self.rotary:
+            q, _, _ = ds.dflash_qk_norm_rope_store(
+                q, k, v, positions, slots, self.k_cache, self.v_cache, self.frequencies,
+                self.q_weight, self.k_weight, k_scale=self.k_scale, v_scale=self.v_scale)
+        else:
+            ds.dflash_store_kv(k, v, slots, self.k_cache, self.v_cache, self.k_scale, self.v_scale)
         out, _ = ds.dflash_paged_attention(
             q, self.k_cache, self.v_cache, self.table, start, kv_lens, window_left=self.window - 1,
             window_right=window_right, softcap=self.softcap, k_scale=self.k_scale,
@@ -102,8 +123,8 @@ class Drafter:
         self.attend(torch.cat(prompts), lens, window_right=0)
         self.context = self.context + lens
 
-    def draft(self, last: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
-        """Tokens [R, S] drafted behind the requests' last tokens [R], and their paths' scores."""
+    def candidates(self, last: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+        """Candidates [R, S, K] behind the requests' last tokens [R], and their edge scores."""
         block = torch.full((self.R, 1 + self.S), self.mask_token, device=last.device)
         block[:, 0] = last
         new = torch.full((self.R,), 1 + self.S, dtype=torch.int32, device=last.device)
@@ -111,8 +132,23 @@ class Drafter:
         masks = x.view(self.R, 1 + self.S, -1)[:, 1:].contiguous()
         ids, _, _, edges = ds.dflash_selector_lmhead(masks, self.lm_head, self.w_proj, self.pred_cb,
                                                      self.succ_cb, last.to(torch.int32), self.K)
+        return ids, edges
+
+    def draft(self, last: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+        """Tokens [R, S] drafted behind the requests' last tokens [R], and their paths' scores."""
+        ids, edges = self.candidates(last)
         _, tokens, score = ds.dflash_best_path(edges, ids)
         return tokens, score
+
+    def logits(self, last: torch.Tensor, drafts: torch.Tensor) -> tuple[torch.Tensor, torch.Tensor]:
+        """Logits [R * (S + 1), vocab] of the last tokens and drafts, each token seeing those before it,
+        and where each request's rows start."""
+        n = 1 + drafts.shape[1]
+        block = torch.cat([last[:, None].long(), drafts.long()], 1)
+        new = torch.full((self.R,), n, dtype=torch.int32, device=last.device)
+        x = self.attend(block.view(-1), new, window_right=0)
+        return x @ self.lm_head.t(), torch.arange(0, self.R * n + 1, n, dtype=torch.int32,
+                                                  device=last.device)
 
     def take(self, count: torch.Tensor) -> None:
         """Moves the contexts on by the tokens taken (the last one and those that follow it)."""
@@ -146,6 +182,49 @@ def run(requests=8, prompt=400, steps=4, page_size=16, cache_dtype=torch.bfloat1
     return torch.stack(tokens), torch.stack(scores)
 
 
+def run_sampled(requests=8, prompt=400, steps=4, page_size=16, cache_dtype=torch.bfloat16, seed=0,
+                device="cuda", show=False, temperature=0.8) -> list[tuple[torch.Tensor, ...]]:
+    """Of each step (tokens [R, S + 1], counts [R], logprobs [R, S + 1]): what a target model that samples
+    at `temperature` takes of the drafts behind seeded prompts, and adds to them."""
+    g = torch.Generator().manual_seed(seed)
+    room = prompt + (steps + 1) * 16
+    pages = requests * -(-room // page_size)
+    drafter, target = (Drafter(requests, pages, page_size, room, cache_dtype=cache_dtype, seed=s,
+                               device=device, rotary=True, window=w, softcap=0.0)
+                       for s, w in ((seed, 1024), (seed + 1, room)))
+    # As a drafter's, its embeddings and head are the target's.
+    drafter.embed, drafter.lm_head = target.embed, target.lm_head
+    lens = torch.randint(1, prompt + 1, (requests,), generator=g).tolist()
+    prompts = [torch.randint(drafter.mask_token, (n,), generator=g).to(device) for n in lens]
+    drafter.prompts(prompts)
+    target.prompts(prompts)
+    last = torch.randint(drafter.mask_token, (requests,), generator=g).to(device)
+
+    def uniforms(*shape):
+        return torch.rand(shape, generator=g).to(device)
+
+    taken = []
+    for step in range(steps):
+        t0 = time.perf_counter()
+        ids, edges = drafter.candidates(last)
+        _, drafts, probs = ds.dflash_sample_path(edges, ids, uniforms(requests, drafter.S),
+                                                 temperature=temperature)
+        logits, start = target.logits(last, drafts)
+        tokens, counts, logprobs = ds.dflash_verify_drafts(
+            logits, start, drafts, uniforms(requests, drafter.S), uniforms(requests), ids, probs,
+            temperature=temperature)
+        last = tokens.gather(1, counts[:, None].long() - 1)[:, 0].long()
+        drafter.take(counts)
+        target.take(counts)
+        taken.append((tokens, counts, logprobs))
+        if show:
+            torch.cuda.synchronize()
+            print(f"step {step}: {1e3 * (time.perf_counter() - t0):.2f} ms, taken "
+                  f"{counts.tolist()}, request 0 {tokens[0, :int(counts[0])].tolist()}")
+    check_status()
+    return taken
+
+
 def main() -> None:
     a = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     a.add_argument("--requests", type=int, default=8)
@@ -153,9 +232,15 @@ def main() -> None:
     a.add_argument("--steps", type=int, default=4)
     a.add_argument("--page-size", type=int, default=16)
     a.add_argument("--cache", choices=["bf16", "e4m3"], default="bf16")
+    a.add_argument("--temperature", type=float,
+                   help="draw the drafts, and verify them with a target model")
     a = a.parse_args()
-    run(a.requests, a.prompt, a.steps, a.page_size,
-        torch.float8_e4m3fn if a.cache == "e4m3" else torch.bfloat16, show=True)
+    cache = torch.float8_e4m3fn if a.cache == "e4m3" else torch.bfloat16
+    if a.temperature is None:
+        run(a.requests, a.prompt, a.steps, a.page_size, cache, show=True)
+    else:
+        run_sampled(a.requests, a.prompt, a.steps, a.page_size, cache, show=True,
+                    temperature=a.temperature)
 
 
 if __name__ == "__main__":

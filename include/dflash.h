@@ -369,7 +369,7 @@ dflash_status dflash_sample_path(const float* edges, const int32_t* cand_ids, co
  * order, past T or more than S + 1 is refused: count 0, tokens -1 (DFLASH_DEVICE_BAD_LENGTH). Rows
  * behind a request's first rejected draft have no effect. Rows at and behind query_start[R] are not read.
  * 0 <= S <= 255, K <= 32 (DFLASH_UNSUPPORTED beyond). Equal calls give equal bits. It can be captured
- * in a CUDA graph.
+ * in a CUDA graph; make one call on the device before capturing.
  * ---------------------------------------------------------------------------------- */
 size_t dflash_verify_drafts_workspace_bytes(int R, int T, int V);
 
