@@ -988,6 +988,9 @@ dflash_status dflash_verify_drafts(const void* logits, int dtype, int T, int V, 
                     V, R, T, S);
     if (S > dflash::kMaxDrafts)
         return fail(DFLASH_UNSUPPORTED, "S=%d: the verification supports S <= %d", S, dflash::kMaxDrafts);
+    if (V > dflash::kMaxVerifyVocab)
+        return fail(DFLASH_UNSUPPORTED, "V=%d: the verification supports V <= %d", V,
+                    dflash::kMaxVerifyVocab);
     if (T > 1 && row_stride < V)
         return fail(DFLASH_INVALID_ARGUMENT, "row_stride=%lld must be >= V=%d", row_stride, V);
     if ((cand_ids == nullptr) != (draft_probs == nullptr) && S > 0)

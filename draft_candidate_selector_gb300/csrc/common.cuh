@@ -171,6 +171,7 @@ cudaError_t launch_sample_path(const SamplePathArgs& a, cudaStream_t stream);
 // ---------------------------------------------------------------- verification (verify.cu)
 
 constexpr int kMaxDrafts = 255;      // drafts per request the verification supports
+constexpr int kMaxVerifyVocab = 1 << 20;   // up to which the error of its fp32 sums is bounded
 
 struct VerifyArgs {
     const void* logits;

@@ -246,10 +246,11 @@ __device__ __forceinline__ float draft_probability(const VerifyArgs& a, long lon
 
 // ---------------------------------------------------------------- sums of tiles
 
-// Error of the fp32 sums, relative to a row's sum: an element's exponent is rounded once in the
-// difference and its T 2^-22.4 off, so the sum is within 2^-22 sum p |z| <= 2^-22 (ln V + 1); ex2 is within
-// 2^-22, at most 24 additions in a row within 24 * 2^-24, joining the tiles (a difference, a product,
-// an exponential, additions) no more than that again. In all below 2^-17 for V < 2^31.
+// Error of the fp32 sums, relative to a row's sum, in units of 2^-24 and for V <= 2^20: the exponents' roundings
+// 2.5 |z| (log2(e) / T is 1.5 off), and sum p |z| <= ln V + 1, so 37; ex2, twice, 4 each; a tile's additions, 16 in
+// a lane and 7 across, 23, and what takes mc's rounding back 5; joining up to 1024 tiles, 32 additions in a lane, 5
+// across and a product, 38: 111, below 2^-17. A border is a difference of two such sums, and inside a tile exponents
+// are rounded once more: below 240, 2^-16.
 constexpr float kSlack = 0x1p-16f;
 
 enum : int { kTaken = 0, kRejected = 1, kUnsure = 2, kBad = 3 };   // drafts

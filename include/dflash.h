@@ -368,7 +368,7 @@ dflash_status dflash_sample_path(const float* edges, const int32_t* cand_ids, co
  * that is outside is left out of q, and DFLASH_DEVICE_BAD_ID is set. A request whose rows are out of
  * order, past T or more than S + 1 is refused: count 0, tokens -1 (DFLASH_DEVICE_BAD_LENGTH). Rows
  * behind a request's first rejected draft have no effect. Rows at and behind query_start[R] are not read.
- * 0 <= S <= 255, K <= 32 (DFLASH_UNSUPPORTED beyond). Equal calls give equal bits. It can be captured
+ * 0 <= S <= 255, K <= 32, V <= 2^20 (DFLASH_UNSUPPORTED beyond). Equal calls give equal bits. It can be captured
  * in a CUDA graph; make one call on the device before capturing.
  * ---------------------------------------------------------------------------------- */
 size_t dflash_verify_drafts_workspace_bytes(int R, int T, int V);
@@ -523,7 +523,8 @@ typedef struct {
  * positions   [T] int32, of any sign; not read if rotary_dim is 0
  * query_out, key_out  out, of the same shapes and type at their own strides. Each may be its own input
  *             (the same address and strides); else outputs must not overlap inputs.
- * Sums and products are fp32, rounded once at the end. head_dim is a multiple of 8 up to 256. A head
+ * Sums and products are fp32, rounded once at the end. (A head of zeros with eps 0 gives NaN, as the
+ * formula does.) head_dim is a multiple of 8 up to 256. A head
  * whose sum of squares passes fp32's range is taken 2^-72 as large (eps then counts as 0). T = 0
  * does nothing. One launch, no workspace.
  * ---------------------------------------------------------------------------------- */

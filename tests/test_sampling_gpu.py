@@ -417,6 +417,22 @@ def test_large_batches(dev, dtype, V, R, S, K):
             assert torch.equal(x, y)
 
 
+def test_no_rows(dev):
+    """No tokens at all: nothing is read."""
+    b = Batch(dev, [0, 0, 0], 100, 4, K=3, pad_t=1)
+    got = ds.dflash_verify_drafts(b.logits[:0], *b.args()[1:])
+    assert (got[0] == -1).all() and not got[1].any() and not got[2].any()
+    clean()
+
+
+def test_the_largest_vocabulary(dev):
+    b = Batch(dev, [2, 3, 1], 2 ** 20, K=4, spread=1.0, seed=6)
+    b.check()
+    b = Batch(dev, [1] * 3, 2 ** 20, 0, 0, BF, spread=0.01, seed=7)
+    b.check()
+    clean()
+
+
 def test_rows_past_2_to_the_31_elements(dev):
     """Logits of more than 2^31 elements: the last requests' rows."""
     V = 262144

@@ -165,6 +165,7 @@ def test_verify_refusals(lib):
     for name in ("V", "R"):
         assert verify(lib, **{name: 0}) == BAD
     assert verify(lib, T=-1) == BAD and verify(lib, S=-1) == BAD and verify(lib, S=256) == UNS
+    assert verify(lib, V=2 ** 20 + 1, stride=2 ** 20 + 1) == UNS
     assert verify(lib, stride=99) == BAD and verify(lib, K=0) == BAD and verify(lib, K=33) == UNS
     for t in (-0.5, math.nan, math.inf):
         assert verify(lib, t=t) == BAD
