@@ -295,8 +295,8 @@ template <typename T>
 __device__ __forceinline__ float weight_sum(const uint4 (&v)[kVecs], float m, float c) {
     constexpr int kN = Vec<T>::kN;
     const float mc = __fmul_rn(m, c);
-    if (fabsf(mc) < 0x1p60f) {
-        // x c - mc in one rounding, two at a time; mc's own is taken back at the end.
+    if (fabsf(mc) < 0x1p22f) {
+        // x c - mc in one rounding, two at a time; mc's own, at most 1/8, is taken back at the end.
         const uint64_t cc = ptx::pair_of(c, c), mm = ptx::pair_of(-mc, -mc);
         uint64_t s[2] = {0, 0};
 #pragma unroll

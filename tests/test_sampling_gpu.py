@@ -280,6 +280,19 @@ def test_temperatures(dev, dtype):
         b.check()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+def test_low_temperatures_and_large_logits(dev, dtype):
+    """Largest logits of up to 2^70 temperatures, where a product with 1 / T is many units off."""
+    t = torch.tensor([10.0 ** -k for k in range(20)], device=dev)
+    for K in (0, 4):
+        b = Batch(dev, [4] * 20, 5003, K=K, dtype=dtype, seed=9, t=t)
+        b.check()
+        if dtype != FP:
+            b.logits.mul_(10.0 ** 6)
+            b.t = t * 10.0 ** 7
+            b.check()
+
+
 def test_greedy_ties(dev):
     """The first of equal largest logits, in the same tile and in a later one; -0 equals +0."""
     b = Batch(dev, [3] * 6, 9000, K=0, t=0.0)
