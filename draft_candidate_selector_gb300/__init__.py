@@ -14,6 +14,11 @@ Method (page "vllm.models.beam.nvidia.dflash2"): for request r and step p,
   3. E[r,p,q,c] = unary[r,p,c]
                   + <pred_cb[cand[r,p-1,q]] * h[r,p], succ_cb[cand[r,p,c]]>
      with the anchor token as the predecessor at p = 0 (DFlash2BeamCandidateSelector)
+
+Before it, the draft step's attention: dflash_qk_norm_rope (norm and rotation of queries and keys, with
+the store into the paged cache in dflash_qk_norm_rope_store), dflash_block_tables, dflash_store_kv and
+dflash_paged_attention. Behind it, the drafts: dflash_best_path, or dflash_sample_path where they are drawn,
+and dflash_verify_drafts, which takes or rejects them against the target model's logits.
 """
 
 from __future__ import annotations
@@ -845,7 +850,7 @@ def dflash_verify_drafts(logits: torch.Tensor, query_start: torch.Tensor,
     """Drafts taken or rejected against the target's logits: returns (tokens int32 [R, S + 1], counts
     int32 [R], logprobs fp32 [R, S + 1]).
 
-    logits [T, V] bf16, fp16 or fp32 (rows may be strided) hold a row for each request's last token
+    logits [T, V] bf16, fp16 or fp32 (rows may be strided; V up to 2^20) hold a row for each request's last token
     and one for each of its drafts, at query_start int32 [R + 1] as dflash_block_tables gives it;
     draft_tokens int32 [R, S]. cand_ids and draft_probs [R, S, K] are what dflash_sample_path drew them
     from; without them each draft was certain. accept_uniforms fp32 [R, S] and sample_uniforms fp32 [R]

@@ -390,7 +390,8 @@ cudaError_t launch_sample_path(const SamplePathArgs& a, cudaStream_t stream) {
     // at a time); others at an odd distance.
     const bool wide = a.K % 4 == 0 && (reinterpret_cast<uintptr_t>(a.edges) & 15) == 0;
     const int stride = wide ? a.K + 4 : a.K | 1;
-    constexpr int kRoom = 40 * 1024;                     // five CTAs an SM, and no more than 48 KB in all
+    // (512 requests of 15 steps of 32: 22 us, 28 with single floats.)
+    constexpr int kRoom = 40 * 1024;                     // five CTAs an SM, and no more than 48 KB in all; half: 26 us
     const int most = kRoom / (a.K * stride * 4), chunks = (a.S + most - 1) / most;
     const int chunk = (a.S + chunks - 1) / chunks;
     const size_t smem = (size_t)chunk * a.K * stride * 4 + (size_t)a.S * 5 + (size_t)chunk * a.K;

@@ -31,7 +31,9 @@
  *     boundaries itself), `anchors`, `cand_ids`, `unary`, `edges` and the best path's
  *     `path`, `tokens` and `score` (accessed one element at a time, or staged with copies
  *     as wide as their alignment allows): their natural
- *     4-byte alignment suffices, so a slice of requests out of larger arrays stays valid.
+ *     4-byte alignment suffices, so a slice of requests out of larger arrays stays valid. The same
+ *     holds for every int32, int64 or fp32 array (positions, slots, frequencies, numbers and temperatures,
+ *     probabilities, counts) of the norm and rotation, the sampled path and the verification.
  *     `hidden`, `h_out`, the weights and the workspace stay 16-byte aligned.
  *   - Calls are asynchronous on `stream` (NULL = the legacy default stream). They
  *     allocate no device memory and do not synchronise the device; dflash_device_status,
@@ -359,17 +361,18 @@ dflash_status dflash_sample_path(const float* edges, const int32_t* cand_ids, co
  * is not, a token is drawn from max(p - q, 0), normalised (from p, should less than 2^-36 be left); if all
  * are taken, from p of the last row. Drawn: the smallest v with sum_{j<=v} weight_j > u sum_j weight_j.
  * Tokens are those of exact arithmetic; only where a border is within about 2^-38 of a row's sum may
- * they differ. T = 0 (so T < 0 and NaN): p is 1 at the first of the row's largest logits; T counts as at least 2^-99 and at
- * most 2^100. Masked
- * logits may be -inf or the type's lowest value; weights below 2^-125 of the largest may count as 0.
+ * they differ. T = 0 (so T < 0 and NaN): p is 1 at the first of the row's largest logits; T counts as at
+ * least 2^-99 and at most 2^100. Masked logits may be -inf or the type's lowest value; weights below
+ * 2^-125 of the largest may count as 0.
  * A sample uniform outside [0, 1) counts as the nearer end, NaN as 0.
  * A row that is reached and has a NaN, +inf or nothing but -inf ends its request without a token
  * (DFLASH_DEVICE_BAD_LOGITS). A draft that is reached and is outside [0, V) is not taken, a candidate
  * that is outside is left out of q, and DFLASH_DEVICE_BAD_ID is set. A request whose rows are out of
- * order, past T or more than S + 1 is refused: count 0, tokens -1 (DFLASH_DEVICE_BAD_LENGTH). Rows
- * behind a request's first rejected draft have no effect. Rows at and behind query_start[R] are not read.
- * 0 <= S <= 255, K <= 32, V <= 2^20 (DFLASH_UNSUPPORTED beyond). Equal calls give equal bits. It can be captured
- * in a CUDA graph; make one call on the device before capturing.
+ * order, past T or more than S + 1 is refused: count 0, tokens -1 (DFLASH_DEVICE_BAD_LENGTH); if it makes
+ * two other requests' rows overlap, their tokens are undefined. Rows behind a request's first rejected
+ * draft have no effect. Rows at and behind query_start[R] are not read.
+ * 0 <= S <= 255, K <= 32, V <= 2^20 (DFLASH_UNSUPPORTED beyond). Equal calls give equal bits. It can be
+ * captured in a CUDA graph; make one call on the device before capturing.
  * ---------------------------------------------------------------------------------- */
 size_t dflash_verify_drafts_workspace_bytes(int R, int T, int V);
 
@@ -524,9 +527,8 @@ typedef struct {
  * query_out, key_out  out, of the same shapes and type at their own strides. Each may be its own input
  *             (the same address and strides); else outputs must not overlap inputs.
  * Sums and products are fp32, rounded once at the end. (A head of zeros with eps 0 gives NaN, as the
- * formula does.) head_dim is a multiple of 8 up to 256. A head
- * whose sum of squares passes fp32's range is taken 2^-72 as large (eps then counts as 0). T = 0
- * does nothing. One launch, no workspace.
+ * formula does.) head_dim is a multiple of 8 up to 256. A head whose sum of squares passes fp32's range is
+ * taken 2^-72 as large (eps then counts as 0). T = 0 does nothing. One launch, no workspace.
  * ---------------------------------------------------------------------------------- */
 dflash_status dflash_qk_norm_rope(const void* query, const void* key, int dtype,
                                   const int32_t* positions, int T, int q_heads, int kv_heads,

@@ -404,7 +404,8 @@ def test_bad_lengths(dev):
 
 
 @pytest.mark.parametrize("dtype,V,R,S,K", [(BF, 32768, 100, 15, 8), (F32, 32768, 64, 15, 0), (FP, 30011, 130, 11, 4),
-                                           (BF, 151936, 40, 7, 5)])
+                                           (BF, 151936, 40, 7, 5), (BF, 32768, 250, 15, 8), (FP, 30011, 400, 11, 4),
+                                           (BF, 151936, 40, 12, 5)])
 def test_large_batches(dev, dtype, V, R, S, K):
     """Batches that pass over rows behind a surely rejected draft, ragged ones too."""
     g = np.random.default_rng(R)
