@@ -375,21 +375,22 @@ struct Handout {
     const VerifyPlan& p;
     const int lane;
     long long at;       // rows are not passed over: the next item; else the first row with anything left
+    int look = 0;       // the first of the rows that are looked at, at or behind `at`
     int turn;
     int more = 0;       // items in hand behind the last
     Item last;
-    int4 alive[2], handed[2];   // of the 8 rows that this lane looks at from `at` on
+    int4 alive[2], handed[2];   // of the 8 rows that this lane looks at
 
     __device__ Handout(const VerifyPlan& plan)
         : p(plan), lane(threadIdx.x & 31), at(plan.alive ? 0 : blockIdx.x), turn(blockIdx.x) {
         if (p.alive) ask();
     }
 
-    // Asks for the rows from `at` on; the answers are first needed when the next item is.
+    // Asks for the rows from `look` on; the answers are first needed when the next item is.
     __device__ __forceinline__ void ask() {
 #pragma unroll
         for (int g = 0; g < 2; ++g) {
-            const int x = (int)at + 128 * g + 4 * lane;
+            const int x = look + 128 * g + 4 * lane;
             alive[g] = handed[g] = make_int4(-1, -1, -1, -1);
             if (x >= (p.a.S + 1) * p.padded) continue;
             alive[g] = __ldcg(reinterpret_cast<const int4*>(p.alive + (x - (int)p.by_padded.of(x) * p.padded)));
@@ -424,6 +425,12 @@ struct Handout {
         }
     }
 
+    // The next rows to look at: up to a position further on, else from the first again. (Without it CTAs try the same
+    // few rows that are left, again and again: 1024 requests of 16 rows of 32768 bf16 logits 235 us, with it 194.)
+    __device__ __forceinline__ void further() {
+        look = look + 256 - (int)at <= p.a.R && look + 256 < (p.a.S + 1) * p.padded ? look + 256 : (int)at;
+    }
+
     // Looks at 256 rows, 8 a lane; takes of the turn-th of the first `window` that have anything left.
     __device__ void of_the_living() {
         const int rows = (p.a.S + 1) * p.padded;
@@ -432,7 +439,7 @@ struct Handout {
             unsigned left = 0;                                       // a bit for each of the lane's rows
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-                const int i = (int)p.by_padded.of((int)at + 128 * g + 4 * lane);
+                const int i = (int)p.by_padded.of(look + 128 * g + 4 * lane);
                 left |= ((alive[g].x >= i && handed[g].x + 1 < p.groups) |
                          (alive[g].y >= i && handed[g].y + 1 < p.groups) << 1 |
                          (alive[g].z >= i && handed[g].z + 1 < p.groups) << 2 |
@@ -451,7 +458,8 @@ struct Handout {
                 total1 += __popc(b1) << k;
             }
             if (total0 + total1 == 0) {
-                at += 256;
+                if (look == (int)at) look = (int)(at += 256);
+                else further();
                 continue;
             }
             const int pick = turn % min(total0 + total1, p.window);
@@ -462,16 +470,19 @@ struct Handout {
                 const int g = pick < total0 ? 0 : 1;
                 unsigned bits = g ? left >> 4 : left & 15u;
                 for (int k = g ? pick - total0 - below1 : pick - below0; k > 0; --k) bits &= bits - 1;
-                row = (int)at + 128 * g + 4 * lane + __ffs(bits) - 1;
+                row = look + 128 * g + 4 * lane + __ffs(bits) - 1;
                 count = (int)(atomicAdd(&p.handed[row], 1) + 1);
                 const int r = row - (int)p.by_padded.of(row) * p.padded;
                 start = p.a.query_start[r];
                 end = p.a.query_start[r + 1];
             }
             const int from = __ffs(__ballot_sync(kFull, row >= 0)) - 1;
-            if (total0 == 0) at += 128;
+            if (total0 == 0 && look == (int)at) look = (int)(at += 128);
             count = __shfl_sync(kFull, count, from);
-            if (count >= p.groups) continue;                         // others were quicker
+            if (count >= p.groups) {                                 // others were quicker
+                further();
+                continue;
+            }
             row = __shfl_sync(kFull, row, from);
             start = __shfl_sync(kFull, start, from);
             end = __shfl_sync(kFull, end, from);
@@ -536,8 +547,8 @@ row_sums_kernel(const __grid_constant__ VerifyPlan p, uint32_t* status) {
     if (warp == kSumWarps) {                                         // finds and copies
         Handout handout(p);
         for (int n = 0;; ++n) {
+            const Item item = handout.next();                        // while the slot is still in use
             if (n >= kSlots && !await(&sh.done[slot], parity ^ 1)) break;
-            const Item item = handout.next();
             if (lane == 0) {
                 sh.items[slot] = item;
                 const uint32_t bar = ptx::smem_u32(&sh.full[slot]);
@@ -1301,11 +1312,13 @@ cudaError_t launch(const DeviceInfo& dev, const VerifyArgs& a, void* workspace, 
         p.alive = reinterpret_cast<int*>(at + list_bytes(a.R));
         p.handed = p.alive + p.padded;
         // To find an item takes about 2500 clocks, much of it waiting for other SMs' counts, and all CTAs ask at few
-        // addresses: up to 8 at a time (256 KB) where a position has two such groups for each CTA. (512 greedy
-        // requests over 151936: 309 us with one at a time, 263, 252 and 240 with 2, 4 and 8. 64 of them: 89, 91, 95
-        // and 99, since more is read that is not needed.)
-        p.group = (int)std::min(8LL, std::max(1LL, (long long)a.R * p.chunks / (2 * most)));
-        p.groups = (p.chunks + p.group - 1) / p.group;
+        // addresses: up to 5 at a time (160 KB), a row in equal parts, where a position has 1.5 such groups for each
+        // CTA. (One at a time / 2 / 5 / 8 / whole rows of 10: 512 greedy requests 298, 259, 234, 239 and 226 us, 256 of
+        // them 167, 153, 146, 151 and 145; 64 sampled ones 87, 89, 94, 99 and 101, and over rows of 32 items 130, 126, 134,
+        // 147 and 160: more is read that is not needed.)
+        const int most_group = (int)std::min(5LL, std::max(1LL, (long long)a.R * p.chunks * 2 / (3 * most)));
+        p.groups = (p.chunks + most_group - 1) / most_group;
+        p.group = (p.chunks + p.groups - 1) / p.groups;
         p.window = (int)std::min(256LL, std::max(1LL, 2 * most / p.groups));
         const long long most_start = (long long)a.T * p.tiles / (2 * 8 * kStartThreads) + 1;
         start_kernel<<<(unsigned)std::min(most_start, 4LL * dev.sm_count), kStartThreads, 0, stream>>>(p);
