@@ -26,7 +26,7 @@
 // Bounds: row_sums is to be bound by memory, and reads more than it needs, since a row's draft is judged while the
 // next positions' rows stream in; choose and settle by the latency of their steps. 64 requests of 16 rows of 151936
 // bf16 logits: 86 us on an idle GPU with nothing in L2, of which sums 42, choose 15, settle 22 (8 requests have a draw
-// that fp32 does not settle); 94.5 MB are needed, 14 us. 512 requests, greedy: 239 us, sums 220, 961 MB needed, 144 us.
+// that fp32 does not settle); 94.5 MB are needed, 14 us. 512 requests, greedy: 223 us, sums 205, 961 MB needed, 144 us.
 // 256 of 262144 fp32 logits: 322 us, sums 268, 1657 MB needed, 248 us: 93% of what a copy reaches. One request: 20 us.
 //
 // Rows behind the first rejected draft are not needed. Where the batch is large, row_sums goes through
@@ -258,6 +258,12 @@ __device__ __forceinline__ float draft_probability(const VerifyArgs& a, long lon
 // across and a product, 38: 111, below 2^-17. A border is a difference of two such sums, and inside a tile exponents
 // are rounded once more: below 240, 2^-16.
 constexpr float kSlack = 0x1p-16f;
+// A draft's u q Z against its weight 2^z: one such sum, the sum of up to 32 equal candidates' q (5) and two products,
+// 118, 2^-17; and ex2, 4, with an exponent rounded three times, 2.5 |z| ln 2. Drafts within it, one in a hundred
+// thousand, are looked at again by their request's CTA alone, 120 us for 262144 logits: a wider bound would be dear.
+__device__ __forceinline__ float draft_slack(float uq, float w, float z) {
+    return 0x1p-17f * uq + (0x1p-21f - z * 0x1p-22f) * w;
+}
 
 enum : int { kTaken = 0, kRejected = 1, kUnsure = 2, kBad = 3 };   // drafts
 
@@ -351,7 +357,7 @@ __device__ __noinline__ int judge(const VerifyPlan& p, int r, int i, long long r
     const float q = draft_probability(a, draft, token, lane);
     const float z = (l - M) * temp.c;
     const float w = ptx::ex2(z), uq = a.accept_uniforms[draft] * q * Z;
-    return uq > w * (1.f + kSlack - z * 0x1p-20f) + kSlack * uq ? kRejected : kTaken;
+    return uq - w > draft_slack(uq, w, z) ? kRejected : kTaken;
 }
 
 // Slots: two are not enough (batches of 64 and 256 as above: 104 and 355 us instead of 86 and 322); items of half the
@@ -716,28 +722,51 @@ __device__ __forceinline__ Two inverse(float t) {
     return {h, h * __fmaf_rn(-t, h, 1.f)};
 }
 
+// Two of them, which the pipes take in one instruction.
+struct TwoPair {
+    uint64_t h, l;
+};
+__device__ __forceinline__ uint64_t both(float x) { return ptx::pair_of(x, x); }
+__device__ __forceinline__ uint64_t minus(uint64_t a, uint64_t b) { return ptx::fma_pair(b, both(-1.f), a); }   // a - b
+__device__ __forceinline__ TwoPair two_sum(uint64_t a, uint64_t b) {
+    const uint64_t s = ptx::add_pair(a, b), bb = minus(s, a);
+    return {s, ptx::add_pair(minus(a, minus(s, bb)), minus(b, bb))};
+}
+
 // exp((x - M) / T), within about 2^-39 of it; 0 below e^-87. With y = (x - M) / T = n ln 2 / 64 + s,
 // |s| < 0.0055: e^y = 2^(n / 64) e^s, e^s by Taylor's series to s^4 (s^5 / 120 is below 2^-44), whose terms
-// from s^2 on are below 2^-16 and need one float. powers: kPowers, in shared memory.
+// from s^2 on are below 2^-16 and need one float. powers: kPowers, in shared memory. Two logits at a time.
+__device__ __forceinline__ TwoPair exp_two(uint64_t x, float M, Two inv_t, const Two* powers) {
+    using namespace ptx;
+    const TwoPair d = two_sum(x, both(-M));
+    const uint64_t ih = both(inv_t.h), p = mul_pair(d.h, ih);
+    const uint64_t e = fma_pair(d.l, ih, fma_pair(d.h, both(inv_t.l), fma_pair(d.h, ih, mul_pair(p, both(-1.f)))));
+    const uint64_t magic = fma_pair(p, both(0x1.715476p+6f), both(12582912.f));   // 64 / ln 2; rounds to a whole
+    const uint64_t n = add_pair(magic, both(-12582912.f));
+    const uint64_t sh = fma_pair(n, both(-0x1.62e43p-7f), p);                // exact: ln 2 / 64 has 21 bits here
+    const uint64_t sl = fma_pair(n, both(0x1.05c61p-35f), e);
+    const uint64_t s = add_pair(sh, sl);
+    const uint64_t tail =
+        fma_pair(mul_pair(s, s), fma_pair(s, fma_pair(s, both(1.f / 24.f), both(1.f / 6.f)), both(0.5f)), sl);
+    const uint64_t one = add_pair(both(1.f), sh);
+    const uint64_t low = add_pair(minus(sh, add_pair(one, both(-1.f))), tail);
+    const float2 m = halves_of(magic), q = halves_of(p);
+    const int k0 = __float_as_int(m.x) - 0x4b400000, k1 = __float_as_int(m.y) - 0x4b400000;
+    const Two b0 = powers[k0 & 63], b1 = powers[k1 & 63];
+    const uint64_t bh = pair_of(b0.h, b1.h), bl = pair_of(b0.l, b1.l);
+    const uint64_t h = mul_pair(one, bh);
+    const uint64_t rest =
+        fma_pair(low, bh, fma_pair(one, bl, fma_pair(one, bh, mul_pair(h, both(-1.f)))));
+    const uint64_t scale =
+        pair_of(__int_as_float(((k0 >> 6) + 127) << 23), __int_as_float(((k1 >> 6) + 127) << 23));
+    const uint64_t w = add_pair(h, rest);
+    const float2 wh = halves_of(mul_pair(w, scale)), wl = halves_of(mul_pair(minus(rest, minus(w, h)), scale));
+    return {pair_of(q.x > -87.f ? wh.x : 0.f, q.y > -87.f ? wh.y : 0.f),
+            pair_of(q.x > -87.f ? wl.x : 0.f, q.y > -87.f ? wl.y : 0.f)};
+}
 __device__ __forceinline__ Two exp_two(float x, float M, Two inv_t, const Two* powers) {
-    const Two d = two_sum(x, -M);
-    const float p = __fmul_rn(d.h, inv_t.h);
-    const float e = __fmaf_rn(d.l, inv_t.h, __fmaf_rn(d.h, inv_t.l, __fmaf_rn(d.h, inv_t.h, -p)));
-    const float magic = __fmaf_rn(p, 0x1.715476p+6f, 12582912.f);          // 64 / ln 2; rounds to a whole
-    const float n = __fsub_rn(magic, 12582912.f);
-    const int k = __float_as_int(magic) - 0x4b400000;
-    const float sh = __fmaf_rn(n, -0x1.62e43p-7f, p);                       // exact: ln 2 / 64 has 21 bits here
-    const float sl = __fmaf_rn(n, 0x1.05c61p-35f, e);
-    const float s = __fadd_rn(sh, sl);
-    const float tail = __fmaf_rn(__fmul_rn(s, s), __fmaf_rn(s, __fmaf_rn(s, 1.f / 24.f, 1.f / 6.f), 0.5f), sl);
-    const float one = __fadd_rn(1.f, sh);
-    const float low = __fadd_rn(__fsub_rn(sh, __fsub_rn(one, 1.f)), tail);
-    const Two b = powers[k & 63];
-    const float h = __fmul_rn(one, b.h);
-    const Two w = quick_sum(h, __fmaf_rn(low, b.h, __fmaf_rn(one, b.l, __fmaf_rn(one, b.h, -h))));
-    const float scale = __int_as_float(((k >> 6) + 127) << 23);
-    const bool some = p > -87.f;
-    return {some ? w.h * scale : 0.f, some ? w.l * scale : 0.f};
+    const TwoPair w = exp_two(both(x), M, inv_t, powers);
+    return {ptx::halves_of(w.h).x, ptx::halves_of(w.l).x};
 }
 
 // The sum of the weights of half of a tile, by a warp. stage: room for it in shared memory.
@@ -760,18 +789,16 @@ __device__ __noinline__ Two exact_half(const Row<T>& x, int t, int half, float M
     for (int k = 0; k < kHalf; ++k) stage[32 * k + lane] = v[k];
     __syncwarp();
     const T* f = reinterpret_cast<const T*>(stage);
-    Two sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+    TwoPair sum = {0, 0};
     // (Not unrolled further: the code runs once or twice, and is fetched from far.)
 #pragma unroll 1
     for (int e = lane - 64; e < Row<T>::kTile / 2; e += 64) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float v = e < 0 ? (k ? -INFINITY : edge) : to_float(f[e + 32 * k]);
-            const Two w = exp_two(v, M, inv_t, powers), to = two_sum(sum[k].h, w.h);
-            sum[k] = {to.h, sum[k].l + (to.l + w.l)};
-        }
+        const uint64_t v = e < 0 ? ptx::pair_of(edge, -INFINITY) : ptx::pair_of(to_float(f[e]), to_float(f[e + 32]));
+        const TwoPair w = exp_two(v, M, inv_t, powers), to = two_sum(sum.h, w.h);
+        sum = {to.h, ptx::add_pair(sum.l, ptx::add_pair(to.l, w.l))};
     }
-    return warp_sum(sum[0] + sum[1]);
+    const float2 h = ptx::halves_of(sum.h), l = ptx::halves_of(sum.l);
+    return warp_sum(Two{h.x, l.x} + Two{h.y, l.y});
 }
 
 // ---------------------------------------------------------------- the choice
@@ -1094,8 +1121,7 @@ struct Chooser {
                 state = l == M && argmax(row, M) == token ? kTaken : kRejected;
             } else {
                 const float z = (l - M) * temp.c, w = ptx::ex2(z), uq = u * q * Z;
-                const float slack = kSlack * uq + (kSlack - z * 0x1p-20f) * w;
-                state = fabsf(uq - w) <= slack ? kUnsure : uq < w ? kTaken : kRejected;
+                state = fabsf(uq - w) <= draft_slack(uq, w, z) ? kUnsure : uq < w ? kTaken : kRejected;
                 logprob = (l - M) / temp.t - logf(Z);
             }
         }
@@ -1339,8 +1365,10 @@ cudaError_t launch(const DeviceInfo& dev, const VerifyArgs& a, void* workspace, 
     if (e != cudaSuccess) return e;
     e = launch_kernel(choose_kernel<T>, (unsigned)a.R, kChooseThreads, 0, true, stream, p, status);
     if (e != cudaSuccess) return e;
+    // More CTAs than fit at once, since the last ones of a row also draw (512 requests of 8 rows of 262144 fp32 logits:
+    // 456, 425 and 412 us with 3, 5 and 8 an SM).
     const long long chunks = (long long)a.R * ((p.tiles + kTiles - 1) / kTiles);
-    return launch_kernel(settle_kernel<T>, (unsigned)std::min(chunks, 3LL * dev.sm_count), kChooseThreads, 0,
+    return launch_kernel(settle_kernel<T>, (unsigned)std::min(chunks, 8LL * dev.sm_count), kChooseThreads, 0,
                          true, stream, p);
 }
 
