@@ -60,6 +60,33 @@ __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
                  : "memory");
 }
 
+// What other SMs write while this one reads: each access is single, and is seen by all of the GPU. (A vector of two
+// floats would be two accesses, in no order.)
+__device__ __forceinline__ void store_shared_by_all(void* p, float x, float y) {
+    asm volatile("st.relaxed.gpu.global.b64 [%0], %1;" ::"l"(p),
+                 "l"((uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x))
+                 : "memory");
+}
+__device__ __forceinline__ uint64_t load_shared_by_all(const void* p) {
+    uint64_t v;
+    asm volatile("ld.relaxed.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ int load_shared_by_all(const int* p) {
+    int v;
+    asm volatile("ld.relaxed.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+// Four such numbers, in no order.
+__device__ __forceinline__ int4 load_shared_by_all(const int4* p) {
+    int4 v;
+    asm volatile("ld.relaxed.gpu.global.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
 // A copy of contiguous bytes; both addresses and the size are multiples of 16.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
     asm volatile(

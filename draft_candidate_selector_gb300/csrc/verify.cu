@@ -217,6 +217,12 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
+// A tile's sum, as other CTAs may be writing it: whole, or as it was before.
+__device__ __forceinline__ float2 tile_sum(const float2* at) {
+    const uint64_t v = ptx::load_shared_by_all(static_cast<const void*>(at));
+    return ptx::halves_of(v);
+}
+
 // The largest logit of a row and the sum of its weights relative to it, from the tiles' sums, by a
 // warp. The sum is NaN where the row has a NaN or +inf, and 0 where all of it is -inf. False if a tile's
 // is not there yet.
@@ -226,7 +232,7 @@ __device__ __forceinline__ bool join_tiles(const float2* sums, int tiles, float 
     M = -INFINITY;
 #pragma unroll 4
     for (int t = lane; t < tiles; t += 32) {
-        const float m = __ldcg(&sums[t]).x;
+        const float m = tile_sum(&sums[t]).x;
         there &= __float_as_uint(m) != 0xffffffffu;
         M = fmaxf(M, m);
     }
@@ -235,7 +241,7 @@ __device__ __forceinline__ bool join_tiles(const float2* sums, int tiles, float 
     Z = 0.f;
 #pragma unroll 4
     for (int t = lane; t < tiles; t += 32) {
-        const float2 x = __ldcg(&sums[t]);
+        const float2 x = tile_sum(&sums[t]);
         Z += x.y * (x.x == -INFINITY ? (x.y == x.y ? 0.f : 1.f) : ptx::ex2((x.x - M) * c));
     }
     Z = warp_sum(Z);
@@ -337,13 +343,13 @@ __device__ __forceinline__ float weight_sum(const uint4 (&v)[kVecs], float m, fl
 }
 
 // Whether draft i of request r is surely rejected; kUnsure if not all of its row's sums are there. A warp.
-// Sums are 8 bytes, written at once, and are all ones before: each tells by itself that it is there, and no
-// order between them is needed.
+// Sums are 8 bytes, written and read in one access, and are all ones before: each tells by itself that it is there,
+// and no order between them is needed.
 template <typename T>
 __device__ __noinline__ int judge(const VerifyPlan& p, int r, int i, long long row, const volatile bool* over) {
     const VerifyArgs& a = p.a;
     const int lane = threadIdx.x & 31;
-    if (__any_sync(kFull, __ldcg(&p.alive[r]) < i)) return kTaken;   // an earlier draft is rejected: no matter
+    if (__any_sync(kFull, ptx::load_shared_by_all(&p.alive[r]) < i)) return kTaken;   // an earlier draft is rejected: no matter
     const Temperature temp(a, r);
     const float2* sums = p.sums + row * p.tiles;
     float M, Z;
@@ -399,8 +405,9 @@ struct Handout {
             const int x = look + 128 * g + 4 * lane;
             alive[g] = handed[g] = make_int4(-1, -1, -1, -1);
             if (x >= (p.a.S + 1) * p.padded) continue;
-            alive[g] = __ldcg(reinterpret_cast<const int4*>(p.alive + (x - (int)p.by_padded.of(x) * p.padded)));
-            handed[g] = __ldcg(reinterpret_cast<const int4*>(p.handed + x));
+            alive[g] = ptx::load_shared_by_all(
+                reinterpret_cast<const int4*>(p.alive + (x - (int)p.by_padded.of(x) * p.padded)));
+            handed[g] = ptx::load_shared_by_all(reinterpret_cast<const int4*>(p.handed + x));
         }
     }
 
@@ -598,6 +605,7 @@ row_sums_kernel(const __grid_constant__ VerifyPlan p, uint32_t* status) {
             const Item row = sh.queue[popped % kQueue];
             const int state = judge<T>(p, row.r, row.i, row.row, &sh.over);
             if (state == kRejected && lane == 0) atomicMin(&p.alive[row.r], row.i);
+            __threadfence_block();                                   // the item is read before its place is free
             __syncwarp();
             if (lane == 0 && state != kUnsure) sh.popped = popped + 1;
             __syncwarp();
@@ -618,7 +626,7 @@ row_sums_kernel(const __grid_constant__ VerifyPlan p, uint32_t* status) {
             float s = weight_sum<T>(v, m, c);
             if (__any_sync(kFull, edge > -INFINITY || edge != edge)) s += ptx::ex2((edge - fmaxf(m, -FLT_MAX)) * c);
             s = warp_sum(s);
-            if (lane == 0) __stcg(&p.sums[now.row * p.tiles + t], make_float2(m, s));
+            if (lane == 0) ptx::store_shared_by_all(&p.sums[now.row * p.tiles + t], m, s);
         }
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&sh.done[slot]));
