@@ -271,15 +271,16 @@ struct Rows {
 
     // Norms row x in place, by weights w.
     __device__ __forceinline__ void norm(uint64_t (&x)[8], const uint64_t (&w)[8]) const {
-        float sum = squares(x);
-        // Squares past fp32's range (bf16 values from 2^60 on): once more, 2^-72 as large.
+        float sum = squares(x), eps = p.a.eps;
+        // Squares past fp32's range (bf16 values from 2^60 on): once more, 2^-72 as large, and eps with the squares.
         if (__any_sync(0xffffffffu, sum > FLT_MAX)) {
             const float down = sum > FLT_MAX ? 0x1p-72f : 1.f;
 #pragma unroll
             for (int k = 0; k < 8; ++k) x[k] = ptx::mul_pair(x[k], ptx::pair_of(down, down));
             sum = squares(x);
+            eps = eps * down * down;
         }
-        const float r = rsqrtf(fmaf(sum, p.inv_dim, p.a.eps));
+        const float r = rsqrtf(fmaf(sum, p.inv_dim, eps));
         const uint64_t rr = ptx::pair_of(r, r);
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = ptx::mul_pair(x[k], ptx::mul_pair(w[k], rr));
