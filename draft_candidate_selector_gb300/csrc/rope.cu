@@ -271,16 +271,19 @@ struct Rows {
 
     // Norms row x in place, by weights w.
     __device__ __forceinline__ void norm(uint64_t (&x)[8], const uint64_t (&w)[8]) const {
-        float sum = squares(x), eps = p.a.eps;
-        // Squares past fp32's range (bf16 values from 2^60 on): once more, 2^-72 as large, and eps with the squares.
-        if (__any_sync(0xffffffffu, sum > FLT_MAX)) {
-            const float down = sum > FLT_MAX ? 0x1p-72f : 1.f;
+        float sum = squares(x), eps = p.a.eps, of = fmaf(sum, p.inv_dim, eps);
+        // Where fp32's range ends: squares past it (bf16 values from 2^60 on) once more with the head 2^-72 as large; and
+        // where the root is of less than 2^-100, with it 2^72 as large, since squares below 2^-126 lose bits (from
+        // 2^-100 on, 2^-150 for each of them does not show). eps goes with the squares.
+        if (__any_sync(0xffffffffu, !(of >= 0x1p-100f && of <= FLT_MAX))) {
+            const float by = of > FLT_MAX ? 0x1p-72f : of < 0x1p-100f ? 0x1p72f : 1.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = ptx::mul_pair(x[k], ptx::pair_of(down, down));
+            for (int k = 0; k < 8; ++k) x[k] = ptx::mul_pair(x[k], ptx::pair_of(by, by));
             sum = squares(x);
-            eps = eps * down * down;
+            eps = eps * by * by;
+            of = fmaf(sum, p.inv_dim, eps);
         }
-        const float r = rsqrtf(fmaf(sum, p.inv_dim, eps));
+        const float r = rsqrtf(of);
         const uint64_t rr = ptx::pair_of(r, r);
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[k] = ptx::mul_pair(x[k], ptx::mul_pair(w[k], rr));

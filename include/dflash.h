@@ -528,7 +528,8 @@ typedef struct {
  *             (the same address and strides); else outputs must not overlap inputs.
  * Sums and products are fp32, rounded once at the end. (A head of zeros with eps 0 gives NaN, as the
  * formula does.) head_dim is a multiple of 8 up to 256. A head whose sum of squares passes fp32's range is
- * taken 2^-72 as large, and eps with it. T = 0 does nothing. One launch, no workspace.
+ * taken 2^-72 as large, one whose mean square and eps come to less than 2^-100 2^72 as large, and eps with it.
+ * T = 0 does nothing. One launch, no workspace.
  * ---------------------------------------------------------------------------------- */
 dflash_status dflash_qk_norm_rope(const void* query, const void* key, int dtype,
                                   const int32_t* positions, int T, int q_heads, int kv_heads,

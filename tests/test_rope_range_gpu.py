@@ -54,3 +54,26 @@ def test_squares_past_the_range_with_the_store(dev):                            
     step.close_heads(q, *c.want(c.query, c.q_weight, fp32(1e-6)), BF)
     step.close_heads(kc.flatten(0, 1)[c.slots], *c.want(c.key, c.k_weight, fp32(1e-6)), BF)
     clean()
+
+
+@pytest.mark.parametrize("D", [64, 80, 128, 256])
+@pytest.mark.parametrize("eps", [0.0, 1e-40, 1e-30, 1e-20, 1e-6])
+def test_squares_below_the_range(dev, D, eps):                                        # noqa: F811
+    """Heads whose squares are below fp32's range, with an eps that is as small; with none, a head of zeros has no
+    norm, as the formula says."""
+    powers = [-49, 0, -50, -52, -60, 3, -63, -70, -72, -74, 61, -75, -80, -100, -110, -1, -126, 126]
+    c = Case(dev, len(powers), 3, 2, D)
+    spread(c, powers, D)
+    check_norm(c, eps)
+    c.qkv[4] = 0
+    got = c.run(eps=eps)[0]
+    assert torch.isnan(got[4]).all() if eps == 0 else not got[4].any()
+    assert torch.isfinite(got[torch.arange(len(powers)) != 4]).all()
+    clean()
+
+
+def test_small_fp16_values(dev):                                                      # noqa: F811
+    c = Case(dev, 6, 3, 2, 128, FP)
+    spread(c, [-24, -20, -14, 0, 8, 14])
+    c.qkv[c.qkv == 0] = 2.0 ** -24
+    check_norm(c, 0.0)
