@@ -289,21 +289,56 @@ struct Rows {
         for (int k = 0; k < 8; ++k) x[k] = ptx::mul_pair(x[k], ptx::mul_pair(w[k], rr));
     }
 
-    // Rotates row x of token t in place.
+    // Pairs 2c and 2c + 1 of the thread's, rotated.
+    __device__ __forceinline__ void rotated(const uint64_t (&x)[8], int c, const float4& f, uint64_t& u, uint64_t& v) const {
+        if constexpr (!kInterleaved) {
+            const uint64_t cc = ptx::pair_of(f.x, f.y), ss = ptx::pair_of(f.z, f.w);
+            const uint64_t minus = ptx::pair_of(-f.z, -f.w);
+            u = ptx::fma_pair(x[c + 4], minus, ptx::mul_pair(x[c], cc));
+            v = ptx::fma_pair(x[c], ss, ptx::mul_pair(x[c + 4], cc));
+        } else {
+            const float2 a = ptx::halves_of(x[2 * c]), b = ptx::halves_of(x[2 * c + 1]);
+            u = ptx::pair_of(a.x * f.x - a.y * f.z, a.y * f.x + a.x * f.z);
+            v = ptx::pair_of(b.x * f.y - b.y * f.w, b.y * f.y + b.x * f.w);
+        }
+    }
+
+    // Rotates row x of token t in place. Pairs behind rotary_dim are left alone (by a cosine of 1 and a sine of 0 an
+    // infinity would make its partner NaN, and -0 would turn 0). Pairs of a unit are rotated together or not at all:
+    // units of 4 by a way out between them, of 2 by choosing between results (20001 tokens of 40 heads of 80, rotated by 40
+    // and by 20: 71 and 86 us by ways out, 73 and 81 by choosing; 69 and 79 without a difference).
     __device__ __forceinline__ void rotate(uint64_t (&x)[8], int t) const {
+        constexpr int kTogether = kInterleaved ? 1 : kUnit;
+        constexpr int kStep = kInterleaved ? 1 : 4;
+        const int turn = p.a.rotary_dim / 2 - 8 * j;                 // so many of the thread's pairs, all where 8 or more
+        if (kTogether != 2 && turn <= 0) return;
         const float4* cs = table + (size_t)t * 4 * p.per + j;
+        if (kTogether > 1 || turn >= 8) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if (kTogether == 4 && c == 2 && turn <= 4) return;
+                const bool on = kTogether != 2 || 2 * c < turn;
+                const int at = kInterleaved ? 2 * c : c;
+                uint64_t u, v;
+                rotated(x, c, cs[c * p.per], u, v);
+                x[at] = on ? u : x[at];
+                x[at + kStep] = on ? v : x[at + kStep];
+            }
+            return;
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-            const float4 f = cs[c * p.per];
-            if constexpr (!kInterleaved) {
-                const uint64_t cc = ptx::pair_of(f.x, f.y), ss = ptx::pair_of(f.z, f.w);
-                const uint64_t minus = ptx::pair_of(-f.z, -f.w), u = x[c], v = x[c + 4];
-                x[c] = ptx::fma_pair(v, minus, ptx::mul_pair(u, cc));
-                x[c + 4] = ptx::fma_pair(u, ss, ptx::mul_pair(v, cc));
-            } else {
-                const float2 u = ptx::halves_of(x[2 * c]), v = ptx::halves_of(x[2 * c + 1]);
-                x[2 * c] = ptx::pair_of(u.x * f.x - u.y * f.z, u.y * f.x + u.x * f.z);
-                x[2 * c + 1] = ptx::pair_of(v.x * f.y - v.y * f.w, v.y * f.y + v.x * f.w);
+            if (2 * c >= turn) return;
+            const int at = kInterleaved ? 2 * c : c;
+            const bool both = 2 * c + 1 < turn;
+            uint64_t u, v;
+            rotated(x, c, cs[c * p.per], u, v);
+            if constexpr (kInterleaved) {                            // u is the first pair, v the second
+                x[at] = u;
+                if (both) x[at + kStep] = v;
+            } else {                                                 // the pairs' a and their b
+                x[at] = both ? u : ptx::pair_of(ptx::halves_of(u).x, ptx::halves_of(x[at]).y);
+                x[at + kStep] = both ? v : ptx::pair_of(ptx::halves_of(v).x, ptx::halves_of(x[at + kStep]).y);
             }
         }
     }
@@ -379,7 +414,7 @@ norm_rope_kernel(const __grid_constant__ RopePlan p, uint32_t* status) {
     if (a.q_heads > 0) rows.template load<kQuery>(rows.group, first);
     else rows.template load<kKey>(rows.group, first);
     if (a.rotary_dim > 0) {
-        // Cosines and sines; pairs past rotary_dim stay as they are.
+        // Cosines and sines (of pairs behind rotary_dim none are used).
         const int pairs = 8 * p.per;
         for (int e = threadIdx.x; e < rows.tokens * pairs; e += kThreads) {
             const int t = kFull ? e >> p.pairs_shift : e / pairs, pair = e - t * pairs;

@@ -518,7 +518,8 @@ typedef struct {
  * their rotation. The pages show the call; the arithmetic is the standard one:
  *   y = x w / sqrt(mean(x^2) + eps) over a head's head_dim values (no norm where the weight is NULL),
  *   (a, b) -> rope_scale (a cos t - b sin t, b cos t + a sin t), t = positions[token] f_j,
- * for the pairs j of the first rotary_dim values; the others stay as they are (normed).
+ * for the pairs j of the first rotary_dim values; the others stay as they are, normed (without a norm: bit for
+ * bit, but that a NaN may become another NaN).
  *
  * query, key  [T, q_heads, head_dim], [T, kv_heads, head_dim] of type dtype (DFLASH_BF16 or
  *             DFLASH_FP16) at the given strides (elements, multiples of 8, below 2^31). Either may have no

@@ -77,3 +77,28 @@ def test_small_fp16_values(dev):                                                
     spread(c, [-24, -20, -14, 0, 8, 14])
     c.qkv[c.qkv == 0] = 2.0 ** -24
     check_norm(c, 0.0)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rotary", [(128, 64), (128, 2), (64, 62), (248, 34), (80, 20), (96, 0), (256, 16)])
+def test_values_behind_the_rotated_ones(dev, D, rotary, interleaved):                 # noqa: F811
+    """Without a norm they stay as they are: infinities, NaN and -0 among them, none of which reaches another."""
+    for dtype in (BF, FP):
+        c = Case(dev, 5, 3, 2, D, dtype, rotary, interleaved, norm="")
+        want = [x.clone() for x in c.run()]
+        g = torch.Generator().manual_seed(D)
+        odd = torch.tensor([float("inf"), -float("inf"), float("nan"), -0.0, 0.0])
+        which = torch.randint(0, 10, (5, 7, D - rotary), generator=g)
+        tail = c.qkv[:, :, rotary:].cpu()
+        tail = torch.where(which < 5, odd[which.clamp(max=4)].to(dtype), tail)
+        c.qkv[:, :, rotary:] = tail.to(dev)
+        kc, vc = caches(dev, 2, 16, 2, D, dtype)
+        stored = ds.dflash_qk_norm_rope_store(c.query, c.key, c.value, c.positions, c.slots, kc, vc, **c.how)
+        for got in (c.run(), (stored[0], kc.flatten(0, 1)[c.slots])):
+            for x, y, w in zip((c.query, c.key), got, want):
+                assert torch.equal(y[..., :rotary], w[..., :rotary])
+                x, y = x[..., rotary:].contiguous(), y[..., rotary:].contiguous()
+                assert torch.equal(torch.isnan(x), torch.isnan(y))
+                bits = lambda v: v.nan_to_num(nan=1.0, posinf=2.0, neginf=3.0).view(torch.int16)     # noqa: E731
+                assert torch.equal(torch.isinf(x), torch.isinf(y)) and torch.equal(bits(x), bits(y))
+        clean()
