@@ -267,8 +267,9 @@ constexpr float kSlack = 0x1p-16f;
 // A draft's u q Z against its weight 2^z: one such sum, the sum of up to 32 equal candidates' q (5) and two products,
 // 118, 2^-17; and ex2, 4, with an exponent rounded three times, 2.5 |z| ln 2. Drafts within it, one in a hundred
 // thousand, are looked at again by their request's CTA alone, 120 us for 262144 logits: a wider bound would be dear.
+// z is taken as -150 below that, where w is 0: a masked draft's is -inf, whose product with 0 would be no bound.
 __device__ __forceinline__ float draft_slack(float uq, float w, float z) {
-    return 0x1p-17f * uq + (0x1p-21f - z * 0x1p-22f) * w;
+    return 0x1p-17f * uq + (0x1p-21f - fmaxf(z, -150.f) * 0x1p-22f) * w;
 }
 
 enum : int { kTaken = 0, kRejected = 1, kUnsure = 2, kBad = 3 };   // drafts
@@ -363,7 +364,7 @@ __device__ __noinline__ int judge(const VerifyPlan& p, int r, int i, long long r
     const float q = draft_probability(a, draft, token, lane);
     const float z = (l - M) * temp.c;
     const float w = ptx::ex2(z), uq = a.accept_uniforms[draft] * q * Z;
-    return uq - w > draft_slack(uq, w, z) ? kRejected : kTaken;
+    return uq - w >= draft_slack(uq, w, z) ? kRejected : kTaken;
 }
 
 // Slots: two are not enough (batches of 64 and 256 as above: 104 and 355 us instead of 86 and 322); items of half the
@@ -1129,7 +1130,8 @@ struct Chooser {
                 state = l == M && argmax(row, M) == token ? kTaken : kRejected;
             } else {
                 const float z = (l - M) * temp.c, w = ptx::ex2(z), uq = u * q * Z;
-                state = fabsf(uq - w) <= draft_slack(uq, w, z) ? kUnsure : uq < w ? kTaken : kRejected;
+                // (Both are 0 where a draft is masked and u or q is 0: 0 < 0 does not hold.)
+                state = fabsf(uq - w) < draft_slack(uq, w, z) ? kUnsure : uq < w ? kTaken : kRejected;
                 logprob = (l - M) / temp.t - logf(Z);
             }
         }

@@ -189,3 +189,25 @@ def test_two_streams_at_once(dev):
             for x, y in zip(got, want):
                 assert torch.equal(x, y)
     assert ds.dflash_device_status(clear=True) == 0
+
+
+@pytest.mark.parametrize("mask", ["-inf", "lowest"])
+@pytest.mark.parametrize("dtype,K", [(BF, 0), (BF, 4), (F32, 4), (FP, 4)])
+def test_masked_drafts(dev, dtype, K, mask):
+    """Drafts that the target masks are surely rejected, and the rows behind them are passed over."""
+    R, S, V = 64, 15, 100003
+    b = Large(dev, dtype, V, [S + 1] * R, S, K, seed=7)
+    low = -INF if mask == "-inf" else torch.finfo(dtype).min
+    keep = torch.zeros(V, dtype=torch.bool, device=dev)
+    keep[torch.arange(11, V, 1999, device=dev)] = True
+    keep[b.ids.flatten().long() if K else b.drafts.flatten().long()] = False
+    assert int(keep.sum()) > 20
+    b.logits[:, ~keep] = low
+    b.accept.clamp_(min=2.0 ** -20)
+    got = b.check_passing(least=b.tiles() // 4)
+    assert (got[1] == 1).all() and keep[got[0][:, 0].long()].all()
+    b.accept[::2] = 0.0                                              # 0 < p does not hold either
+    b.check_passing(least=b.tiles() // 4)
+    if K:
+        b.probs.zero_()
+        b.check_passing(least=b.tiles() // 4)
