@@ -936,6 +936,28 @@ struct Chooser {
         __syncthreads();
     }
 
+    // The tile to look in after `tile` where `from` has nothing to draw: the nearest behind it with any weight, then
+    // the nearest before it; -1: none is left.
+    __device__ __noinline__ int next_tile(long long row, float M, int from, int tile) {
+        const int tid = threadIdx.x;
+        if (tile >= from) {
+            for (int t0 = tile + 1; t0 < p.tiles; t0 += kChooseThreads) {
+                const int t = t0 + tid;
+                __syncthreads();
+                const int at = first_thread(t < p.tiles && rounded(tile_weight<Two>(row, t, M)) > 0.f, sh);
+                if (at >= 0) return t0 + at;
+            }
+            tile = from;
+        }
+        for (int t0 = tile - 1; t0 >= 0; t0 -= kChooseThreads) {
+            const int t = t0 - tid;
+            __syncthreads();
+            const int at = first_thread(t >= 0 && rounded(tile_weight<Two>(row, t, M)) > 0.f, sh);
+            if (at >= 0) return t0 - at;
+        }
+        return -1;
+    }
+
     // Draws a token of the row, into sh.found; whether fp32 sums settle it. Z: the sum of weights.
     template <typename F>
     __device__ bool draw(long long row, float M, F Z) {
@@ -1007,10 +1029,13 @@ struct Chooser {
         constexpr int kEach = ((Row<T>::kTile + kN - 1 + kChooseThreads - 1) / kChooseThreads) | 1;   // odd: no bank conflicts
         static_assert(kEach * kChooseThreads * sizeof(F) <= kRoom, "a tile's weights fit");
         F* w = reinterpret_cast<F*>(sh.room);
-        const int tile = sh.tile;
+        const F* own = w + tid * kEach;
         const F before = *reinterpret_cast<F*>(&sh.before);
-        const int lo = x.first(tile), n = x.first(tile + 1) - lo;
-        {
+        F here;
+        int tile = sh.tile, lo, holder;
+        for (;;) {
+            lo = x.first(tile);
+            const int n = x.first(tile + 1) - lo;
             // A vector a thread; what is in none, one by one; 0 behind the end.
             int whole;
             const int skip = x.body(tile, whole) - lo;               // elements before the first vector
@@ -1027,30 +1052,33 @@ struct Chooser {
 #pragma unroll
                 for (int k = 0; k < kN; ++k) w[skip + tid * kN + k] = weight<F>(l[k], M, inv_t);
             }
-        }
-        __syncthreads();
-        if (tid < taken) {
-            const int e = sh.less_at[tid] - lo;
-            if (e >= 0 && e < n) w[e] = w[e] > less[tid] ? w[e] - less[tid] : zero;
-        }
-        __syncthreads();
-        const F* own = w + tid * kEach;
-        run = zero;
+            __syncthreads();
+            if (tid < taken) {
+                const int e = sh.less_at[tid] - lo;
+                if (e >= 0 && e < n) w[e] = w[e] > less[tid] ? w[e] - less[tid] : zero;
+            }
+            __syncthreads();
+            run = zero;
 #pragma unroll 1
-        for (int e = 0; e < kEach; ++e) run = run + own[e];
-        F in_tile;
-        const F here = before + block_scan(run, sh, in_tile);
-        int holder = first_thread(here > border, sh);
-        // The tile's sum and its elements' may differ by a rounding: then the last with any weight.
-        if (holder < 0) {
-            if (!kExact) return false;
+            for (int e = 0; e < kEach; ++e) run = run + own[e];
+            F in_tile;
+            here = before + block_scan(run, sh, in_tile);
+            holder = first_thread(run > zero && here > border, sh);
+            if (!kExact) break;
+            if (holder >= 0) break;
+            // The tile's sum and its elements' may differ by a rounding: then the last with any weight.
             __syncthreads();
             const unsigned b = __ballot_sync(kFull, run > zero);
             if ((tid & 31) == 0) sh.owner[tid >> 5] = b ? tid + 31 - __clz(b) : -1;
             __syncthreads();
             for (int k = 0; k < kWarps; ++k) holder = max(holder, sh.owner[k]);
-            if (holder < 0 && tid == 0) sh.found = min(lo, p.a.V - 1);
+            if (holder >= 0) break;
+            // Nor has the tile any, where the candidates took all of it, and what was left of its sum was rounding.
+            tile = next_tile(row, M, sh.tile, tile);
+            if (tile < 0) break;
         }
+        if (!kExact && holder < 0) return false;
+        if (holder < 0 && tid == 0) sh.found = min(x.first(sh.tile), p.a.V - 1);
         if (tid == holder) {
             F at = here - run, after = at;
             int pick = -1;

@@ -361,7 +361,7 @@ dflash_status dflash_sample_path(const float* edges, const int32_t* cand_ids, co
  * is not, a token is drawn from max(p - q, 0), normalised (from p, should less than 2^-36 be left); if all
  * are taken, from p of the last row. Drawn: the smallest v with sum_{j<=v} weight_j > u sum_j weight_j.
  * Tokens are those of exact arithmetic; only where a border is within about 2^-38 of a row's sum may
- * they differ. T = 0 (so T < 0 and NaN): p is 1 at the first of the row's largest logits; T counts as at
+ * they differ, and then too the token drawn has some weight. T = 0 (so T < 0 and NaN): p is 1 at the first of the row's largest logits; T counts as at
  * least 2^-99 and at most 2^100. Masked logits may be -inf or the type's lowest value; weights below
  * 2^-125 of the largest may count as 0.
  * A sample uniform outside [0, 1) counts as the nearer end, NaN as 0.

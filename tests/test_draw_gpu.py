@@ -1,0 +1,43 @@
+"""Tokens without any probability are never drawn, however near the number is to a border."""
+
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import draft_candidate_selector_gb300 as ds
+from test_sampling_gpu import BF, F32, FP, INF, Batch, clean, dev   # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("at", [0, 1500, 6000, -9])
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+def test_tiles_that_the_draft_takes_whole(dev, dtype, at):                            # noqa: F811
+    """All tokens of a tile that are not masked are the draft's, and likelier under it: nothing of the tile is
+    left, though a rounding of its sum may be. The number is 0, or the last below 1."""
+    R, V, K = 200, 20008, 8                              # rows of whole vectors: tiles from 0 on
+    b = Batch(dev, [2] * R, V, 1, K, dtype, spread=1.5, likely=False, seed=3)
+    g = torch.Generator(device=dev).manual_seed(at + 50)
+    tile = 4096 // b.logits.element_size()
+    first = (V + at if at < 0 else at) // tile * tile
+    x = b.logits.float()
+    inside = torch.arange(V, device=dev) // tile == first // tile
+    x[:, inside] = -INF
+    n = int(inside.sum())
+    ids = first + torch.rand((R, n), generator=g, device=dev).argsort(1)[:, :K]
+    x[::2].scatter_(1, ids, 9 + 1.5 * torch.randn((R, K), generator=g, device=dev))
+    x[:, ::3] = torch.where(inside[::3], x[:, ::3], torch.full_like(x[:, ::3], -INF))
+    b.logits = x.to(dtype)
+    p = torch.softmax(b.logits[::2].double(), 1).gather(1, ids)
+    b.ids, b.probs = ids.to(torch.int32)[:, None].contiguous(), (p / p.sum(1, keepdim=True)).float()[:, None].contiguous()
+    b.drafts = b.ids[:, :, 0].contiguous()
+    b.accept.fill_(1 - 2.0 ** -24)
+    assert (b.probs[:, 0].double() > p).all()
+    for u in (0.0, 1 - 2.0 ** -24):
+        b.sample.fill_(u)
+        got = b.check()
+        assert (got[1] == 1).all()
+        x = b.logits[::2].gather(1, got[0][:, :1].long())
+        assert torch.isfinite(x).all() and not (got[0][:, :1] == b.ids[:, 0]).any()
