@@ -227,7 +227,7 @@ __device__ __forceinline__ uint32_t order_of(float x) {
     return x != x ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
 }
 
-// The first lane whose running sum of w passes u times the sum of all; the last with w > 0 if none does.
+// The first lane with w > 0 whose running sum of w passes u times the sum of all; the last with w > 0 if none does.
 __device__ __forceinline__ int invert(double w, double u, int lane) {
     double run = w;
 #pragma unroll
@@ -236,7 +236,8 @@ __device__ __forceinline__ int invert(double w, double u, int lane) {
         if (lane >= d) run += other;
     }
     const double total = __shfl_sync(kFull, run, 31);
-    const unsigned past = __ballot_sync(kFull, run > u * total), any = __ballot_sync(kFull, w > 0.0);
+    // (Lanes add in different orders, so one without weight may be a rounding past the lane before it.)
+    const unsigned past = __ballot_sync(kFull, w > 0.0 && run > u * total), any = __ballot_sync(kFull, w > 0.0);
     return past ? __ffs(past) - 1 : 31 - __clz(any | 1u);
 }
 

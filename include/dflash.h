@@ -321,7 +321,8 @@ dflash_status dflash_best_path(const float* edges, const int32_t* cand_ids, int 
  *
  * With the row E[r, p, c_{p-1}, :] (at p = 0: q = 0), probs[c] = w_c / sum_j w_j, w_c =
  * exp((E_c - max E) / T), and c_p is the smallest c with sum_{j<=c} w_j > u sum_j w_j. The choice is
- * made as with exact sums (it may differ where a sum is within 2^-45 of the border); probs are fp32.
+ * made as with exact sums (it may differ where a sum is within 2^-45 of the border, and then too is of a
+ * candidate with some weight); probs are fp32.
  * T below 2^-100 counts as 2^-100.
  * T = 0 takes the largest score (so do T < 0 and NaN), the first of equals, with probability 1; a row
  * whose largest score is +inf, or which has none but -inf and NaN, is taken the same way. In other rows
@@ -361,9 +362,9 @@ dflash_status dflash_sample_path(const float* edges, const int32_t* cand_ids, co
  * is not, a token is drawn from max(p - q, 0), normalised (from p, should less than 2^-36 be left); if all
  * are taken, from p of the last row. Drawn: the smallest v with sum_{j<=v} weight_j > u sum_j weight_j.
  * Tokens are those of exact arithmetic; only where a border is within about 2^-38 of a row's sum may
- * they differ, and then too the token drawn has some weight. T = 0 (so T < 0 and NaN): p is 1 at the first of the row's largest logits; T counts as at
- * least 2^-99 and at most 2^100. Masked logits may be -inf or the type's lowest value; weights below
- * 2^-125 of the largest may count as 0.
+ * they differ, and then too the token drawn has some weight. T = 0 (so T < 0 and NaN): p is 1 at the
+ * first of the row's largest logits; T counts as at least 2^-99 and at most 2^100. Masked logits may be
+ * -inf or the type's lowest value; weights below 2^-125 of the largest may count as 0.
  * A sample uniform outside [0, 1) counts as the nearer end, NaN as 0.
  * A row that is reached and has a NaN, +inf or nothing but -inf ends its request without a token
  * (DFLASH_DEVICE_BAD_LOGITS). A draft that is reached and is outside [0, V) is not taken, a candidate

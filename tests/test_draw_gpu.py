@@ -41,3 +41,23 @@ def test_tiles_that_the_draft_takes_whole(dev, dtype, at):                      
         assert (got[1] == 1).all()
         x = b.logits[::2].gather(1, got[0][:, :1].long())
         assert torch.isfinite(x).all() and not (got[0][:, :1] == b.ids[:, 0]).any()
+
+
+@pytest.mark.parametrize("K", [7, 13, 32])
+def test_masked_candidates(dev, K):                                                   # noqa: F811
+    """A path's rows of equal parts with masked candidates between them, numbers that are borders between the
+    parts: sums in another order differ in their last bit, which must not let a masked candidate in."""
+    R = 4000
+    g = torch.Generator(device=dev).manual_seed(K)
+    n = (K - 1) // 2
+    part = torch.randn((R, n), generator=g, device=dev)
+    row = torch.full((R, K), -INF, device=dev)
+    row[:, :n], row[:, n + 1:2 * n + 1] = part, part
+    edges = row[:, None, None, :].expand(R, 1, K, K).contiguous()
+    ids = torch.arange(K, dtype=torch.int32, device=dev).expand(R, 1, K).contiguous()
+    path, _, probs = ds.dflash_sample_path(edges, ids, torch.full((R, 1), 0.5, device=dev))
+    of_pick = probs[:, 0].gather(1, path.long())
+    assert (of_pick > 0).all(), int((of_pick == 0).sum())
+    # exact sums: the first of the second part; off by a rounding, the last of the first part
+    assert ((path == n + 1) | (path == n - 1)).all()
+    clean()
