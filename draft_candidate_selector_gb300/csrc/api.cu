@@ -862,12 +862,14 @@ dflash_status dflash_rope_frequencies(int rotary_dim, double base, double factor
                                                        (turns_fast - turns_slow)));
             if (factor != 1.0) f = f / factor * (1.0 - keep) + f * keep;
         }
-        double turns = f / two_pi;
+        double turns = std::fabs(f) / two_pi;
         turns -= std::floor(turns);                          // whole turns do not show
-        // Two halves of 32 bits, each exact.
+        // Two halves of 32 bits, each exact. (Backward turns are those forward, negated: the rest of a small one to 1
+        // would be rounded to 2^-53.)
         const double high = std::floor(turns * 4294967296.0);
         const double low = std::floor((turns * 4294967296.0 - high) * 4294967296.0 + 0.5);
-        frequencies[j] = (int64_t)(((uint64_t)high << 32) + (uint64_t)low);
+        const uint64_t whole = ((uint64_t)high << 32) + (uint64_t)low;
+        frequencies[j] = (int64_t)(f < 0 ? 0 - whole : whole);
     }
     return ok();
 }
