@@ -861,6 +861,9 @@ dflash_status dflash_rope_frequencies(int rotary_dim, double base, double factor
                 keep = std::min(1.0, std::max(0.0, (original_len * f / two_pi - turns_slow) /
                                                        (turns_fast - turns_slow)));
             if (factor != 1.0) f = f / factor * (1.0 - keep) + f * keep;
+            if (!std::isfinite(f))
+                return fail(DFLASH_INVALID_ARGUMENT, "the frequency of pair %d is not finite: base=%g, factor=%g", j,
+                            base, factor);
         }
         double turns = std::fabs(f) / two_pi;
         turns -= std::floor(turns);                          // whole turns do not show

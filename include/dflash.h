@@ -495,6 +495,7 @@ dflash_status dflash_store_kv(const void* key, const void* value, int dtype, con
  *              positions is, one that makes turns_fast or more is not, and in between f_j goes over
  *              linearly in the number of turns from the one to the other.
  * frequencies  host, [rotary_dim / 2] out: copy them to device memory
+ * A frequency that is not finite is refused.
  * A host function: no device is needed, and nothing is launched.
  * ---------------------------------------------------------------------------------- */
 dflash_status dflash_rope_frequencies(int rotary_dim, double base, double factor,
