@@ -869,6 +869,26 @@ __device__ __forceinline__ int first_thread(bool here, ChooseShared& sh) {
     return owner == INT_MAX ? -1 : owner;
 }
 
+// The tile to look in after `tile` where `from` has nothing to draw: the nearest behind it with any weight, then the
+// nearest before it; -1: none is left. sums: the row's tiles', each a Two. The whole block.
+__device__ __noinline__ int next_tile(const float2* sums, int tiles, int from, int tile, ChooseShared& sh) {
+    const int tid = threadIdx.x;
+    if (tile >= from) {
+        for (int t0 = tile + 1; t0 < tiles; t0 += kChooseThreads) {
+            __syncthreads();
+            const int at = first_thread(t0 + tid < tiles && __ldcg(&sums[min(t0 + tid, tiles - 1)]).x > 0.f, sh);
+            if (at >= 0) return t0 + at;
+        }
+        tile = from;
+    }
+    for (int t0 = tile - 1; t0 >= 0; t0 -= kChooseThreads) {
+        __syncthreads();
+        const int at = first_thread(t0 - tid >= 0 && __ldcg(&sums[max(t0 - tid, 0)]).x > 0.f, sh);
+        if (at >= 0) return t0 - at;
+    }
+    return -1;
+}
+
 template <typename T>
 struct Chooser {
     const VerifyPlan& p;
@@ -934,28 +954,6 @@ struct Chooser {
             if (lane == 0) sh.n_less = n;
         }
         __syncthreads();
-    }
-
-    // The tile to look in after `tile` where `from` has nothing to draw: the nearest behind it with any weight, then
-    // the nearest before it; -1: none is left.
-    __device__ __noinline__ int next_tile(long long row, float M, int from, int tile) {
-        const int tid = threadIdx.x;
-        if (tile >= from) {
-            for (int t0 = tile + 1; t0 < p.tiles; t0 += kChooseThreads) {
-                const int t = t0 + tid;
-                __syncthreads();
-                const int at = first_thread(t < p.tiles && rounded(tile_weight<Two>(row, t, M)) > 0.f, sh);
-                if (at >= 0) return t0 + at;
-            }
-            tile = from;
-        }
-        for (int t0 = tile - 1; t0 >= 0; t0 -= kChooseThreads) {
-            const int t = t0 - tid;
-            __syncthreads();
-            const int at = first_thread(t >= 0 && rounded(tile_weight<Two>(row, t, M)) > 0.f, sh);
-            if (at >= 0) return t0 - at;
-        }
-        return -1;
     }
 
     // Draws a token of the row, into sh.found; whether fp32 sums settle it. Z: the sum of weights.
@@ -1074,7 +1072,7 @@ struct Chooser {
             for (int k = 0; k < kWarps; ++k) holder = max(holder, sh.owner[k]);
             if (holder >= 0) break;
             // Nor has the tile any, where the candidates took all of it, and what was left of its sum was rounding.
-            tile = next_tile(row, M, sh.tile, tile);
+            tile = next_tile(p.sums + row * p.tiles, p.tiles, sh.tile, tile, sh);
             if (tile < 0) break;
         }
         if (!kExact && holder < 0) return false;
