@@ -830,7 +830,7 @@ struct ChooseShared {
     int n_less, less_at[kMaxK];
     Two less_q[kMaxK], less[kMaxK];
     // answers that one thread has for all
-    int tile, found, unsure;
+    int tile, found, unsure, taken;
     Two before;
     bool last;
 };
@@ -871,7 +871,7 @@ __device__ __forceinline__ int first_thread(bool here, ChooseShared& sh) {
 
 // The tile to look in after `tile` where `from` has nothing to draw: the nearest behind it with any weight, then the
 // nearest before it; -1: none is left. sums: the row's tiles', each a Two. The whole block.
-__device__ __noinline__ int next_tile(const float2* sums, int tiles, int from, int tile, ChooseShared& sh) {
+__device__ __forceinline__ int next_tile(const float2* sums, int tiles, int from, int tile, ChooseShared& sh) {
     const int tid = threadIdx.x;
     if (tile >= from) {
         for (int t0 = tile + 1; t0 < tiles; t0 += kChooseThreads) {
@@ -887,6 +887,37 @@ __device__ __noinline__ int next_tile(const float2* sums, int tiles, int from, i
         if (at >= 0) return t0 - at;
     }
     return -1;
+}
+
+// Where an exact draw's tile has no weight: the first token with some in the next tile that has any, into sh.found; in
+// a tile before it the last one. The whole block. (Apart from the draw, which it would slow down: seldom in need.)
+template <typename T>
+__device__ __noinline__ void draw_elsewhere(const VerifyPlan& p, long long row, float M, float t, ChooseShared& sh) {
+    const Row<T> x(p.a, row);
+    const Two inv_t = inverse(t);
+    const float2* sums = p.sums + row * p.tiles;
+    const int tid = threadIdx.x, from = sh.tile, taken = sh.taken;
+    int found = -1;
+    for (int tile = from; found < 0 && (tile = next_tile(sums, p.tiles, from, tile, sh)) >= 0;) {
+        const bool behind = tile > from;
+        const int lo = x.first(tile), hi = x.first(tile + 1);
+        unsigned best = 0;                                           // the nearer, the larger; 0: none
+        for (int v = lo + tid; v < hi; v += kChooseThreads) {
+            Two w = exp_two(to_float(x.x[v]), M, inv_t, sh.powers);
+            for (int k = 0; k < taken; ++k)
+                if (sh.less_at[k] == v) w = w > sh.less[k] ? w - sh.less[k] : Two{0.f, 0.f};
+            if (w > Two{0.f, 0.f}) best = max(best, (unsigned)(behind ? hi - v : v - lo + 1));
+        }
+        best = __reduce_max_sync(kFull, best);
+        __syncthreads();
+        if ((tid & 31) == 0) sh.owner[tid >> 5] = (int)best;
+        __syncthreads();
+        for (int k = 0; k < kWarps; ++k) best = max(best, (unsigned)sh.owner[k]);
+        if (best) found = behind ? hi - (int)best : lo + (int)best - 1;
+    }
+    __syncthreads();
+    if (tid == 0) sh.found = found >= 0 ? found : min(x.first(from), p.a.V - 1);
+    __syncthreads();
 }
 
 template <typename T>
@@ -994,6 +1025,7 @@ struct Chooser {
         const bool any = n_less == 0 || rounded(Z - lost) > (kExact ? 0x1p-36f : kSlack) * rounded(Z);
         if (!kExact && !any) return false;
         const int taken = any ? n_less : 0;          // nothing left over: from p itself
+        if (kExact && tid == 0) sh.taken = taken;
 #pragma unroll 1
         for (int k = 0; k < taken; ++k) {
             const int t = x.tile_of(sh.less_at[k]);
@@ -1027,13 +1059,10 @@ struct Chooser {
         constexpr int kEach = ((Row<T>::kTile + kN - 1 + kChooseThreads - 1) / kChooseThreads) | 1;   // odd: no bank conflicts
         static_assert(kEach * kChooseThreads * sizeof(F) <= kRoom, "a tile's weights fit");
         F* w = reinterpret_cast<F*>(sh.room);
-        const F* own = w + tid * kEach;
+        const int tile = sh.tile;
         const F before = *reinterpret_cast<F*>(&sh.before);
-        F here;
-        int tile = sh.tile, lo, holder;
-        for (;;) {
-            lo = x.first(tile);
-            const int n = x.first(tile + 1) - lo;
+        const int lo = x.first(tile), n = x.first(tile + 1) - lo;
+        {
             // A vector a thread; what is in none, one by one; 0 behind the end.
             int whole;
             const int skip = x.body(tile, whole) - lo;               // elements before the first vector
@@ -1050,33 +1079,30 @@ struct Chooser {
 #pragma unroll
                 for (int k = 0; k < kN; ++k) w[skip + tid * kN + k] = weight<F>(l[k], M, inv_t);
             }
-            __syncthreads();
-            if (tid < taken) {
-                const int e = sh.less_at[tid] - lo;
-                if (e >= 0 && e < n) w[e] = w[e] > less[tid] ? w[e] - less[tid] : zero;
-            }
-            __syncthreads();
-            run = zero;
+        }
+        __syncthreads();
+        if (tid < taken) {
+            const int e = sh.less_at[tid] - lo;
+            if (e >= 0 && e < n) w[e] = w[e] > less[tid] ? w[e] - less[tid] : zero;
+        }
+        __syncthreads();
+        const F* own = w + tid * kEach;
+        run = zero;
 #pragma unroll 1
-            for (int e = 0; e < kEach; ++e) run = run + own[e];
-            F in_tile;
-            here = before + block_scan(run, sh, in_tile);
-            holder = first_thread(run > zero && here > border, sh);
-            if (!kExact) break;
-            if (holder >= 0) break;
-            // The tile's sum and its elements' may differ by a rounding: then the last with any weight.
+        for (int e = 0; e < kEach; ++e) run = run + own[e];
+        F in_tile;
+        const F here = before + block_scan(run, sh, in_tile);
+        int holder = first_thread(run > zero && here > border, sh);
+        // The tile's sum and its elements' may differ by a rounding: then the last with any weight. (The tile may have
+        // none: where the candidates took all of it, rounding may have left some of its sum.)
+        if (holder < 0) {
+            if (!kExact) return false;
             __syncthreads();
             const unsigned b = __ballot_sync(kFull, run > zero);
             if ((tid & 31) == 0) sh.owner[tid >> 5] = b ? tid + 31 - __clz(b) : -1;
             __syncthreads();
             for (int k = 0; k < kWarps; ++k) holder = max(holder, sh.owner[k]);
-            if (holder >= 0) break;
-            // Nor has the tile any, where the candidates took all of it, and what was left of its sum was rounding.
-            tile = next_tile(p.sums + row * p.tiles, p.tiles, sh.tile, tile, sh);
-            if (tile < 0) break;
         }
-        if (!kExact && holder < 0) return false;
-        if (holder < 0 && tid == 0) sh.found = min(x.first(sh.tile), p.a.V - 1);
         if (tid == holder) {
             F at = here - run, after = at;
             int pick = -1;
@@ -1256,10 +1282,11 @@ struct Chooser {
         block_scan(mine, sh, Z);
         gather_less(u.i, u.i < n - 1, nullptr);
         draw<Two>(row, u.M, Z);
+        if (sh.found < 0) draw_elsewhere<T>(p, row, u.M, temp.t, sh);
         if (tid == 0) {
             const long long at = (long long)r * (a.S + 1) + u.i;
             a.tokens[at] = sh.found;
-            if (a.logprobs && sh.found >= 0)
+            if (a.logprobs)
                 a.logprobs[at] = (to_float(Row<T>(a, row).x[sh.found]) - u.M) / temp.t - logf(Z.h);
         }
     }
