@@ -644,7 +644,8 @@ def dflash_rope_frequencies(rotary_dim: int, base: float = 10000.0, factor: floa
     inv_freq [rotary_dim / 2] gives radians per position; without it they are
     base^(-2 j / rotary_dim). For long contexts they are divided by factor: all of them if
     original_len is 0, else those that make at most turns_slow turns over original_len positions,
-    those with turns_fast or more not at all, and the others in between.
+    those with turns_fast or more not at all, and the others in between, linearly in their turns.
+    (Model configurations labelled yarn mostly go over in the pair's index j: give their inv_freq.)
     """
     lib = _native._lib or _native.load()
     out = torch.empty((max(rotary_dim, 0) // 2,), dtype=torch.int64)

@@ -12,8 +12,8 @@
 // for pair j of the first rotary_dim values: (j, j + rotary_dim / 2), or (2j, 2j + 1) interleaved.
 //
 // Angles: f_j is kept in turns, as a whole number of 2^-64, so position * f_j modulo one turn is
-// the low 64 bits of an integer product: what is left of f_j's own rounding is 2^-33 of a turn at
-// position 2^31.
+// the low 64 bits of an integer product, exact for the f_j that is kept. That one is made in doubles, off by a
+// few 2^-53 of itself, and rounded to 2^-64: within 2^-25.5 of a turn at position 2^31 for base 10^4, 2^-24.3 for 10^6.
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -399,10 +399,12 @@ struct Rows {
     }
 };
 
-// Bound by memory and, into an e4m3 cache, as much by instructions: 55 to 64% of the issue slots go to 227
+// Bound by memory and, into an e4m3 cache, as much by instructions: 55 to 64% of the issue slots go to 235
 // instructions for every four rows of 128. 40001 tokens of 32 + 8 + 8 heads of 128: with a bf16 cache 175 us, 984 MB,
 // 5.6 TB/s; with an e4m3 cache 174 us, 902 MB, 5.2 TB/s. 16411 tokens of 48 heads of 64, rotated by halves: 39 us, 202 MB.
-// One token: 5 us. (Two rows loaded ahead instead of one, 80 registers: 171 and 190 us for the first two, 181 in CTAs of
+// 8 key and 8 value heads of 128 of 20001 tokens, without queries: 42 us, 164 MB. One token: 5 us. An e4m3 scale that is
+// no power of two is divided by: 201 us for both scales of that kind, 188 for one of them, 176 for none (the same bits).
+// (Two rows loaded ahead instead of one, 80 registers: 171 and 190 us for the first two, 181 in CTAs of
 // 128 threads; two CTAs an SM: 196 and 204; single floats instead of pairs: 5 us more.)
 template <typename T, bool kInterleaved, int kUnit, bool kFull>
 __global__ void __launch_bounds__(kThreads, kBlocks)
@@ -493,7 +495,8 @@ cudaError_t launch_norm_rope(const DeviceInfo& dev, const NormRopeArgs& a, uint3
     // Tokens of a CTA, up to 16 KB of cosines and sines: the number that makes waves times a CTA's time
     // least, which is its rounds of rows, each kind's rounded up, and about kFixed rounds for cosines, sines and
     // weights. (Without kFixed 183 us instead of 175 for 40001 tokens of 48 heads of 128, 80 instead of 69 at
-    // head_dim 80; kFixed = 8 the same as 2; one token a CTA 350 us, and 116 instead of 18 with 8 heads of keys only.)
+    // head_dim 80; kFixed = 8 the same as 2; one token a CTA 350 us, and 116 instead of 18 with one query and one key head
+    // of 128 of 20001 tokens.)
     constexpr int kFixed = 2;
     const long long groups = kThreads / p.lanes, resident = (long long)kBlocks * dev.sm_count;
     long long least = LLONG_MAX;

@@ -31,8 +31,8 @@
 //
 // Rows behind the first rejected draft are not needed. Where the batch is large, row_sums goes through
 // the requests' first rows, then their second ones, and so on; the warp that finishes a row looks whether
-// its draft is surely rejected, and later rows of that request are passed over.
-// Bound by HBM: the rows up to the first rejected draft are read once.
+// its draft is surely rejected, and later rows of that request are passed over. (64 requests of 16 rows of 151936 bf16
+// logits, all but 50 of a row masked and the first drafts among the masked: 68 of 315 MB are read, in 46 us.)
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -1350,7 +1350,9 @@ __global__ void __launch_bounds__(kChooseThreads) settle_kernel(const __grid_con
 size_t padded_bytes(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t list_bytes(int R) { return padded_bytes(16 + (size_t)R * sizeof(Unsettled)); }
 // (Counters are by position and request, (S + 1) R of them, of which at most T + R are of use: where they are more
-// than 4 (T + R), because few requests have many rows, rows are not passed over.)
+// than 4 (T + R), because few requests have many rows, rows are not passed over. 512 requests of up to 16 rows of 151936
+// bf16 logits, 1535 and 1536 rows in all, read whole and passed over: 218 and 189 us; 68 and 69 of them with 16 rows, the others
+// with one: 255 and 239. Read whole, each empty place is looked at: 512 single rows 200 us with S = 0, 233 with S = 15.)
 size_t counter_bytes(int R, int T) { return padded_bytes((4 * ((size_t)T + R) + R + 8) * 4); }
 
 int tiles_of(int V, int size) {

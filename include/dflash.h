@@ -486,14 +486,17 @@ dflash_status dflash_store_kv(const void* key, const void* value, int dtype, con
 
 /* ------------------------------------------------------------------------------------
  * Rotation frequencies, as the calls below take them: the turns that pair j of a head makes from
- * one position to the next, f_j / (2 pi) modulo 1, as a whole number of 2^-64. Angles are then exact
- * modulo one turn at every position of 32 bits.
+ * one position to the next, f_j / (2 pi) modulo 1, as a whole number of 2^-64. Angles are exact modulo one
+ * turn at every position of 32 bits for the frequency that is kept, which is off by a few 2^-53 of itself and
+ * half of 2^-64.
  *
  * inv_freq     host, [rotary_dim / 2] radians per position; or NULL, and then
  *              f_j = base^(-2 j / rotary_dim), for long contexts divided by factor: every pair if
  *              original_len is 0; else a pair that makes at most turns_slow turns over original_len
  *              positions is, one that makes turns_fast or more is not, and in between f_j goes over
- *              linearly in the number of turns from the one to the other.
+ *              linearly in the number of turns from the one to the other. (Rules that go over in the
+ *              pair's index j, as model configurations labelled yarn usually mean, are not this one: give
+ *              their inv_freq.)
  * frequencies  host, [rotary_dim / 2] out: copy them to device memory
  * A frequency that is not finite is refused.
  * A host function: no device is needed, and nothing is launched.
