@@ -43,6 +43,32 @@ def test_tiles_that_the_draft_takes_whole(dev, dtype, at):                      
         assert torch.isfinite(x).all() and not (got[0][:, :1] == b.ids[:, 0]).any()
 
 
+@pytest.mark.parametrize("where", ["first", "last"])
+@pytest.mark.parametrize("dtype", [F32, BF, FP])
+def test_little_left_beside_a_tile(dev, dtype, where):                                # noqa: F811
+    """All but about 2^-30 of a row is in one tile, which the draft takes whole; rounding is 2^-46 of the row, far more
+    than from the border to the end of what is left. That is four like tokens in a tile far behind or before."""
+    R, V, K = 200, 20008, 8
+    b = Batch(dev, [2] * R, V, 1, K, dtype, likely=False, seed=5)
+    g = torch.Generator(device=dev).manual_seed(9)
+    tile = 4096 // b.logits.element_size()
+    first, other = (0, 15000) if where == "first" else (V // tile * tile, 2100)
+    ids = first + torch.rand((R, min(tile, V - first)), generator=g, device=dev).argsort(1)[:, :K]
+    x = torch.full((2 * R, V), -INF, device=dev)
+    top = 8 + 1.5 * torch.randn((R, K), generator=g, device=dev)
+    x[::2].scatter_(1, ids, top)
+    x[::2, other:other + 40:10] = (top.logsumexp(1) - 22.2)[:, None]
+    x[1::2, 7] = 0.0
+    b.logits = x.to(dtype)
+    p = torch.softmax(b.logits[::2].double(), 1).gather(1, ids)
+    b.ids, b.probs = ids.to(torch.int32)[:, None].contiguous(), (p * 1.0001).float()[:, None].contiguous()
+    b.drafts = b.ids[:, :, 0].contiguous()
+    b.accept.fill_(1 - 2.0 ** -24)
+    for u, token in ((0.0, other), (1 - 2.0 ** -24, other + 30)):
+        b.sample.fill_(u)
+        assert (b.check()[0][:, 0] == token).all()
+
+
 @pytest.mark.parametrize("K", [7, 13, 32])
 def test_masked_candidates(dev, K):                                                   # noqa: F811
     """A path's rows of equal parts with masked candidates between them, numbers that are borders between the
